@@ -546,6 +546,150 @@ ha_status hash_attn_merge_n(const float* outs, int64_t out_seg_stride, const flo
                             int32_t d, void* stream);
 
 /*
+ * ---- Prompts and chunks of new tokens: append, prefill, chunk ----
+ *
+ * The decode step above reads a cache that something has filled, and follows a
+ * prompt that something has attended over. These calls do both, for batches of
+ * sequences of different lengths whose new tokens are packed one after the other:
+ * the rows of sequence s are cu[s] .. cu[s + 1) of q, k, v, out and lse.
+ *
+ * hash_attn_append writes new keys and values into a cache of pages, rotating
+ * keys (and queries) by their positions on the way; hash_attn_chunk attends over
+ * such a cache, for one new token per sequence or for many; hash_attn_prefill
+ * attends over whole prompts whose K and V are packed like the queries. All give
+ * (out, lse) pairs that hash_attn_merge and hash_attn_merge_n join with others.
+ * A cache of one page per sequence (page_size = n_cap, table[s] = s) is the cache
+ * [batch, h_kv, n_cap, d] that hash_attn_decode reads.
+ *
+ * ha_tokens: the packed new tokens.
+ *   n_seq      sequences (>= 1); total: rows of q, k, v, out, lse (0: the call does
+ *              nothing). Rows that no sequence owns are neither read for a result
+ *              nor written.
+ *   h_q, h_kv, d   as ha_shape; h_q % h_kv == 0
+ *   dtype      ha_dtype of q, k and v
+ *   out_dtype  ha_dtype of out (prefill, chunk). HA_F32 results are float32
+ *              throughout; HA_BF16 results round the attention weights to bf16
+ *              before they meet V, and the output at the end
+ *   reserved   must be 0
+ *   q [total, h_q, d], k and v [total, h_kv, d] at x + row * x_st + head * x_sh,
+ *              d contiguous
+ * The strides of an extent over 1 are at least d; rows start on 16-byte
+ * boundaries (pointers, and strides times the element size).
+ */
+typedef struct {
+    int32_t n_seq, total, h_q, h_kv, d;
+    int32_t dtype, out_dtype, reserved;
+    int64_t q_st, q_sh;
+    int64_t k_st, k_sh;
+    int64_t v_st, v_sh;
+} ha_tokens;
+
+/*
+ * A cache of pages. Token i of sequence s is row i % page_size of page
+ * table[s * table_st + i / page_size]; table entries past a sequence's last token
+ * are not read. K [n_pages, h_kv, page_size, d] at K + page * k_sp + head * k_sh +
+ * row * k_sn (any order in memory: [page, token, head, d] as well), V likewise, and
+ * the keys' codes k_sig at k_sig + page * ks_sp + head * ks_sh + row.
+ * Requirements: n_pages, page_size, max_pages >= 1; max_pages * page_size <= 2^30;
+ * table_st >= max_pages for more than one sequence; strides and alignment as
+ * ha_tokens; for hash_attn_chunk, page_size is a multiple of 16, or max_pages is 1.
+ */
+typedef struct {
+    int32_t dtype;                     /* ha_dtype of K and V */
+    int32_t n_pages, page_size;
+    int32_t max_pages;                 /* pages per sequence that the table has room for */
+    int64_t table_st;                  /* entries between the table's rows */
+    int64_t k_sp, k_sh, k_sn;
+    int64_t v_sp, v_sh, v_sn;
+    int64_t ks_sp, ks_sh;              /* only read when codes are written */
+} ha_cache;
+
+/*
+ * Rotary position rotation: pair p < rot_dim / 2 of a row at position pos turns by
+ * the angle pos * inv_freq[p]. The pairs are (x[p], x[p + rot_dim / 2]), or with
+ * interleaved = 1 (x[2 p], x[2 p + 1]); dims from rot_dim on stay as they are.
+ *   inv_freq  float32 [rot_dim / 2], device, finite
+ *   rot_dim   a multiple of 16, 16 <= rot_dim <= d
+ * The angle is exact modulo a turn to 2^-31 of a half turn at every position.
+ */
+typedef struct {
+    const float* inv_freq;
+    int32_t rot_dim;
+    int32_t interleaved;
+} ha_rope;
+
+/*
+ * Append the packed new tokens to the cache. seq_lens[s] is sequence s's length
+ * with its new tokens in: the new token i of nq sits at position
+ * seq_lens[s] - nq + i.
+ *   rope        the rotation of q and k by the position, or NULL (none)
+ *   q, q_out    queries to rotate, and where they go: contiguous [total, h_q, d] of
+ *               tokens->dtype (q itself, if that is contiguous). Both NULL: none.
+ *   k, v        the new keys and values (tokens->dtype); stored in cache->dtype
+ *               (HA_F32 or HA_BF16, each from either)
+ *   W, k_sig    float32 [h_kv, 32, d] and the code pool, or both NULL: also writes the
+ *               sign-projection code of every appended key as it is stored (the same
+ *               bits as hash_attn_encode_keys)
+ *   cu          int32 [n_seq + 1], seq_lens int32 [n_seq], table (device)
+ *   dev_flags   optional device uint32; bits are OR-ed in: HA_DEVERR_SEQLEN for a
+ *               sequence with bad bounds (cu outside [0, total] or falling, seq_lens
+ *               outside [0, max_pages * page_size]): none of its tokens is written;
+ *               HA_DEVERR_INDEX for a position below 0 (that token is skipped) or a
+ *               table entry outside [0, n_pages) (its keys and values are skipped).
+ * Two tokens that share a place in the pool (a page given twice) leave one of them
+ * there, not said which.
+ * Errors: HA_ERR_INVALID_ARG / HA_ERR_UNSUPPORTED before anything is enqueued.
+ */
+ha_status hash_attn_append(const ha_tokens* tokens, const ha_cache* cache, const ha_rope* rope, const void* q,
+                           const void* k, const void* v, const float* W, const int32_t* table, const int32_t* cu,
+                           const int32_t* seq_lens, void* q_out, void* K, void* V, uint32_t* k_sig,
+                           uint32_t* dev_flags, void* stream);
+
+/*
+ * Bytes of workspace that hash_attn_prefill and hash_attn_chunk need for these
+ * tokens (n_seq, total, h_q, h_kv, d are read). Its first word is the device error
+ * word (hash_attn_workspace_init zeroes it, hash_attn_device_status reads it); the
+ * rest needs no zeroing and carries nothing from call to call, so one workspace
+ * sized for the largest total and head counts serves calls in turn.
+ */
+ha_status hash_attn_packed_workspace_size(const ha_tokens* tokens, size_t* bytes);
+
+/*
+ * Causal attention over whole prompts: token i of a sequence attends to its tokens
+ * 0 .. i, query head h to KV head h / (h_q / h_kv), scores scaled by 1 / sqrt(d).
+ *   q, K, V    packed (ha_tokens), HA_BF16
+ *   cu         int32 [n_seq + 1] (device), 0 <= cu[s] <= cu[s + 1] <= total; a
+ *              sequence that breaks this is skipped and flagged HA_DEVERR_SEQLEN
+ *   out        contiguous [total, h_q, d] of out_dtype, 16-byte aligned
+ *   lse        float32 [total, h_q] (natural log)
+ *   workspace  >= hash_attn_packed_workspace_size bytes, 256-byte aligned
+ * h_q / h_kv <= 128. V must be finite within a sequence (a weight of 0 multiplies
+ * tokens that a row does not see); what lies outside it does not matter.
+ * Errors: HA_ERR_INVALID_ARG, HA_ERR_UNSUPPORTED (an HA_F32 q, K or V; more than
+ * 128 query heads per KV head; strides that a tensor map cannot hold),
+ * HA_ERR_WORKSPACE before launch; HA_ERR_CUDA on a failed launch.
+ */
+ha_status hash_attn_prefill(const ha_tokens* tokens, const void* q, const void* K, const void* V, const int32_t* cu,
+                            void* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Attention of each sequence's new tokens over its pages of the cache, causal from
+ * the end: the new token i of nq attends to the keys j <= seq_lens[s] - nq + i (the
+ * new tokens' own keys are in the cache already). nq = 1 is a decode step. A row
+ * that sees no key gives out = 0, lse = -inf.
+ *   q          packed queries (HA_BF16; tokens' k_* and v_* strides are not read)
+ *   K, V       the pools (HA_BF16)
+ *   table, cu, seq_lens   as hash_attn_append; a sequence with bad cu is skipped,
+ *              one with a bad seq_lens counts as empty of keys (both flagged
+ *              HA_DEVERR_SEQLEN); a bad table entry counts as a page of zeros
+ *              (flagged HA_DEVERR_INDEX)
+ *   out, lse, workspace, limits and errors as hash_attn_prefill
+ */
+ha_status hash_attn_chunk(const ha_tokens* tokens, const ha_cache* cache, const void* q, const void* K, const void* V,
+                          const int32_t* table, const int32_t* cu, const int32_t* seq_lens, void* out, float* lse,
+                          void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Synchronise `stream`, read and clear the workspace's device error word.
  * Returns HA_OK, HA_ERR_TIMEOUT (timeout flag set) or HA_ERR_DEVICE (any other
  * flag); *flags (optional) receives the raw HA_DEVERR_* bits.

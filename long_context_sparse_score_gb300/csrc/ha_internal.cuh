@@ -286,6 +286,55 @@ struct RecallParams {
     float* recall;
 };
 
+// An item (sequence, KV head, tokens row0 .. row0 + tokens) whose keys span CTAs:
+// the CTA where it begins and the parts - 1 that follow.
+struct SplitItem {
+    int parts, row0, head, tokens;
+};
+
+// k_packed_att: causal attention of packed queries over packed (seq_lens and
+// table null) or paged keys.
+struct PackedParams {
+    const int32_t* cu;         // [n_seq + 1] first row of every sequence's new tokens
+    const int32_t* seq_lens;   // [n_seq] keys of every sequence, or null: its new tokens
+    const int32_t* table;      // [n_seq] rows of pages, table_st apart, or null: K and V packed like q
+    int64_t table_st;
+    int n_seq, total;
+    int Hq, Hkv, G, TQ;        // TQ tokens x G heads in a tile of 128 rows
+    int page_size, n_pages, max_len;
+    int box_log2;              // rows of a K/V copy: 2^box_log2
+    void* out;
+    float* lse;
+    uint32_t* err;
+    SplitItem* items;          // [grid] (workspace)
+    float2* part_ml;           // [2 grid][slot_rows] (m, l) of a part (workspace)
+    float* part_o;             // [2 grid][slot_rows][d] unnormalised O of a part
+    int slot_rows;
+    float qscale;              // log2(e) / sqrt(d)
+};
+
+// k_append: rotation of queries and keys, keys and values into the cache.
+struct AppendParams {
+    const void *q, *k, *v;     // q may be null
+    int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh;
+    void* q_out;
+    char *K, *V;
+    int64_t k_sp, k_sc, k_sn, v_sp, v_sc, v_sn;  // page, head and token strides of the cache (elements)
+    const int32_t* cu;
+    const int32_t* seq_lens;
+    const int32_t* table;
+    int64_t table_st;
+    int n_seq, total, Hq, Hkv, d;
+    int page_size, n_pages, max_len;
+    const float* inv_freq;     // null: no rotation
+    int rot, inter;
+    const float* W;            // [Hkv][32][d] or null: no codes
+    uint32_t* codes;
+    int64_t c_sp, c_sh;
+    uint32_t* flags;           // optional HA_DEVERR_* word
+    int row_splits;            // CTAs that share a block of tokens (k_append)
+};
+
 struct MergeNParams {
     const float* outs; int64_t out_seg_stride;
     const float* lses; int64_t lse_seg_stride;
@@ -345,6 +394,10 @@ cudaError_t launch_scores_tc(const ExactParams& p, int d, cudaStream_t st, bool*
 cudaError_t launch_recall(const RecallParams& p, cudaStream_t st);
 cudaError_t launch_score_wide(const WideParams& p, int batch_hkv, cudaStream_t st);
 cudaError_t launch_select_wide(const WideParams& p, int batch_hkv, cudaStream_t st, bool pdl);
+
+// Keys per tile of k_packed_att.
+int packed_key_tile(bool f32_out);
+cudaError_t launch_append(const AppendParams& p, bool in_bf16, bool cache_bf16, cudaStream_t st);
 
 // Query-head groups per KV head: group g of k per KV head reads KV head g / k. The
 // kernels divide by a multiply-high with kv_magic(k) = ceil(2^32 / k), exact for

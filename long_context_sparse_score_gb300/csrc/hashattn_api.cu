@@ -6,10 +6,11 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 
-#include "ha_internal.cuh"
+#include "tc_common.cuh"
 
 namespace ha {
 
@@ -1380,5 +1381,269 @@ extern "C" ha_status hash_attn_gather_att_noalloc(const ha_shape* shape, const v
         e = cudaMemcpyAsync(dev_flags, ws, sizeof(uint32_t), cudaMemcpyDeviceToDevice, st);
         if (e != cudaSuccess) return cuda_fail(e, "copying the error word");
     }
+    return HA_OK;
+}
+
+// ---------------------------------------------------------------- packed tokens: append, prefill, chunk
+
+namespace ha {
+namespace {
+
+constexpr int64_t kMaxKeys = (int64_t)1 << 30;     // max_pages * page_size
+constexpr int64_t kMaxStride = (int64_t)1 << 36;   // elements; a tensor map holds strides below 2^40 bytes
+constexpr int kMaxGroup = 128;                     // query heads per KV head in a tile of 128 rows
+
+ha_status check_tokens(const ha_tokens* t) {
+    if (t == nullptr) return fail(HA_ERR_INVALID_ARG, "tokens is NULL");
+    if (t->n_seq < 1 || t->n_seq > (1 << 20)) return fail(HA_ERR_INVALID_ARG, "n_seq must be in [1, 2^20] (got %d)", t->n_seq);
+    if (t->total < 0 || t->total > kMaxCap)
+        return fail(HA_ERR_INVALID_ARG, "total must be in [0, %lld] (got %d)", (long long)kMaxCap, t->total);
+    if (t->h_q < 1 || t->h_kv < 1 || t->h_q > (1 << 14) || t->h_q % t->h_kv != 0)
+        return fail(HA_ERR_INVALID_ARG, "h_q must be a multiple of h_kv, in [1, 2^14] (got %d, %d)", t->h_q, t->h_kv);
+    if (t->d != 64 && t->d != 128) return fail(HA_ERR_UNSUPPORTED, "d must be 64 or 128 (got %d)", t->d);
+    if (t->dtype != HA_F32 && t->dtype != HA_BF16) return fail(HA_ERR_UNSUPPORTED, "dtype must be HA_F32 or HA_BF16 (got %d)", t->dtype);
+    if (t->reserved != 0) return fail(HA_ERR_INVALID_ARG, "ha_tokens.reserved must be zero");
+    return HA_OK;
+}
+
+// Rows of a tensor: pointer and strides (those of an extent over 1) on 16-byte boundaries.
+ha_status check_rows(const char* what, const void* ptr, int dtype, int d, std::initializer_list<std::pair<int64_t, int64_t>> dims) {
+    if (ptr == nullptr) return fail(HA_ERR_INVALID_ARG, "%s is NULL", what);
+    if (!aligned16(ptr)) return fail(HA_ERR_INVALID_ARG, "%s must be 16-byte aligned", what);
+    for (const auto& [extent, stride] : dims) {
+        if (extent <= 1) continue;
+        if (stride < d || stride > kMaxStride)
+            return fail(HA_ERR_INVALID_ARG, "strides of %s must be in [d, 2^36] (got %lld)", what, (long long)stride);
+        if (stride * elem_size(dtype) % 16 != 0)
+            return fail(HA_ERR_INVALID_ARG, "strides of %s times the element size must be multiples of 16 bytes", what);
+    }
+    return HA_OK;
+}
+
+ha_status check_cache(const ha_cache* c, const ha_tokens* t, const void* K, const void* V, const int32_t* table) {
+    if (c == nullptr) return fail(HA_ERR_INVALID_ARG, "cache is NULL");
+    if (c->dtype != HA_F32 && c->dtype != HA_BF16)
+        return fail(HA_ERR_UNSUPPORTED, "the cache's dtype must be HA_F32 or HA_BF16 (got %d)", c->dtype);
+    if (c->n_pages < 1 || c->page_size < 1 || c->max_pages < 1 || (int64_t)c->max_pages * c->page_size > kMaxKeys)
+        return fail(HA_ERR_INVALID_ARG, "n_pages, page_size and max_pages must be >= 1 and max_pages * page_size <= 2^30 (got %d, %d, %d)",
+                    c->n_pages, c->page_size, c->max_pages);
+    if (table == nullptr) return fail(HA_ERR_INVALID_ARG, "table is NULL");
+    if (t->n_seq > 1 && c->table_st < c->max_pages)
+        return fail(HA_ERR_INVALID_ARG, "table_st (%lld) must be at least max_pages (%d)", (long long)c->table_st, c->max_pages);
+    HA_TRY(check_rows("K", K, c->dtype, t->d, {{c->n_pages, c->k_sp}, {t->h_kv, c->k_sh}, {c->page_size, c->k_sn}}));
+    return check_rows("V", V, c->dtype, t->d, {{c->n_pages, c->v_sp}, {t->h_kv, c->v_sh}, {c->page_size, c->v_sn}});
+}
+
+struct PackedLayout {
+    int grid_max = kSMs;
+    int tq = 1, slot_rows = 256;
+    size_t off_items = 0, off_ml = 0, off_o = 0, total = 0;
+};
+
+PackedLayout packed_layout(const ha_tokens* t) {
+    PackedLayout L;
+    const int G = t->h_q / t->h_kv;
+    L.tq = kMaxGroup / G;
+    // a batch of at most one row tile has no more rows than it has
+    if (t->total <= L.tq) L.slot_rows = (int)align_up((size_t)(t->total > 0 ? t->total : 1) * G, 8);
+    size_t off = 256;
+    L.off_items = off;
+    off = align_up(off + sizeof(SplitItem) * kSMs, 256);
+    L.off_ml = off;
+    off = align_up(off + (size_t)2 * kSMs * L.slot_rows * sizeof(float2), 256);
+    L.off_o = off;
+    off = align_up(off + (size_t)2 * kSMs * L.slot_rows * t->d * sizeof(float), 256);
+    L.total = off;
+    return L;
+}
+
+bool encode_map(CUtensorMap* m, const void* base, int d, const int64_t (&extent)[3], const int64_t (&stride)[3], int box1, int box2) {
+    const EncodeTiledFn enc = encode_fn();
+    if (enc == nullptr) return false;
+    cuuint64_t dim[4] = {(cuuint64_t)d, 0, 0, 0}, str[3];
+    for (int i = 0; i < 3; ++i) {
+        dim[i + 1] = (cuuint64_t)extent[i];
+        str[i] = (cuuint64_t)(extent[i] > 1 ? stride[i] : d) * 2u;
+    }
+    const cuuint32_t box[4] = {64u, (cuuint32_t)box1, (cuuint32_t)box2, 1u}, unit[4] = {1u, 1u, 1u, 1u};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dim, str, box, unit,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// prefill (cache null: K and V packed like q) and chunk
+ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q, const void* K, const void* V,
+                           const int32_t* table, const int32_t* cu, const int32_t* seq_lens, void* out, float* lse,
+                           void* workspace, size_t ws_bytes, void* stream) {
+    HA_TRY(check_tokens(t));
+    if (t->dtype != HA_BF16 || (c != nullptr && c->dtype != HA_BF16))
+        return fail(HA_ERR_UNSUPPORTED, "prefill and chunk take bf16 q, K and V");
+    if (t->out_dtype != HA_F32 && t->out_dtype != HA_BF16)
+        return fail(HA_ERR_UNSUPPORTED, "out_dtype must be HA_F32 or HA_BF16 (got %d)", t->out_dtype);
+    const int G = t->h_q / t->h_kv;
+    if (G > kMaxGroup) return fail(HA_ERR_UNSUPPORTED, "at most %d query heads per KV head (got %d)", kMaxGroup, G);
+    if (cu == nullptr || lse == nullptr || (c != nullptr && seq_lens == nullptr))
+        return fail(HA_ERR_INVALID_ARG, "cu, seq_lens and lse must not be NULL");
+    if (out == nullptr || !aligned16(out)) return fail(HA_ERR_INVALID_ARG, "out must not be NULL and must be 16-byte aligned");
+    HA_TRY(check_rows("q", q, t->dtype, t->d, {{t->total, t->q_st}, {t->h_q, t->q_sh}}));
+    if (c != nullptr) {
+        HA_TRY(check_cache(c, t, K, V, table));
+        if (c->max_pages > 1 && c->page_size % 16 != 0)
+            return fail(HA_ERR_UNSUPPORTED, "page_size must be a multiple of 16 (got %d)", c->page_size);
+    } else {
+        HA_TRY(check_rows("K", K, t->dtype, t->d, {{t->total, t->k_st}, {t->h_kv, t->k_sh}}));
+        HA_TRY(check_rows("V", V, t->dtype, t->d, {{t->total, t->v_st}, {t->h_kv, t->v_sh}}));
+    }
+    const PackedLayout L = packed_layout(t);
+    Layout ws{};
+    ws.total = L.total;
+    HA_TRY(check_ws(ws, workspace, ws_bytes));
+    if (t->total == 0) return HA_OK;
+
+    const bool f32 = t->out_dtype == HA_F32;
+    const int kt = packed_key_tile(f32);
+    PackedParams p{};
+    p.cu = cu;
+    p.n_seq = t->n_seq;
+    p.total = t->total;
+    p.Hq = t->h_q;
+    p.Hkv = t->h_kv;
+    p.G = G;
+    p.TQ = L.tq;
+    p.out = out;
+    p.lse = lse;
+    p.err = at<uint32_t>(workspace, 0);
+    p.items = at<SplitItem>(workspace, L.off_items);
+    p.part_ml = at<float2>(workspace, L.off_ml);
+    p.part_o = at<float>(workspace, L.off_o);
+    p.slot_rows = L.slot_rows;
+    p.qscale = (float)(1.4426950408889634 / std::sqrt((double)t->d));
+    PackedMaps m;
+    // rows of a copy: a tile never crosses the end of a sequence's only page; else
+    // the largest power of two that divides a page
+    int box = kt;
+    bool ok = encode_map(&m.q, q, t->d, {G, t->total, t->h_kv}, {t->q_sh, t->q_st, G * t->q_sh}, G, L.tq);
+    if (c != nullptr) {
+        p.seq_lens = seq_lens;
+        p.table = table;
+        p.table_st = c->table_st;
+        p.page_size = c->page_size;
+        p.n_pages = c->n_pages;
+        p.max_len = c->max_pages * c->page_size;
+        if (c->max_pages > 1 && (c->page_size & -c->page_size) < box) box = c->page_size & -c->page_size;
+        ok = ok && encode_map(&m.k, K, t->d, {c->page_size, t->h_kv, c->n_pages}, {c->k_sn, c->k_sh, c->k_sp}, box, 1) &&
+             encode_map(&m.v, V, t->d, {c->page_size, t->h_kv, c->n_pages}, {c->v_sn, c->v_sh, c->v_sp}, box, 1);
+    } else {
+        p.max_len = t->total;
+        ok = ok && encode_map(&m.k, K, t->d, {t->total, t->h_kv, 1}, {t->k_st, t->k_sh, 0}, box, 1) &&
+             encode_map(&m.v, V, t->d, {t->total, t->h_kv, 1}, {t->v_st, t->v_sh, 0}, box, 1);
+    }
+    if (!ok) return fail(HA_ERR_UNSUPPORTED, "the tensor-map encoder refused the layout of q, K or V");
+    p.box_log2 = 0;
+    while ((1 << p.box_log2) < box) ++p.box_log2;
+    // no more CTAs than the lengths can fill with a tile each, and no merge where an item is one tile
+    const int64_t tiles = ceil_div(p.max_len, kt);
+    const int64_t items = (ceil_div(t->total, 2 * L.tq) + t->n_seq) * t->h_kv;
+    const int grid = (int)std::min<int64_t>(kSMs, items * tiles);
+    HA_LAUNCH(launch_packed_att(p, m, t->d, f32, grid, grid > 1 && tiles > 1, static_cast<cudaStream_t>(stream)),
+              "packed attention launch");
+    return HA_OK;
+}
+
+}  // namespace
+}  // namespace ha
+
+extern "C" ha_status hash_attn_packed_workspace_size(const ha_tokens* tokens, size_t* bytes) {
+    if (bytes == nullptr) return fail(HA_ERR_INVALID_ARG, "bytes is NULL");
+    HA_TRY(check_tokens(tokens));
+    if (tokens->h_q / tokens->h_kv > kMaxGroup)
+        return fail(HA_ERR_UNSUPPORTED, "at most %d query heads per KV head", kMaxGroup);
+    *bytes = packed_layout(tokens).total;
+    return HA_OK;
+}
+
+extern "C" ha_status hash_attn_prefill(const ha_tokens* tokens, const void* q, const void* K, const void* V, const int32_t* cu,
+                                       void* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+    return packed_attention(tokens, nullptr, q, K, V, nullptr, cu, nullptr, out, lse, workspace, ws_bytes, stream);
+}
+
+extern "C" ha_status hash_attn_chunk(const ha_tokens* tokens, const ha_cache* cache, const void* q, const void* K, const void* V,
+                                     const int32_t* table, const int32_t* cu, const int32_t* seq_lens, void* out, float* lse,
+                                     void* workspace, size_t ws_bytes, void* stream) {
+    if (cache == nullptr) return fail(HA_ERR_INVALID_ARG, "cache is NULL");
+    return packed_attention(tokens, cache, q, K, V, table, cu, seq_lens, out, lse, workspace, ws_bytes, stream);
+}
+
+extern "C" ha_status hash_attn_append(const ha_tokens* tokens, const ha_cache* cache, const ha_rope* rope, const void* q,
+                                      const void* k, const void* v, const float* W, const int32_t* table, const int32_t* cu,
+                                      const int32_t* seq_lens, void* q_out, void* K, void* V, uint32_t* k_sig,
+                                      uint32_t* dev_flags, void* stream) {
+    const ha_tokens* t = tokens;
+    const ha_cache* c = cache;
+    HA_TRY(check_tokens(t));
+    HA_TRY(check_cache(c, t, K, V, table));
+    if (cu == nullptr || seq_lens == nullptr) return fail(HA_ERR_INVALID_ARG, "cu and seq_lens must not be NULL");
+    HA_TRY(check_rows("k", k, t->dtype, t->d, {{t->total, t->k_st}, {t->h_kv, t->k_sh}}));
+    HA_TRY(check_rows("v", v, t->dtype, t->d, {{t->total, t->v_st}, {t->h_kv, t->v_sh}}));
+    if ((q == nullptr) != (q_out == nullptr)) return fail(HA_ERR_INVALID_ARG, "q and q_out must both be given or both be NULL");
+    if (q != nullptr) {
+        HA_TRY(check_rows("q", q, t->dtype, t->d, {{t->total, t->q_st}, {t->h_q, t->q_sh}}));
+        if (!aligned16(q_out)) return fail(HA_ERR_INVALID_ARG, "q_out must be 16-byte aligned");
+        const bool packed = (t->h_q == 1 || t->q_sh == t->d) && (t->total <= 1 || t->q_st == (int64_t)t->h_q * t->d);
+        if (q == q_out && !packed) return fail(HA_ERR_INVALID_ARG, "q_out may be q only if q is contiguous");
+    }
+    if (rope != nullptr) {
+        if (rope->inv_freq == nullptr) return fail(HA_ERR_INVALID_ARG, "rope->inv_freq is NULL");
+        if (rope->rot_dim < 16 || rope->rot_dim > t->d || rope->rot_dim % 16 != 0)
+            return fail(HA_ERR_INVALID_ARG, "rope->rot_dim must be a multiple of 16 in [16, d] (got %d)", rope->rot_dim);
+        if (rope->interleaved != 0 && rope->interleaved != 1)
+            return fail(HA_ERR_INVALID_ARG, "rope->interleaved must be 0 or 1 (got %d)", rope->interleaved);
+    }
+    if ((W == nullptr) != (k_sig == nullptr)) return fail(HA_ERR_INVALID_ARG, "W and k_sig must both be given or both be NULL");
+    if (W != nullptr && ((t->h_kv > 1 && c->ks_sh < c->page_size) || (c->n_pages > 1 && c->ks_sp < c->page_size)))
+        return fail(HA_ERR_INVALID_ARG, "ks_sh and ks_sp must be at least page_size");
+    if (t->total == 0) return HA_OK;
+    AppendParams p{};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_st = t->q_st;
+    p.q_sh = t->q_sh;
+    p.k_st = t->k_st;
+    p.k_sh = t->k_sh;
+    p.v_st = t->v_st;
+    p.v_sh = t->v_sh;
+    p.q_out = q_out;
+    p.K = static_cast<char*>(K);
+    p.V = static_cast<char*>(V);
+    p.k_sp = c->k_sp;
+    p.k_sc = c->k_sh;
+    p.k_sn = c->k_sn;
+    p.v_sp = c->v_sp;
+    p.v_sc = c->v_sh;
+    p.v_sn = c->v_sn;
+    p.cu = cu;
+    p.seq_lens = seq_lens;
+    p.table = table;
+    p.table_st = c->table_st;
+    p.n_seq = t->n_seq;
+    p.total = t->total;
+    p.Hq = t->h_q;
+    p.Hkv = t->h_kv;
+    p.d = t->d;
+    p.page_size = c->page_size;
+    p.n_pages = c->n_pages;
+    p.max_len = c->max_pages * c->page_size;
+    if (rope != nullptr) {
+        p.inv_freq = rope->inv_freq;
+        p.rot = rope->rot_dim;
+        p.inter = rope->interleaved;
+    }
+    p.W = W;
+    p.codes = k_sig;
+    p.c_sp = c->ks_sp;
+    p.c_sh = c->ks_sh;
+    p.flags = dev_flags;
+    HA_LAUNCH(launch_append(p, t->dtype == HA_BF16, c->dtype == HA_BF16, static_cast<cudaStream_t>(stream)), "append launch");
     return HA_OK;
 }

@@ -1,0 +1,919 @@
+// Causal attention of packed queries: whole prompts (K and V packed like the
+// queries) and chunks of new tokens over a paged cache.
+//
+// Row (token i of sequence s, query head h) with g = h / G attends to the keys
+// j < L(i) = nk - nq + i + 1 of its sequence (nq new tokens, nk keys in all):
+//   z_j = <q, K_j> / sqrt(d),  out = sum_j e^{z_j} V_j / sum_j e^{z_j},
+//   lse = log sum_j e^{z_j}    (L(i) <= 0: out = 0, lse = -inf)
+// (HashAttention: Semantic Sparsity for Faster Inference, Sec. 4 estimator with
+// every visible token selected; lse as in Nectar, Eq. (3.1)).
+//
+// One pass over the keys with a running reference maximum m and mass l per row:
+// S = Q K^T (tcgen05.mma, float32 accumulator in tensor memory), P = 2^{(S - m)
+// log2(e)/sqrt(d)} rounded to bf16 in tensor memory, O += P V (P read as the
+// MMA's A operand from tensor memory). O is rescaled only when a row's maximum
+// grows by more than 2^8 over its reference: until then P <= 2^8, which costs
+// neither range nor precision, as bf16 keeps its relative step. l is summed in
+// float32 from the values before they are rounded. With a float32 output, P
+// enters as three bf16 parts, each the rounding of what the earlier ones left
+// (together all 24 bits of p), for three times the P V products; their tiles are
+// 64 keys, so that the parts fit where S was.
+//
+// Rows: the G query heads of a KV head share its K and V, so a tile packs
+// TQ = floor(128 / G) tokens x G heads (row = token * G + head). An item is
+// (sequence, KV head, 2 TQ tokens): two tiles, one softmax warpgroup each, so
+// that one tile's exponentials run under the other tile's products. An item of
+// at most TQ tokens (decode) has one tile: its warpgroups take the even and the
+// odd key tiles, each with its own m, l, O, which are joined at the end.
+//
+// Work is cut at key tiles, not at items: CTA c of P takes the tiles
+// [c U / P, (c + 1) U / P) of all items in order, so any mix of lengths fills
+// the GPU. A boundary close to an item's edge moves to it. Parts of an item that
+// spans CTAs go to the workspace (unnormalised O, m, l) and k_packed_merge joins
+// them, in order, so results do not depend on timing.
+//
+// 10 warps: two softmax warpgroups (thread = row: a tcgen05.ld gives a thread
+// its whole row of S, no shuffles), one warp that issues the MMAs, one that
+// loads by TMA (128-byte swizzle; ring of K/V tiles). Waits are bounded: one
+// that gives up flags HA_DEVERR_TIMEOUT, stops the other roles, lets the copies
+// and products in flight land and frees the tensor memory before the CTA exits.
+#include "tc_common.cuh"
+
+namespace ha {
+namespace {
+
+constexpr int kAttThreads = 320;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kMinSpan = 2;           // fewest tiles of a CTA
+constexpr uint32_t kTmemCols = 512;   // S0, S1 (128 each; P overlays them), O0, O1
+constexpr float kRescale = 8.f;       // growth of the maximum (log2) that makes O be rescaled
+
+template <int D, bool F32OUT>
+struct AttCfg {
+    static constexpr int kKeys = F32OUT ? 64 : 128;      // keys per tile
+    static constexpr int kHalves = D / 64;               // 128-byte swizzle spans of a row
+    static constexpr int kQTile = 128 * D * 2;           // bytes of a Q tile
+    static constexpr int kTile = kKeys * D * 2;          // bytes of a K or V tile
+    static constexpr int kSpan = kKeys * 128;            // bytes of one span of its rows
+    static constexpr int kStages = 5 * 32768 / kTile;
+    static constexpr int kParts = F32OUT ? 3 : 1;        // bf16 parts of P
+    static constexpr int kBars = 2 * kStages + 13;
+    static constexpr int kSmem = 2 * kQTile + kStages * kTile + 2048 + 8 * kBars + 128;
+    static_assert(kSmem <= 232448, "shared memory of a CTA");
+};
+
+struct SeqInfo {
+    int q0, nq, nk;
+};
+
+// Sequence s, or an empty one (flagged) where its bounds are bad.
+__device__ __forceinline__ SeqInfo seq_info(const PackedParams& p, int s, bool report) {
+    SeqInfo i;
+    const int a = p.cu[s], b = p.cu[s + 1];
+    const bool bad = a < 0 || b < a || b > p.total;
+    i.q0 = a;
+    i.nq = bad ? 0 : b - a;
+    i.nk = i.nq;
+    bool badk = false;
+    if (p.seq_lens != nullptr) {
+        i.nk = p.seq_lens[s];
+        badk = i.nk < 0 || i.nk > p.max_len;
+        if (badk) i.nk = 0;
+    }
+    if (report && (bad || badk)) flag_error(p.err, HA_DEVERR_SEQLEN);
+    return i;
+}
+
+// sum over i < n of floor((a i + b) / m), m <= 128, a <= 256
+__device__ __forceinline__ unsigned long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+    unsigned long long ans = 0;
+    while (n != 0) {
+        if (a >= m) {
+            ans += ((unsigned long long)n * (n - 1) >> 1) * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            ans += (unsigned long long)n * (b / m);
+            b %= m;
+        }
+        const uint32_t y = a * n + b;
+        if (y < m) break;
+        n = y / m;
+        b = y - n * m;
+        const uint32_t t = m;
+        m = a;
+        a = t;
+    }
+    return ans;
+}
+
+// Keys that the first `upto` new tokens of the sequence see.
+__device__ __forceinline__ int keys_seen(const SeqInfo& i, int upto) {
+    const int k = i.nk - i.nq + min(upto, i.nq);
+    return max(k, 0);
+}
+
+template <int KT>
+__device__ __forceinline__ int key_tiles(int keys) {
+    return (keys + KT - 1) / KT;
+}
+
+// Tiles of the items 0 .. qt - 1 of one head (an item without keys counts one,
+// so that its rows are written), qt < the number of items.
+template <int KT>
+__device__ __forceinline__ unsigned long long tiles_before(const SeqInfo& i, int t2, int qt) {
+    const int base = i.nk - i.nq;
+    int z = 0;  // items that see no key
+    if (base < 0) z = min(qt, (-base) / t2);
+    const int n = qt - z;
+    if (n <= 0) return (unsigned)z;
+    return (unsigned)z + floor_sum((uint32_t)n, KT, (uint32_t)t2, (uint32_t)(base + (z + 1) * t2 + KT - 1));
+}
+
+template <int KT>
+__device__ __forceinline__ int item_tiles(const SeqInfo& i, int t2, int qt) {
+    return max(1, key_tiles<KT>(keys_seen(i, (qt + 1) * t2)));
+}
+
+template <int KT>
+__device__ __forceinline__ unsigned long long head_tiles(const SeqInfo& i, int t2) {
+    if (i.nq == 0) return 0;
+    const int nqt = (i.nq + t2 - 1) / t2;
+    return tiles_before<KT>(i, t2, nqt - 1) + (unsigned)item_tiles<KT>(i, t2, nqt - 1);
+}
+
+// A place in the order of all tiles: tile j of item (s, head, qt).
+struct Place {
+    unsigned long long w;
+    int s, head, qt, j;
+};
+
+// The part of an item that this CTA works on.
+template <int KT>
+struct Segment {
+    int s, head, qt;
+    int q0, nq, nk;
+    int jb, je, len;     // tiles [jb, je) of the item's len
+    int kend;            // keys that the item's last token sees
+    int tokens;          // its tokens
+    int parity;          // one tile of rows: warpgroups take every other key tile
+    int n0;              // key tiles of row tile 0 (two row tiles)
+    // tiles of stream (warpgroup) t in this segment
+    __device__ __forceinline__ int tiles() const { return max(0, min(je, key_tiles<KT>(kend)) - jb); }
+    __device__ __forceinline__ int stream_tiles(int t) const {
+        if (parity) return (tiles() + 1 - t) >> 1;
+        return t == 0 ? max(0, min(je, n0) - jb) : tiles();
+    }
+};
+
+template <int KT>
+struct SegIter {
+    unsigned long long left;
+    int s, head, qt, j, nqt;
+    SeqInfo i;
+    __device__ __forceinline__ void start(const PackedParams& p, const Place& a, unsigned long long w1) {
+        s = a.s;
+        head = a.head;
+        qt = a.qt;
+        j = a.j;
+        left = w1 - a.w;
+        if (left == 0) return;
+        load(p);
+        if (j >= item_tiles<KT>(i, 2 * p.TQ, qt)) step(p);
+    }
+    __device__ __forceinline__ void load(const PackedParams& p) {
+        i = seq_info(p, s, false);
+        nqt = (i.nq + 2 * p.TQ - 1) / (2 * p.TQ);
+    }
+    // the next item
+    __device__ __forceinline__ void step(const PackedParams& p) {
+        j = 0;
+        if (++qt < nqt) return;
+        qt = 0;
+        if (++head < p.Hkv) return;
+        head = 0;
+        do {
+            if (++s >= p.n_seq) {
+                left = 0;
+                return;
+            }
+            load(p);
+        } while (i.nq == 0);
+    }
+    __device__ __forceinline__ bool next(const PackedParams& p, Segment<KT>& g) {
+        if (left == 0) return false;
+        const int t2 = 2 * p.TQ;
+        g.s = s;
+        g.head = head;
+        g.qt = qt;
+        g.q0 = i.q0;
+        g.nq = i.nq;
+        g.nk = i.nk;
+        g.len = item_tiles<KT>(i, t2, qt);
+        g.jb = j;
+        const unsigned long long rest = (unsigned long long)(g.len - j);
+        g.je = rest <= left ? g.len : j + (int)left;
+        left -= (unsigned long long)(g.je - g.jb);
+        g.kend = keys_seen(i, (qt + 1) * t2);
+        g.tokens = min(t2, i.nq - qt * t2);
+        g.parity = g.tokens <= p.TQ;
+        g.n0 = key_tiles<KT>(keys_seen(i, qt * t2 + p.TQ));
+        j = g.je;
+        if (left != 0 && j >= g.len) step(p);
+        return true;
+    }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// two bf16 values, the first in the low half
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+template <int D, bool F32OUT>
+__global__ void __launch_bounds__(kAttThreads, 1)
+    k_packed_att(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV, const PackedParams p) {
+    using C = AttCfg<D, F32OUT>;
+    constexpr int S = C::kStages, KT = C::kKeys;
+    extern __shared__ __align__(1024) uint8_t s_raw[];
+    const uint32_t base = smem_addr(s_raw);
+    const uint32_t s_q = base, s_ring = base + 2 * C::kQTile;
+    uint8_t* g_tail = s_raw + 2 * C::kQTile + S * C::kTile;
+    float2* s_ml = reinterpret_cast<float2*>(g_tail);                 // [2][128] (m, l) of the two warpgroups
+    const uint32_t bars = base + (uint32_t)(2 * C::kQTile + S * C::kTile) + 2048u;
+    uint8_t* g_misc = g_tail + 2048 + 8 * C::kBars;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(g_misc);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(g_misc + 4);
+    Place* s_place = reinterpret_cast<Place*>(g_misc + 8);            // [2] first and last place
+    unsigned long long* s_scan = reinterpret_cast<unsigned long long*>(g_tail);  // before the roles start
+    auto full = [&](int s) { return bars + 8u * (uint32_t)s; };
+    auto empty = [&](int s) { return bars + 8u * (uint32_t)(S + s); };
+    auto bar_at = [&](int i) { return bars + 8u * (uint32_t)(2 * S + i); };
+    const uint32_t q_full = bar_at(0), q_empty = bar_at(1), x_bar = bar_at(10), done = bar_at(11), seg_done = bar_at(12);
+    auto s_full = [&](int t) { return bar_at(2 + t); };
+    auto p_full = [&](int t) { return bar_at(4 + t); };
+    auto o_done = [&](int t) { return bar_at(6 + t); };
+    auto o_free = [&](int t) { return bar_at(8 + t); };
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if ((base & 1023u) != 0u) {  // the swizzle atoms need it; shared memory starts there
+        pdl_wait();
+        if (tid == 0) {
+            p.items[blockIdx.x].parts = 0;
+            flag_error(p.err, HA_DEVERR_STATE);
+        }
+        return;
+    }
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(s_full(t), 1);
+            mbar_init(p_full(t), 4);
+            mbar_init(o_done(t), 1);
+            mbar_init(o_free(t), 8);
+        }
+        mbar_init(x_bar, 8);
+        mbar_init(done, 1);
+        mbar_init(seg_done, 1);
+        *s_abort = 0;
+        mbar_fence_init();
+        tmap_prefetch(&tmQ);
+        tmap_prefetch(&tmK);
+        tmap_prefetch(&tmV);
+    }
+    if (warp == kMmaWarp) tmem_alloc(smem_addr(s_tmem), kTmemCols);
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // ---- plan: this CTA's range of tiles
+    const int t2 = 2 * p.TQ;
+    const int per = (p.n_seq + kAttThreads - 1) / kAttThreads;
+    const int sa = min(p.n_seq, tid * per), sb = min(p.n_seq, sa + per);
+    unsigned long long mine = 0;
+    for (int s = sa; s < sb; ++s) mine += (unsigned long long)p.Hkv * head_tiles<KT>(seq_info(p, s, blockIdx.x == 0), t2);
+    unsigned long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    unsigned long long before = 0, U = 0;
+    for (int w = 0; w < kAttThreads / 32; ++w) {
+        const unsigned long long v = s_scan[w];
+        if (w < warp) before += v;
+        U += v;
+    }
+    before += incl - mine;
+    // CTAs that work: as many as there are spans of kMinSpan tiles
+    const unsigned long long most = U / kMinSpan;
+    const unsigned P = most < gridDim.x ? (most > 0 ? (unsigned)most : 1u) : gridDim.x;
+    // a boundary within an eighth of a span of an item's edge moves to it
+    const unsigned long long tol = U / P / 8;
+    const bool works = blockIdx.x < P && U > 0;
+    const uint32_t tmem = *s_tmem;
+    if (works) {
+#pragma unroll 1
+        for (int e = 0; e < 2; ++e) {
+            const unsigned c = blockIdx.x + e;
+            const unsigned long long b = c == P ? U : U * c / P;
+            if (b == U) {
+                if (tid == 0) s_place[e] = Place{U, 0, 0, 0, 0};
+            } else if (b >= before && b < before + mine) {
+                unsigned long long rem = b - before, uh = 0;
+                int s = sa;
+                SeqInfo i;
+                for (;; ++s) {
+                    i = seq_info(p, s, false);
+                    uh = head_tiles<KT>(i, t2);
+                    if (rem < uh * p.Hkv) break;
+                    rem -= uh * p.Hkv;
+                }
+                const int head = (int)(rem / uh);
+                rem -= uh * head;
+                int lo = 0, hi = (i.nq + t2 - 1) / t2 - 1;  // the last item that begins at or before rem
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (tiles_before<KT>(i, t2, mid) <= rem) lo = mid;
+                    else hi = mid - 1;
+                }
+                const unsigned long long off = rem - tiles_before<KT>(i, t2, lo);
+                const unsigned long long to_end = (unsigned long long)item_tiles<KT>(i, t2, lo) - off;
+                Place a{b, s, head, lo, (int)off};
+                if (off <= tol && off <= to_end) {
+                    a.w -= off;
+                    a.j = 0;
+                } else if (to_end <= tol) {
+                    a.w += to_end;
+                    a.j = (int)(off + to_end);
+                }
+                s_place[e] = a;
+            }
+        }
+    }
+    __syncthreads();
+    Place first{0, 0, 0, 0, 0};
+    unsigned long long w1 = 0;
+    if (works) {
+        first = s_place[0];
+        w1 = s_place[1].w;
+    }
+    if (tid == 0) p.items[blockIdx.x].parts = 0;
+    __syncthreads();  // s_scan's space becomes s_ml
+
+    auto give_up = [&]() {
+        flag_error(p.err, HA_DEVERR_TIMEOUT);
+        *s_abort = 1;
+    };
+    SegIter<KT> it;
+    it.left = 0;
+    if (w1 > first.w) it.start(p, first, w1);
+    Segment<KT> g;
+
+    if (warp == kLoadWarp) {
+        const int lg = p.box_log2;               // rows of a box: 2^lg
+        const int nbox = KT >> lg;
+        const int box = lane & (nbox - 1), half = lane / nbox;
+        int n = 0, nq = 0;
+        bool ok = true;
+        while (ok && it.next(p, g)) {
+            const int nt = g.tiles();
+            if (nt == 0) continue;
+            const int jend = g.jb + nt;
+            if (!mbar_wait_bounded(q_empty, (uint32_t)(nq & 1) ^ 1u, s_abort)) {
+                ok = false;
+                break;
+            }
+            const int qtiles = g.parity ? 1 : 2;
+            if (lane == 0) mbar_arrive_expect_tx(q_full, (uint32_t)(qtiles * p.TQ * p.G * D * 2));
+            __syncwarp();
+            if (lane < qtiles * C::kHalves) {
+                const int t = lane / C::kHalves, h = lane % C::kHalves;
+                tma_load_4d(s_q + (uint32_t)(t * C::kQTile + h * 16384), &tmQ, q_full, h * 64, 0,
+                            g.q0 + g.qt * t2 + t * p.TQ, g.head);
+            }
+            ++nq;
+            const int32_t* table = p.table != nullptr ? p.table + (int64_t)g.s * p.table_st : nullptr;
+            // page and row of this lane's box of tile j
+            auto where = [&](int j, int& page, int& row) {
+                const int key = j * KT + (box << lg);
+                page = 0;
+                row = g.q0 + key;
+                if (table != nullptr && key < g.kend) {
+                    const int e = key / p.page_size;
+                    row = key - e * p.page_size;
+                    page = table[e];
+                    if (page < 0 || page >= p.n_pages) {
+                        flag_error(p.err, HA_DEVERR_INDEX);
+                        page = p.n_pages;  // past the pool: the copy fills its rows with zeros
+                    }
+                }
+            };
+            int page, row;
+            where(g.jb, page, row);
+            for (int j = g.jb; ok && j < jend; ++j) {
+                const int rows = min(KT, g.kend - j * KT);
+                const int boxes = (rows + (1 << lg) - 1) >> lg;
+                int page_n = 0, row_n = 0;
+                if (j + 1 < jend) where(j + 1, page_n, row_n);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int s = n % S;
+                    if (!mbar_wait_bounded(empty(s), ((uint32_t)(n / S) & 1u) ^ 1u, s_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(full(s), (uint32_t)((boxes << lg) * D * 2));
+                    __syncwarp();
+                    if (box < boxes && half < C::kHalves)
+                        tma_load_4d(s_ring + (uint32_t)(s * C::kTile + half * C::kSpan + (box << lg) * 128),
+                                    kv == 0 ? &tmK : &tmV, full(s), half * 64, row, g.head, page);
+                    ++n;
+                }
+                page = page_n;
+                row = row_n;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) {
+            if (!ok) give_up();
+            // before the CTA can exit: the products have released the last stages, or,
+            // after a timeout, at least the copies into them have landed
+            const bool clean = *s_abort == 0;
+            for (int j = (n > S ? n - S : 0); j < n; ++j)
+                mbar_wait_drain(clean ? empty(j % S) : full(j % S), (uint32_t)(j / S) & 1u);
+            if (nq > 0) mbar_wait_drain(clean ? q_empty : q_full, (uint32_t)(nq - 1) & 1u);
+        }
+    } else if (warp == kMmaWarp) {
+        constexpr uint32_t kIdS = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(KT >> 3) << 17) | ((128u >> 4) << 24);
+        constexpr uint32_t kIdO = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
+                                  ((128u >> 4) << 24);
+        int n = 0, nq = 0, nseg = 0;
+        int cnt0 = 0, cnt1 = 0;  // tiles of the two streams so far
+        bool ok = true;
+        // S_t = Q_t K^T of the K tile in ring slot s
+        auto issue_s = [&](int t, int qtile, int s) {
+            if (lane == 0) {
+                const uint32_t a = s_q + (uint32_t)(qtile * C::kQTile), b = s_ring + (uint32_t)(s * C::kTile);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t h = (uint32_t)(kk >> 2), o = (uint32_t)(kk & 3) * 32u;
+                    tc_mma(tmem + (uint32_t)(t * 128), sw128_desc(a + h * 16384u + o),
+                           sw128_desc(b + h * (uint32_t)C::kSpan + o), kIdS, kk > 0 ? 1u : 0u);
+                }
+                tc_commit(s_full(t));
+            }
+        };
+        // O_t (+)= P_t V of the V tile in ring slot s
+        auto issue_o = [&](int t, int s, bool acc) {
+            if (lane == 0) {
+                const uint32_t b = s_ring + (uint32_t)(s * C::kTile);
+#pragma unroll
+                for (int part = 0; part < C::kParts; ++part)
+#pragma unroll
+                    for (int kk = 0; kk < KT / 16; ++kk)
+                        tc_mma_ts(tmem + 256u + (uint32_t)(t * 128), tmem + (uint32_t)(t * 128 + part * (KT / 2) + kk * 8),
+                                  sw128_desc_mn(b + (uint32_t)kk * 2048u, (uint32_t)C::kSpan), kIdO,
+                                  (acc || part > 0 || kk > 0) ? 1u : 0u);
+                tc_commit(o_done(t));
+            }
+        };
+        auto release = [&](int s) {
+            if (lane == 0) tc_commit(empty(s));
+        };
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            const bool r = mbar_wait_bounded(bar, parity, s_abort);
+            tc_fence_after();
+            return __all_sync(0xffffffffu, r);
+        };
+        auto wait_slot = [&](int k) { return wait(full(k % S), (uint32_t)(k / S) & 1u); };
+        while (ok && it.next(p, g)) {
+            const int nt = g.tiles();
+            const uint32_t free_ph = (uint32_t)(nseg & 1) ^ 1u;
+            ++nseg;
+            // Every segment waits once for both O's of the one before it and then ends with
+            // an arrival on seg_done, which every softmax warp waits for before it gives
+            // the O's of this one back: so neither side is ever two phases ahead, also
+            // where a stream has no tiles and nothing else holds its warps back.
+            auto wait_free = [&](int t) { return wait(o_free(t), free_ph); };
+            if (nt == 0) {
+                ok = wait_free(0) && wait_free(1);
+                if (ok && lane == 0) tc_commit(seg_done);
+                continue;
+            }
+            const int jend = g.jb + nt;
+            // rows of the V tile past the last key: zeros (what lies there may be no number)
+            auto clear_tail = [&](int j, int s) {
+                const int rows = g.kend - j * KT;
+                if (rows < KT) {
+                    for (int i = lane; i < (KT - rows) * 8 * C::kHalves; i += 32) {
+                        const int h = i / ((KT - rows) * 8), k = i - h * ((KT - rows) * 8);
+                        *reinterpret_cast<uint4*>(s_raw + 2 * C::kQTile + s * C::kTile + h * C::kSpan + rows * 128 + k * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_shared();
+                    __syncwarp();
+                }
+            };
+            const int n0 = n;  // ring index of K(jb); K(j) is n0 + 2 (j - jb), V(j) the next
+            auto K = [&](int j) { return n0 + 2 * (j - g.jb); };
+            ok = wait(q_full, (uint32_t)(nq & 1));
+            ++nq;
+            bool o_ok = false;  // the last segment's O has been read
+            if (g.parity) {
+                const int last = jend - 1;
+                for (int j = g.jb; ok && j < min(jend, g.jb + 2); ++j) {
+                    ok = wait_slot(K(j));
+                    if (!ok) break;
+                    issue_s(j - g.jb, 0, K(j) % S);
+                    release(K(j) % S);
+                    if (j == last && lane == 0) tc_commit(q_empty);
+                }
+                for (int j = g.jb; ok && j < jend; ++j) {
+                    const int t = (j - g.jb) & 1;
+                    int& c = t ? cnt1 : cnt0;
+                    ok = wait_slot(K(j) + 1) && wait(p_full(t), (uint32_t)(c & 1));
+                    if (ok && !o_ok) {
+                        ok = wait_free(0) && wait_free(1);
+                        o_ok = true;
+                    }
+                    if (!ok) break;
+                    clear_tail(j, (K(j) + 1) % S);
+                    issue_o(t, (K(j) + 1) % S, j >= g.jb + 2);
+                    release((K(j) + 1) % S);
+                    ++c;
+                    if (j + 2 < jend) {
+                        ok = wait_slot(K(j + 2));
+                        if (!ok) break;
+                        issue_s(t, 0, K(j + 2) % S);
+                        release(K(j + 2) % S);
+                        if (j + 2 == last && lane == 0) tc_commit(q_empty);
+                    }
+                }
+            } else {
+                const int e0 = g.jb + g.stream_tiles(0);  // row tile 0 takes [jb, e0), row tile 1 [jb, jend)
+                if (ok) ok = wait_slot(K(g.jb));
+                if (ok) {
+                    if (g.jb < e0) issue_s(0, 0, K(g.jb) % S);
+                    issue_s(1, 1, K(g.jb) % S);
+                    release(K(g.jb) % S);
+                    if (nt == 1 && lane == 0) tc_commit(q_empty);
+                }
+                for (int j = g.jb; ok && j < jend; ++j) {
+                    const int sv = (K(j) + 1) % S, sk = K(j + 1) % S;
+                    ok = wait_slot(K(j) + 1);
+                    if (!ok) break;
+                    clear_tail(j, sv);
+                    bool have_k = false;
+                    if (j < e0) {
+                        ok = wait(p_full(0), (uint32_t)(cnt0 & 1));
+                        if (ok && j == g.jb) ok = wait_free(0);
+                        if (!ok) break;
+                        issue_o(0, sv, j > g.jb);
+                        ++cnt0;
+                        if (j + 1 < e0) {
+                            ok = wait_slot(K(j + 1));
+                            if (!ok) break;
+                            have_k = true;
+                            issue_s(0, 0, sk);
+                        }
+                    }
+                    ok = wait(p_full(1), (uint32_t)(cnt1 & 1));
+                    if (ok && j == g.jb) ok = (e0 > g.jb || wait_free(0)) && wait_free(1);
+                    if (!ok) break;
+                    issue_o(1, sv, j > g.jb);
+                    release(sv);
+                    ++cnt1;
+                    if (j + 1 < jend) {
+                        if (!have_k) ok = wait_slot(K(j + 1));
+                        if (!ok) break;
+                        issue_s(1, 1, sk);
+                        release(sk);
+                        if (j + 2 == jend && lane == 0) tc_commit(q_empty);
+                    }
+                }
+            }
+            n = n0 + 2 * nt;
+            if (ok && lane == 0) tc_commit(seg_done);
+        }
+        if (lane == 0) {
+            if (!ok) give_up();
+            tc_commit(done);  // every product issued above has finished once this arrives
+            mbar_wait_drain(done, 0u);
+        }
+        __syncwarp();
+    } else {
+        const int t = warp >> 2, r = tid & 127;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_off + (uint32_t)(t * 128);
+        const uint32_t tO = tmem + lane_off + 256u;
+        const int rtok = r / p.G, rhead = r - rtok * p.G;
+        const bool in_tile = rtok < p.TQ;
+        int cnt[2] = {0, 0};
+        int nx = 0, nseg = 0;
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            const bool w = mbar_wait_bounded(bar, parity, s_abort);
+            tc_fence_after();
+            return (bool)__all_sync(0xffffffffu, w);
+        };
+        while (ok && it.next(p, g)) {
+            const int ltok = (g.parity ? 0 : t * p.TQ) + rtok;       // token of this row within the item
+            const bool valid = in_tile && ltok < g.tokens;
+            const int kmax = valid ? min(g.nk, max(0, g.nk - g.nq + g.qt * t2 + ltok + 1)) : 0;
+            const bool any = __any_sync(0xffffffffu, valid);
+            const int st0 = g.stream_tiles(0), st1 = g.stream_tiles(1);
+            const int nt = t == 0 ? st0 : st1;
+            const int jstep = g.parity ? 2 : 1, j0 = g.parity ? g.jb + t : g.jb;
+            float m = -INFINITY, l = 0.f;
+            for (int i = 0; ok && i < nt; ++i) {
+                const int c = cnt[t] + i;
+                ok = wait(s_full(t), (uint32_t)(c & 1));
+                if (!ok) break;
+                if (any) {
+                    uint32_t x[KT];
+                    if constexpr (KT == 128) tmem_ld128_wait(tS, x);
+                    else tmem_ld64_wait(tS, x);
+                    const int lim = kmax - (j0 + i * jstep) * KT;  // columns of this tile the row sees
+                    if (__any_sync(0xffffffffu, lim < KT)) {
+#pragma unroll
+                        for (int k = 0; k < KT; ++k)
+                            if (k >= lim) x[k] = 0xff800000u;
+                    }
+                    float mx = __uint_as_float(x[0]);
+#pragma unroll
+                    for (int k = 1; k < KT; ++k) mx = fmaxf(mx, __uint_as_float(x[k]));
+                    const bool grow = (mx - m) * p.qscale > kRescale;  // false while m is -inf and mx too
+                    const bool resc = grow && m != -INFINITY;
+                    if (__any_sync(0xffffffffu, resc)) {
+                        // the products of the previous tile must have landed in O
+                        ok = wait(o_done(t), (uint32_t)((c - 1) & 1));
+                        if (!ok) break;
+                        const float a = resc ? ex2((m - mx) * p.qscale) : 1.f;
+                        l *= a;
+#pragma unroll 1
+                        for (int cc = 0; cc < D; cc += 32) {
+                            uint32_t o[32];
+                            tmem_ld32_wait(tO + (uint32_t)(t * 128 + cc), o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+                            tmem_st32(tO + (uint32_t)(t * 128 + cc), o);
+                        }
+                    }
+                    if (grow) m = mx;
+                    const float sub = m == -INFINITY ? 0.f : m * p.qscale;
+                    float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+                    for (int cc = 0; cc < KT / 32; ++cc) {
+                        uint32_t w[16], w1[16], w2[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            float a = ex2(fmaf(__uint_as_float(x[cc * 32 + 2 * k]), p.qscale, -sub));
+                            float b = ex2(fmaf(__uint_as_float(x[cc * 32 + 2 * k + 1]), p.qscale, -sub));
+                            sum0 += a;
+                            sum1 += b;
+                            w[k] = pack_bf16(a, b);
+                            if (F32OUT) {
+                                a -= bf16lo(w[k]);
+                                b -= bf16hi(w[k]);
+                                w1[k] = pack_bf16(a, b);
+                                w2[k] = pack_bf16(a - bf16lo(w1[k]), b - bf16hi(w1[k]));
+                            }
+                        }
+                        tmem_st16(tS + (uint32_t)(cc * 16), w);
+                        if (F32OUT) {
+                            tmem_st16(tS + (uint32_t)(KT / 2 + cc * 16), w1);
+                            tmem_st16(tS + (uint32_t)(KT + cc * 16), w2);
+                        }
+                    }
+                    l += sum0 + sum1;
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(t));
+            }
+            if (!ok) break;
+            cnt[0] += st0;
+            cnt[1] += st1;
+            const bool whole = g.jb == 0 && g.je == g.len;
+            // row of out / lse, or of this CTA's part of the item
+            const int64_t grow_ = ((int64_t)(g.q0 + g.qt * t2 + ltok) * p.Hq + g.head * p.G + rhead);
+            const int64_t prow = (int64_t)(2 * blockIdx.x + (g.jb == 0 ? 1 : 0)) * p.slot_rows + (g.parity ? r : t * 128 + r);
+            float ca = 0.f, cb = 0.f;          // factors of O0 (or of this stream's O) and O1
+            int col0 = 0, cols = D;
+            bool both = false;
+            if (g.parity) {
+                if (st0 > 0) {
+                    // own stream first: its last product follows all but the last of the other's
+                    if (nt > 0) ok = wait(o_done(t), (uint32_t)((cnt[t] - 1) & 1));
+                    if (ok && (t == 1 || st1 > 0)) ok = wait(o_done(t ^ 1), (uint32_t)((cnt[t ^ 1] - 1) & 1));
+                    if (!ok) break;
+                    s_ml[t * 128 + r] = make_float2(m, l);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(x_bar);
+                    ok = wait(x_bar, (uint32_t)(nx & 1));
+                    ++nx;
+                    if (!ok) break;
+                    const float2 A = s_ml[r], B = s_ml[128 + r];
+                    m = fmaxf(A.x, B.x);
+                    const float ms = m == -INFINITY ? 0.f : m;
+                    ca = ex2((A.x - ms) * p.qscale);
+                    cb = ex2((B.x - ms) * p.qscale);
+                    l = A.y * ca + B.y * cb;
+                    both = st1 > 0;
+                }
+                col0 = t * (D / 2);
+                cols = D / 2;
+            } else {
+                if (nt > 0) {
+                    ok = wait(o_done(t), (uint32_t)((cnt[t] - 1) & 1));
+                    if (!ok) break;
+                }
+                ca = 1.f;
+            }
+            const bool have = g.parity ? st0 > 0 : nt > 0;
+            const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
+            ca *= inv;
+            cb *= inv;
+            if (any) {
+                const uint32_t oa = tO + (g.parity ? 0u : (uint32_t)(t * 128));
+#pragma unroll 1
+                for (int cc = col0; cc < col0 + cols; cc += 32) {
+                    uint32_t o[32];
+                    if (have) {
+                        tmem_ld32_wait(oa + (uint32_t)cc, o);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * ca);
+                        if (both) {
+                            uint32_t o1[32];
+                            tmem_ld32_wait(tO + 128u + (uint32_t)cc, o1);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                o[k] = __float_as_uint(fmaf(__uint_as_float(o1[k]), cb, __uint_as_float(o[k])));
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = 0u;
+                    }
+                    if (valid) {
+                        if (whole && !F32OUT) {
+                            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + grow_ * D + cc);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int u = 0; u < 4; ++u)
+                                    w[u] = pack_bf16(__uint_as_float(o[8 * k + 2 * u]), __uint_as_float(o[8 * k + 2 * u + 1]));
+                                dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        } else {
+                            float* f = whole ? reinterpret_cast<float*>(p.out) + grow_ * D + cc : p.part_o + prow * D + cc;
+                            uint4* dst = reinterpret_cast<uint4*>(f);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        }
+                    }
+                }
+                if (valid && (!g.parity || t == 0)) {
+                    if (whole)
+                        p.lse[grow_] = l == 0.f ? -INFINITY : fmaf(m, p.qscale, log2f(l)) * 0.6931471805599453f;
+                    else
+                        p.part_ml[prow] = make_float2(m, l);
+                }
+            }
+            tc_fence_before();
+            ok = wait(seg_done, (uint32_t)(nseg & 1));
+            ++nseg;
+            if (!ok) break;
+            if (lane == 0) {
+                if (g.parity) {
+                    mbar_arrive(o_free(0));
+                    mbar_arrive(o_free(1));
+                } else {
+                    mbar_arrive(o_free(t));
+                    mbar_arrive(o_free(t));
+                }
+            }
+            // the item begins here and goes on in the next CTAs: what the merge needs to know
+            if (tid == 0 && g.jb == 0 && !whole) {
+                const unsigned long long w_end = w1 + (unsigned long long)(g.len - g.je);
+                const unsigned long long last = (w_end - tol) * P;
+                const unsigned stop = (unsigned)((last + U - 1) / U);  // the boundary at which it has ended
+                SplitItem d;
+                d.parts = (int)(stop - blockIdx.x);
+                d.row0 = g.q0 + g.qt * t2;
+                d.head = g.head;
+                d.tokens = g.tokens;
+                p.items[blockIdx.x] = d;
+            }
+        }
+        if (!ok && lane == 0) give_up();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Joins the parts of every item that spans CTAs: grid (CTA in which an item may
+// begin, slices of its rows), one warp per row.
+template <int D, bool F32OUT>
+__global__ void __launch_bounds__(256) k_packed_merge(const PackedParams p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const SplitItem d = p.items[blockIdx.x];
+    if (d.parts <= 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool two = d.tokens > p.TQ;
+    const int rows = d.tokens * p.G;
+    constexpr int E = D / 32;
+    for (int i = blockIdx.y * 8 + warp; i < rows; i += gridDim.y * 8) {
+        const int tok = i / p.G, h = i - tok * p.G;
+        const int row = two && tok >= p.TQ ? 128 + (tok - p.TQ) * p.G + h : i;
+        auto at = [&](int k) { return (int64_t)(2 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * p.slot_rows + row; };
+        float m = -INFINITY;
+        for (int k = lane; k < d.parts; k += 32) m = fmaxf(m, p.part_ml[at(k)].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float ms = m == -INFINITY ? 0.f : m;
+        float l = 0.f, acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < d.parts; ++k) {
+            const float2 ml = p.part_ml[at(k)];
+            const float w = ex2((ml.x - ms) * p.qscale);
+            const float* o = p.part_o + at(k) * D + lane * E;
+            l = fmaf(ml.y, w, l);
+            float v[E];
+            if (E == 4) {
+                const float4 f = *reinterpret_cast<const float4*>(o);
+                v[0] = f.x;
+                v[1] = f.y;
+                v[E - 2] = f.z;
+                v[E - 1] = f.w;
+            } else {
+                const float2 f = *reinterpret_cast<const float2*>(o);
+                v[0] = f.x;
+                v[1] = f.y;
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(v[e], w, acc[e]);
+        }
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        const int64_t orow = (int64_t)(d.row0 + tok) * p.Hq + d.head * p.G + h;
+        if (F32OUT) {
+            float* o = reinterpret_cast<float*>(p.out) + orow * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(o + e) = make_float2(acc[e] * inv, acc[e + 1] * inv);
+        } else {
+            uint32_t* o = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * D + lane * E);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) o[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+        }
+        if (lane == 0) p.lse[orow] = l == 0.f ? -INFINITY : fmaf(m, p.qscale, log2f(l)) * 0.6931471805599453f;
+    }
+}
+
+template <int D, bool F32OUT>
+cudaError_t launch_t(const PackedParams& p, const PackedMaps& m, int grid, bool merge, cudaStream_t st) {
+    using C = AttCfg<D, F32OUT>;
+    cudaError_t e = cudaFuncSetAttribute(k_packed_att<D, F32OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_ex(k_packed_att<D, F32OUT>, dim3((unsigned)grid), dim3(kAttThreads), C::kSmem, st, true, m.q, m.k, m.v, p);
+    if (e != cudaSuccess || !merge) return e;
+    return launch_ex(k_packed_merge<D, F32OUT>, dim3((unsigned)grid, 4), dim3(256), 0, st, true, p);
+}
+
+}  // namespace
+
+int packed_key_tile(bool f32_out) { return f32_out ? 64 : 128; }
+
+cudaError_t launch_packed_att(const PackedParams& p, const PackedMaps& m, int d, bool f32_out, int grid, bool merge,
+                              cudaStream_t st) {
+    if (d == 128) return f32_out ? launch_t<128, true>(p, m, grid, merge, st) : launch_t<128, false>(p, m, grid, merge, st);
+    return f32_out ? launch_t<64, true>(p, m, grid, merge, st) : launch_t<64, false>(p, m, grid, merge, st);
+}
+
+}  // namespace ha

@@ -44,6 +44,7 @@ EXPORTED = [
     "hash_attn_encode_queries", "hash_attn_encode_keys", "hash_attn_encode_queries_mlp",
     "hash_attn_encode_keys_mlp", "hash_attn_decode_mapped", "hash_attn_topk_exact_workspace_size",
     "hash_attn_topk_exact", "hash_attn_topk_exact_timed", "hash_attn_recall",
+    "hash_attn_append", "hash_attn_packed_workspace_size", "hash_attn_prefill", "hash_attn_chunk",
     "hash_attn_device_status",
     "hash_attn_status_string", "hash_attn_last_error",
 ]
@@ -114,6 +115,35 @@ class HAShape(ctypes.Structure):
     ]
 
 
+class HATokens(ctypes.Structure):
+    """Mirror of ``ha_tokens`` (packed new tokens; strides in elements)."""
+
+    _fields_ = [
+        ("n_seq", ctypes.c_int32), ("total", ctypes.c_int32), ("h_q", ctypes.c_int32), ("h_kv", ctypes.c_int32),
+        ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("q_st", ctypes.c_int64), ("q_sh", ctypes.c_int64), ("k_st", ctypes.c_int64), ("k_sh", ctypes.c_int64),
+        ("v_st", ctypes.c_int64), ("v_sh", ctypes.c_int64),
+    ]
+
+
+class HACache(ctypes.Structure):
+    """Mirror of ``ha_cache`` (a paged KV cache; strides in elements)."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32), ("table_st", ctypes.c_int64),
+        ("k_sp", ctypes.c_int64), ("k_sh", ctypes.c_int64), ("k_sn", ctypes.c_int64),
+        ("v_sp", ctypes.c_int64), ("v_sh", ctypes.c_int64), ("v_sn", ctypes.c_int64),
+        ("ks_sp", ctypes.c_int64), ("ks_sh", ctypes.c_int64),
+    ]
+
+
+class HARope(ctypes.Structure):
+    """Mirror of ``ha_rope``."""
+
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
 class HashAttnError(RuntimeError):
     def __init__(self, status: int, detail: str):
         super().__init__(f"{status_string(status)} ({status}): {detail}")
@@ -170,6 +200,11 @@ def lib() -> ctypes.CDLL:
     L.hash_attn_topk_exact.argtypes = [SP, _P, _P, _P, _I32, _P, _I32, _P, _P, _SZ, _P]
     L.hash_attn_topk_exact_timed.argtypes = [SP, _P, _P, _P, _I32, _P, _I32, _P, _P, _SZ, _P, ctypes.POINTER(_P)]
     L.hash_attn_recall.argtypes = [_P, _P, _I32, _P, _P, _I32, _I32, _P, _P]
+    TP, CP = ctypes.POINTER(HATokens), ctypes.POINTER(HACache)
+    L.hash_attn_append.argtypes = [TP, CP, ctypes.POINTER(HARope)] + [_P] * 13
+    L.hash_attn_packed_workspace_size.argtypes = [TP, ctypes.POINTER(_SZ)]
+    L.hash_attn_prefill.argtypes = [TP] + [_P] * 7 + [_SZ, _P]
+    L.hash_attn_chunk.argtypes = [TP, CP] + [_P] * 9 + [_SZ, _P]
     L.hash_attn_device_status.argtypes = [_P, _P, ctypes.POINTER(ctypes.c_uint32)]
     L.hash_attn_status_string.argtypes = [_I32]
     L.hash_attn_status_string.restype = ctypes.c_char_p
@@ -458,6 +493,90 @@ def hash_attn_recall(sel_idx, sel_cnt, ref_idx, ref_cnt, recall, stream=None) ->
     heads = sel_cnt.numel()
     _check(lib().hash_attn_recall(_ptr(sel_idx), _ptr(sel_cnt), sel_idx.shape[-1], _ptr(ref_idx), _ptr(ref_cnt),
                                   ref_idx.shape[-1], heads, _ptr(recall), _stream(stream)))
+
+
+def make_tokens(q, k, v, n_seq: int, *, h_kv: int | None = None, out_dtype=None) -> HATokens:
+    """ha_tokens from packed tensors: q [total, Hq, d], k and v [total, Hkv, d] (None
+    with ``h_kv`` where only the queries are packed). ``out_dtype``: torch.float32
+    (the default) or torch.bfloat16."""
+    import torch
+    t = HATokens()
+    t.total, t.h_q, t.d = q.shape
+    t.n_seq = int(n_seq)
+    t.h_kv = int(h_kv) if k is None else k.shape[1]
+    t.dtype = _dtype_code(q)
+    t.out_dtype = HA_BF16 if out_dtype == torch.bfloat16 else HA_F32
+    if out_dtype not in (None, torch.float32, torch.bfloat16):
+        raise ValueError(f"unsupported out_dtype {out_dtype}")
+    t.q_st, t.q_sh = _rows(q, "q", t.dtype, (t.total, t.h_q, t.d))[:2]
+    if k is not None:
+        t.k_st, t.k_sh = _rows(k, "k", t.dtype, (t.total, t.h_kv, t.d))[:2]
+        t.v_st, t.v_sh = _rows(v, "v", t.dtype, (t.total, t.h_kv, t.d))[:2]
+    return t
+
+
+def _rows(x, what, dtype, shape):
+    """Strides of a tensor that must have this shape, type and contiguous rows."""
+    if tuple(x.shape) != tuple(shape) or _dtype_code(x) != dtype or (x.shape[-1] > 1 and x.stride(-1) != 1):
+        raise ValueError(f"{what} must be {tuple(shape)} of one dtype with contiguous rows")
+    return x.stride()
+
+
+def make_cache(K, V, page_table, k_sig=None) -> HACache:
+    """ha_cache from pools K, V [n_pages, Hkv, page_size, d] (for [page, token, head, d]
+    in memory pass ``pool.permute(0, 2, 1, 3)``), page_table int32 [n_seq, max_pages]
+    and, where codes are written, k_sig [n_pages, Hkv, page_size]."""
+    c = HACache()
+    c.n_pages, h_kv, c.page_size, d = K.shape
+    c.dtype = _dtype_code(K)
+    c.k_sp, c.k_sh, c.k_sn = _rows(K, "K", c.dtype, K.shape)[:3]
+    c.v_sp, c.v_sh, c.v_sn = _rows(V, "V", c.dtype, K.shape)[:3]
+    if page_table.dim() != 2 or page_table.element_size() != 4 or page_table.stride(1) != 1 and page_table.shape[1] > 1:
+        raise ValueError("page_table must be int32 [n_seq, max_pages] with contiguous rows")
+    c.max_pages, c.table_st = page_table.shape[1], page_table.stride(0)
+    if k_sig is not None:
+        if tuple(k_sig.shape) != tuple(K.shape[:3]) or k_sig.element_size() != 4 or k_sig.stride(2) != 1 and c.page_size > 1:
+            raise ValueError("k_sig must be 32-bit [n_pages, Hkv, page_size] with contiguous rows")
+        c.ks_sp, c.ks_sh = k_sig.stride(0), k_sig.stride(1)
+    return c
+
+
+def rope(inv_freq, interleaved: bool = False) -> HARope:
+    """HARope over a float32 device tensor inv_freq [rot_dim / 2] (kept by the caller)."""
+    r = HARope()
+    r.inv_freq = _ptr(inv_freq)
+    r.rot_dim = 2 * inv_freq.numel()
+    r.interleaved = 1 if interleaved else 0
+    return r
+
+
+def hash_attn_append(tokens, cache, q, k, v, page_table, cu, seq_lens, q_out, K, V, *, rope=None, W=None, k_sig=None,
+                     dev_flags=None, stream=None) -> None:
+    """Rotate the packed new tokens' q (into ``q_out``) and k by position and write k, v
+    (and with ``W`` the keys' codes) into the paged cache; ``q`` and ``q_out`` may be None."""
+    _check(lib().hash_attn_append(ctypes.byref(tokens), ctypes.byref(cache), None if rope is None else ctypes.byref(rope),
+                                  _ptr(q), _ptr(k), _ptr(v), _ptr(W), _ptr(page_table), _ptr(cu), _ptr(seq_lens),
+                                  _ptr(q_out), _ptr(K), _ptr(V), _ptr(k_sig), _ptr(dev_flags), _stream(stream)))
+
+
+def hash_attn_packed_workspace_size(tokens) -> int:
+    out = _SZ(0)
+    _check(lib().hash_attn_packed_workspace_size(ctypes.byref(tokens), ctypes.byref(out)))
+    return out.value
+
+
+def hash_attn_prefill(tokens, q, K, V, cu, out, lse, *, workspace, stream=None) -> None:
+    """Causal attention over packed prompts; out [total, Hq, d], lse [total, Hq] contiguous."""
+    ws, nb = _ws(workspace)
+    _check(lib().hash_attn_prefill(ctypes.byref(tokens), _ptr(q), _ptr(K), _ptr(V), _ptr(cu), _ptr(out), _ptr(lse), ws, nb,
+                                   _stream(stream)))
+
+
+def hash_attn_chunk(tokens, cache, q, K, V, page_table, cu, seq_lens, out, lse, *, workspace, stream=None) -> None:
+    """Attention of the packed new tokens over the paged cache (their keys are in it already)."""
+    ws, nb = _ws(workspace)
+    _check(lib().hash_attn_chunk(ctypes.byref(tokens), ctypes.byref(cache), _ptr(q), _ptr(K), _ptr(V), _ptr(page_table),
+                                 _ptr(cu), _ptr(seq_lens), _ptr(out), _ptr(lse), ws, nb, _stream(stream)))
 
 
 def hash_attn_device_status(workspace, stream=None) -> tuple[int, int]:

@@ -1,0 +1,587 @@
+"""Prompts and chunks of new tokens: hash_attn_append, hash_attn_prefill and
+hash_attn_chunk against the float64 oracle.
+
+Tolerances, from the arithmetic (u = half a step: 2^-8 for bf16, 2^-24 for float32):
+
+* out in bf16: each weight is rounded to bf16 once (u relative), so the weighted sum
+  moves by at most u sum_j p_j |v_j| = u mag; the result is rounded once (u |out|).
+* scores and weights in float32: a score sums d exact products (at most d steps of
+  2 u zmax, if the adder truncates), its exponent is formed with one rounding of at
+  most 2 u log2(e) |z - max| + u and 2^-22 for the exponential; l and O sum n terms
+  (at most 2 u each). Together at most E = 2^-23 (d zmax + 4 zmax + n + 16) relative
+  per weight, twice (numerator and denominator): 2 E mag.
+* lse: E + 2^-22 (1 + |lse|).
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import packed_oracle as PO
+
+pytestmark = pytest.mark.gpu
+
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def H():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    from long_context_sparse_score_gb300 import _build
+    _build.build()
+    from long_context_sparse_score_gb300 import hashattn
+    hashattn.lib()
+    return hashattn
+
+
+def rand(g, *shape, dtype=torch.bfloat16):
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
+def cumulative(new):
+    return torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+
+
+def check_rows(got_out, got_lse, ref, bf16, what):
+    out, lse, mag, zmax, n = ref
+    d = out.shape[1]
+    E = 2.0 ** -23 * (d * zmax + 4 * zmax + n + 16)
+    tol = 2 * E[:, None] * mag + 1e-30
+    if bf16:
+        tol = tol + 2.0 ** -8 * mag * (1 + 2 * E[:, None]) + 2.0 ** -8 * np.abs(out) * (1 + 2.0 ** -7)
+    got = got_out.double().cpu().numpy()
+    err = np.abs(got - out)
+    assert np.all(err <= tol), f"{what}: out off by {np.nanmax(err):.3g}, worst ratio {np.nanmax(err / tol):.3g}"
+    gl = got_lse.double().cpu().numpy()
+    none = np.isneginf(lse)
+    assert np.array_equal(np.isneginf(gl), none), f"{what}: rows without keys"
+    fin = ~none
+    lt = E[fin] + 2.0 ** -22 * (1 + np.abs(lse[fin]))
+    assert np.all(np.abs(gl[fin] - lse[fin]) <= lt), f"{what}: lse off by {np.abs(gl[fin] - lse[fin]).max():.3g}"
+
+
+def run_chunk(H, q, K, V, table, new, lens, Hkv, out_dtype=torch.bfloat16, ws=None, cu=None, lens_t=None):
+    T = q.shape[0]
+    tok = H.make_tokens(q, None, None, len(new), h_kv=Hkv, out_dtype=out_dtype)
+    cache = H.make_cache(K, V, table)
+    if ws is None:
+        ws = torch.full((H.hash_attn_packed_workspace_size(tok),), 0xFF, dtype=torch.uint8, device="cuda")
+        H.hash_attn_workspace_init(ws[:256])
+    out = torch.full((T, q.shape[1], q.shape[2]), NAN, dtype=out_dtype, device="cuda")
+    lse = torch.full((T, q.shape[1]), NAN, device="cuda")
+    cu = cumulative(new) if cu is None else cu
+    lens_t = torch.tensor(lens, dtype=torch.int32, device="cuda") if lens_t is None else lens_t
+    H.hash_attn_chunk(tok, cache, q, K, V, table, cu, lens_t, out, lse, workspace=ws)
+    return out, lse, H.hash_attn_device_status(ws)
+
+
+def run_prefill(H, q, k, v, new, out_dtype=torch.bfloat16, ws=None, cu=None):
+    tok = H.make_tokens(q, k, v, len(new), out_dtype=out_dtype)
+    if ws is None:
+        ws = torch.full((H.hash_attn_packed_workspace_size(tok),), 0xFF, dtype=torch.uint8, device="cuda")
+        H.hash_attn_workspace_init(ws[:256])
+    out = torch.full(tuple(q.shape), NAN, dtype=out_dtype, device="cuda")
+    lse = torch.full(tuple(q.shape[:2]), NAN, device="cuda")
+    H.hash_attn_prefill(tok, q, k, v, cumulative(new) if cu is None else cu, out, lse, workspace=ws)
+    return out, lse, H.hash_attn_device_status(ws)
+
+
+def pages(g, seqs, ps, Hkv, d, order="token", extra=2, dirty=True):
+    """Random pool, a table that scatters its pages; rows behind the sequences are NaN."""
+    need = [(n + ps - 1) // ps for n in seqs]
+    n_pages = sum(need) + extra
+    shape = (n_pages, ps, Hkv, d) if order == "token" else (n_pages, Hkv, ps, d)
+    K, V = rand(g, *shape), rand(g, *shape)
+    if order == "token":
+        K, V = K.permute(0, 2, 1, 3), V.permute(0, 2, 1, 3)
+    perm = torch.randperm(n_pages, generator=g, device="cuda").to(torch.int32)
+    table = torch.full((len(seqs), max(1, max(need))), -5, dtype=torch.int32, device="cuda")  # unused entries are bad
+    own = torch.zeros(n_pages, ps, dtype=torch.bool, device="cuda")
+    at = 0
+    for s, n in enumerate(seqs):
+        table[s, :need[s]] = perm[at:at + need[s]]
+        for i in range(need[s]):
+            own[perm[at + i], :min(ps, n - i * ps)] = True
+        at += need[s]
+    if dirty:
+        bad = ~own[:, None, :, None].expand(K.shape)
+        K[bad] = NAN
+        V[bad] = float("inf")
+    return K, V, table
+
+
+def check_chunk(q, K, V, table, new, lens, out, lse, Hkv, what="", heads=None):
+    G = q.shape[1] // Hkv
+    qh, tb = q.double().cpu().numpy(), table.cpu().numpy()
+    a = 0
+    for s, (nq, nk) in enumerate(zip(new, lens)):
+        for g in range(Hkv):
+            if heads is not None and g not in heads:
+                continue
+            Kh = PO.page_rows(K[:, g].double().cpu().numpy(), tb[s], nk)
+            Vh = PO.page_rows(V[:, g].double().cpu().numpy(), tb[s], nk)
+            for h in range(g * G, (g + 1) * G):
+                ref = (*PO.causal_attention(qh[a:a + nq, h], Kh, Vh), nk)
+                if nq:
+                    check_rows(out[a:a + nq, h], lse[a:a + nq, h], ref, out.dtype == torch.bfloat16, f"{what} seq {s} head {h}")
+        a += nq
+
+
+def check_prefill(q, k, v, new, out, lse, what="", heads=None):
+    Hkv = k.shape[1]
+    G = q.shape[1] // Hkv
+    qh, kh, vh = (x.double().cpu().numpy() for x in (q, k, v))
+    a = 0
+    for s, n in enumerate(new):
+        for h in range(q.shape[1]) if heads is None else heads:
+            if n:
+                ref = (*PO.causal_attention(qh[a:a + n, h], kh[a:a + n, h // G], vh[a:a + n, h // G]), n)
+                check_rows(out[a:a + n, h], lse[a:a + n, h], ref, out.dtype == torch.bfloat16, f"{what} seq {s} head {h}")
+        a += n
+
+
+# ---------------------------------------------------------------- prefill
+
+PREFILL = [
+    # name, lengths, Hq, Hkv, d
+    ("one-token", [1], 1, 1, 128),
+    ("tile-edges", [127, 128, 129, 255, 256, 257], 2, 1, 64),
+    ("g4", [5, 0, 300, 64, 1], 8, 2, 128),
+    ("g3-odd-tile", [200, 85, 43], 6, 2, 128),
+    ("g7", [19, 150], 7, 1, 64),
+    ("g16", [100, 31], 16, 1, 128),
+    ("g128", [9, 2], 128, 1, 64),
+    ("long", [700], 2, 2, 128),
+]
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("case", PREFILL, ids=[c[0] for c in PREFILL])
+def test_prefill(H, case, out_dtype):
+    _, new, Hq, Hkv, d = case
+    g = torch.Generator(device="cuda").manual_seed(11)
+    T = sum(new)
+    q, k, v = rand(g, T, Hq, d), rand(g, T, Hkv, d), rand(g, T, Hkv, d)
+    out, lse, st = run_prefill(H, q, k, v, new, out_dtype)
+    assert st == (0, 0)
+    check_prefill(q, k, v, new, out, lse)
+
+
+def test_prefill_strided_inputs_and_rows_behind(H):
+    """q, k, v as views of one fused projection; rows that no sequence owns stay as they
+    were, and NaN in them or in other sequences reaches nobody."""
+    g = torch.Generator(device="cuda").manual_seed(12)
+    new, Hq, Hkv, d = [70, 33], 4, 2, 64
+    T = sum(new) + 9
+    qkv = rand(g, T, Hq + 2 * Hkv, d)
+    qkv[sum(new):] = NAN
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    out, lse, st = run_prefill(H, q, k, v, new)
+    assert st == (0, 0)
+    check_prefill(q, k, v, new, out, lse)
+    assert torch.isnan(out[sum(new):]).all() and torch.isnan(lse[sum(new):]).all()
+    qkv[:70] = NAN  # the first sequence is no number: the second does not see it
+    out2, lse2, _ = run_prefill(H, q, k, v, new)
+    assert torch.equal(out2[70:103], out[70:103]) and torch.equal(lse2[70:103], lse[70:103])
+    assert torch.isnan(out2[:70]).all()
+
+
+@pytest.mark.parametrize("scale", [30.0, 1000.0])
+def test_prefill_large_scores(H, scale):
+    """Scores far apart: the running maximum grows again and again (O is rescaled)."""
+    g = torch.Generator(device="cuda").manual_seed(13)
+    T, d = 640, 128
+    q, k, v = rand(g, T, 2, d), rand(g, T, 1, d), rand(g, T, 1, d)
+    k = (k.float() * torch.linspace(0.01, scale, T, device="cuda")[:, None, None]).bfloat16()
+    out, lse, st = run_prefill(H, q, k, v, [T], torch.float32)
+    assert st == (0, 0)
+    check_prefill(q, k, v, [T], out, lse)
+
+
+def test_prefill_bad_bounds_are_flagged(H):
+    g = torch.Generator(device="cuda").manual_seed(14)
+    q, k, v = rand(g, 60, 2, 64), rand(g, 60, 1, 64), rand(g, 60, 1, 64)
+    cu = torch.tensor([0, 20, 10, 61, 60, 60], dtype=torch.int32, device="cuda")  # only [0, 20) is in order
+    out, lse, st = run_prefill(H, q, k, v, [20, 0, 0, 0, 0], cu=cu)
+    assert st == (H.HA_ERR_DEVICE, H.HA_DEVERR_SEQLEN)
+    check_prefill(q[:20], k[:20], v[:20], [20], out[:20], lse[:20])
+    assert torch.isnan(out[20:]).all()
+
+
+# ---------------------------------------------------------------- chunk
+
+CHUNK = [
+    # name, new, lens, Hq, Hkv, d, page, order
+    ("decode-1", [1], [1], 4, 1, 128, 16, "token"),
+    ("decode-ragged", [1] * 6, [1, 15, 16, 129, 400, 1000], 8, 2, 128, 16, "token"),
+    ("decode-g8", [1] * 3, [700, 64, 65], 16, 2, 64, 32, "head"),
+    ("decode-g1", [1, 1], [300, 40], 3, 3, 128, 48, "head"),
+    ("chunk", [40, 7, 130], [300, 7, 900], 4, 2, 128, 64, "token"),
+    ("chunk-80", [100, 3], [333, 500], 6, 2, 64, 80, "head"),
+    ("mixed", [1, 60, 1, 0, 33], [200, 500, 3, 77, 33], 8, 1, 64, 128, "token"),
+    ("rows-without-keys", [50, 4, 9], [20, 0, 9], 4, 2, 128, 16, "token"),
+    ("parity-items-split", [3], [2000], 4, 1, 128, 256, "head"),
+    ("two-tiles-split", [96], [1500], 4, 1, 128, 16, "head"),
+    ("g128", [2, 1], [150, 70], 128, 1, 128, 16, "token"),
+]
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("case", CHUNK, ids=[c[0] for c in CHUNK])
+def test_chunk(H, case, out_dtype):
+    """Rows of the pages behind the sequences hold NaN and infinities, unused table entries are bad."""
+    _, new, lens, Hq, Hkv, d, ps, order = case
+    g = torch.Generator(device="cuda").manual_seed(21)
+    K, V, table = pages(g, lens, ps, Hkv, d, order)
+    q = rand(g, sum(new), Hq, d)
+    out, lse, st = run_chunk(H, q, K, V, table, new, lens, Hkv, out_dtype)
+    assert st == (0, 0), hex(st[1])
+    check_chunk(q, K, V, table, new, lens, out, lse, Hkv)
+    again = run_chunk(H, q, K, V, table, new, lens, Hkv, out_dtype)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)  # the split's order is fixed
+
+
+def test_chunk_contiguous_cache_of_any_length(H):
+    """One page per sequence: the cache [batch, h_kv, n_cap, d] of the decode step, n_cap odd."""
+    g = torch.Generator(device="cuda").manual_seed(22)
+    B, Hq, Hkv, d, cap = 3, 8, 2, 128, 613
+    K, V = rand(g, B, Hkv, cap, d), rand(g, B, Hkv, cap, d)
+    table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None]
+    lens, new = [613, 100, 257], [2, 1, 5]
+    q = rand(g, sum(new), Hq, d)
+    out, lse, st = run_chunk(H, q, K, V, table, new, lens, Hkv)
+    assert st == (0, 0)
+    check_chunk(q, K, V, table, new, lens, out, lse, Hkv)
+
+
+def test_chunk_agrees_with_dense_decode(H):
+    """One new token per sequence is the decode step's dense path."""
+    g = torch.Generator(device="cuda").manual_seed(23)
+    B, Hq, Hkv, d, cap = 4, 16, 4, 128, 2048
+    K, V, q = rand(g, B, Hkv, cap, d), rand(g, B, Hkv, cap, d), rand(g, B, Hq, d)
+    lens = [2048, 1, 777, 1500]
+    lt = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    shape = H.make_shape(q, K, V)
+    ws = torch.empty(H.hash_attn_workspace_size(shape, cap, 0, 0), dtype=torch.uint8, device="cuda")
+    H.hash_attn_workspace_init(ws)
+    ro, rl = torch.empty(B, Hq, d, device="cuda"), torch.empty(B, Hq, device="cuda")
+    H.hash_attn_decode(shape, q, None, None, K, V, lt, None, cap, 0, 0, ro, rl, workspace=ws)
+    assert H.hash_attn_device_status(ws)[0] == 0
+    table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None]
+    out, lse, st = run_chunk(H, q, K, V, table, [1] * B, lens, Hkv, torch.float32)
+    assert st == (0, 0)
+    check_chunk(q, K, V, table, [1] * B, lens, out, lse, Hkv)
+    # the decode step's own parity tolerance
+    assert torch.all((out - ro).abs() <= 2e-3 * (1 + ro.abs())) and torch.all((lse - rl).abs() <= 1e-4 * (1 + rl.abs()))
+
+
+def test_chunk_device_errors(H):
+    """Bad lengths count as empty, bad bounds are skipped, a bad page is one of zeros."""
+    g = torch.Generator(device="cuda").manual_seed(24)
+    lens, Hkv, d, ps = [64, 64, 64], 1, 64, 16
+    K, V, table = pages(g, lens, ps, Hkv, d)
+    q = rand(g, 3, 2, d)
+    bad = torch.tensor([64, 65, -1], dtype=torch.int32, device="cuda")
+    out, lse, st = run_chunk(H, q, K, V, table, [1, 1, 1], lens, Hkv, lens_t=bad)
+    assert st == (H.HA_ERR_DEVICE, H.HA_DEVERR_SEQLEN)
+    check_chunk(q[:1], K, V, table, [1], [64], out[:1], lse[:1], Hkv)
+    assert torch.all(out[1:] == 0) and torch.all(torch.isneginf(lse[1:]))
+    cu = torch.tensor([0, 1, 9, 3], dtype=torch.int32, device="cuda")
+    out, lse, st = run_chunk(H, q, K, V, table, [1, 1, 1], lens, Hkv, cu=cu)
+    assert st == (H.HA_ERR_DEVICE, H.HA_DEVERR_SEQLEN)
+    check_chunk(q[:1], K, V, table, [1], [64], out[:1], lse[:1], Hkv)
+    assert torch.isnan(out[1:]).all()
+    zeros = table.clone()
+    zeros[1, 2] = K.shape[0]
+    zeros[2, 0] = -1
+    out, lse, st = run_chunk(H, q, K, V, zeros, [1, 1, 1], lens, Hkv)
+    assert st == (H.HA_ERR_DEVICE, H.HA_DEVERR_INDEX)
+    K2, V2 = torch.cat([K, torch.zeros_like(K[:1])]), torch.cat([V, torch.zeros_like(V[:1])])
+    zeros[1, 2] = zeros[2, 0] = K.shape[0]
+    check_chunk(q, K2, V2, zeros, [1, 1, 1], lens, out, lse, Hkv)
+
+
+def test_workspace_serves_calls_in_turn(H):
+    """One workspace, calls of several shapes back to back with nothing between them."""
+    g = torch.Generator(device="cuda").manual_seed(25)
+    ws = None
+    runs = []
+    for new, lens, Hq, Hkv, d in [([200, 3], [900, 3], 8, 2, 128), ([1, 1], [3000, 50], 8, 1, 128), ([7], [1999], 4, 4, 64)]:
+        K, V, table = pages(g, lens, 32, Hkv, d)
+        q = rand(g, sum(new), Hq, d)
+        tok = H.make_tokens(q, None, None, len(new), h_kv=Hkv)
+        size = H.hash_attn_packed_workspace_size(tok)
+        if ws is None or ws.numel() < size:
+            ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+        runs.append((tok, H.make_cache(K, V, table), q, K, V, table, cumulative(new),
+                     torch.tensor(lens, dtype=torch.int32, device="cuda"), new, lens, Hkv))
+    outs = [(torch.empty(r[2].shape, device="cuda"), torch.empty(r[2].shape[:2], device="cuda")) for r in runs for _ in range(2)]
+    for i, (o, l) in enumerate(outs):
+        tok, cache, q, K, V, table, cu, lt = runs[i // 2][:8]
+        H.hash_attn_chunk(tok, cache, q, K, V, table, cu, lt, o, l, workspace=ws)
+    assert H.hash_attn_device_status(ws) == (0, 0)
+    for i, (o, l) in enumerate(outs):
+        _, _, q, K, V, table, _, _, new, lens, Hkv = runs[i // 2]
+        check_chunk(q, K, V, table, new, lens, o, l, Hkv, f"call {i}")
+
+
+def test_large_pool_offsets(H):
+    """Rows more than 2^31 elements into the pool."""
+    g = torch.Generator(device="cuda").manual_seed(26)
+    Hkv, d, ps = 8, 128, 64
+    n_pages = (1 << 31) // (Hkv * d * ps) + 40
+    K = torch.zeros(n_pages, ps, Hkv, d, dtype=torch.bfloat16, device="cuda").permute(0, 2, 1, 3)
+    V = torch.zeros_like(K)
+    table = torch.tensor([[n_pages - 1, 3, n_pages - 2]], dtype=torch.int32, device="cuda")
+    k, v, q = rand(g, 130, Hkv, d), rand(g, 130, Hkv, d), rand(g, 130, Hkv, d)
+    tok = H.make_tokens(q, k, v, 1, out_dtype=torch.float32)
+    cache = H.make_cache(K, V, table)
+    cu, lt = cumulative([130]), torch.tensor([130], dtype=torch.int32, device="cuda")
+    H.hash_attn_append(tok, cache, None, k, v, table, cu, lt, None, K, V)
+    assert torch.equal(K[n_pages - 1].permute(1, 0, 2), k[:64]) and torch.equal(V[n_pages - 2, :, :2].permute(1, 0, 2), v[128:])
+    out, lse, st = run_chunk(H, q, K, V, table, [130], [130], Hkv, torch.float32)
+    assert st == (0, 0)
+    check_prefill(q, k, v, [130], out, lse, heads=[0, 7])
+
+
+# ---------------------------------------------------------------- append
+
+def inv_freq(rot, base=500000.0):
+    return torch.tensor([base ** (-2.0 * i / rot) for i in range(rot // 2)], device="cuda")
+
+
+def run_append(H, q, k, v, table, new, lens, q_out, K, V, rope=None, cu=None, lens_t=None, W=None, k_sig=None, flags=None):
+    tok = H.make_tokens(k if q is None else q, k, v, len(new))
+    H.hash_attn_append(tok, H.make_cache(K, V, table, k_sig), q, k, v, table, cumulative(new) if cu is None else cu,
+                       torch.tensor(lens, dtype=torch.int32, device="cuda") if lens_t is None else lens_t, q_out, K, V,
+                       rope=rope, W=W, k_sig=k_sig, dev_flags=flags)
+
+
+def close_rotated(got, ref, x, dtype, what):
+    """A rotated value a c - b s in float32: the angle is off by 2^-24 turns at most (2^-31
+    half turns and one rounding of the product's 2^-25), cos and sin by 2 steps: at most
+    2^-21 |pair|; then one rounding to dtype."""
+    u = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
+    tol = 2.0 ** -21 * np.abs(x) + u * np.abs(ref) * 1.01 + 1e-30
+    err = np.abs(got - ref)
+    assert np.all(err <= tol), f"{what}: off by {err.max():.3g}, worst ratio {(err / tol).max():.3g}"
+
+
+APPEND = [
+    # name, new, lens, Hq, Hkv, d, page, order, rot, interleaved, dtype, cache dtype
+    ("decode", [1, 1, 1], [1, 17, 1000000], 8, 2, 128, 16, "token", 128, False, torch.bfloat16, torch.bfloat16),
+    ("prompts", [40, 0, 130], [40, 9, 300], 6, 2, 64, 48, "head", 64, False, torch.bfloat16, torch.bfloat16),
+    ("interleaved-f32", [33, 5], [33, 70], 4, 1, 64, 7, "token", 64, True, torch.float32, torch.float32),
+    ("partial", [20], [500], 2, 2, 128, 64, "token", 32, False, torch.float32, torch.bfloat16),
+    ("partial-interleaved", [20], [90], 2, 1, 128, 128, "head", 96, True, torch.bfloat16, torch.float32),
+    ("smallest-rotation", [9], [9], 1, 1, 64, 5, "head", 16, False, torch.float32, torch.float32),
+]
+
+
+@pytest.mark.parametrize("case", APPEND, ids=[c[0] for c in APPEND])
+def test_append(H, case):
+    _, new, lens, Hq, Hkv, d, ps, order, rot, inter, dt, cdt = case
+    g = torch.Generator(device="cuda").manual_seed(31)
+    T, n = sum(new), len(new)
+    q, k, v = rand(g, T, Hq, d, dtype=dt), rand(g, T, Hkv, d, dtype=dt), rand(g, T, Hkv, d, dtype=dt)
+    first = [(b - a) // ps for a, b in zip(new, lens)]
+    need = [(b + ps - 1) // ps for b in lens]
+    n_pages = sum(b - a for a, b in zip(first, need)) + 3
+    shape = (n_pages, ps, Hkv, d) if order == "token" else (n_pages, Hkv, ps, d)
+    K, V = rand(g, *shape, dtype=cdt), rand(g, *shape, dtype=cdt)
+    if order == "token":
+        K, V = K.permute(0, 2, 1, 3), V.permute(0, 2, 1, 3)
+    table = torch.full((n, max(need)), -9, dtype=torch.int32, device="cuda")
+    perm = torch.randperm(n_pages, generator=g, device="cuda").to(torch.int32)
+    at = 0
+    for s in range(n):
+        table[s, first[s]:need[s]] = perm[at:at + need[s] - first[s]]
+        at += need[s] - first[s]
+    K0, V0 = K.clone(), V.clone()
+    w = inv_freq(rot)
+    rope = H.rope(w, inter)
+    q_out = torch.full((T, Hq, d), NAN, dtype=dt, device="cuda")
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    run_append(H, q, k, v, table, new, lens, q_out, K, V, rope, flags=flags)
+    torch.cuda.synchronize()
+    assert int(flags) == 0
+    wh, tb = w.double().cpu().numpy(), table.cpu().numpy()
+    qh, kh, vh = (x.double().cpu().numpy() for x in (q, k, v))
+    touched = torch.zeros(n_pages, ps, dtype=torch.bool, device="cuda")
+    t = 0
+    pair = lambda x: np.sqrt(2) * np.abs(x).max()  # noqa: E731
+    for s in range(n):
+        for i in range(new[s]):
+            pos = lens[s] - new[s] + i
+            pg, row = tb[s, pos // ps], pos % ps
+            touched[pg, row] = True
+            close_rotated(q_out[t].double().cpu().numpy(), PO.rotate(qh[t], pos, wh, inter), pair(qh[t]), dt, f"q {s} {i}")
+            close_rotated(K[pg, :, row].double().cpu().numpy(), PO.rotate(kh[t], pos, wh, inter), pair(kh[t]), cdt, f"k {s} {i}")
+            assert torch.equal(V[pg, :, row], v[t].to(cdt))
+            assert torch.equal(q_out[t, :, rot:], q[t, :, rot:]) and torch.equal(K[pg, :, row, rot:], k[t, :, rot:].to(cdt))
+            t += 1
+    keep = ~touched[:, None, :, None].expand(K.shape)
+    assert torch.equal(K[keep], K0[keep]) and torch.equal(V[keep], V0[keep])
+    # in place, and without queries
+    q2 = q.clone()
+    run_append(H, q2, k, v, table, new, lens, q2, K, V, rope)
+    assert torch.equal(q2, q_out)
+    K1, V1 = K0.clone(), V0.clone()
+    run_append(H, None, k, v, table, new, lens, None, K1, V1, rope)
+    assert torch.equal(K1, K) and torch.equal(V1, V)
+
+
+def test_append_far_positions(H):
+    """Every position keeps its angle to 2^-21, up to the longest cache (2^30 tokens)."""
+    d, ps = 64, 1 << 10
+    x = torch.zeros(1, 1, d, device="cuda")
+    x[..., : d // 2] = 1.0
+    K, V = torch.zeros(1, 1, ps, d, device="cuda"), torch.zeros(1, 1, ps, d, device="cuda")
+    table = torch.zeros(1, 1 << 20, dtype=torch.int32, device="cuda")
+    w = torch.cat([inv_freq(d)[:16], torch.tensor([1.0, 0.3333333, 3.0, 1e-9, 1e-30, 0.0, -0.7, 65504.0], device="cuda"),
+                   inv_freq(d)[24:]])
+    for pos in [0, 1, 12345, 1 << 20, (1 << 24) + 1, (1 << 30) - 1]:
+        q_out = torch.empty(1, 1, d, device="cuda")
+        run_append(H, x, x, x, table, [1], [pos + 1], q_out, K, V, H.rope(w))
+        ref = PO.rotate(x[0, 0].cpu().numpy(), pos, w.double().cpu().numpy())
+        # inv_freq * pos is exact in 64 bits, its cosine to 2^-52 of an angle below 2^46
+        err = np.abs(q_out[0, 0].double().cpu().numpy() - ref)
+        assert err.max() <= 2.0 ** -21 + 2.0 ** -24 + 2.0 ** (math.log2(65504.0 * (pos + 1)) - 53), (pos, err.max())
+
+
+def test_append_codes_equal_encode_keys(H):
+    """The codes written with the keys are those of hash_attn_encode_keys on the stored keys."""
+    g = torch.Generator(device="cuda").manual_seed(33)
+    for d, cdt in ((128, torch.bfloat16), (64, torch.float32)):
+        B, Hkv, cap = 3, 2, 200
+        new, lens = [150, 1, 90], [150, 40, 200]
+        T = sum(new)
+        k, v = rand(g, T, Hkv, d), rand(g, T, Hkv, d)
+        K, V = torch.zeros(B, Hkv, cap, d, dtype=cdt, device="cuda"), torch.zeros(B, Hkv, cap, d, dtype=cdt, device="cuda")
+        W = torch.randn(Hkv, 32, d, generator=g, device="cuda")
+        table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None]
+        sig = torch.full((B, Hkv, cap), 0x55, dtype=torch.int32, device="cuda")
+        run_append(H, None, k, v, table, new, lens, None, K, V, H.rope(inv_freq(d)), W=W, k_sig=sig)
+        ref = torch.full((B, Hkv, cap), 0x55, dtype=torch.int32, device="cuda")
+        shape = H.make_shape(torch.zeros(B, Hkv, d, dtype=torch.bfloat16, device="cuda"), K, V, ref)
+        for i in range(max(new)):
+            pos = torch.tensor([b - a + i if i < a else -1 for a, b in zip(new, lens)], dtype=torch.int32, device="cuda")
+            H.hash_attn_encode_keys(shape, K, W, pos, ref)
+        assert torch.equal(sig, ref)
+
+
+def test_append_device_errors_skip_and_flag(H):
+    g = torch.Generator(device="cuda").manual_seed(34)
+    Hkv, d, ps = 2, 64, 16
+    new = [4, 3, 2, 5]
+    k, v, q = rand(g, 14, Hkv, d), rand(g, 14, Hkv, d), rand(g, 14, 4, d)
+    K, V = torch.zeros(6, Hkv, ps, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(6, Hkv, ps, d, dtype=torch.bfloat16, device="cuda")
+    table = torch.tensor([[0, 1], [2, 6], [3, 4], [5, 5]], dtype=torch.int32, device="cuda")
+    sig = torch.zeros(6, Hkv, ps, dtype=torch.int32, device="cuda")
+    W = torch.randn(Hkv, 32, d, generator=g, device="cuda")
+
+    def call(lens, cu=None):
+        K.zero_(), V.zero_(), sig.zero_()
+        flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+        q_out = torch.full((14, 4, d), NAN, dtype=torch.bfloat16, device="cuda")
+        run_append(H, q, k, v, table, new, lens, q_out, K, V, None, W=W, k_sig=sig, flags=flags, cu=cu)
+        return int(flags), q_out, (V != 0).any(-1).any(1), (sig != 0).any(1)
+
+    # a page outside the pool: its keys and values are skipped, its queries are not
+    fl, qo, wrote, coded = call([4, 18, 2, 5])
+    assert fl == H.HA_DEVERR_INDEX and torch.equal(qo, q)
+    want = torch.zeros(6, ps, dtype=torch.bool)
+    want[0, :4] = want[3, :2] = want[5, :5] = True
+    want[2, 15] = True
+    assert torch.equal(wrote.cpu(), want) and torch.equal(coded.cpu(), want)
+    # lengths outside the table, and new tokens that start before the sequence
+    fl, qo, wrote, _ = call([33, 3, -1, 3])
+    assert fl == H.HA_DEVERR_SEQLEN | H.HA_DEVERR_INDEX
+    want.zero_()
+    want[2, :3] = want[5, :3] = True
+    assert torch.equal(wrote.cpu(), want)
+    assert torch.isnan(qo[:4]).all() and torch.equal(qo[4:7], q[4:7]) and torch.isnan(qo[7:11]).all() and torch.equal(qo[11:], q[11:])
+    # bounds that fall, and rows behind the last sequence
+    fl, qo, wrote, _ = call([4, 3, 2, 5], cu=torch.tensor([0, 4, 2, 5, 9], dtype=torch.int32, device="cuda"))
+    assert fl & H.HA_DEVERR_SEQLEN and torch.isnan(qo[9:]).all()
+
+
+# ---------------------------------------------------------------- together
+
+def test_prompt_then_chunks_then_decode(H):
+    """As a serving loop runs them: prompts are attended over and appended with their codes,
+    a second chunk follows, then single tokens by the chunk call and by the sparse decode
+    step on the same cache; all captured once into a graph and replayed as well."""
+    g = torch.Generator(device="cuda").manual_seed(41)
+    B, Hq, Hkv, d, cap = 2, 8, 2, 128, 512
+    W = torch.randn(Hkv, 32, d, generator=g, device="cuda")
+    K, V = torch.zeros(B, Hkv, cap, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(B, Hkv, cap, d, dtype=torch.bfloat16, device="cuda")
+    sig = torch.zeros(B, Hkv, cap, dtype=torch.int32, device="cuda")
+    table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None]
+    rope = H.rope(w := inv_freq(d))
+    steps = [[200, 131], [60, 3], [1, 1]]
+    data, done = [], [0, 0]
+    for new in steps:
+        done = [a + b for a, b in zip(done, new)]
+        T = sum(new)
+        q, k, v = rand(g, T, Hq, d), rand(g, T, Hkv, d), rand(g, T, Hkv, d)
+        data.append((H.make_tokens(q, k, v, B, out_dtype=torch.float32), q, k, v, cumulative(new),
+                     torch.tensor(done, dtype=torch.int32, device="cuda"), torch.empty_like(q),
+                     torch.empty(T, Hq, d, device="cuda"), torch.empty(T, Hq, device="cuda")))
+    cache = H.make_cache(K, V, table, sig)
+    ws = torch.zeros(max(H.hash_attn_packed_workspace_size(x[0]) for x in data), dtype=torch.uint8, device="cuda")
+    shape = H.make_shape(data[2][1], K, V, sig)
+    m = 48
+    wd = torch.empty(H.hash_attn_workspace_size(shape, m, 4, 8), dtype=torch.uint8, device="cuda")
+    H.hash_attn_workspace_init(wd)
+    q_sig = torch.empty(B, Hq, dtype=torch.int32, device="cuda")
+    so, sl = torch.empty(B, Hq, d, device="cuda"), torch.empty(B, Hq, device="cuda")
+    first = torch.empty_like(data[0][7]), torch.empty_like(data[0][8])
+
+    def loop():
+        for i, (tok, q, k, v, cu, lt, qr, out, lse) in enumerate(data):
+            H.hash_attn_append(tok, cache, q, k, v, table, cu, lt, qr, K, V, rope=rope, W=W, k_sig=sig)
+            H.hash_attn_chunk(tok, cache, qr, K, V, table, cu, lt, out, lse, workspace=ws)
+        qr, lt = data[2][6], data[2][5]
+        H.hash_attn_encode_queries(shape, qr, W, q_sig)
+        H.hash_attn_decode(shape, qr, q_sig, sig, K, V, lt, None, m, 4, 8, so, sl, workspace=wd)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        loop()
+        assert H.hash_attn_device_status(ws)[0] == 0 and H.hash_attn_device_status(wd)[0] == 0
+    torch.cuda.current_stream().wait_stream(side)
+    eager = [x.clone() for e in data for x in (e[7], e[8])] + [so.clone(), sl.clone(), K.clone(), sig.clone()]
+    # against the oracle: the rotated queries over the cache as it stood at each step
+    for (tok, q, k, v, cu, lt, qr, out, lse), new in zip(data, steps):
+        check_chunk(qr, K, V, table, new, lt.tolist(), out, lse, Hkv)
+    # whole prompts: prefill over the rotated rows says the same as the chunk over the cache
+    kr = torch.cat([K[0, :, :200], K[1, :, :131]], 1).permute(1, 0, 2).contiguous()
+    vr = torch.cat([V[0, :, :200], V[1, :, :131]], 1).permute(1, 0, 2).contiguous()
+    H.hash_attn_prefill(H.make_tokens(data[0][6], kr, vr, B, out_dtype=torch.float32), data[0][6], kr, vr, data[0][4], *first,
+                        workspace=ws)
+    check_prefill(data[0][6], kr, vr, steps[0], *first)
+    # the sparse step against the oracle's selection on these codes
+    from oracle import hashattn_oracle as O
+    for b, h in [(0, 0), (1, 5)]:
+        n = int(data[2][5][b])
+        idx, _, ro, rl = O.decode_head(data[2][6][b, h].float().cpu().numpy(), int(q_sig[b, h]) & 0xFFFFFFFF,
+                                       sig[b, h // 4].cpu().numpy().astype(np.int64) & 0xFFFFFFFF, K[b, h // 4].float().cpu().numpy(),
+                                       V[b, h // 4].float().cpu().numpy(), n, m, 4, 8)
+        assert np.all(np.abs(so[b, h].cpu().numpy() - ro) <= 2e-3 * (1 + np.abs(ro)))
+    # captured and replayed on new storage contents
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loop()
+    K.zero_(), sig.zero_()
+    for e in data:
+        e[7].fill_(NAN)
+    so.fill_(NAN)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert H.hash_attn_device_status(ws)[0] == 0
+    for a, b in zip(eager, [x for e in data for x in (e[7], e[8])] + [so, sl, K, sig]):
+        assert torch.equal(a, b)
