@@ -14,10 +14,12 @@
 // MMA's A operand from tensor memory). O is rescaled only when a row's maximum
 // grows by more than 2^8 over its reference: until then P <= 2^8, which costs
 // neither range nor precision, as bf16 keeps its relative step. l is summed in
-// float32 from the values before they are rounded. With a float32 output, P
-// enters as three bf16 parts, each the rounding of what the earlier ones left
-// (together all 24 bits of p), for three times the P V products; their tiles are
-// 64 keys, so that the parts fit where S was.
+// float32 from the values before they are rounded.
+// With a float32 output, P enters as three bf16 parts, each the rounding of what the
+// earlier ones left (together all 24 bits of p), for three times the P V products;
+// tiles are 64 keys, so that the parts fit beside and over S. The tensor cores'
+// accumulator cuts off instead of rounding (measured: 2e-8 a step, 1.2e-5 of O after
+// 3,500 keys), so a tile's O is added to float32 sums in registers.
 //
 // Rows: the G query heads of a KV head share its K and V, so a tile packs
 // TQ = floor(128 / G) tokens x G heads (row = token * G + head). An item is
@@ -42,8 +44,11 @@
 namespace ha {
 namespace {
 
-constexpr int kAttThreads = 320;
+constexpr int kAttThreads = 384;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
+// Registers of a softmax thread and of the others: 256 x 208 + 128 x 88 is what 384
+// threads are launched with (168 each).
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kMinSpan = 2;           // fewest tiles of a CTA
 constexpr uint32_t kTmemCols = 512;   // S0, S1 (128 each; P overlays them), O0, O1
 constexpr float kRescale = 8.f;       // growth of the maximum (log2) that makes O be rescaled
@@ -57,6 +62,9 @@ struct AttCfg {
     static constexpr int kSpan = kKeys * 128;            // bytes of one span of its rows
     static constexpr int kStages = 5 * 32768 / kTile;
     static constexpr int kParts = F32OUT ? 3 : 1;        // bf16 parts of P
+    // First tensor memory column of a part: P takes the columns of S; three parts of 32
+    // columns take the second half, beside S's 64, and S's first 32 once they are read.
+    static constexpr __host__ __device__ int part_col(int i) { return !F32OUT || i == 2 ? 0 : 64 + 32 * i; }
     static constexpr int kBars = 2 * kStages + 13;
     static constexpr int kSmem = 2 * kQTile + kStages * kTile + 2048 + 8 * kBars + 128;
     static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -224,10 +232,35 @@ struct SegIter {
     }
 };
 
+template <int T>
+struct Stream {
+    static constexpr int value = T;
+};
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Two float32 lanes of a 64-bit register.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // two bf16 values, the first in the low half
@@ -235,6 +268,42 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// x[k] for a row that sees the first lim of n columns: -inf from there on.
+template <int N>
+__device__ __forceinline__ void mask_columns(uint32_t (&x)[N], int lim) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (k >= lim) x[k] = 0xff800000u;
+}
+
+// max(a, max of x): four chains, so that they overlap.
+template <int N>
+__device__ __forceinline__ float max_of(const uint32_t (&x)[N], float a) {
+    float m[4] = {a, a, a, a};
+#pragma unroll
+    for (int k = 0; k < N; k += 8)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            m[u] = fmaxf(fmaxf(m[u], __uint_as_float(x[k + 2 * u])), __uint_as_float(x[k + 2 * u + 1]));
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// The weights 2^{x qscale - sub} of N columns as bf16 pairs in w; their float32 sum
+// is added to sum.
+template <int N>
+__device__ __forceinline__ void weights(const uint32_t* x, uint64_t qscale2, uint64_t nsub2, uint32_t (&w)[N / 2],
+                                        uint64_t (&sum)[2]) {
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) {
+        float a, b;
+        unpack2(fma2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), qscale2, nsub2), a, b);
+        a = ex2(a);
+        b = ex2(b);
+        sum[k & 1] = add2(sum[k & 1], pack2(a, b));
+        w[k] = pack_bf16(a, b);
+    }
 }
 
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -388,6 +457,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     if (w1 > first.w) it.start(p, first, w1);
     Segment<KT> g;
 
+    if (warp >= kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kLoadWarp) {
         const int lg = p.box_log2;               // rows of a box: 2^lg
         const int nbox = KT >> lg;
@@ -467,38 +538,51 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         constexpr uint32_t kIdO = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
                                   ((128u >> 4) << 24);
         int n = 0, nq = 0, nseg = 0;
-        int cnt0 = 0, cnt1 = 0;  // tiles of the two streams so far
+        uint32_t cnt = 0;  // bit t: parity of stream t's tiles so far
         bool ok = true;
-        // S_t = Q_t K^T of the K tile in ring slot s
-        auto issue_s = [&](int t, int qtile, int s) {
-            if (lane == 0) {
-                const uint32_t a = s_q + (uint32_t)(qtile * C::kQTile), b = s_ring + (uint32_t)(s * C::kTile);
+        // Low halves of the descriptors: Q (K-major, leading offset unused), the first ring
+        // slot as K (the same) and as V, whose keys are the MMA's K dimension and the rows
+        // of the layout (MN-major): the next 64 dims lie kSpan bytes further, 16 keys 2048.
+        const uint32_t q_lo = uniform(((s_q & 0x3FFFFu) >> 4) | (1u << 16));
+        const uint32_t k_lo = uniform(((s_ring & 0x3FFFFu) >> 4) | (1u << 16));
+        const uint32_t v_lo = uniform(((s_ring & 0x3FFFFu) >> 4) | ((uint32_t)(C::kSpan >> 4) << 16));
+        const uint32_t tm = uniform(tmem);
+        // S_t = Q K^T of the K tile in ring slot s
+        auto issue_s = [&](auto T, uint32_t qtile, uint32_t s) {
+            constexpr uint32_t t = decltype(T)::value;
+            const uint32_t a = q_lo + qtile * (uint32_t)(C::kQTile >> 4), b = k_lo + s * (uint32_t)(C::kTile >> 4);
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t h = (uint32_t)(kk >> 2), o = (uint32_t)(kk & 3) * 32u;
-                    tc_mma(tmem + (uint32_t)(t * 128), sw128_desc(a + h * 16384u + o),
-                           sw128_desc(b + h * (uint32_t)C::kSpan + o), kIdS, kk > 0 ? 1u : 0u);
+                    const uint32_t h = (uint32_t)(kk >> 2), o = (uint32_t)(kk & 3) * 2u;
+                    tc_mma(tm + t * 128u, sw128_desc_of(a + h * 1024u + o),
+                           sw128_desc_of(b + h * (uint32_t)(C::kSpan >> 4) + o), kIdS, kk > 0 ? 1u : 0u);
                 }
                 tc_commit(s_full(t));
             }
+            __syncwarp();
         };
         // O_t (+)= P_t V of the V tile in ring slot s
-        auto issue_o = [&](int t, int s, bool acc) {
-            if (lane == 0) {
-                const uint32_t b = s_ring + (uint32_t)(s * C::kTile);
+        auto issue_o = [&](auto T, uint32_t s, uint32_t acc) {
+            constexpr uint32_t t = decltype(T)::value;
+            const uint32_t b = v_lo + s * (uint32_t)(C::kTile >> 4);
+            if (elect_one()) {
 #pragma unroll
                 for (int part = 0; part < C::kParts; ++part)
 #pragma unroll
                     for (int kk = 0; kk < KT / 16; ++kk)
-                        tc_mma_ts(tmem + 256u + (uint32_t)(t * 128), tmem + (uint32_t)(t * 128 + part * (KT / 2) + kk * 8),
-                                  sw128_desc_mn(b + (uint32_t)kk * 2048u, (uint32_t)C::kSpan), kIdO,
-                                  (acc || part > 0 || kk > 0) ? 1u : 0u);
+                        tc_mma_ts(tm + 256u + t * 128u, tm + t * 128u + (uint32_t)(C::part_col(part) + kk * 8),
+                                  sw128_desc_of(b + (uint32_t)kk * 128u), kIdO, part > 0 || kk > 0 ? 1u : acc);
                 tc_commit(o_done(t));
             }
+            __syncwarp();
         };
-        auto release = [&](int s) {
-            if (lane == 0) tc_commit(empty(s));
+        auto commit = [&](uint32_t bar) {
+            if (elect_one()) tc_commit(bar);
+            __syncwarp();
         };
+        // slot of ring index k, and the wait for what is loaded into it
+        auto slot = [&](int k) { return uniform((uint32_t)(k % S)); };
         auto wait = [&](uint32_t bar, uint32_t parity) {
             const bool r = mbar_wait_bounded(bar, parity, s_abort);
             tc_fence_after();
@@ -513,106 +597,59 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             // an arrival on seg_done, which every softmax warp waits for before it gives
             // the O's of this one back: so neither side is ever two phases ahead, also
             // where a stream has no tiles and nothing else holds its warps back.
-            auto wait_free = [&](int t) { return wait(o_free(t), free_ph); };
+            auto wait_free = [&]() { return wait(o_free(0), free_ph) && wait(o_free(1), free_ph); };
             if (nt == 0) {
-                ok = wait_free(0) && wait_free(1);
-                if (ok && lane == 0) tc_commit(seg_done);
+                ok = wait_free();
+                if (ok) commit(seg_done);
                 continue;
             }
             const int jend = g.jb + nt;
-            // rows of the V tile past the last key: zeros (what lies there may be no number)
-            auto clear_tail = [&](int j, int s) {
-                const int rows = g.kend - j * KT;
-                if (rows < KT) {
-                    for (int i = lane; i < (KT - rows) * 8 * C::kHalves; i += 32) {
-                        const int h = i / ((KT - rows) * 8), k = i - h * ((KT - rows) * 8);
-                        *reinterpret_cast<uint4*>(s_raw + 2 * C::kQTile + s * C::kTile + h * C::kSpan + rows * 128 + k * 16) =
-                            make_uint4(0, 0, 0, 0);
-                    }
-                    fence_async_shared();
-                    __syncwarp();
-                }
-            };
             const int n0 = n;  // ring index of K(jb); K(j) is n0 + 2 (j - jb), V(j) the next
+            // Row tile 0 of two takes the key tiles [jb, e0), row tile 1 all; with one row
+            // tile the streams take every other one. S of a stream's next tile is issued
+            // right behind P V of this one, which reads P where that S goes: the products
+            // run in the order of their issue.
+            const int e0 = g.parity ? jend : g.jb + g.stream_tiles(0);
+            const int step = g.parity ? 2 : 1;
             auto K = [&](int j) { return n0 + 2 * (j - g.jb); };
+            // S of stream t's tile j, where it has one; K(j) is free behind its last reader
+            auto next_s = [&](auto T, int j) {
+                constexpr int t = decltype(T)::value;
+                if (j >= (t == 0 ? e0 : jend)) return true;
+                if (!wait_slot(K(j))) return false;
+                const uint32_t s = slot(K(j));
+                issue_s(T, g.parity ? 0u : (uint32_t)t, s);
+                if (t == 1 || g.parity) {
+                    commit(empty(s));
+                    if (j == jend - 1) commit(q_empty);
+                }
+                return true;
+            };
+            bool free_ok = false;
+            // P V of stream t's tile j, and its next S; `last`: nobody reads V(j) after it
+            auto advance = [&](auto T, int j, uint32_t sv, bool last) {
+                constexpr int t = decltype(T)::value;
+                if (!wait(p_full(t), (cnt >> t) & 1u)) return false;
+                cnt ^= 1u << t;
+                if (!free_ok && !wait_free()) return false;
+                free_ok = true;
+                issue_o(T, sv, !F32OUT && j >= g.jb + step ? 1u : 0u);
+                if (last) commit(empty(sv));
+                return next_s(T, j + step);
+            };
             ok = wait(q_full, (uint32_t)(nq & 1));
             ++nq;
-            bool o_ok = false;  // the last segment's O has been read
-            if (g.parity) {
-                const int last = jend - 1;
-                for (int j = g.jb; ok && j < min(jend, g.jb + 2); ++j) {
-                    ok = wait_slot(K(j));
-                    if (!ok) break;
-                    issue_s(j - g.jb, 0, K(j) % S);
-                    release(K(j) % S);
-                    if (j == last && lane == 0) tc_commit(q_empty);
-                }
-                for (int j = g.jb; ok && j < jend; ++j) {
-                    const int t = (j - g.jb) & 1;
-                    int& c = t ? cnt1 : cnt0;
-                    ok = wait_slot(K(j) + 1) && wait(p_full(t), (uint32_t)(c & 1));
-                    if (ok && !o_ok) {
-                        ok = wait_free(0) && wait_free(1);
-                        o_ok = true;
-                    }
-                    if (!ok) break;
-                    clear_tail(j, (K(j) + 1) % S);
-                    issue_o(t, (K(j) + 1) % S, j >= g.jb + 2);
-                    release((K(j) + 1) % S);
-                    ++c;
-                    if (j + 2 < jend) {
-                        ok = wait_slot(K(j + 2));
-                        if (!ok) break;
-                        issue_s(t, 0, K(j + 2) % S);
-                        release(K(j + 2) % S);
-                        if (j + 2 == last && lane == 0) tc_commit(q_empty);
-                    }
-                }
-            } else {
-                const int e0 = g.jb + g.stream_tiles(0);  // row tile 0 takes [jb, e0), row tile 1 [jb, jend)
-                if (ok) ok = wait_slot(K(g.jb));
-                if (ok) {
-                    if (g.jb < e0) issue_s(0, 0, K(g.jb) % S);
-                    issue_s(1, 1, K(g.jb) % S);
-                    release(K(g.jb) % S);
-                    if (nt == 1 && lane == 0) tc_commit(q_empty);
-                }
-                for (int j = g.jb; ok && j < jend; ++j) {
-                    const int sv = (K(j) + 1) % S, sk = K(j + 1) % S;
-                    ok = wait_slot(K(j) + 1);
-                    if (!ok) break;
-                    clear_tail(j, sv);
-                    bool have_k = false;
-                    if (j < e0) {
-                        ok = wait(p_full(0), (uint32_t)(cnt0 & 1));
-                        if (ok && j == g.jb) ok = wait_free(0);
-                        if (!ok) break;
-                        issue_o(0, sv, j > g.jb);
-                        ++cnt0;
-                        if (j + 1 < e0) {
-                            ok = wait_slot(K(j + 1));
-                            if (!ok) break;
-                            have_k = true;
-                            issue_s(0, 0, sk);
-                        }
-                    }
-                    ok = wait(p_full(1), (uint32_t)(cnt1 & 1));
-                    if (ok && j == g.jb) ok = (e0 > g.jb || wait_free(0)) && wait_free(1);
-                    if (!ok) break;
-                    issue_o(1, sv, j > g.jb);
-                    release(sv);
-                    ++cnt1;
-                    if (j + 1 < jend) {
-                        if (!have_k) ok = wait_slot(K(j + 1));
-                        if (!ok) break;
-                        issue_s(1, 1, sk);
-                        release(sk);
-                        if (j + 2 == jend && lane == 0) tc_commit(q_empty);
-                    }
-                }
+            ok = ok && next_s(Stream<0>{}, g.jb) && next_s(Stream<1>{}, g.parity ? g.jb + 1 : g.jb);
+#pragma unroll 1
+            for (int j = g.jb; ok && j < jend; ++j) {
+                ok = wait_slot(K(j) + 1);
+                const uint32_t sv = slot(K(j) + 1);
+                const bool even = ((j - g.jb) & 1) == 0;
+                if (ok && (g.parity ? even : j < e0)) ok = advance(Stream<0>{}, j, sv, g.parity);
+                if (ok && (!g.parity || !even)) ok = advance(Stream<1>{}, j, sv, true);
             }
             n = n0 + 2 * nt;
-            if (ok && lane == 0) tc_commit(seg_done);
+            if (ok) commit(seg_done);
         }
         if (lane == 0) {
             if (!ok) give_up();
@@ -620,7 +657,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             mbar_wait_drain(done, 0u);
         }
         __syncwarp();
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int t = warp >> 2, r = tid & 127;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_off + (uint32_t)(t * 128);
@@ -628,7 +667,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         const int rtok = r / p.G, rhead = r - rtok * p.G;
         const bool in_tile = rtok < p.TQ;
         int cnt[2] = {0, 0};
-        int nx = 0, nseg = 0;
+        int nx = 0, nseg = 0, ring = 0;
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) {
             const bool w = mbar_wait_bounded(bar, parity, s_abort);
@@ -644,72 +683,178 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             const int nt = t == 0 ? st0 : st1;
             const int jstep = g.parity ? 2 : 1, j0 = g.parity ? g.jb + t : g.jb;
             float m = -INFINITY, l = 0.f;
+            float acc[F32OUT ? D : 1];  // float32 output: O is added up here, tile by tile
+            if constexpr (F32OUT) {
+#pragma unroll
+                for (int k = 0; k < D; ++k) acc[k] = 0.f;
+            }
+            auto add_o = [&]() {
+                if constexpr (F32OUT) {
+#pragma unroll
+                    for (int cc = 0; cc < D; cc += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + (uint32_t)(t * 128 + cc), o);
+                        tmem_landed(o);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) acc[cc + k] += __uint_as_float(o[k]);
+                    }
+                }
+            };
+            const uint64_t qscale2 = pack2(p.qscale, p.qscale);
+            const int jlast = g.jb + g.tiles() - 1;  // the V tile that may hold rows past the last key
+            // Those rows become zeros (what lies there may be no number, and its weight of 0
+            // would not help): by the first stream that uses them, before its P is full.
+            const bool clears = g.kend < (jlast + 1) * KT && (t == 0 || g.parity || jlast >= g.jb + st0);
+            auto clear_tail = [&]() {
+                const int k = ring + 2 * (jlast - g.jb) + 1, s = k % S;
+                const bool r = wait(full(s), (uint32_t)(k / S) & 1u);
+                const int rows = g.kend - jlast * KT, chunks = (KT - rows) * 8;
+                for (int i = tid & 127; i < chunks * C::kHalves; i += 128) {
+                    const int h = i >= chunks ? 1 : 0;
+                    *reinterpret_cast<uint4*>(s_raw + 2 * C::kQTile + s * C::kTile + h * C::kSpan + rows * 128 +
+                                              (i - h * chunks) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_async_shared();
+                return r;
+            };
             for (int i = 0; ok && i < nt; ++i) {
                 const int c = cnt[t] + i;
-                ok = wait(s_full(t), (uint32_t)(c & 1));
-                if (!ok) break;
-                if (any) {
-                    uint32_t x[KT];
-                    if constexpr (KT == 128) tmem_ld128_wait(tS, x);
-                    else tmem_ld64_wait(tS, x);
-                    const int lim = kmax - (j0 + i * jstep) * KT;  // columns of this tile the row sees
-                    if (__any_sync(0xffffffffu, lim < KT)) {
-#pragma unroll
-                        for (int k = 0; k < KT; ++k)
-                            if (k >= lim) x[k] = 0xff800000u;
-                    }
-                    float mx = __uint_as_float(x[0]);
-#pragma unroll
-                    for (int k = 1; k < KT; ++k) mx = fmaxf(mx, __uint_as_float(x[k]));
-                    const bool grow = (mx - m) * p.qscale > kRescale;  // false while m is -inf and mx too
-                    const bool resc = grow && m != -INFINITY;
-                    if (__any_sync(0xffffffffu, resc)) {
-                        // the products of the previous tile must have landed in O
+                const int lim = kmax - (j0 + i * jstep) * KT;  // columns of this tile the row sees
+                const bool part = __any_sync(0xffffffffu, lim < KT);
+                if constexpr (F32OUT) {
+                    if (i > 0) {
                         ok = wait(o_done(t), (uint32_t)((c - 1) & 1));
-                        if (!ok) break;
-                        const float a = resc ? ex2((m - mx) * p.qscale) : 1.f;
-                        l *= a;
-#pragma unroll 1
-                        for (int cc = 0; cc < D; cc += 32) {
-                            uint32_t o[32];
-                            tmem_ld32_wait(tO + (uint32_t)(t * 128 + cc), o);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-                            tmem_st32(tO + (uint32_t)(t * 128 + cc), o);
-                        }
+                        if (ok && any) add_o();
                     }
-                    if (grow) m = mx;
-                    const float sub = m == -INFINITY ? 0.f : m * p.qscale;
-                    float sum0 = 0.f, sum1 = 0.f;
+                    ok = ok && wait(s_full(t), (uint32_t)(c & 1));
+                    if (!ok) break;
+                    if (any) {
+                        float mx = m;
+                        {
+                            uint32_t x[64];
+                            tmem_ld64(tS, x);
+                            tmem_landed(x);
+                            if (part) mask_columns(x, lim);
+                            mx = max_of(x, mx);
+                        }
+                        const float ms = mx == -INFINITY ? 0.f : mx;
+                        const float a = ex2((m - ms) * p.qscale);
+                        if (__any_sync(0xffffffffu, mx > m)) {
 #pragma unroll
-                    for (int cc = 0; cc < KT / 32; ++cc) {
-                        uint32_t w[16], w1[16], w2[16];
+                            for (int k = 0; k < D; ++k) acc[k] *= a;
+                            l *= a;
+                        }
+                        m = mx;
+                        const float sub = ms * p.qscale;
+                        float sum[2] = {0.f, 0.f};
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            float a = ex2(fmaf(__uint_as_float(x[cc * 32 + 2 * k]), p.qscale, -sub));
-                            float b = ex2(fmaf(__uint_as_float(x[cc * 32 + 2 * k + 1]), p.qscale, -sub));
-                            sum0 += a;
-                            sum1 += b;
-                            w[k] = pack_bf16(a, b);
-                            if (F32OUT) {
-                                a -= bf16lo(w[k]);
-                                b -= bf16hi(w[k]);
-                                w1[k] = pack_bf16(a, b);
-                                w2[k] = pack_bf16(a - bf16lo(w1[k]), b - bf16hi(w1[k]));
+                        for (int cc = 0; cc < 64; cc += 32) {
+                            uint32_t x[32];
+                            tmem_ld32(tS + (uint32_t)cc, x);
+                            tmem_landed(x);
+                            if (part) mask_columns(x, lim - cc);
+#pragma unroll
+                            for (int q = 0; q < 32; q += 16) {
+                                uint32_t w[3][8];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) {
+                                    float u = ex2(fmaf(__uint_as_float(x[q + 2 * k]), p.qscale, -sub));
+                                    float v = ex2(fmaf(__uint_as_float(x[q + 2 * k + 1]), p.qscale, -sub));
+                                    sum[0] += u;
+                                    sum[1] += v;
+#pragma unroll
+                                    for (int e = 0; e < 3; ++e) {
+                                        w[e][k] = pack_bf16(u, v);
+                                        u -= bf16lo(w[e][k]);
+                                        v -= bf16hi(w[e][k]);
+                                    }
+                                }
+#pragma unroll
+                                for (int e = 0; e < 3; ++e) tmem_st8(tS + (uint32_t)(C::part_col(e) + (cc + q) / 2), w[e]);
                             }
                         }
-                        tmem_st16(tS + (uint32_t)(cc * 16), w);
-                        if (F32OUT) {
-                            tmem_st16(tS + (uint32_t)(KT / 2 + cc * 16), w1);
-                            tmem_st16(tS + (uint32_t)(KT + cc * 16), w2);
-                        }
+                        l += sum[0] + sum[1];
+                        tmem_wait_st();
                     }
-                    l += sum0 + sum1;
-                    tmem_wait_st();
+                } else {
+                    ok = wait(s_full(t), (uint32_t)(c & 1));
+                    if (!ok) break;
+                    if (any) {
+                        uint32_t x0[64], x1[64];
+                        tmem_ld64(tS, x0);
+                        tmem_landed(x0);
+                        tmem_ld64(tS + 64u, x1);
+                        if (part) mask_columns(x0, lim);
+                        float mx = max_of(x0, m);
+                        tmem_landed(x1);
+                        if (part) mask_columns(x1, lim - 64);
+                        mx = max_of(x1, mx);
+                        const bool grow = (mx - m) * p.qscale > kRescale;  // false where both are -inf
+                        const bool resc = grow && m != -INFINITY;
+                        if (__any_sync(0xffffffffu, resc)) {
+                            // the products of the previous tile must have landed in O
+                            ok = wait(o_done(t), (uint32_t)((c - 1) & 1));
+                            if (!ok) break;
+                            const float a = resc ? ex2((m - mx) * p.qscale) : 1.f;
+                            l *= a;
+#pragma unroll 1
+                            for (int cc = 0; cc < D; cc += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(tO + (uint32_t)(t * 128 + cc), o);
+                                tmem_landed(o);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+                                tmem_st32(tO + (uint32_t)(t * 128 + cc), o);
+                            }
+                        }
+                        if (grow) m = mx;
+                        const float sub = m == -INFINITY ? 0.f : m * p.qscale;
+                        const uint64_t nsub2 = pack2(-sub, -sub);
+                        uint64_t sum[2] = {0, 0};
+#pragma unroll
+                        for (int cc = 0; cc < 64; cc += 32) {
+                            uint32_t w[16];
+                            weights<32>(x0 + cc, qscale2, nsub2, w, sum);
+                            tmem_st16(tS + (uint32_t)(cc / 2), w);
+                        }
+#pragma unroll
+                        for (int cc = 0; cc < 64; cc += 32) {
+                            uint32_t w[16];
+                            weights<32>(x1 + cc, qscale2, nsub2, w, sum);
+                            tmem_st16(tS + (uint32_t)(32 + cc / 2), w);
+                        }
+                        float a, b;
+                        unpack2(add2(sum[0], sum[1]), a, b);
+                        l += a + b;
+                        tmem_wait_st();
+                    }
+                }
+                if (clears && j0 + i * jstep == jlast) {
+                    ok = clear_tail();
+                    if (!ok) break;
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full(t));
+            }
+            ring += 2 * g.tiles();
+            if constexpr (F32OUT) {
+                // the whole O goes where the epilogue reads it
+                if (ok && nt > 0) {
+                    ok = wait(o_done(t), (uint32_t)((cnt[t] + nt - 1) & 1));
+                    if (ok && any) {
+                        add_o();
+#pragma unroll
+                        for (int cc = 0; cc < D; cc += 32) {
+                            uint32_t o[32];
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(acc[cc + k]);
+                            tmem_st32(tO + (uint32_t)(t * 128 + cc), o);
+                        }
+                        tmem_wait_st();
+                    }
+                    tc_fence_before();
+                }
             }
             if (!ok) break;
             cnt[0] += st0;
@@ -760,12 +905,14 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 for (int cc = col0; cc < col0 + cols; cc += 32) {
                     uint32_t o[32];
                     if (have) {
-                        tmem_ld32_wait(oa + (uint32_t)cc, o);
+                        tmem_ld32(oa + (uint32_t)cc, o);
+                        tmem_landed(o);
 #pragma unroll
                         for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * ca);
                         if (both) {
                             uint32_t o1[32];
-                            tmem_ld32_wait(tO + 128u + (uint32_t)cc, o1);
+                            tmem_ld32(tO + 128u + (uint32_t)cc, o1);
+                            tmem_landed(o1);
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
                                 o[k] = __float_as_uint(fmaf(__uint_as_float(o1[k]), cb, __uint_as_float(o[k])));
