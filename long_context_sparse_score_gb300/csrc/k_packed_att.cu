@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         constexpr uint32_t kIdS = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(KT >> 3) << 17) | ((128u >> 4) << 24);
         constexpr uint32_t kIdO = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
                                   ((128u >> 4) << 24);
-        int n = 0, nq = 0, nseg = 0;
+        int nq = 0, nseg = 0;
         uint32_t cnt = 0;  // bit t: parity of stream t's tiles so far
         bool ok = true;
         // Low halves of the descriptors: Q (K-major, leading offset unused), the first ring
@@ -551,46 +551,46 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         auto issue_s = [&](auto T, uint32_t qtile, uint32_t s) {
             constexpr uint32_t t = decltype(T)::value;
             const uint32_t a = q_lo + qtile * (uint32_t)(C::kQTile >> 4), b = k_lo + s * (uint32_t)(C::kTile >> 4);
-            if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t h = (uint32_t)(kk >> 2), o = (uint32_t)(kk & 3) * 2u;
-                    tc_mma(tm + t * 128u, sw128_desc_of(a + h * 1024u + o),
-                           sw128_desc_of(b + h * (uint32_t)(C::kSpan >> 4) + o), kIdS, kk > 0 ? 1u : 0u);
-                }
-                tc_commit(s_full(t));
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t h = (uint32_t)(kk >> 2), o = (uint32_t)(kk & 3) * 2u;
+                tc_mma(tm + t * 128u, sw128_desc_of(a + h * 1024u + o),
+                       sw128_desc_of(b + h * (uint32_t)(C::kSpan >> 4) + o), kIdS, kk > 0 ? 1u : 0u);
             }
-            __syncwarp();
+            tc_commit(s_full(t));
         };
         // O_t (+)= P_t V of the V tile in ring slot s
         auto issue_o = [&](auto T, uint32_t s, uint32_t acc) {
             constexpr uint32_t t = decltype(T)::value;
             const uint32_t b = v_lo + s * (uint32_t)(C::kTile >> 4);
-            if (elect_one()) {
 #pragma unroll
-                for (int part = 0; part < C::kParts; ++part)
+            for (int part = 0; part < C::kParts; ++part)
 #pragma unroll
-                    for (int kk = 0; kk < KT / 16; ++kk)
-                        tc_mma_ts(tm + 256u + t * 128u, tm + t * 128u + (uint32_t)(C::part_col(part) + kk * 8),
-                                  sw128_desc_of(b + (uint32_t)kk * 128u), kIdO, part > 0 || kk > 0 ? 1u : acc);
-                tc_commit(o_done(t));
-            }
-            __syncwarp();
+                for (int kk = 0; kk < KT / 16; ++kk)
+                    tc_mma_ts(tm + 256u + t * 128u, tm + t * 128u + (uint32_t)(C::part_col(part) + kk * 8),
+                              sw128_desc_of(b + (uint32_t)kk * 128u), kIdO, part > 0 || kk > 0 ? 1u : acc);
         };
         auto commit = [&](uint32_t bar) {
             if (elect_one()) tc_commit(bar);
             __syncwarp();
         };
-        // slot of ring index k, and the wait for what is loaded into it
-        auto slot = [&](int k) { return uniform((uint32_t)(k % S)); };
         auto wait = [&](uint32_t bar, uint32_t parity) {
             const bool r = mbar_wait_bounded(bar, parity, s_abort);
             tc_fence_after();
-            return __all_sync(0xffffffffu, r);
+            return (bool)__all_sync(0xffffffffu, r);
         };
-        auto wait_slot = [&](int k) { return wait(full(k % S), (uint32_t)(k / S) & 1u); };
+        uint32_t slot = 0, round = 0;  // ring slot and parity of the next tile to be read
+        // the ring place d tiles on (d < S)
+        auto ahead = [&](uint32_t d, uint32_t& s, uint32_t& r) {
+            s = slot + d;
+            r = round;
+            if (s >= (uint32_t)S) {
+                s -= (uint32_t)S;
+                r ^= 1u;
+            }
+        };
         while (ok && it.next(p, g)) {
-            const int nt = g.tiles();
+            const int nt = (int)uniform((uint32_t)g.tiles());
             const uint32_t free_ph = (uint32_t)(nseg & 1) ^ 1u;
             ++nseg;
             // Every segment waits once for both O's of the one before it and then ends with
@@ -603,52 +603,84 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 if (ok) commit(seg_done);
                 continue;
             }
-            const int jend = g.jb + nt;
-            const int n0 = n;  // ring index of K(jb); K(j) is n0 + 2 (j - jb), V(j) the next
-            // Row tile 0 of two takes the key tiles [jb, e0), row tile 1 all; with one row
-            // tile the streams take every other one. S of a stream's next tile is issued
-            // right behind P V of this one, which reads P where that S goes: the products
-            // run in the order of their issue.
-            const int e0 = g.parity ? jend : g.jb + g.stream_tiles(0);
-            const int step = g.parity ? 2 : 1;
-            auto K = [&](int j) { return n0 + 2 * (j - g.jb); };
-            // S of stream t's tile j, where it has one; K(j) is free behind its last reader
-            auto next_s = [&](auto T, int j) {
+            // Tiles i = 0 .. nt - 1 of the segment. Row tile 0 of two takes the first e0,
+            // row tile 1 all; with one row tile the streams take every other one. S of a
+            // stream's next tile is issued right behind P V of this one, which reads P where
+            // that S goes: the products run in the order of their issue.
+            const bool parity = uniform((uint32_t)g.parity) != 0u;
+            const int e0 = parity ? nt : (int)uniform((uint32_t)g.stream_tiles(0));
+            const int step = parity ? 2 : 1;
+            bool free_ok = false;
+            int k_ready = -1;  // last K tile that has been waited for
+            // K tile i, 2 (i - now) tiles ahead in the ring
+            auto wait_k = [&](int i, int now, uint32_t& s) {
+                uint32_t r;
+                ahead(2u * (uint32_t)(i - now), s, r);
+                if (i <= k_ready) return true;
+                k_ready = i;
+                return wait(full(s), r);
+            };
+            // behind S of tile i for the last time: K(i) is free, and Q after the last tile
+            auto release_k = [&](uint32_t s, int i) {
+                tc_commit(empty(s));
+                if (i == nt - 1) tc_commit(q_empty);
+            };
+            // the first S of a stream
+            auto first = [&](auto T, int i) {
                 constexpr int t = decltype(T)::value;
-                if (j >= (t == 0 ? e0 : jend)) return true;
-                if (!wait_slot(K(j))) return false;
-                const uint32_t s = slot(K(j));
-                issue_s(T, g.parity ? 0u : (uint32_t)t, s);
-                if (t == 1 || g.parity) {
-                    commit(empty(s));
-                    if (j == jend - 1) commit(q_empty);
+                uint32_t s;
+                if (i >= (t == 0 ? e0 : nt)) return true;
+                if (!wait_k(i, 0, s)) return false;
+                if (elect_one()) {
+                    issue_s(T, parity ? 0u : (uint32_t)t, s);
+                    if (t == 1 || parity) release_k(s, i);
                 }
+                __syncwarp();
                 return true;
             };
-            bool free_ok = false;
-            // P V of stream t's tile j, and its next S; `last`: nobody reads V(j) after it
-            auto advance = [&](auto T, int j, uint32_t sv, bool last) {
+            // P V of stream t's tile i and S of its next; `last`: nobody reads V(i) after it
+            auto advance = [&](auto T, int i, uint32_t sv, bool last) {
                 constexpr int t = decltype(T)::value;
-                if (!wait(p_full(t), (cnt >> t) & 1u)) return false;
-                cnt ^= 1u << t;
+                const int ni = i + step;
+                const bool more = ni < (t == 0 ? e0 : nt);
+                uint32_t sk = 0;
+                if (more && !wait_k(ni, i, sk)) return false;
                 if (!free_ok && !wait_free()) return false;
                 free_ok = true;
-                issue_o(T, sv, !F32OUT && j >= g.jb + step ? 1u : 0u);
-                if (last) commit(empty(sv));
-                return next_s(T, j + step);
+                if (!wait(p_full(t), (cnt >> t) & 1u)) return false;
+                cnt ^= 1u << t;
+                if (elect_one()) {
+                    issue_o(T, sv, !F32OUT && i >= step ? 1u : 0u);
+                    if (F32OUT || !more) tc_commit(o_done(t));
+                    if (last) tc_commit(empty(sv));
+                }
+                __syncwarp();
+                if (last && i + 1 < nt) {
+                    uint32_t s, r;
+                    ahead(3, s, r);
+                    if (!wait(full(s), r)) return false;
+                    if (!parity && i + 2 < nt && !wait_k(i + 2, i, s)) return false;
+                }
+                if (more && elect_one()) {
+                    issue_s(T, parity ? 0u : (uint32_t)t, sk);
+                    if (t == 1 || parity) release_k(sk, ni);
+                }
+                __syncwarp();
+                return true;
             };
             ok = wait(q_full, (uint32_t)(nq & 1));
             ++nq;
-            ok = ok && next_s(Stream<0>{}, g.jb) && next_s(Stream<1>{}, g.parity ? g.jb + 1 : g.jb);
+            ok = ok && first(Stream<0>{}, 0) && first(Stream<1>{}, parity ? 1 : 0);
 #pragma unroll 1
-            for (int j = g.jb; ok && j < jend; ++j) {
-                ok = wait_slot(K(j) + 1);
-                const uint32_t sv = slot(K(j) + 1);
-                const bool even = ((j - g.jb) & 1) == 0;
-                if (ok && (g.parity ? even : j < e0)) ok = advance(Stream<0>{}, j, sv, g.parity);
-                if (ok && (!g.parity || !even)) ok = advance(Stream<1>{}, j, sv, true);
+            for (int i = 0; ok && i < nt; ++i) {
+                uint32_t sv, rv;
+                ahead(1, sv, rv);
+                ok = wait(full(sv), rv);
+                const bool even = (i & 1) == 0;
+                if (ok && (parity ? even : i < e0)) ok = advance(Stream<0>{}, i, sv, parity);
+                if (ok && (!parity || !even)) ok = advance(Stream<1>{}, i, sv, true);
+                ahead(2, slot, round);
             }
-            n = n0 + 2 * nt;
             if (ok) commit(seg_done);
         }
         if (lane == 0) {
@@ -666,7 +698,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         const uint32_t tO = tmem + lane_off + 256u;
         const int rtok = r / p.G, rhead = r - rtok * p.G;
         const bool in_tile = rtok < p.TQ;
-        int cnt[2] = {0, 0};
+        int cnt[2] = {0, 0}, odc[2] = {0, 0};
         int nx = 0, nseg = 0, ring = 0;
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -781,47 +813,59 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     if (!ok) break;
                     if (any) {
                         uint32_t x0[64], x1[64];
+                        uint64_t sum[2];
+                        // all weights against the reference m, into P's columns
+                        auto all_weights = [&](bool landed) {
+                            const float sub = m == -INFINITY ? 0.f : m * p.qscale;
+                            const uint64_t nsub2 = pack2(-sub, -sub);
+                            uint32_t w[16];
+                            sum[0] = sum[1] = 0;
+                            weights<32>(x0, qscale2, nsub2, w, sum);
+                            if (!landed) {
+                                tmem_landed(x1);
+                                if (part) mask_columns(x1, lim - 64);
+                            }
+                            tmem_st16(tS, w);
+                            weights<32>(x0 + 32, qscale2, nsub2, w, sum);
+                            tmem_st16(tS + 16u, w);
+                            weights<32>(x1, qscale2, nsub2, w, sum);
+                            tmem_st16(tS + 32u, w);
+                            weights<32>(x1 + 32, qscale2, nsub2, w, sum);
+                            tmem_st16(tS + 48u, w);
+                        };
                         tmem_ld64(tS, x0);
                         tmem_landed(x0);
                         tmem_ld64(tS + 64u, x1);
                         if (part) mask_columns(x0, lim);
-                        float mx = max_of(x0, m);
-                        tmem_landed(x1);
-                        if (part) mask_columns(x1, lim - 64);
-                        mx = max_of(x1, mx);
+                        // A row's maximum seldom passes its reference by more than 2^8 after its
+                        // first tile: the weights do not wait for it, and are made again if it does.
+                        const bool guess = i > 0;
+                        if (guess) {
+                            all_weights(false);
+                        } else {
+                            tmem_landed(x1);
+                            if (part) mask_columns(x1, lim - 64);
+                        }
+                        const float mx = max_of(x1, max_of(x0, m));
                         const bool grow = (mx - m) * p.qscale > kRescale;  // false where both are -inf
-                        const bool resc = grow && m != -INFINITY;
-                        if (__any_sync(0xffffffffu, resc)) {
-                            // the products of the previous tile must have landed in O
-                            ok = wait(o_done(t), (uint32_t)((c - 1) & 1));
-                            if (!ok) break;
-                            const float a = resc ? ex2((m - mx) * p.qscale) : 1.f;
-                            l *= a;
+                        if (!guess || __any_sync(0xffffffffu, grow)) {
+                            // O holds the products of the tiles before: S of this one came behind them
+                            if (guess) {
+                                tmem_wait_st();  // the first weights are out before the second are
+                                const float a = grow ? ex2((m - mx) * p.qscale) : 1.f;  // 0 from -inf
+                                l *= a;
 #pragma unroll 1
-                            for (int cc = 0; cc < D; cc += 32) {
-                                uint32_t o[32];
-                                tmem_ld32(tO + (uint32_t)(t * 128 + cc), o);
-                                tmem_landed(o);
+                                for (int cc = 0; cc < D; cc += 32) {
+                                    uint32_t o[32];
+                                    tmem_ld32(tO + (uint32_t)(t * 128 + cc), o);
+                                    tmem_landed(o);
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-                                tmem_st32(tO + (uint32_t)(t * 128 + cc), o);
+                                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+                                    tmem_st32(tO + (uint32_t)(t * 128 + cc), o);
+                                }
                             }
-                        }
-                        if (grow) m = mx;
-                        const float sub = m == -INFINITY ? 0.f : m * p.qscale;
-                        const uint64_t nsub2 = pack2(-sub, -sub);
-                        uint64_t sum[2] = {0, 0};
-#pragma unroll
-                        for (int cc = 0; cc < 64; cc += 32) {
-                            uint32_t w[16];
-                            weights<32>(x0 + cc, qscale2, nsub2, w, sum);
-                            tmem_st16(tS + (uint32_t)(cc / 2), w);
-                        }
-#pragma unroll
-                        for (int cc = 0; cc < 64; cc += 32) {
-                            uint32_t w[16];
-                            weights<32>(x1 + cc, qscale2, nsub2, w, sum);
-                            tmem_st16(tS + (uint32_t)(32 + cc / 2), w);
+                            if (grow) m = mx;
+                            all_weights(true);
                         }
                         float a, b;
                         unpack2(add2(sum[0], sum[1]), a, b);
@@ -857,8 +901,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 }
             }
             if (!ok) break;
-            cnt[0] += st0;
-            cnt[1] += st1;
+            // o_done: every tile with a float32 output, else a stream's last one
+            cnt[t] += nt;
+            odc[0] += F32OUT ? st0 : (st0 > 0 ? 1 : 0);
+            odc[1] += F32OUT ? st1 : (st1 > 0 ? 1 : 0);
             const bool whole = g.jb == 0 && g.je == g.len;
             // row of out / lse, or of this CTA's part of the item
             const int64_t grow_ = ((int64_t)(g.q0 + g.qt * t2 + ltok) * p.Hq + g.head * p.G + rhead);
@@ -869,8 +915,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             if (g.parity) {
                 if (st0 > 0) {
                     // own stream first: its last product follows all but the last of the other's
-                    if (nt > 0) ok = wait(o_done(t), (uint32_t)((cnt[t] - 1) & 1));
-                    if (ok && (t == 1 || st1 > 0)) ok = wait(o_done(t ^ 1), (uint32_t)((cnt[t ^ 1] - 1) & 1));
+                    if (nt > 0) ok = wait(o_done(t), (uint32_t)((odc[t] - 1) & 1));
+                    if (ok && (t == 1 || st1 > 0)) ok = wait(o_done(t ^ 1), (uint32_t)((odc[t ^ 1] - 1) & 1));
                     if (!ok) break;
                     s_ml[t * 128 + r] = make_float2(m, l);
                     __syncwarp();
@@ -890,7 +936,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 cols = D / 2;
             } else {
                 if (nt > 0) {
-                    ok = wait(o_done(t), (uint32_t)((cnt[t] - 1) & 1));
+                    ok = wait(o_done(t), (uint32_t)((odc[t] - 1) & 1));
                     if (!ok) break;
                 }
                 ca = 1.f;
