@@ -485,6 +485,26 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     }
 }
 
+// For warps whose lanes wait together in a tight loop: no value comes back and no vote
+// is taken (that alone takes 45 cycles of the 105). After kWaitTries tries, or once
+// another wait has given up, *abort is set and the wait ends; whoever goes on works on
+// data that is never used and looks at *abort when it can afford to.
+constexpr uint32_t kWaitTries = 1u << 22;
+__device__ __forceinline__ void mbar_wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort) {
+    if (!mbar_try_wait(bar, parity)) {
+        uint32_t n = 0;
+#pragma unroll 1
+        while (!mbar_try_wait(bar, parity)) {
+            if (*abort) break;
+            if (++n >= kWaitTries) {
+                *abort = 1;
+                break;
+            }
+        }
+    }
+    __syncwarp();
+}
+
 // 1-D bulk copy global -> shared (TMA engine), completion counted in bytes on `bar`.
 __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile(

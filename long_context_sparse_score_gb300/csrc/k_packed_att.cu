@@ -575,10 +575,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             __syncwarp();
         };
         auto wait = [&](uint32_t bar, uint32_t parity) {
-            const bool r = mbar_wait_bounded(bar, parity, s_abort);
+            mbar_wait_or_abort(bar, parity, s_abort);
             tc_fence_after();
-            return (bool)__all_sync(0xffffffffu, r);
         };
+        auto aborted = [&]() { return (bool)__any_sync(0xffffffffu, *s_abort != 0); };
         uint32_t slot = 0, round = 0;  // ring slot and parity of the next tile to be read
         // the ring place d tiles on (d < S)
         auto ahead = [&](uint32_t d, uint32_t& s, uint32_t& r) {
@@ -597,28 +597,36 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             // an arrival on seg_done, which every softmax warp waits for before it gives
             // the O's of this one back: so neither side is ever two phases ahead, also
             // where a stream has no tiles and nothing else holds its warps back.
-            auto wait_free = [&]() { return wait(o_free(0), free_ph) && wait(o_free(1), free_ph); };
+            auto wait_free = [&]() {
+                wait(o_free(0), free_ph);
+                wait(o_free(1), free_ph);
+            };
             if (nt == 0) {
-                ok = wait_free();
-                if (ok) commit(seg_done);
+                wait_free();
+                commit(seg_done);
+                ok = !aborted();
                 continue;
             }
             // Tiles i = 0 .. nt - 1 of the segment. Row tile 0 of two takes the first e0,
             // row tile 1 all; with one row tile the streams take every other one. S of a
             // stream's next tile is issued right behind P V of this one, which reads P where
-            // that S goes: the products run in the order of their issue.
+            // that S goes: the products run in the order of their issue. The queue of the
+            // tensor cores holds two or three products of 64 cycles: what is waited for
+            // between the products of a batch costs nothing, what is waited for before it
+            // leaves them idle, so only P is.
             const bool parity = uniform((uint32_t)g.parity) != 0u;
             const int e0 = parity ? nt : (int)uniform((uint32_t)g.stream_tiles(0));
             const int step = parity ? 2 : 1;
-            bool free_ok = false;
             int k_ready = -1;  // last K tile that has been waited for
             // K tile i, 2 (i - now) tiles ahead in the ring
-            auto wait_k = [&](int i, int now, uint32_t& s) {
-                uint32_t r;
+            auto wait_k = [&](int i, int now) {
+                uint32_t s, r;
                 ahead(2u * (uint32_t)(i - now), s, r);
-                if (i <= k_ready) return true;
-                k_ready = i;
-                return wait(full(s), r);
+                if (i > k_ready) {
+                    k_ready = i;
+                    wait(full(s), r);
+                }
+                return s;
             };
             // behind S of tile i for the last time: K(i) is free, and Q after the last tile
             auto release_k = [&](uint32_t s, int i) {
@@ -628,26 +636,20 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             // the first S of a stream
             auto first = [&](auto T, int i) {
                 constexpr int t = decltype(T)::value;
-                uint32_t s;
-                if (i >= (t == 0 ? e0 : nt)) return true;
-                if (!wait_k(i, 0, s)) return false;
+                if (i >= (t == 0 ? e0 : nt)) return;
+                const uint32_t s = wait_k(i, 0);
                 if (elect_one()) {
                     issue_s(T, parity ? 0u : (uint32_t)t, s);
                     if (t == 1 || parity) release_k(s, i);
                 }
                 __syncwarp();
-                return true;
             };
             // P V of stream t's tile i and S of its next; `last`: nobody reads V(i) after it
             auto advance = [&](auto T, int i, uint32_t sv, bool last) {
                 constexpr int t = decltype(T)::value;
                 const int ni = i + step;
                 const bool more = ni < (t == 0 ? e0 : nt);
-                uint32_t sk = 0;
-                if (more && !wait_k(ni, i, sk)) return false;
-                if (!free_ok && !wait_free()) return false;
-                free_ok = true;
-                if (!wait(p_full(t), (cnt >> t) & 1u)) return false;
+                wait(p_full(t), (cnt >> t) & 1u);
                 cnt ^= 1u << t;
                 if (elect_one()) {
                     issue_o(T, sv, !F32OUT && i >= step ? 1u : 0u);
@@ -655,36 +657,43 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     if (last) tc_commit(empty(sv));
                 }
                 __syncwarp();
+                uint32_t sk = 0;
+                if (more) sk = wait_k(ni, i);
                 if (last && i + 1 < nt) {
                     uint32_t s, r;
                     ahead(3, s, r);
-                    if (!wait(full(s), r)) return false;
-                    if (!parity && i + 2 < nt && !wait_k(i + 2, i, s)) return false;
+                    wait(full(s), r);
                 }
                 if (more && elect_one()) {
                     issue_s(T, parity ? 0u : (uint32_t)t, sk);
                     if (t == 1 || parity) release_k(sk, ni);
                 }
                 __syncwarp();
-                return true;
             };
-            ok = wait(q_full, (uint32_t)(nq & 1));
+            wait(q_full, (uint32_t)(nq & 1));
             ++nq;
-            ok = ok && first(Stream<0>{}, 0) && first(Stream<1>{}, parity ? 1 : 0);
+            first(Stream<0>{}, 0);
+            first(Stream<1>{}, parity ? 1 : 0);
+            {
+                uint32_t s, r;
+                ahead(1, s, r);
+                wait(full(s), r);
+            }
+            wait_free();
 #pragma unroll 1
-            for (int i = 0; ok && i < nt; ++i) {
+            for (int i = 0; i < nt; ++i) {
                 uint32_t sv, rv;
                 ahead(1, sv, rv);
-                ok = wait(full(sv), rv);
                 const bool even = (i & 1) == 0;
-                if (ok && (parity ? even : i < e0)) ok = advance(Stream<0>{}, i, sv, parity);
-                if (ok && (!parity || !even)) ok = advance(Stream<1>{}, i, sv, true);
+                if (parity ? even : i < e0) advance(Stream<0>{}, i, sv, parity);
+                if (!parity || !even) advance(Stream<1>{}, i, sv, true);
                 ahead(2, slot, round);
             }
-            if (ok) commit(seg_done);
+            commit(seg_done);
+            ok = !aborted();
         }
         if (lane == 0) {
-            if (!ok) give_up();
+            if (!ok || *s_abort != 0) give_up();
             tc_commit(done);  // every product issued above has finished once this arrives
             mbar_wait_drain(done, 0u);
         }
@@ -702,10 +711,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         int nx = 0, nseg = 0, ring = 0;
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) {
-            const bool w = mbar_wait_bounded(bar, parity, s_abort);
+            mbar_wait_or_abort(bar, parity, s_abort);
             tc_fence_after();
-            return (bool)__all_sync(0xffffffffu, w);
+            return true;
         };
+        auto aborted = [&]() { return (bool)__any_sync(0xffffffffu, *s_abort != 0); };
         while (ok && it.next(p, g)) {
             const int ltok = (g.parity ? 0 : t * p.TQ) + rtok;       // token of this row within the item
             const bool valid = in_tile && ltok < g.tokens;
@@ -753,6 +763,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 const int c = cnt[t] + i;
                 const int lim = kmax - (j0 + i * jstep) * KT;  // columns of this tile the row sees
                 const bool part = __any_sync(0xffffffffu, lim < KT);
+                if (aborted()) ok = false;
+                if (!ok) break;
                 if constexpr (F32OUT) {
                     if (i > 0) {
                         ok = wait(o_done(t), (uint32_t)((c - 1) & 1));
@@ -1019,7 +1031,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 p.items[blockIdx.x] = d;
             }
         }
-        if (!ok && lane == 0) give_up();
+        if (lane == 0 && (!ok || *s_abort != 0)) give_up();
     }
     tc_fence_before();
     __syncthreads();
