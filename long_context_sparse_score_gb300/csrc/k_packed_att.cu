@@ -34,9 +34,10 @@
 // spans CTAs go to the workspace (unnormalised O, m, l) and k_packed_merge joins
 // them, in order, so results do not depend on timing.
 //
-// 10 warps: two softmax warpgroups (thread = row: a tcgen05.ld gives a thread
-// its whole row of S, no shuffles), one warp that issues the MMAs, one that
-// loads by TMA (128-byte swizzle; ring of K/V tiles). Waits are bounded: one
+// 12 warps: two softmax warpgroups (thread = row: a tcgen05.ld gives a thread
+// its whole row of S, no shuffles), one warp that issues the MMAs, one that loads K
+// and V by TMA (128-byte swizzle; a ring of tiles), one that loads Q, and one that
+// hands out the items (its code would cost every other role the instruction cache). Waits are bounded: one
 // that gives up flags HA_DEVERR_TIMEOUT, stops the other roles, lets the copies
 // and products in flight land and frees the tensor memory before the CTA exits.
 #include "tc_common.cuh"
@@ -45,12 +46,14 @@ namespace ha {
 namespace {
 
 constexpr int kAttThreads = 384;
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kQWarp = 10, kPlanWarp = 11;
 // Registers of a softmax thread and of the others: 256 x 208 + 128 x 88 is what 384
 // threads are launched with (168 each).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kMinSpan = 2;           // fewest tiles of a CTA
 constexpr uint32_t kTmemCols = 512;   // S0, S1 (128 each; P overlays them), O0, O1
+constexpr int kItemCost = 1;           // tiles that an item's start and end cost beside its own
+constexpr int kQueue = 4;              // segments that the scheduler is ahead
 constexpr float kRescale = 8.f;       // growth of the maximum (log2) that makes O be rescaled
 
 template <int D, bool F32OUT>
@@ -65,8 +68,8 @@ struct AttCfg {
     // First tensor memory column of a part: P takes the columns of S; three parts of 32
     // columns take the second half, beside S's 64, and S's first 32 once they are read.
     static constexpr __host__ __device__ int part_col(int i) { return !F32OUT || i == 2 ? 0 : 64 + 32 * i; }
-    static constexpr int kBars = 2 * kStages + 13;
-    static constexpr int kSmem = 2 * kQTile + kStages * kTile + 2048 + 8 * kBars + 128;
+    static constexpr int kBars = 2 * kStages + 13 + 2 * kQueue;
+    static constexpr int kSmem = 2 * kQTile + kStages * kTile + 2048 + 8 * kBars + 64 * kQueue + 16;
     static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
 
@@ -126,16 +129,16 @@ __device__ __forceinline__ int key_tiles(int keys) {
     return (keys + KT - 1) / KT;
 }
 
-// Tiles of the items 0 .. qt - 1 of one head (an item without keys counts one,
-// so that its rows are written), qt < the number of items.
+// Cost of the items 0 .. qt - 1 of one head, qt < the number of items: their tiles
+// (an item without keys counts one, so that its rows are written) and kItemCost each.
 template <int KT>
-__device__ __forceinline__ unsigned long long tiles_before(const SeqInfo& i, int t2, int qt) {
+__device__ unsigned long long cost_before(const SeqInfo& i, int t2, int qt) {
     const int base = i.nk - i.nq;
     int z = 0;  // items that see no key
     if (base < 0) z = min(qt, (-base) / t2);
-    const int n = qt - z;
-    if (n <= 0) return (unsigned)z;
-    return (unsigned)z + floor_sum((uint32_t)n, KT, (uint32_t)t2, (uint32_t)(base + (z + 1) * t2 + KT - 1));
+    unsigned long long c = (unsigned long long)(unsigned)z + (unsigned long long)(unsigned)qt * kItemCost;
+    if (qt > z) c += floor_sum((uint32_t)(qt - z), KT, (uint32_t)t2, (uint32_t)(base + (z + 1) * t2 + KT - 1));
+    return c;
 }
 
 template <int KT>
@@ -144,92 +147,34 @@ __device__ __forceinline__ int item_tiles(const SeqInfo& i, int t2, int qt) {
 }
 
 template <int KT>
-__device__ __forceinline__ unsigned long long head_tiles(const SeqInfo& i, int t2) {
+__device__ __forceinline__ unsigned long long head_cost(const SeqInfo& i, int t2) {
     if (i.nq == 0) return 0;
-    const int nqt = (i.nq + t2 - 1) / t2;
-    return tiles_before<KT>(i, t2, nqt - 1) + (unsigned)item_tiles<KT>(i, t2, nqt - 1);
+    const int last = (i.nq + t2 - 1) / t2 - 1;
+    return cost_before<KT>(i, t2, last) + (unsigned)(item_tiles<KT>(i, t2, last) + kItemCost);
 }
 
-// A place in the order of all tiles: tile j of item (s, head, qt).
+// A place in the order of all work: tile j of item (s, head, qt), after w units.
 struct Place {
     unsigned long long w;
     int s, head, qt, j;
 };
 
-// The part of an item that this CTA works on.
-template <int KT>
+// The part of an item that this CTA works on, as the scheduler warp hands it to the
+// others (16 ints in shared memory).
 struct Segment {
-    int s, head, qt;
-    int q0, nq, nk;
-    int jb, je, len;     // tiles [jb, je) of the item's len
-    int kend;            // keys that the item's last token sees
-    int tokens;          // its tokens
-    int parity;          // one tile of rows: warpgroups take every other key tile
-    int n0;              // key tiles of row tile 0 (two row tiles)
-    // tiles of stream (warpgroup) t in this segment
-    __device__ __forceinline__ int tiles() const { return max(0, min(je, key_tiles<KT>(kend)) - jb); }
-    __device__ __forceinline__ int stream_tiles(int t) const {
-        if (parity) return (tiles() + 1 - t) >> 1;
-        return t == 0 ? max(0, min(je, n0) - jb) : tiles();
-    }
-};
-
-template <int KT>
-struct SegIter {
-    unsigned long long left;
-    int s, head, qt, j, nqt;
-    SeqInfo i;
-    __device__ __forceinline__ void start(const PackedParams& p, const Place& a, unsigned long long w1) {
-        s = a.s;
-        head = a.head;
-        qt = a.qt;
-        j = a.j;
-        left = w1 - a.w;
-        if (left == 0) return;
-        load(p);
-        if (j >= item_tiles<KT>(i, 2 * p.TQ, qt)) step(p);
-    }
-    __device__ __forceinline__ void load(const PackedParams& p) {
-        i = seq_info(p, s, false);
-        nqt = (i.nq + 2 * p.TQ - 1) / (2 * p.TQ);
-    }
-    // the next item
-    __device__ __forceinline__ void step(const PackedParams& p) {
-        j = 0;
-        if (++qt < nqt) return;
-        qt = 0;
-        if (++head < p.Hkv) return;
-        head = 0;
-        do {
-            if (++s >= p.n_seq) {
-                left = 0;
-                return;
-            }
-            load(p);
-        } while (i.nq == 0);
-    }
-    __device__ __forceinline__ bool next(const PackedParams& p, Segment<KT>& g) {
-        if (left == 0) return false;
-        const int t2 = 2 * p.TQ;
-        g.s = s;
-        g.head = head;
-        g.qt = qt;
-        g.q0 = i.q0;
-        g.nq = i.nq;
-        g.nk = i.nk;
-        g.len = item_tiles<KT>(i, t2, qt);
-        g.jb = j;
-        const unsigned long long rest = (unsigned long long)(g.len - j);
-        g.je = rest <= left ? g.len : j + (int)left;
-        left -= (unsigned long long)(g.je - g.jb);
-        g.kend = keys_seen(i, (qt + 1) * t2);
-        g.tokens = min(t2, i.nq - qt * t2);
-        g.parity = g.tokens <= p.TQ;
-        g.n0 = key_tiles<KT>(keys_seen(i, qt * t2 + p.TQ));
-        j = g.je;
-        if (left != 0 && j >= g.len) step(p);
-        return true;
-    }
+    int nt;       // its key tiles (0: an item without keys; -1: no more)
+    int jb;       // the first of them
+    int e0;       // two row tiles: those that row tile 0 sees; else nt
+    int flags;    // 1: one row tile (streams take every other key tile); 2: the whole item
+    int row0;     // row of its first token in q, out, lse
+    int head;     // KV head
+    int kend;     // keys that its last token sees
+    int tokens;
+    int kfirst;   // keys that the token before its first one sees (below 0: none, by that many)
+    int nk;       // keys of the sequence
+    int s, q0;    // sequence and its first row
+    int begins;   // the item begins here
+    int pad[3];
 };
 
 template <int T>
@@ -290,17 +235,17 @@ __device__ __forceinline__ float max_of(const uint32_t (&x)[N], float a) {
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// The weights 2^{x qscale - sub} of N columns as bf16 pairs in w; their float32 sum
-// is added to sum.
-template <int N>
-__device__ __forceinline__ void weights(const uint32_t* x, uint64_t qscale2, uint64_t nsub2, uint32_t (&w)[N / 2],
-                                        uint64_t (&sum)[2]) {
+// The weights 2^{x qscale - sub} of 32 columns as bf16 pairs in w; their float32 sum is
+// added to sum, and mt takes part in the columns' maximum.
+__device__ __forceinline__ void weights32(const uint32_t* x, uint64_t qscale2, uint64_t nsub2, uint32_t (&w)[16],
+                                          uint64_t (&sum)[2], float (&mt)[4]) {
 #pragma unroll
-    for (int k = 0; k < N / 2; ++k) {
+    for (int k = 0; k < 16; ++k) {
         float a, b;
         unpack2(fma2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), qscale2, nsub2), a, b);
         a = ex2(a);
         b = ex2(b);
+        mt[k & 3] = fmaxf(fmaxf(mt[k & 3], __uint_as_float(x[2 * k])), __uint_as_float(x[2 * k + 1]));
         sum[k & 1] = add2(sum[k & 1], pack2(a, b));
         w[k] = pack_bf16(a, b);
     }
@@ -321,10 +266,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     float2* s_ml = reinterpret_cast<float2*>(g_tail);                 // [2][128] (m, l) of the two warpgroups
     const uint32_t bars = base + (uint32_t)(2 * C::kQTile + S * C::kTile) + 2048u;
     uint8_t* g_misc = g_tail + 2048 + 8 * C::kBars;
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(g_misc);
-    volatile int* s_abort = reinterpret_cast<volatile int*>(g_misc + 4);
-    Place* s_place = reinterpret_cast<Place*>(g_misc + 8);            // [2] first and last place
+    Segment* s_seg = reinterpret_cast<Segment*>(g_misc);              // [kQueue]
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(g_misc + kQueue * sizeof(Segment));
+    volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
     unsigned long long* s_scan = reinterpret_cast<unsigned long long*>(g_tail);  // before the roles start
+    Place* s_place = reinterpret_cast<Place*>(g_tail + 128);                     // likewise: first and last place
     auto full = [&](int s) { return bars + 8u * (uint32_t)s; };
     auto empty = [&](int s) { return bars + 8u * (uint32_t)(S + s); };
     auto bar_at = [&](int i) { return bars + 8u * (uint32_t)(2 * S + i); };
@@ -333,6 +279,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     auto p_full = [&](int t) { return bar_at(4 + t); };
     auto o_done = [&](int t) { return bar_at(6 + t); };
     auto o_free = [&](int t) { return bar_at(8 + t); };
+    auto seg_full = [&](int i) { return bar_at(13 + i); };
+    auto seg_read = [&](int i) { return bar_at(13 + kQueue + i); };
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if ((base & 1023u) != 0u) {  // the swizzle atoms need it; shared memory starts there
@@ -359,6 +307,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         mbar_init(x_bar, 8);
         mbar_init(done, 1);
         mbar_init(seg_done, 1);
+        for (int i = 0; i < kQueue; ++i) {
+            mbar_init(seg_full(i), 1);
+            mbar_init(seg_read(i), kPlanWarp);  // every warp but the scheduler
+        }
         *s_abort = 0;
         mbar_fence_init();
         tmap_prefetch(&tmQ);
@@ -369,14 +321,15 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     pdl_launch_dependents();
     pdl_wait();
 
-    // ---- plan: this CTA's range of tiles
+    // ---- plan: this CTA's range of work
     const int t2 = 2 * p.TQ;
     const int per = (p.n_seq + kAttThreads - 1) / kAttThreads;
     const int sa = min(p.n_seq, tid * per), sb = min(p.n_seq, sa + per);
     unsigned long long mine = 0;
-    for (int s = sa; s < sb; ++s) mine += (unsigned long long)p.Hkv * head_tiles<KT>(seq_info(p, s, blockIdx.x == 0), t2);
+#pragma unroll 1
+    for (int s = sa; s < sb; ++s) mine += (unsigned long long)p.Hkv * head_cost<KT>(seq_info(p, s, blockIdx.x == 0), t2);
     unsigned long long incl = mine;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const unsigned long long v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
@@ -386,6 +339,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     __syncthreads();
     tc_fence_after();
     unsigned long long before = 0, U = 0;
+#pragma unroll 1
     for (int w = 0; w < kAttThreads / 32; ++w) {
         const unsigned long long v = s_scan[w];
         if (w < warp) before += v;
@@ -393,13 +347,13 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     }
     before += incl - mine;
     // CTAs that work: as many as there are spans of kMinSpan tiles
-    const unsigned long long most = U / kMinSpan;
+    const unsigned long long most = U / (kMinSpan + kItemCost);
     const unsigned P = most < gridDim.x ? (most > 0 ? (unsigned)most : 1u) : gridDim.x;
     // a boundary within an eighth of a span of an item's edge moves to it
     const unsigned long long tol = U / P / 8;
-    const bool works = blockIdx.x < P && U > 0;
     const uint32_t tmem = *s_tmem;
-    if (works) {
+    if (tid == 0) p.items[blockIdx.x].parts = 0;
+    if (blockIdx.x < P && U > 0) {
 #pragma unroll 1
         for (int e = 0; e < 2; ++e) {
             const unsigned c = blockIdx.x + e;
@@ -410,295 +364,364 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 unsigned long long rem = b - before, uh = 0;
                 int s = sa;
                 SeqInfo i;
+#pragma unroll 1
                 for (;; ++s) {
                     i = seq_info(p, s, false);
-                    uh = head_tiles<KT>(i, t2);
+                    uh = head_cost<KT>(i, t2);
                     if (rem < uh * p.Hkv) break;
                     rem -= uh * p.Hkv;
                 }
                 const int head = (int)(rem / uh);
                 rem -= uh * head;
                 int lo = 0, hi = (i.nq + t2 - 1) / t2 - 1;  // the last item that begins at or before rem
+#pragma unroll 1
                 while (lo < hi) {
                     const int mid = (lo + hi + 1) >> 1;
-                    if (tiles_before<KT>(i, t2, mid) <= rem) lo = mid;
+                    if (cost_before<KT>(i, t2, mid) <= rem) lo = mid;
                     else hi = mid - 1;
                 }
-                const unsigned long long off = rem - tiles_before<KT>(i, t2, lo);
-                const unsigned long long to_end = (unsigned long long)item_tiles<KT>(i, t2, lo) - off;
-                Place a{b, s, head, lo, (int)off};
-                if (off <= tol && off <= to_end) {
+                const unsigned long long off = rem - cost_before<KT>(i, t2, lo);
+                const int tiles = item_tiles<KT>(i, t2, lo);
+                const unsigned long long to_end = (unsigned long long)(tiles + kItemCost) - off;
+                Place a{b, s, head, lo, (int)off - kItemCost};
+                if (off <= kItemCost || (off <= tol && off <= to_end)) {
                     a.w -= off;
                     a.j = 0;
                 } else if (to_end <= tol) {
                     a.w += to_end;
-                    a.j = (int)(off + to_end);
+                    a.j = tiles;
                 }
                 s_place[e] = a;
             }
         }
+    } else if (tid == 0) {
+        s_place[0] = s_place[1] = Place{0, 0, 0, 0, 0};
     }
     __syncthreads();
-    Place first{0, 0, 0, 0, 0};
-    unsigned long long w1 = 0;
-    if (works) {
-        first = s_place[0];
-        w1 = s_place[1].w;
-    }
-    if (tid == 0) p.items[blockIdx.x].parts = 0;
-    __syncthreads();  // s_scan's space becomes s_ml
+    const Place first_place = s_place[0];
+    const unsigned long long w1 = s_place[1].w;
+    __syncthreads();  // their space becomes s_ml
 
     auto give_up = [&]() {
         flag_error(p.err, HA_DEVERR_TIMEOUT);
         *s_abort = 1;
     };
-    SegIter<KT> it;
-    it.left = 0;
-    if (w1 > first.w) it.start(p, first, w1);
-    Segment<KT> g;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        mbar_wait_or_abort(bar, parity, s_abort);
+        tc_fence_after();
+    };
+    auto aborted = [&]() { return (bool)__any_sync(0xffffffffu, *s_abort != 0); };
+    // The next segment (n counts them): false when there is none, or after a timeout.
+    auto next_segment = [&](int& n, Segment& g) {
+        const int i = n % kQueue;
+        wait(seg_full(i), (uint32_t)(n / kQueue) & 1u);
+        g = s_seg[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(seg_read(i));
+        ++n;
+        return !aborted() && g.nt >= 0;
+    };
+    Segment g;
+    int nseg = 0;
 
     if (warp >= kMmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kLoadWarp) {
-        const int lg = p.box_log2;               // rows of a box: 2^lg
-        const int nbox = KT >> lg;
-        const int box = lane & (nbox - 1), half = lane / nbox;
-        int n = 0, nq = 0;
-        bool ok = true;
-        while (ok && it.next(p, g)) {
-            const int nt = g.tiles();
-            if (nt == 0) continue;
-            const int jend = g.jb + nt;
-            if (!mbar_wait_bounded(q_empty, (uint32_t)(nq & 1) ^ 1u, s_abort)) {
-                ok = false;
-                break;
+        if (warp == kPlanWarp) {
+            // ---- the items between the two places, in order
+            unsigned long long left = w1 - first_place.w;
+            int s = first_place.s, head = first_place.head, qt = first_place.qt, j = first_place.j;
+            SeqInfo i{0, 0, 0};
+            int nqt = 0, n = 0;
+            if (left > 0) {
+                i = seq_info(p, s, false);
+                nqt = (i.nq + t2 - 1) / t2;
             }
-            const int qtiles = g.parity ? 1 : 2;
-            if (lane == 0) mbar_arrive_expect_tx(q_full, (uint32_t)(qtiles * p.TQ * p.G * D * 2));
-            __syncwarp();
-            if (lane < qtiles * C::kHalves) {
-                const int t = lane / C::kHalves, h = lane % C::kHalves;
-                tma_load_4d(s_q + (uint32_t)(t * C::kQTile + h * 16384), &tmQ, q_full, h * 64, 0,
-                            g.q0 + g.qt * t2 + t * p.TQ, g.head);
-            }
-            ++nq;
-            const int32_t* table = p.table != nullptr ? p.table + (int64_t)g.s * p.table_st : nullptr;
-            // page and row of this lane's box of tile j
-            auto where = [&](int j, int& page, int& row) {
-                const int key = j * KT + (box << lg);
-                page = 0;
-                row = g.q0 + key;
-                if (table != nullptr && key < g.kend) {
-                    const int e = key / p.page_size;
-                    row = key - e * p.page_size;
-                    page = table[e];
-                    if (page < 0 || page >= p.n_pages) {
-                        flag_error(p.err, HA_DEVERR_INDEX);
-                        page = p.n_pages;  // past the pool: the copy fills its rows with zeros
-                    }
-                }
-            };
-            int page, row;
-            where(g.jb, page, row);
-            for (int j = g.jb; ok && j < jend; ++j) {
-                const int rows = min(KT, g.kend - j * KT);
-                const int boxes = (rows + (1 << lg) - 1) >> lg;
-                int page_n = 0, row_n = 0;
-                if (j + 1 < jend) where(j + 1, page_n, row_n);
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const int s = n % S;
-                    if (!mbar_wait_bounded(empty(s), ((uint32_t)(n / S) & 1u) ^ 1u, s_abort)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) mbar_arrive_expect_tx(full(s), (uint32_t)((boxes << lg) * D * 2));
-                    __syncwarp();
-                    if (box < boxes && half < C::kHalves)
-                        tma_load_4d(s_ring + (uint32_t)(s * C::kTile + half * C::kSpan + (box << lg) * 128),
-                                    kv == 0 ? &tmK : &tmV, full(s), half * 64, row, g.head, page);
-                    ++n;
-                }
-                page = page_n;
-                row = row_n;
-            }
-        }
-        __syncwarp();
-        if (lane == 0) {
-            if (!ok) give_up();
-            // before the CTA can exit: the products have released the last stages, or,
-            // after a timeout, at least the copies into them have landed
-            const bool clean = *s_abort == 0;
-            for (int j = (n > S ? n - S : 0); j < n; ++j)
-                mbar_wait_drain(clean ? empty(j % S) : full(j % S), (uint32_t)(j / S) & 1u);
-            if (nq > 0) mbar_wait_drain(clean ? q_empty : q_full, (uint32_t)(nq - 1) & 1u);
-        }
-    } else if (warp == kMmaWarp) {
-        constexpr uint32_t kIdS = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(KT >> 3) << 17) | ((128u >> 4) << 24);
-        constexpr uint32_t kIdO = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
-                                  ((128u >> 4) << 24);
-        int nq = 0, nseg = 0;
-        uint32_t cnt = 0;  // bit t: parity of stream t's tiles so far
-        bool ok = true;
-        // Low halves of the descriptors: Q (K-major, leading offset unused), the first ring
-        // slot as K (the same) and as V, whose keys are the MMA's K dimension and the rows
-        // of the layout (MN-major): the next 64 dims lie kSpan bytes further, 16 keys 2048.
-        const uint32_t q_lo = uniform(((s_q & 0x3FFFFu) >> 4) | (1u << 16));
-        const uint32_t k_lo = uniform(((s_ring & 0x3FFFFu) >> 4) | (1u << 16));
-        const uint32_t v_lo = uniform(((s_ring & 0x3FFFFu) >> 4) | ((uint32_t)(C::kSpan >> 4) << 16));
-        const uint32_t tm = uniform(tmem);
-        // S_t = Q K^T of the K tile in ring slot s
-        auto issue_s = [&](auto T, uint32_t qtile, uint32_t s) {
-            constexpr uint32_t t = decltype(T)::value;
-            const uint32_t a = q_lo + qtile * (uint32_t)(C::kQTile >> 4), b = k_lo + s * (uint32_t)(C::kTile >> 4);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t h = (uint32_t)(kk >> 2), o = (uint32_t)(kk & 3) * 2u;
-                tc_mma(tm + t * 128u, sw128_desc_of(a + h * 1024u + o),
-                       sw128_desc_of(b + h * (uint32_t)(C::kSpan >> 4) + o), kIdS, kk > 0 ? 1u : 0u);
-            }
-            tc_commit(s_full(t));
-        };
-        // O_t (+)= P_t V of the V tile in ring slot s
-        auto issue_o = [&](auto T, uint32_t s, uint32_t acc) {
-            constexpr uint32_t t = decltype(T)::value;
-            const uint32_t b = v_lo + s * (uint32_t)(C::kTile >> 4);
-#pragma unroll
-            for (int part = 0; part < C::kParts; ++part)
-#pragma unroll
-                for (int kk = 0; kk < KT / 16; ++kk)
-                    tc_mma_ts(tm + 256u + t * 128u, tm + t * 128u + (uint32_t)(C::part_col(part) + kk * 8),
-                              sw128_desc_of(b + (uint32_t)kk * 128u), kIdO, part > 0 || kk > 0 ? 1u : acc);
-        };
-        auto commit = [&](uint32_t bar) {
-            if (elect_one()) tc_commit(bar);
-            __syncwarp();
-        };
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-            mbar_wait_or_abort(bar, parity, s_abort);
-            tc_fence_after();
-        };
-        auto aborted = [&]() { return (bool)__any_sync(0xffffffffu, *s_abort != 0); };
-        uint32_t slot = 0, round = 0;  // ring slot and parity of the next tile to be read
-        // the ring place d tiles on (d < S)
-        auto ahead = [&](uint32_t d, uint32_t& s, uint32_t& r) {
-            s = slot + d;
-            r = round;
-            if (s >= (uint32_t)S) {
-                s -= (uint32_t)S;
-                r ^= 1u;
-            }
-        };
-        while (ok && it.next(p, g)) {
-            const int nt = (int)uniform((uint32_t)g.tiles());
-            const uint32_t free_ph = (uint32_t)(nseg & 1) ^ 1u;
-            ++nseg;
-            // Every segment waits once for both O's of the one before it and then ends with
-            // an arrival on seg_done, which every softmax warp waits for before it gives
-            // the O's of this one back: so neither side is ever two phases ahead, also
-            // where a stream has no tiles and nothing else holds its warps back.
-            auto wait_free = [&]() {
-                wait(o_free(0), free_ph);
-                wait(o_free(1), free_ph);
-            };
-            if (nt == 0) {
-                wait_free();
-                commit(seg_done);
-                ok = !aborted();
-                continue;
-            }
-            // Tiles i = 0 .. nt - 1 of the segment. Row tile 0 of two takes the first e0,
-            // row tile 1 all; with one row tile the streams take every other one. S of a
-            // stream's next tile is issued right behind P V of this one, which reads P where
-            // that S goes: the products run in the order of their issue. The queue of the
-            // tensor cores holds two or three products of 64 cycles: what is waited for
-            // between the products of a batch costs nothing, what is waited for before it
-            // leaves them idle, so only P is.
-            const bool parity = uniform((uint32_t)g.parity) != 0u;
-            const int e0 = parity ? nt : (int)uniform((uint32_t)g.stream_tiles(0));
-            const int step = parity ? 2 : 1;
-            int k_ready = -1;  // last K tile that has been waited for
-            // K tile i, 2 (i - now) tiles ahead in the ring
-            auto wait_k = [&](int i, int now) {
-                uint32_t s, r;
-                ahead(2u * (uint32_t)(i - now), s, r);
-                if (i > k_ready) {
-                    k_ready = i;
-                    wait(full(s), r);
-                }
-                return s;
-            };
-            // behind S of tile i for the last time: K(i) is free, and Q after the last tile
-            auto release_k = [&](uint32_t s, int i) {
-                tc_commit(empty(s));
-                if (i == nt - 1) tc_commit(q_empty);
-            };
-            // the first S of a stream
-            auto first = [&](auto T, int i) {
-                constexpr int t = decltype(T)::value;
-                if (i >= (t == 0 ? e0 : nt)) return;
-                const uint32_t s = wait_k(i, 0);
-                if (elect_one()) {
-                    issue_s(T, parity ? 0u : (uint32_t)t, s);
-                    if (t == 1 || parity) release_k(s, i);
-                }
-                __syncwarp();
-            };
-            // P V of stream t's tile i and S of its next; `last`: nobody reads V(i) after it
-            auto advance = [&](auto T, int i, uint32_t sv, bool last) {
-                constexpr int t = decltype(T)::value;
-                const int ni = i + step;
-                const bool more = ni < (t == 0 ? e0 : nt);
-                wait(p_full(t), (cnt >> t) & 1u);
-                cnt ^= 1u << t;
-                if (elect_one()) {
-                    issue_o(T, sv, !F32OUT && i >= step ? 1u : 0u);
-                    if (F32OUT || !more) tc_commit(o_done(t));
-                    if (last) tc_commit(empty(sv));
-                }
-                __syncwarp();
-                uint32_t sk = 0;
-                if (more) sk = wait_k(ni, i);
-                if (last && i + 1 < nt) {
-                    uint32_t s, r;
-                    ahead(3, s, r);
-                    wait(full(s), r);
-                }
-                if (more && elect_one()) {
-                    issue_s(T, parity ? 0u : (uint32_t)t, sk);
-                    if (t == 1 || parity) release_k(sk, ni);
-                }
-                __syncwarp();
-            };
-            wait(q_full, (uint32_t)(nq & 1));
-            ++nq;
-            first(Stream<0>{}, 0);
-            first(Stream<1>{}, parity ? 1 : 0);
-            {
-                uint32_t s, r;
-                ahead(1, s, r);
-                wait(full(s), r);
-            }
-            wait_free();
+            bool more = left > 0, stop = false;
 #pragma unroll 1
-            for (int i = 0; i < nt; ++i) {
-                uint32_t sv, rv;
-                ahead(1, sv, rv);
-                const bool even = (i & 1) == 0;
-                if (parity ? even : i < e0) advance(Stream<0>{}, i, sv, parity);
-                if (!parity || !even) advance(Stream<1>{}, i, sv, true);
-                ahead(2, slot, round);
+            while (!stop) {
+                Segment o{};
+                o.nt = -1;
+                if (more) {
+                    const int len = item_tiles<KT>(i, t2, qt);
+                    if (j < len) {
+                        const unsigned long long rest = (unsigned long long)(len - j + (j == 0 ? kItemCost : 0));
+                        const int je = rest <= left ? len : j + (int)left - (j == 0 ? kItemCost : 0);
+                        left -= rest <= left ? rest : left;
+                        o.jb = j;
+                        o.kend = keys_seen(i, (qt + 1) * t2);
+                        o.nt = max(0, min(je, key_tiles<KT>(o.kend)) - j);
+                        o.tokens = min(t2, i.nq - qt * t2);
+                        const bool one = o.tokens <= p.TQ;
+                        o.e0 = one ? o.nt : max(0, min(je, key_tiles<KT>(keys_seen(i, qt * t2 + p.TQ))) - j);
+                        o.flags = (one ? 1 : 0) | (j == 0 && je == len ? 2 : 0);
+                        o.row0 = i.q0 + qt * t2;
+                        o.head = head;
+                        o.kfirst = i.nk - i.nq + qt * t2;
+                        o.nk = i.nk;
+                        o.s = s;
+                        o.q0 = i.q0;
+                        o.begins = j == 0;
+                        // the item begins here and goes on in the next CTAs: what the merge needs
+                        if (j == 0 && je < len && lane == 0) {
+                            const unsigned long long last = (w1 + (unsigned long long)(len - je) - tol) * P;
+                            SplitItem d;
+                            d.parts = (int)((last + U - 1) / U) - (int)blockIdx.x;  // to the boundary at which it has ended
+                            d.row0 = o.row0;
+                            d.head = head;
+                            d.tokens = o.tokens;
+                            p.items[blockIdx.x] = d;
+                        }
+                    }
+                    // the next item
+                    j = 0;
+                    if (++qt >= nqt) {
+                        qt = 0;
+                        if (++head >= p.Hkv) {
+                            head = 0;
+                            if (left > 0) {
+                                do {
+                                    ++s;
+                                    if (s >= p.n_seq) left = 0;
+                                    else i = seq_info(p, s, false);
+                                } while (left > 0 && i.nq == 0);
+                                nqt = (i.nq + t2 - 1) / t2;
+                            }
+                        }
+                    }
+                    more = left > 0;
+                    if (o.nt < 0 && more) continue;  // the first place was an item's end
+                }
+                wait(seg_read(n % kQueue), ((uint32_t)(n / kQueue) & 1u) ^ 1u);
+                if (lane == 0) {
+                    s_seg[n % kQueue] = o;
+                    mbar_arrive(seg_full(n % kQueue));
+                }
+                __syncwarp();
+                ++n;
+                stop = o.nt < 0 || aborted();
             }
-            commit(seg_done);
-            ok = !aborted();
+        } else if (warp == kQWarp) {
+            int nq = 0;
+#pragma unroll 1
+            while (next_segment(nseg, g)) {
+                if (g.nt == 0) continue;
+                wait(q_empty, (uint32_t)(nq & 1) ^ 1u);
+                if (aborted()) break;
+                const int qtiles = (g.flags & 1) ? 1 : 2;
+                if (lane == 0) mbar_arrive_expect_tx(q_full, (uint32_t)(qtiles * p.TQ * p.G * D * 2));
+                __syncwarp();
+                if (lane < qtiles * C::kHalves) {
+                    const int t = lane / C::kHalves, h = lane % C::kHalves;
+                    tma_load_4d(s_q + (uint32_t)(t * C::kQTile + h * 16384), &tmQ, q_full, h * 64, 0, g.row0 + t * p.TQ, g.head);
+                }
+                ++nq;
+            }
+            __syncwarp();
+            // before the CTA can exit: the products have read it, or at least it has landed
+            if (lane == 0 && nq > 0) mbar_wait_drain(*s_abort == 0 ? q_empty : q_full, (uint32_t)(nq - 1) & 1u);
+        } else if (warp == kLoadWarp) {
+            const int lg = p.box_log2;               // rows of a box: 2^lg
+            const int nbox = KT >> lg;
+            const int box = lane & (nbox - 1), half = lane / nbox;
+            int n = 0;
+            bool ok = true;
+#pragma unroll 1
+            while (ok && next_segment(nseg, g)) {
+                if (g.nt == 0) continue;
+                const int jend = g.jb + g.nt;
+                const int32_t* table = p.table != nullptr ? p.table + (int64_t)g.s * p.table_st : nullptr;
+                // page and row of this lane's box of tile j
+                auto where = [&](int j, int& page, int& row) {
+                    const int key = j * KT + (box << lg);
+                    page = 0;
+                    row = g.q0 + key;
+                    if (table != nullptr && key < g.kend) {
+                        const int e = key / p.page_size;
+                        row = key - e * p.page_size;
+                        page = table[e];
+                        if (page < 0 || page >= p.n_pages) {
+                            flag_error(p.err, HA_DEVERR_INDEX);
+                            page = p.n_pages;  // past the pool: the copy fills its rows with zeros
+                        }
+                    }
+                };
+                int page_n, row_n;
+                where(g.jb, page_n, row_n);
+#pragma unroll 1
+                for (int j = g.jb; ok && j < jend; ++j) {
+                    const int page = page_n, row = row_n;
+                    const int boxes = (min(KT, g.kend - j * KT) + (1 << lg) - 1) >> lg;
+                    if (j + 1 < jend) where(j + 1, page_n, row_n);
+#pragma unroll 1
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const int s = n % S;
+                        wait(empty(s), ((uint32_t)(n / S) & 1u) ^ 1u);
+                        if (aborted()) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(full(s), (uint32_t)((boxes << lg) * D * 2));
+                        __syncwarp();
+                        if (box < boxes && half < C::kHalves)
+                            tma_load_4d(s_ring + (uint32_t)(s * C::kTile + half * C::kSpan + (box << lg) * 128),
+                                        kv == 0 ? &tmK : &tmV, full(s), half * 64, row, g.head, page);
+                        ++n;
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) {
+                // before the CTA can exit: the products have released the last stages, or,
+                // after a timeout, at least the copies into them have landed
+                const bool clean = *s_abort == 0;
+                for (int j = (n > S ? n - S : 0); j < n; ++j)
+                    mbar_wait_drain(clean ? empty(j % S) : full(j % S), (uint32_t)(j / S) & 1u);
+            }
+        } else {
+            constexpr uint32_t kIdS = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(KT >> 3) << 17) | ((128u >> 4) << 24);
+            constexpr uint32_t kIdO = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
+                                      ((128u >> 4) << 24);
+            int nq = 0;
+            uint32_t cnt = 0;  // bit t: parity of stream t's tiles so far
+            // Low halves of the descriptors: Q (K-major, leading offset unused), the first ring
+            // slot as K (the same) and as V, whose keys are the MMA's K dimension and the rows
+            // of the layout (MN-major): the next 64 dims lie kSpan bytes further, 16 keys 2048.
+            const uint32_t q_lo = uniform(((s_q & 0x3FFFFu) >> 4) | (1u << 16));
+            const uint32_t k_lo = uniform(((s_ring & 0x3FFFFu) >> 4) | (1u << 16));
+            const uint32_t v_lo = uniform(((s_ring & 0x3FFFFu) >> 4) | ((uint32_t)(C::kSpan >> 4) << 16));
+            const uint32_t tm = uniform(tmem);
+            // S_t = Q K^T of the K tile in ring slot s
+            auto issue_s = [&](auto T, uint32_t qtile, uint32_t s) {
+                constexpr uint32_t t = decltype(T)::value;
+                const uint32_t a = q_lo + qtile * (uint32_t)(C::kQTile >> 4), b = k_lo + s * (uint32_t)(C::kTile >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t h = (uint32_t)(kk >> 2), o = (uint32_t)(kk & 3) * 2u;
+                    tc_mma(tm + t * 128u, sw128_desc_of(a + h * 1024u + o),
+                           sw128_desc_of(b + h * (uint32_t)(C::kSpan >> 4) + o), kIdS, kk > 0 ? 1u : 0u);
+                }
+                tc_commit(s_full(t));
+            };
+            // O_t (+)= P_t V of the V tile in ring slot s
+            auto issue_o = [&](auto T, uint32_t s, uint32_t acc) {
+                constexpr uint32_t t = decltype(T)::value;
+                const uint32_t b = v_lo + s * (uint32_t)(C::kTile >> 4);
+#pragma unroll
+                for (int part = 0; part < C::kParts; ++part)
+#pragma unroll
+                    for (int kk = 0; kk < KT / 16; ++kk)
+                        tc_mma_ts(tm + 256u + t * 128u, tm + t * 128u + (uint32_t)(C::part_col(part) + kk * 8),
+                                  sw128_desc_of(b + (uint32_t)kk * 128u), kIdO, part > 0 || kk > 0 ? 1u : acc);
+            };
+            auto commit = [&](uint32_t bar) {
+                if (elect_one()) tc_commit(bar);
+                __syncwarp();
+            };
+            uint32_t slot = 0, round = 0;  // ring slot and parity of the next tile to be read
+            // the ring place d tiles on (d < S)
+            auto ahead = [&](uint32_t d, uint32_t& s, uint32_t& r) {
+                s = slot + d;
+                r = round;
+                if (s >= (uint32_t)S) {
+                    s -= (uint32_t)S;
+                    r ^= 1u;
+                }
+            };
+#pragma unroll 1
+            while (next_segment(nseg, g)) {
+                const int nt = (int)uniform((uint32_t)g.nt);
+                // Every segment waits once for both O's of the one before it and then ends with
+                // an arrival on seg_done, which every softmax warp waits for before it gives
+                // the O's of this one back: so neither side is ever two phases ahead, also
+                // where a stream has no tiles and nothing else holds its warps back.
+                const uint32_t free_ph = (uint32_t)nseg & 1u;
+                // Tiles i = 0 .. nt - 1 of the segment. Row tile 0 of two takes the first e0,
+                // row tile 1 all; with one row tile the streams take every other one. S of a
+                // stream's next tile is issued right behind P V of this one, which reads P where
+                // that S goes: the products run in the order of their issue. The queue of the
+                // tensor cores holds two or three products of 64 cycles: what is waited for
+                // between the products of a batch costs nothing, what is waited for before it
+                // leaves them idle, so only P is.
+                const bool parity = uniform((uint32_t)g.flags & 1u) != 0u;
+                const int e0 = (int)uniform((uint32_t)g.e0);
+                const int step = parity ? 2 : 1;
+                int k_ready = -1;  // last K tile that has been waited for
+                // K tile i, 2 (i - now) tiles ahead in the ring
+                auto wait_k = [&](int i, int now) {
+                    uint32_t s, r;
+                    ahead(2u * (uint32_t)(i - now), s, r);
+                    if (i > k_ready) {
+                        k_ready = i;
+                        wait(full(s), r);
+                    }
+                    return s;
+                };
+                // P V of stream t's tile i (i >= 0) and S of its next; `last`: nobody reads V(i)
+                // after it
+                auto advance = [&](auto T, int i, uint32_t sv, bool last) {
+                    constexpr int t = decltype(T)::value;
+                    const int ni = i < 0 ? (parity ? t : 0) : i + step;
+                    const bool more = ni < (t == 0 ? e0 : nt);
+                    if (i >= 0) {
+                        wait(p_full(t), (cnt >> t) & 1u);
+                        cnt ^= 1u << t;
+                        if (elect_one()) {
+                            issue_o(T, sv, !F32OUT && i >= step ? 1u : 0u);
+                            if (F32OUT || !more) tc_commit(o_done(t));
+                            if (last) tc_commit(empty(sv));
+                        }
+                        __syncwarp();
+                    }
+                    uint32_t sk = 0;
+                    if (more) sk = wait_k(ni, max(i, 0));
+                    if (last && i >= 0 && i + 1 < nt) {
+                        uint32_t s, r;
+                        ahead(3, s, r);
+                        wait(full(s), r);
+                    }
+                    if (more && elect_one()) {
+                        issue_s(T, parity ? 0u : (uint32_t)t, sk);
+                        if (t == 1 || parity) {
+                            // S of tile ni for the last time: K(ni) is free, and Q after the last tile
+                            tc_commit(empty(sk));
+                            if (ni == nt - 1) tc_commit(q_empty);
+                        }
+                    }
+                    __syncwarp();
+                };
+                if (nt > 0) {
+                    wait(q_full, (uint32_t)(nq & 1));
+                    ++nq;
+                }
+                // first the S of both streams (i = -1), then the tiles
+#pragma unroll 1
+                for (int i = nt > 0 ? -1 : 0; i < nt; ++i) {
+                    uint32_t sv, rv;
+                    ahead(1, sv, rv);
+                    const bool even = (i & 1) == 0;
+                    if (i < 0 || (parity ? even : i < e0)) advance(Stream<0>{}, i, sv, parity);
+                    if (i < 0 || !parity || !even) advance(Stream<1>{}, i, sv, true);
+                    if (i < 0) {
+                        wait(full(sv), rv);
+                        wait(o_free(0), free_ph);
+                        wait(o_free(1), free_ph);
+                    } else {
+                        ahead(2, slot, round);
+                    }
+                }
+                if (nt == 0) {
+                    wait(o_free(0), free_ph);
+                    wait(o_free(1), free_ph);
+                }
+                commit(seg_done);
+            }
+            if (lane == 0) {
+                if (*s_abort != 0) give_up();
+                tc_commit(done);  // every product issued above has finished once this arrives
+                mbar_wait_drain(done, 0u);
+            }
+            __syncwarp();
         }
-        if (lane == 0) {
-            if (!ok || *s_abort != 0) give_up();
-            tc_commit(done);  // every product issued above has finished once this arrives
-            mbar_wait_drain(done, 0u);
-        }
-        __syncwarp();
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int t = warp >> 2, r = tid & 127;
@@ -706,24 +729,18 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         const uint32_t tS = tmem + lane_off + (uint32_t)(t * 128);
         const uint32_t tO = tmem + lane_off + 256u;
         const int rtok = r / p.G, rhead = r - rtok * p.G;
-        const bool in_tile = rtok < p.TQ;
-        int cnt[2] = {0, 0}, odc[2] = {0, 0};
-        int nx = 0, nseg = 0, ring = 0;
-        bool ok = true;
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-            mbar_wait_or_abort(bar, parity, s_abort);
-            tc_fence_after();
-            return true;
-        };
-        auto aborted = [&]() { return (bool)__any_sync(0xffffffffu, *s_abort != 0); };
-        while (ok && it.next(p, g)) {
-            const int ltok = (g.parity ? 0 : t * p.TQ) + rtok;       // token of this row within the item
-            const bool valid = in_tile && ltok < g.tokens;
-            const int kmax = valid ? min(g.nk, max(0, g.nk - g.nq + g.qt * t2 + ltok + 1)) : 0;
+        const uint64_t qscale2 = pack2(p.qscale, p.qscale);
+        uint32_t cnt = 0, odc[2] = {0, 0}, nx = 0, ring = 0;  // tiles, o_done's, exchanges, ring tiles so far
+#pragma unroll 1
+        while (next_segment(nseg, g)) {
+            const bool parity = (g.flags & 1) != 0, whole = (g.flags & 2) != 0;
+            const int ltok = (parity ? 0 : t * p.TQ) + rtok;       // token of this row within the item
+            const bool valid = rtok < p.TQ && ltok < g.tokens;
+            const int kmax = valid ? min(g.nk, max(0, g.kfirst + ltok + 1)) : 0;
             const bool any = __any_sync(0xffffffffu, valid);
-            const int st0 = g.stream_tiles(0), st1 = g.stream_tiles(1);
+            const int st0 = parity ? (g.nt + 1) >> 1 : g.e0, st1 = parity ? g.nt >> 1 : g.nt;
             const int nt = t == 0 ? st0 : st1;
-            const int jstep = g.parity ? 2 : 1, j0 = g.parity ? g.jb + t : g.jb;
+            const int jstep = parity ? 2 : 1;
             float m = -INFINITY, l = 0.f;
             float acc[F32OUT ? D : 1];  // float32 output: O is added up here, tile by tile
             if constexpr (F32OUT) {
@@ -742,36 +759,23 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     }
                 }
             };
-            const uint64_t qscale2 = pack2(p.qscale, p.qscale);
-            const int jlast = g.jb + g.tiles() - 1;  // the V tile that may hold rows past the last key
-            // Those rows become zeros (what lies there may be no number, and its weight of 0
-            // would not help): by the first stream that uses them, before its P is full.
-            const bool clears = g.kend < (jlast + 1) * KT && (t == 0 || g.parity || jlast >= g.jb + st0);
-            auto clear_tail = [&]() {
-                const int k = ring + 2 * (jlast - g.jb) + 1, s = k % S;
-                const bool r = wait(full(s), (uint32_t)(k / S) & 1u);
-                const int rows = g.kend - jlast * KT, chunks = (KT - rows) * 8;
-                for (int i = tid & 127; i < chunks * C::kHalves; i += 128) {
-                    const int h = i >= chunks ? 1 : 0;
-                    *reinterpret_cast<uint4*>(s_raw + 2 * C::kQTile + s * C::kTile + h * C::kSpan + rows * 128 +
-                                              (i - h * chunks) * 16) = make_uint4(0, 0, 0, 0);
-                }
-                fence_async_shared();
-                return r;
-            };
-            for (int i = 0; ok && i < nt; ++i) {
-                const int c = cnt[t] + i;
-                const int lim = kmax - (j0 + i * jstep) * KT;  // columns of this tile the row sees
+            // The V tile that may hold rows past the last key. They become zeros (what lies
+            // there may be no number, and its weight of 0 would not help): by the first stream
+            // that uses them, before its P is full.
+            const int jlast = g.jb + g.nt - 1;
+            const bool clears = g.kend < (jlast + 1) * KT && (t == 0 || parity || jlast >= g.jb + st0);
+            int j = parity ? g.jb + t : g.jb;
+#pragma unroll 1
+            for (int i = 0; i < nt; ++i, j += jstep) {
+                const int lim = kmax - j * KT;  // columns of this tile the row sees
                 const bool part = __any_sync(0xffffffffu, lim < KT);
-                if (aborted()) ok = false;
-                if (!ok) break;
+                if (aborted()) break;
                 if constexpr (F32OUT) {
                     if (i > 0) {
-                        ok = wait(o_done(t), (uint32_t)((c - 1) & 1));
-                        if (ok && any) add_o();
+                        wait(o_done(t), (cnt - 1u) & 1u);
+                        if (any) add_o();
                     }
-                    ok = ok && wait(s_full(t), (uint32_t)(c & 1));
-                    if (!ok) break;
+                    wait(s_full(t), cnt & 1u);
                     if (any) {
                         float mx = m;
                         {
@@ -818,87 +822,90 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                             }
                         }
                         l += sum[0] + sum[1];
-                        tmem_wait_st();
                     }
                 } else {
-                    ok = wait(s_full(t), (uint32_t)(c & 1));
-                    if (!ok) break;
+                    wait(s_full(t), cnt & 1u);
                     if (any) {
                         uint32_t x0[64], x1[64];
-                        uint64_t sum[2];
-                        // all weights against the reference m, into P's columns
-                        auto all_weights = [&](bool landed) {
-                            const float sub = m == -INFINITY ? 0.f : m * p.qscale;
-                            const uint64_t nsub2 = pack2(-sub, -sub);
-                            uint32_t w[16];
-                            sum[0] = sum[1] = 0;
-                            weights<32>(x0, qscale2, nsub2, w, sum);
-                            if (!landed) {
-                                tmem_landed(x1);
-                                if (part) mask_columns(x1, lim - 64);
-                            }
-                            tmem_st16(tS, w);
-                            weights<32>(x0 + 32, qscale2, nsub2, w, sum);
-                            tmem_st16(tS + 16u, w);
-                            weights<32>(x1, qscale2, nsub2, w, sum);
-                            tmem_st16(tS + 32u, w);
-                            weights<32>(x1 + 32, qscale2, nsub2, w, sum);
-                            tmem_st16(tS + 48u, w);
-                        };
                         tmem_ld64(tS, x0);
                         tmem_landed(x0);
                         tmem_ld64(tS + 64u, x1);
                         if (part) mask_columns(x0, lim);
-                        // A row's maximum seldom passes its reference by more than 2^8 after its
-                        // first tile: the weights do not wait for it, and are made again if it does.
-                        const bool guess = i > 0;
-                        if (guess) {
-                            all_weights(false);
-                        } else {
-                            tmem_landed(x1);
-                            if (part) mask_columns(x1, lim - 64);
-                        }
-                        const float mx = max_of(x1, max_of(x0, m));
-                        const bool grow = (mx - m) * p.qscale > kRescale;  // false where both are -inf
-                        if (!guess || __any_sync(0xffffffffu, grow)) {
-                            // O holds the products of the tiles before: S of this one came behind them
-                            if (guess) {
-                                tmem_wait_st();  // the first weights are out before the second are
-                                const float a = grow ? ex2((m - mx) * p.qscale) : 1.f;  // 0 from -inf
-                                l *= a;
+                        float mx = m;
+                        if (i == 0) mx = max_of(x0, mx);
+                        tmem_landed(x1);
+                        if (part) mask_columns(x1, lim - 64);
+                        if (i == 0) m = max_of(x1, mx);
+                        // After the first tile a row's maximum seldom passes its reference by
+                        // more than 2^8: the weights do not wait for it, and are made again
+                        // where it does.
 #pragma unroll 1
-                                for (int cc = 0; cc < D; cc += 32) {
-                                    uint32_t o[32];
-                                    tmem_ld32(tO + (uint32_t)(t * 128 + cc), o);
-                                    tmem_landed(o);
-#pragma unroll
-                                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-                                    tmem_st32(tO + (uint32_t)(t * 128 + cc), o);
-                                }
+                        for (;;) {
+                            const float sub = m == -INFINITY ? 0.f : m * p.qscale;
+                            const uint64_t nsub2 = pack2(-sub, -sub);
+                            uint64_t sum[2] = {0, 0};
+                            float mt[4] = {m, m, m, m};
+                            uint32_t w[16];
+                            weights32(x0, qscale2, nsub2, w, sum, mt);
+                            tmem_st16(tS, w);
+                            weights32(x0 + 32, qscale2, nsub2, w, sum, mt);
+                            tmem_st16(tS + 16u, w);
+                            weights32(x1, qscale2, nsub2, w, sum, mt);
+                            tmem_st16(tS + 32u, w);
+                            weights32(x1 + 32, qscale2, nsub2, w, sum, mt);
+                            tmem_st16(tS + 48u, w);
+                            mx = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+                            const bool grow = (mx - m) * p.qscale > kRescale;  // false where both are -inf
+                            if (!__any_sync(0xffffffffu, grow)) {
+                                float a, b;
+                                unpack2(add2(sum[0], sum[1]), a, b);
+                                l += a + b;
+                                break;
                             }
+                            // O holds the products of the tiles before: S of this one came behind them
+                            const float a = grow ? ex2((m - mx) * p.qscale) : 1.f;  // 0 from -inf
+                            l *= a;
                             if (grow) m = mx;
-                            all_weights(true);
+                            tmem_wait_st();  // the first weights are out before the second are
+#pragma unroll 1
+                            for (int cc = 0; cc < D; cc += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(tO + (uint32_t)(t * 128 + cc), o);
+                                tmem_landed(o);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+                                tmem_st32(tO + (uint32_t)(t * 128 + cc), o);
+                            }
                         }
-                        float a, b;
-                        unpack2(add2(sum[0], sum[1]), a, b);
-                        l += a + b;
-                        tmem_wait_st();
                     }
                 }
-                if (clears && j0 + i * jstep == jlast) {
-                    ok = clear_tail();
-                    if (!ok) break;
+                ++cnt;
+                if (clears && j == jlast) {
+                    const uint32_t k = ring + 2u * (uint32_t)(jlast - g.jb) + 1u, s = k % (uint32_t)S;
+                    wait(full((int)s), (k / (uint32_t)S) & 1u);
+                    const int rows = g.kend - jlast * KT, chunks = (KT - rows) * 8;
+#pragma unroll 1
+                    for (int e = r; e < chunks * C::kHalves; e += 128) {
+                        const int h = e >= chunks ? 1 : 0;
+                        *reinterpret_cast<uint4*>(s_raw + 2 * C::kQTile + s * C::kTile + h * C::kSpan + rows * 128 +
+                                                  (e - h * chunks) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_shared();
                 }
+                tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full(t));
             }
-            ring += 2 * g.tiles();
+            ring += 2u * (uint32_t)g.nt;
+            // o_done: every tile with a float32 output, else a stream's last one
+            odc[0] += F32OUT ? (uint32_t)st0 : (st0 > 0 ? 1u : 0u);
+            odc[1] += F32OUT ? (uint32_t)st1 : (st1 > 0 ? 1u : 0u);
+            if (nt > 0) wait(o_done(t), (odc[t] - 1u) & 1u);
             if constexpr (F32OUT) {
-                // the whole O goes where the epilogue reads it
-                if (ok && nt > 0) {
-                    ok = wait(o_done(t), (uint32_t)((cnt[t] + nt - 1) & 1));
-                    if (ok && any) {
+                // the whole O goes where the rest reads it
+                if (nt > 0) {
+                    if (any) {
                         add_o();
 #pragma unroll
                         for (int cc = 0; cc < D; cc += 32) {
@@ -912,56 +919,44 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     tc_fence_before();
                 }
             }
-            if (!ok) break;
-            // o_done: every tile with a float32 output, else a stream's last one
-            cnt[t] += nt;
-            odc[0] += F32OUT ? st0 : (st0 > 0 ? 1 : 0);
-            odc[1] += F32OUT ? st1 : (st1 > 0 ? 1 : 0);
-            const bool whole = g.jb == 0 && g.je == g.len;
             // row of out / lse, or of this CTA's part of the item
-            const int64_t grow_ = ((int64_t)(g.q0 + g.qt * t2 + ltok) * p.Hq + g.head * p.G + rhead);
-            const int64_t prow = (int64_t)(2 * blockIdx.x + (g.jb == 0 ? 1 : 0)) * p.slot_rows + (g.parity ? r : t * 128 + r);
-            float ca = 0.f, cb = 0.f;          // factors of O0 (or of this stream's O) and O1
+            const int64_t row = whole ? (int64_t)(g.row0 + ltok) * p.Hq + g.head * p.G + rhead
+                                      : (int64_t)(2 * blockIdx.x + (g.begins ? 1 : 0)) * p.slot_rows + (parity ? r : t * 128 + r);
+            float ca = 1.f, cb = 0.f;          // factors of O0 (or of this stream's O) and O1
+            uint32_t oa = tO + (uint32_t)(t * 128);
             int col0 = 0, cols = D;
-            bool both = false;
-            if (g.parity) {
+            const bool have = parity ? st0 > 0 : nt > 0, both = parity && st1 > 0;
+            if (parity) {
                 if (st0 > 0) {
-                    // own stream first: its last product follows all but the last of the other's
-                    if (nt > 0) ok = wait(o_done(t), (uint32_t)((odc[t] - 1) & 1));
-                    if (ok && (t == 1 || st1 > 0)) ok = wait(o_done(t ^ 1), (uint32_t)((odc[t ^ 1] - 1) & 1));
-                    if (!ok) break;
+                    // the other stream: all but its last product came before ours
+                    if (t == 1 || st1 > 0) wait(o_done(t ^ 1), (odc[t ^ 1] - 1u) & 1u);
                     s_ml[t * 128 + r] = make_float2(m, l);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(x_bar);
-                    ok = wait(x_bar, (uint32_t)(nx & 1));
+                    wait(x_bar, nx & 1u);
                     ++nx;
-                    if (!ok) break;
                     const float2 A = s_ml[r], B = s_ml[128 + r];
                     m = fmaxf(A.x, B.x);
                     const float ms = m == -INFINITY ? 0.f : m;
                     ca = ex2((A.x - ms) * p.qscale);
                     cb = ex2((B.x - ms) * p.qscale);
                     l = A.y * ca + B.y * cb;
-                    both = st1 > 0;
                 }
+                oa = tO;
                 col0 = t * (D / 2);
                 cols = D / 2;
-            } else {
-                if (nt > 0) {
-                    ok = wait(o_done(t), (uint32_t)((odc[t] - 1) & 1));
-                    if (!ok) break;
-                }
-                ca = 1.f;
             }
-            const bool have = g.parity ? st0 > 0 : nt > 0;
-            const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
-            ca *= inv;
-            cb *= inv;
+            if (whole) {
+                const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+                ca *= inv;
+                cb *= inv;
+            }
             if (any) {
-                const uint32_t oa = tO + (g.parity ? 0u : (uint32_t)(t * 128));
 #pragma unroll 1
                 for (int cc = col0; cc < col0 + cols; cc += 32) {
                     uint32_t o[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = 0u;
                     if (have) {
                         tmem_ld32(oa + (uint32_t)cc, o);
                         tmem_landed(o);
@@ -975,13 +970,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                             for (int k = 0; k < 32; ++k)
                                 o[k] = __float_as_uint(fmaf(__uint_as_float(o1[k]), cb, __uint_as_float(o[k])));
                         }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = 0u;
                     }
                     if (valid) {
                         if (whole && !F32OUT) {
-                            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + grow_ * D + cc);
+                            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + row * D + cc);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 uint32_t w[4];
@@ -991,47 +983,28 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                                 dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
                             }
                         } else {
-                            float* f = whole ? reinterpret_cast<float*>(p.out) + grow_ * D + cc : p.part_o + prow * D + cc;
-                            uint4* dst = reinterpret_cast<uint4*>(f);
+                            uint4* dst = reinterpret_cast<uint4*>((whole ? reinterpret_cast<float*>(p.out) : p.part_o) + row * D + cc);
 #pragma unroll
                             for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                         }
                     }
                 }
-                if (valid && (!g.parity || t == 0)) {
+                if (valid && (!parity || t == 0)) {
                     if (whole)
-                        p.lse[grow_] = l == 0.f ? -INFINITY : fmaf(m, p.qscale, log2f(l)) * 0.6931471805599453f;
+                        p.lse[row] = l == 0.f ? -INFINITY : fmaf(m, p.qscale, log2f(l)) * 0.6931471805599453f;
                     else
-                        p.part_ml[prow] = make_float2(m, l);
+                        p.part_ml[row] = make_float2(m, l);
                 }
             }
             tc_fence_before();
-            ok = wait(seg_done, (uint32_t)(nseg & 1));
-            ++nseg;
-            if (!ok) break;
+            wait(seg_done, (uint32_t)(nseg - 1) & 1u);
             if (lane == 0) {
-                if (g.parity) {
-                    mbar_arrive(o_free(0));
-                    mbar_arrive(o_free(1));
-                } else {
-                    mbar_arrive(o_free(t));
-                    mbar_arrive(o_free(t));
-                }
-            }
-            // the item begins here and goes on in the next CTAs: what the merge needs to know
-            if (tid == 0 && g.jb == 0 && !whole) {
-                const unsigned long long w_end = w1 + (unsigned long long)(g.len - g.je);
-                const unsigned long long last = (w_end - tol) * P;
-                const unsigned stop = (unsigned)((last + U - 1) / U);  // the boundary at which it has ended
-                SplitItem d;
-                d.parts = (int)(stop - blockIdx.x);
-                d.row0 = g.q0 + g.qt * t2;
-                d.head = g.head;
-                d.tokens = g.tokens;
-                p.items[blockIdx.x] = d;
+                // eight arrivals each: four warps twice, or all eight once
+                mbar_arrive(o_free(parity ? 0 : t));
+                mbar_arrive(o_free(parity ? 1 : t));
             }
         }
-        if (lane == 0 && (!ok || *s_abort != 0)) give_up();
+        if (lane == 0 && *s_abort != 0) give_up();
     }
     tc_fence_before();
     __syncthreads();
