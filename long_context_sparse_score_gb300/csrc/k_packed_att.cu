@@ -47,12 +47,13 @@ namespace {
 
 constexpr int kAttThreads = 384;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kQWarp = 10, kPlanWarp = 11;
-// Registers of a softmax thread and of the others: 256 x 208 + 128 x 88 is what 384
+// Registers of a softmax thread and of the others: 256 x 216 + 128 x 72 is what 384
 // threads are launched with (168 each).
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr int kMinSpan = 2;           // fewest tiles of a CTA
 constexpr uint32_t kTmemCols = 512;   // S0, S1 (128 each; P overlays them), O0, O1
-constexpr int kItemCost = 1;           // tiles that an item's start and end cost beside its own
+constexpr int kItemCost = 2;           // tiles that an item's start and end cost beside its own
+constexpr int kSplitCost = 4;          // tiles that writing a part of an item and joining it cost
 constexpr int kQueue = 4;              // segments that the scheduler is ahead
 constexpr float kRescale = 8.f;       // growth of the maximum (log2) that makes O be rescaled
 
@@ -238,16 +239,20 @@ __device__ __forceinline__ float max_of(const uint32_t (&x)[N], float a) {
 // The weights 2^{x qscale - sub} of 32 columns as bf16 pairs in w; their float32 sum is
 // added to sum, and mt takes part in the columns' maximum.
 __device__ __forceinline__ void weights32(const uint32_t* x, uint64_t qscale2, uint64_t nsub2, uint32_t (&w)[16],
-                                          uint64_t (&sum)[2], float (&mt)[4]) {
+                                          uint64_t (&sum)[2]) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-        float a, b;
-        unpack2(fma2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), qscale2, nsub2), a, b);
-        a = ex2(a);
-        b = ex2(b);
-        mt[k & 3] = fmaxf(fmaxf(mt[k & 3], __uint_as_float(x[2 * k])), __uint_as_float(x[2 * k + 1]));
-        sum[k & 1] = add2(sum[k & 1], pack2(a, b));
-        w[k] = pack_bf16(a, b);
+    for (int q = 0; q < 16; q += 4) {
+        float e[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            unpack2(fma2(pack2(__uint_as_float(x[2 * (q + k)]), __uint_as_float(x[2 * (q + k) + 1])), qscale2, nsub2), e[2 * k], e[2 * k + 1]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) e[k] = ex2(e[k]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            w[q + k] = pack_bf16(e[2 * k], e[2 * k + 1]);
+            sum[k & 1] = add2(sum[k & 1], pack2(e[2 * k], e[2 * k + 1]));
+        }
     }
 }
 
@@ -349,8 +354,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     // CTAs that work: as many as there are spans of kMinSpan tiles
     const unsigned long long most = U / (kMinSpan + kItemCost);
     const unsigned P = most < gridDim.x ? (most > 0 ? (unsigned)most : 1u) : gridDim.x;
-    // a boundary within an eighth of a span of an item's edge moves to it
-    const unsigned long long tol = U / P / 8;
+    // a boundary close to an item's edge moves to it: within an eighth of a span, and
+    // within what parting the item would cost
+    const unsigned long long tol = min(U / P / 8, (unsigned long long)kSplitCost);
     const uint32_t tmem = *s_tmem;
     if (tid == 0) p.items[blockIdx.x].parts = 0;
     if (blockIdx.x < P && U > 0) {
@@ -831,42 +837,15 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         tmem_landed(x0);
                         tmem_ld64(tS + 64u, x1);
                         if (part) mask_columns(x0, lim);
-                        float mx = m;
-                        if (i == 0) mx = max_of(x0, mx);
+                        float mx = max_of(x0, m);
                         tmem_landed(x1);
                         if (part) mask_columns(x1, lim - 64);
-                        if (i == 0) m = max_of(x1, mx);
-                        // After the first tile a row's maximum seldom passes its reference by
-                        // more than 2^8: the weights do not wait for it, and are made again
-                        // where it does.
-#pragma unroll 1
-                        for (;;) {
-                            const float sub = m == -INFINITY ? 0.f : m * p.qscale;
-                            const uint64_t nsub2 = pack2(-sub, -sub);
-                            uint64_t sum[2] = {0, 0};
-                            float mt[4] = {m, m, m, m};
-                            uint32_t w[16];
-                            weights32(x0, qscale2, nsub2, w, sum, mt);
-                            tmem_st16(tS, w);
-                            weights32(x0 + 32, qscale2, nsub2, w, sum, mt);
-                            tmem_st16(tS + 16u, w);
-                            weights32(x1, qscale2, nsub2, w, sum, mt);
-                            tmem_st16(tS + 32u, w);
-                            weights32(x1 + 32, qscale2, nsub2, w, sum, mt);
-                            tmem_st16(tS + 48u, w);
-                            mx = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
-                            const bool grow = (mx - m) * p.qscale > kRescale;  // false where both are -inf
-                            if (!__any_sync(0xffffffffu, grow)) {
-                                float a, b;
-                                unpack2(add2(sum[0], sum[1]), a, b);
-                                l += a + b;
-                                break;
-                            }
-                            // O holds the products of the tiles before: S of this one came behind them
-                            const float a = grow ? ex2((m - mx) * p.qscale) : 1.f;  // 0 from -inf
+                        mx = max_of(x1, mx);
+                        const bool grow = (mx - m) * p.qscale > kRescale;
+                        if (__any_sync(0xffffffffu, grow)) {
+                            const float a = grow ? ex2((m - mx) * p.qscale) : 1.f;
                             l *= a;
-                            if (grow) m = mx;
-                            tmem_wait_st();  // the first weights are out before the second are
+                            if (i > 0) {
 #pragma unroll 1
                             for (int cc = 0; cc < D; cc += 32) {
                                 uint32_t o[32];
@@ -876,6 +855,25 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                                 for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
                                 tmem_st32(tO + (uint32_t)(t * 128 + cc), o);
                             }
+                            }
+                            if (grow) m = mx;
+                        }
+                        {
+                            const float sub = m == -INFINITY ? 0.f : m * p.qscale;
+                            const uint64_t nsub2 = pack2(-sub, -sub);
+                            uint64_t sum[2] = {0, 0};
+                            uint32_t w[16];
+                            weights32(x0, qscale2, nsub2, w, sum);
+                            tmem_st16(tS, w);
+                            weights32(x0 + 32, qscale2, nsub2, w, sum);
+                            tmem_st16(tS + 16u, w);
+                            weights32(x1, qscale2, nsub2, w, sum);
+                            tmem_st16(tS + 32u, w);
+                            weights32(x1 + 32, qscale2, nsub2, w, sum);
+                            tmem_st16(tS + 48u, w);
+                            float a1, b1;
+                            unpack2(add2(sum[0], sum[1]), a1, b1);
+                            l += a1 + b1;
                         }
                     }
                 }
