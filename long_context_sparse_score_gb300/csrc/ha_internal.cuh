@@ -304,6 +304,7 @@ struct PackedParams {
     int page_size, n_pages, max_len;
     int box_log2;              // rows of a K/V copy: 2^box_log2
     void* out;
+    int out_align32;           // out starts on a 32-byte boundary
     float* lse;
     uint32_t* err;
     SplitItem* items;          // [grid] (workspace)

@@ -1511,6 +1511,7 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
     p.G = G;
     p.TQ = L.tq;
     p.out = out;
+    p.out_align32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
     p.lse = lse;
     p.err = at<uint32_t>(workspace, 0);
     p.items = at<SplitItem>(workspace, L.off_items);

@@ -256,6 +256,58 @@ __device__ __forceinline__ void weights32(const uint32_t* x, uint64_t qscale2, u
     }
 }
 
+// Output rows of a pair of lanes (the even one's and the odd one's; null: not written).
+// A lane holds a row, so its stores of 16 or 32 bytes would touch 32 rows at a time and
+// cost as many tag lookups (5,700 cycles for two row tiles). The lanes of a pair swap
+// halves and write one row together: 16 rows at a time, twice the bytes each.
+struct RowPair {
+    char *even, *odd;
+    bool is_odd;
+};
+__device__ __forceinline__ RowPair pair_rows(char* mine, bool valid, int lane) {
+    const unsigned long long m = valid ? (unsigned long long)mine : 0ull;
+    const unsigned long long o = __shfl_xor_sync(0xffffffffu, m, 1);
+    RowPair r;
+    r.is_odd = (lane & 1) != 0;
+    r.even = reinterpret_cast<char*>(r.is_odd ? o : m);
+    r.odd = reinterpret_cast<char*>(r.is_odd ? m : o);
+    return r;
+}
+
+__device__ __forceinline__ void store32(char* dst, const uint32_t* w, bool aligned32) {
+    if (aligned32) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// N words of this lane's row, `off` bytes into it.
+template <int N>
+__device__ __forceinline__ void store_rows(const uint32_t (&w)[N], const RowPair& r, int off, bool aligned32) {
+    uint32_t keep[N / 2], got[N / 2];
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) {
+        keep[k] = r.is_odd ? w[N / 2 + k] : w[k];
+        got[k] = __shfl_xor_sync(0xffffffffu, r.is_odd ? w[k] : w[N / 2 + k], 1);
+    }
+    off += r.is_odd ? N * 2 : 0;
+    uint32_t e[N / 2], o[N / 2];
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) {
+        e[k] = r.is_odd ? got[k] : keep[k];
+        o[k] = r.is_odd ? keep[k] : got[k];
+    }
+#pragma unroll
+    for (int k = 0; k < N / 2; k += 8) {
+        if (r.even != nullptr) store32(r.even + off + 4 * k, e + k, aligned32);
+        if (r.odd != nullptr) store32(r.odd + off + 4 * k, o + k, aligned32);
+    }
+}
+
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 template <int D, bool F32OUT>
@@ -950,6 +1002,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 cb *= inv;
             }
             if (any) {
+                const RowPair rows = pair_rows(whole ? reinterpret_cast<char*>(p.out) + row * (D * (F32OUT ? 4 : 2))
+                                                     : reinterpret_cast<char*>(p.part_o) + row * (D * 4), valid, lane);
 #pragma unroll 1
                 for (int cc = col0; cc < col0 + cols; cc += 32) {
                     uint32_t o[32];
@@ -969,22 +1023,13 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                                 o[k] = __float_as_uint(fmaf(__uint_as_float(o1[k]), cb, __uint_as_float(o[k])));
                         }
                     }
-                    if (valid) {
-                        if (whole && !F32OUT) {
-                            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + row * D + cc);
+                    if (whole && !F32OUT) {
+                        uint32_t w[16];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int u = 0; u < 4; ++u)
-                                    w[u] = pack_bf16(__uint_as_float(o[8 * k + 2 * u]), __uint_as_float(o[8 * k + 2 * u + 1]));
-                                dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        } else {
-                            uint4* dst = reinterpret_cast<uint4*>((whole ? reinterpret_cast<float*>(p.out) : p.part_o) + row * D + cc);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                        }
+                        for (int k = 0; k < 16; ++k) w[k] = pack_bf16(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
+                        store_rows(w, rows, cc * 2, p.out_align32);
+                    } else {
+                        store_rows(o, rows, cc * 4, !whole || p.out_align32);
                     }
                 }
                 if (valid && (!parity || t == 0)) {
