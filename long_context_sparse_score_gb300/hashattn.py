@@ -238,13 +238,41 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+def _raw_stream(device: int) -> int:
+    """The current stream of a device, without building a torch.cuda.Stream (2.8 us)."""
+    global _raw_stream
+    import torch
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(device)
+
+
+def _device() -> int:
+    global _device
+    import torch
+    _device = torch.cuda.current_device
+    return _device()
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _here(*tensors) -> list:
+    """Addresses of the arguments (tensors, raw addresses or None); a tensor that is not
+    on the current device, whose stream the call uses, is refused."""
+    out = []
+    for t in tensors:
+        if t is not None and not isinstance(t, int):
+            if t.get_device() != _device():
+                raise ValueError(f"tensor on {t.device}: every argument must be on the current CUDA device")
+            t = t.data_ptr()
+        out.append(t)
+    return out
 
 
 def _dtype_code(t) -> int:
@@ -554,9 +582,9 @@ def hash_attn_append(tokens, cache, q, k, v, page_table, cu, seq_lens, q_out, K,
                      dev_flags=None, stream=None) -> None:
     """Rotate the packed new tokens' q (into ``q_out``) and k by position and write k, v
     (and with ``W`` the keys' codes) into the paged cache; ``q`` and ``q_out`` may be None."""
+    a = _here(q, k, v, W, page_table, cu, seq_lens, q_out, K, V, k_sig, dev_flags)
     _check(lib().hash_attn_append(ctypes.byref(tokens), ctypes.byref(cache), None if rope is None else ctypes.byref(rope),
-                                  _ptr(q), _ptr(k), _ptr(v), _ptr(W), _ptr(page_table), _ptr(cu), _ptr(seq_lens),
-                                  _ptr(q_out), _ptr(K), _ptr(V), _ptr(k_sig), _ptr(dev_flags), _stream(stream)))
+                                  *a, _stream(stream)))
 
 
 def hash_attn_packed_workspace_size(tokens) -> int:
@@ -567,16 +595,15 @@ def hash_attn_packed_workspace_size(tokens) -> int:
 
 def hash_attn_prefill(tokens, q, K, V, cu, out, lse, *, workspace, stream=None) -> None:
     """Causal attention over packed prompts; out [total, Hq, d], lse [total, Hq] contiguous."""
-    ws, nb = _ws(workspace)
-    _check(lib().hash_attn_prefill(ctypes.byref(tokens), _ptr(q), _ptr(K), _ptr(V), _ptr(cu), _ptr(out), _ptr(lse), ws, nb,
-                                   _stream(stream)))
+    a = _here(q, K, V, cu, out, lse, workspace)
+    _check(lib().hash_attn_prefill(ctypes.byref(tokens), *a, workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def hash_attn_chunk(tokens, cache, q, K, V, page_table, cu, seq_lens, out, lse, *, workspace, stream=None) -> None:
     """Attention of the packed new tokens over the paged cache (their keys are in it already)."""
-    ws, nb = _ws(workspace)
-    _check(lib().hash_attn_chunk(ctypes.byref(tokens), ctypes.byref(cache), _ptr(q), _ptr(K), _ptr(V), _ptr(page_table),
-                                 _ptr(cu), _ptr(seq_lens), _ptr(out), _ptr(lse), ws, nb, _stream(stream)))
+    a = _here(q, K, V, page_table, cu, seq_lens, out, lse, workspace)
+    _check(lib().hash_attn_chunk(ctypes.byref(tokens), ctypes.byref(cache), *a,
+                                 workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def hash_attn_device_status(workspace, stream=None) -> tuple[int, int]:

@@ -143,6 +143,20 @@ def test_binding_checks_shapes(ha):
         ha.make_cache(pool, pool, table.long())
 
 
+def test_binding_refuses_tensors_elsewhere(ha, monkeypatch):
+    """A host tensor (or one of another device) never reaches a kernel."""
+    import torch
+    monkeypatch.setattr(ha, "_device", lambda: 0)
+    q, k = torch.zeros(5, 4, 64, dtype=torch.bfloat16), torch.zeros(5, 2, 64, dtype=torch.bfloat16)
+    pool, table = torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16), torch.zeros(2, 4, dtype=torch.int32)
+    t, c, i, f = ha.make_tokens(q, k, k, 2), ha.make_cache(pool, pool, table), torch.zeros(3, dtype=torch.int32), torch.zeros(5, 4)
+    for call in (lambda: ha.hash_attn_append(t, c, q, k, k, table, i, i, q, pool, pool, stream=0),
+                 lambda: ha.hash_attn_prefill(t, q, k, k, i, f, f, workspace=f, stream=0),
+                 lambda: ha.hash_attn_chunk(t, c, q, pool, pool, table, i, i, f, f, workspace=f, stream=0)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
+
+
 # ---------------------------------------------------------------- the oracle
 
 def test_oracle_rotation():
