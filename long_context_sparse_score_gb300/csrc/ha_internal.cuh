@@ -286,8 +286,9 @@ struct RecallParams {
     float* recall;
 };
 
-// An item (sequence, KV head, tokens row0 .. row0 + tokens) whose keys span CTAs:
-// the CTA where it begins and the parts - 1 that follow.
+// An item (sequence, KV head, tokens row0 .. row0 + |tokens|) whose keys span CTAs:
+// the CTA where it begins and the parts - 1 that follow. tokens < 0: every part is four
+// parts of 32 rows.
 struct SplitItem {
     int parts, row0, head, tokens;
 };
@@ -301,6 +302,7 @@ struct PackedParams {
     int64_t table_st;
     int n_seq, total;
     int Hq, Hkv, G, TQ;        // TQ tokens x G heads in a tile of 128 rows
+    int TS;                    // tokens whose rows fit 32 (0: G > 32)
     int page_size, n_pages, max_len;
     int box_log2;              // rows of a K/V copy: 2^box_log2
     void* out;

@@ -1444,8 +1444,7 @@ PackedLayout packed_layout(const ha_tokens* t) {
     PackedLayout L;
     const int G = t->h_q / t->h_kv;
     L.tq = kMaxGroup / G;
-    // a batch of at most one row tile has no more rows than it has
-    if (t->total <= L.tq) L.slot_rows = (int)align_up((size_t)(t->total > 0 ? t->total : 1) * G, 8);
+    if (t->total <= L.tq) L.slot_rows = 128;  // no item has a second row tile
     size_t off = 256;
     L.off_items = off;
     off = align_up(off + sizeof(SplitItem) * kSMs, 256);
@@ -1510,6 +1509,7 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
     p.Hkv = t->h_kv;
     p.G = G;
     p.TQ = L.tq;
+    p.TS = 32 / G;
     p.out = out;
     p.out_align32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
     p.lse = lse;
@@ -1524,6 +1524,8 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
     // the largest power of two that divides a page
     int box = kt;
     bool ok = encode_map(&m.q, q, t->d, {G, t->total, t->h_kv}, {t->q_sh, t->q_st, G * t->q_sh}, G, L.tq);
+    m.qs = m.q;
+    if (p.TS > 0) ok = ok && encode_map(&m.qs, q, t->d, {G, t->total, t->h_kv}, {t->q_sh, t->q_st, G * t->q_sh}, G, p.TS);
     if (c != nullptr) {
         p.seq_lens = seq_lens;
         p.table = table;

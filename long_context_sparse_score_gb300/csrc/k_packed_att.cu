@@ -166,7 +166,8 @@ struct Segment {
     int nt;       // its key tiles (0: an item without keys; -1: no more)
     int jb;       // the first of them
     int e0;       // two row tiles: those that row tile 0 sees; else nt
-    int flags;    // 1: one row tile (streams take every other key tile); 2: the whole item
+    int flags;    // 1: one row tile (streams take every other key tile); 2: the whole item;
+                  // 4: its rows four times, once for each warp of a stream
     int row0;     // row of its first token in q, out, lse
     int head;     // KV head
     int kend;     // keys that its last token sees
@@ -308,12 +309,36 @@ __device__ __forceinline__ void store_rows(const uint32_t (&w)[N], const RowPair
     }
 }
 
+// The weights 2^{x qscale - sub} of 16 columns as three bf16 parts each (pairs in q); returns
+// their float32 sum.
+__device__ __forceinline__ float parts16(const uint32_t (&x)[16], float qscale, float sub, uint32_t (&q)[3][8]) {
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        float u = ex2(fmaf(__uint_as_float(x[2 * k]), qscale, -sub));
+        float v = ex2(fmaf(__uint_as_float(x[2 * k + 1]), qscale, -sub));
+        s0 += u;
+        s1 += v;
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+            q[e][k] = pack_bf16(u, v);
+            u -= bf16lo(q[e][k]);
+            v -= bf16hi(q[e][k]);
+        }
+    }
+    return s0 + s1;
+}
+
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[16]) { tmem_ld16(addr, x); }
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[32]) { tmem_ld32(addr, x); }
+
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 template <int D, bool F32OUT>
 __global__ void __launch_bounds__(kAttThreads, 1)
-    k_packed_att(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                 const __grid_constant__ CUtensorMap tmV, const PackedParams p) {
+    k_packed_att(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQs,
+                 const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                 const PackedParams p) {
     using C = AttCfg<D, F32OUT>;
     constexpr int S = C::kStages, KT = C::kKeys;
     extern __shared__ __align__(1024) uint8_t s_raw[];
@@ -326,8 +351,6 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     Segment* s_seg = reinterpret_cast<Segment*>(g_misc);              // [kQueue]
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(g_misc + kQueue * sizeof(Segment));
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
-    unsigned long long* s_scan = reinterpret_cast<unsigned long long*>(g_tail);  // before the roles start
-    Place* s_place = reinterpret_cast<Place*>(g_tail + 128);                     // likewise: first and last place
     auto full = [&](int s) { return bars + 8u * (uint32_t)s; };
     auto empty = [&](int s) { return bars + 8u * (uint32_t)(S + s); };
     auto bar_at = [&](int i) { return bars + 8u * (uint32_t)(2 * S + i); };
@@ -378,87 +401,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     pdl_launch_dependents();
     pdl_wait();
 
-    // ---- plan: this CTA's range of work
-    const int t2 = 2 * p.TQ;
-    const int per = (p.n_seq + kAttThreads - 1) / kAttThreads;
-    const int sa = min(p.n_seq, tid * per), sb = min(p.n_seq, sa + per);
-    unsigned long long mine = 0;
-#pragma unroll 1
-    for (int s = sa; s < sb; ++s) mine += (unsigned long long)p.Hkv * head_cost<KT>(seq_info(p, s, blockIdx.x == 0), t2);
-    unsigned long long incl = mine;
-#pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) s_scan[warp] = incl;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    unsigned long long before = 0, U = 0;
-#pragma unroll 1
-    for (int w = 0; w < kAttThreads / 32; ++w) {
-        const unsigned long long v = s_scan[w];
-        if (w < warp) before += v;
-        U += v;
-    }
-    before += incl - mine;
-    // CTAs that work: as many as there are spans of kMinSpan tiles
-    const unsigned long long most = U / (kMinSpan + kItemCost);
-    const unsigned P = most < gridDim.x ? (most > 0 ? (unsigned)most : 1u) : gridDim.x;
-    // a boundary close to an item's edge moves to it: within an eighth of a span, and
-    // within what parting the item would cost
-    const unsigned long long tol = min(U / P / 8, (unsigned long long)kSplitCost);
     const uint32_t tmem = *s_tmem;
-    if (tid == 0) p.items[blockIdx.x].parts = 0;
-    if (blockIdx.x < P && U > 0) {
-#pragma unroll 1
-        for (int e = 0; e < 2; ++e) {
-            const unsigned c = blockIdx.x + e;
-            const unsigned long long b = c == P ? U : U * c / P;
-            if (b == U) {
-                if (tid == 0) s_place[e] = Place{U, 0, 0, 0, 0};
-            } else if (b >= before && b < before + mine) {
-                unsigned long long rem = b - before, uh = 0;
-                int s = sa;
-                SeqInfo i;
-#pragma unroll 1
-                for (;; ++s) {
-                    i = seq_info(p, s, false);
-                    uh = head_cost<KT>(i, t2);
-                    if (rem < uh * p.Hkv) break;
-                    rem -= uh * p.Hkv;
-                }
-                const int head = (int)(rem / uh);
-                rem -= uh * head;
-                int lo = 0, hi = (i.nq + t2 - 1) / t2 - 1;  // the last item that begins at or before rem
-#pragma unroll 1
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (cost_before<KT>(i, t2, mid) <= rem) lo = mid;
-                    else hi = mid - 1;
-                }
-                const unsigned long long off = rem - cost_before<KT>(i, t2, lo);
-                const int tiles = item_tiles<KT>(i, t2, lo);
-                const unsigned long long to_end = (unsigned long long)(tiles + kItemCost) - off;
-                Place a{b, s, head, lo, (int)off - kItemCost};
-                if (off <= kItemCost || (off <= tol && off <= to_end)) {
-                    a.w -= off;
-                    a.j = 0;
-                } else if (to_end <= tol) {
-                    a.w += to_end;
-                    a.j = tiles;
-                }
-                s_place[e] = a;
-            }
-        }
-    } else if (tid == 0) {
-        s_place[0] = s_place[1] = Place{0, 0, 0, 0, 0};
-    }
-    __syncthreads();
-    const Place first_place = s_place[0];
-    const unsigned long long w1 = s_place[1].w;
-    __syncthreads();  // their space becomes s_ml
+    const int t2 = 2 * p.TQ;
 
     auto give_up = [&]() {
         flag_error(p.err, HA_DEVERR_TIMEOUT);
@@ -485,7 +432,77 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     if (warp >= kMmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kPlanWarp) {
-            // ---- the items between the two places, in order
+            // ---- this CTA's range of work, then its items in order
+            auto cost = [&](int s, bool report) {
+                return s < p.n_seq ? (unsigned long long)p.Hkv * head_cost<KT>(seq_info(p, s, report), t2) : 0ull;
+            };
+            unsigned long long U = 0, cost0 = 0;
+#pragma unroll 1
+            for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
+                const unsigned long long c = cost(s0 + lane, blockIdx.x == 0);
+                if (s0 == 0) cost0 = c;
+                U += c;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) U += __shfl_xor_sync(0xffffffffu, U, o);
+            // CTAs that work: as many as there are spans of kMinSpan tiles
+            const unsigned long long most = U / (kMinSpan + kItemCost);
+            const unsigned P = most < gridDim.x ? (most > 0 ? (unsigned)most : 1u) : gridDim.x;
+            // a boundary close to an item's edge moves to it: within an eighth of a span, and
+            // within what parting the item would cost
+            const unsigned long long tol = min(U / P / 8, (unsigned long long)kSplitCost);
+            if (lane == 0) p.items[blockIdx.x].parts = 0;
+            // the place of boundary c
+            auto place = [&](unsigned c) {
+                Place a{U, 0, 0, 0, 0};
+                const unsigned long long b = c >= P ? U : U * c / P;
+                if (b == U) return a;
+                unsigned long long before = 0, incl = 0, mine = 0;
+                int s0 = 0;
+#pragma unroll 1
+                for (;; s0 += 32) {
+                    mine = s0 == 0 ? cost0 : cost(s0 + lane, false);
+                    incl = mine;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const unsigned long long v = __shfl_up_sync(0xffffffffu, incl, o);
+                        if (lane >= o) incl += v;
+                    }
+                    const unsigned long long all = __shfl_sync(0xffffffffu, incl, 31);
+                    if (b < before + all) break;
+                    before += all;
+                }
+                const int at = __ffs((int)__ballot_sync(0xffffffffu, b < before + incl)) - 1;
+                unsigned long long rem = b - before - __shfl_sync(0xffffffffu, incl - mine, at);
+                const unsigned long long uh = __shfl_sync(0xffffffffu, mine, at) / (unsigned)p.Hkv;
+                a.s = s0 + at;
+                const SeqInfo i = seq_info(p, a.s, false);
+                a.head = (int)(rem / uh);
+                rem -= uh * a.head;
+                int lo = 0, hi = (i.nq + t2 - 1) / t2 - 1;  // the last item that begins at or before rem
+#pragma unroll 1
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (cost_before<KT>(i, t2, mid) <= rem) lo = mid;
+                    else hi = mid - 1;
+                }
+                const unsigned long long off = rem - cost_before<KT>(i, t2, lo);
+                const int tiles = item_tiles<KT>(i, t2, lo);
+                const unsigned long long to_end = (unsigned long long)(tiles + kItemCost) - off;
+                a.w = b;
+                a.qt = lo;
+                a.j = (int)off - kItemCost;
+                if (off <= kItemCost || (off <= tol && off <= to_end)) {
+                    a.w -= off;
+                    a.j = 0;
+                } else if (to_end <= tol) {
+                    a.w += to_end;
+                    a.j = tiles;
+                }
+                return a;
+            };
+            const Place first_place = place(blockIdx.x);
+            const unsigned long long w1 = first_place.w < U ? place(blockIdx.x + 1).w : U;
             unsigned long long left = w1 - first_place.w;
             int s = first_place.s, head = first_place.head, qt = first_place.qt, j = first_place.j;
             SeqInfo i{0, 0, 0};
@@ -511,7 +528,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         o.tokens = min(t2, i.nq - qt * t2);
                         const bool one = o.tokens <= p.TQ;
                         o.e0 = one ? o.nt : max(0, min(je, key_tiles<KT>(keys_seen(i, qt * t2 + p.TQ))) - j);
-                        o.flags = (one ? 1 : 0) | (j == 0 && je == len ? 2 : 0);
+                        const bool whole = j == 0 && je == len, spread = !whole && o.tokens <= p.TS;
+                        o.flags = (one ? 1 : 0) | (whole ? 2 : 0) | (spread ? 4 : 0);
                         o.row0 = i.q0 + qt * t2;
                         o.head = head;
                         o.kfirst = i.nk - i.nq + qt * t2;
@@ -526,7 +544,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                             d.parts = (int)((last + U - 1) / U) - (int)blockIdx.x;  // to the boundary at which it has ended
                             d.row0 = o.row0;
                             d.head = head;
-                            d.tokens = o.tokens;
+                            d.tokens = spread ? -o.tokens : o.tokens;
                             p.items[blockIdx.x] = d;
                         }
                     }
@@ -565,12 +583,14 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 if (g.nt == 0) continue;
                 wait(q_empty, (uint32_t)(nq & 1) ^ 1u);
                 if (aborted()) break;
-                const int qtiles = (g.flags & 1) ? 1 : 2;
-                if (lane == 0) mbar_arrive_expect_tx(q_full, (uint32_t)(qtiles * p.TQ * p.G * D * 2));
+                const bool spread = (g.flags & 4) != 0;
+                const int copies = spread ? 4 : ((g.flags & 1) ? 1 : 2);
+                if (lane == 0) mbar_arrive_expect_tx(q_full, (uint32_t)(copies * (spread ? p.TS : p.TQ) * p.G * D * 2));
                 __syncwarp();
-                if (lane < qtiles * C::kHalves) {
+                if (lane < copies * C::kHalves) {
                     const int t = lane / C::kHalves, h = lane % C::kHalves;
-                    tma_load_4d(s_q + (uint32_t)(t * C::kQTile + h * 16384), &tmQ, q_full, h * 64, 0, g.row0 + t * p.TQ, g.head);
+                    tma_load_4d(s_q + (uint32_t)((spread ? t * 4096 : t * C::kQTile) + h * 16384), spread ? &tmQs : &tmQ, q_full,
+                                h * 64, 0, g.row0 + (spread ? 0 : t * p.TQ), g.head);
                 }
                 ++nq;
             }
@@ -724,7 +744,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         wait(p_full(t), (cnt >> t) & 1u);
                         cnt ^= 1u << t;
                         if (elect_one()) {
-                            issue_o(T, sv, !F32OUT && i >= step ? 1u : 0u);
+                            issue_o(T, sv, F32OUT ? (uint32_t)(parity ? i >> 1 : i) & 1u : (i >= step ? 1u : 0u));
                             if (F32OUT || !more) tc_commit(o_done(t));
                             if (last) tc_commit(empty(sv));
                         }
@@ -786,14 +806,15 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_off + (uint32_t)(t * 128);
         const uint32_t tO = tmem + lane_off + 256u;
-        const int rtok = r / p.G, rhead = r - rtok * p.G;
+        const int rtok = r / p.G, rhead = r - rtok * p.G, stok = lane / p.G, shead = lane - stok * p.G;
         const uint64_t qscale2 = pack2(p.qscale, p.qscale);
         uint32_t cnt = 0, odc[2] = {0, 0}, nx = 0, ring = 0;  // tiles, o_done's, exchanges, ring tiles so far
 #pragma unroll 1
         while (next_segment(nseg, g)) {
-            const bool parity = (g.flags & 1) != 0, whole = (g.flags & 2) != 0;
-            const int ltok = (parity ? 0 : t * p.TQ) + rtok;       // token of this row within the item
-            const bool valid = rtok < p.TQ && ltok < g.tokens;
+            const bool parity = (g.flags & 1) != 0, whole = (g.flags & 2) != 0, spread = (g.flags & 4) != 0;
+            const int hd = spread ? shead : rhead;
+            const int ltok = spread ? stok : (parity ? 0 : t * p.TQ) + rtok;  // token of this row within the item
+            const bool valid = (spread ? stok < p.TS : rtok < p.TQ) && ltok < g.tokens;
             const int kmax = valid ? min(g.nk, max(0, g.kfirst + ltok + 1)) : 0;
             const bool any = __any_sync(0xffffffffu, valid);
             const int st0 = parity ? (g.nt + 1) >> 1 : g.e0, st1 = parity ? g.nt >> 1 : g.nt;
@@ -829,75 +850,30 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 const bool part = __any_sync(0xffffffffu, lim < KT);
                 if (aborted()) break;
                 if constexpr (F32OUT) {
-                    if (i > 0) {
+                    // O holds two tiles at most (24 steps of the accumulator)
+                    if (i > 0 && (i & 1) == 0) {
                         wait(o_done(t), (cnt - 1u) & 1u);
                         if (any) add_o();
                     }
-                    wait(s_full(t), cnt & 1u);
-                    if (any) {
-                        float mx = m;
-                        {
-                            uint32_t x[64];
-                            tmem_ld64(tS, x);
-                            tmem_landed(x);
-                            if (part) mask_columns(x, lim);
-                            mx = max_of(x, mx);
-                        }
-                        const float ms = mx == -INFINITY ? 0.f : mx;
-                        const float a = ex2((m - ms) * p.qscale);
-                        if (__any_sync(0xffffffffu, mx > m)) {
+                }
+                wait(s_full(t), cnt & 1u);
+                if (any) {
+                    // The reference grows to mx: what was added up shrinks by a. S of this tile
+                    // came behind the products of the tiles before, so O holds those.
+                    auto grow_to = [&](float mx, bool grow) {
+                        const float a = grow ? ex2((m - mx) * p.qscale) : 1.f;  // 0 from -inf
+                        l *= a;
+                        if (grow) m = mx;
+                        if constexpr (F32OUT) {
+                            if ((i & 1) != 0) {
+                                add_o();
+                                const uint32_t zero[32] = {};
+#pragma unroll 1
+                                for (int cc = 0; cc < D; cc += 32) tmem_st32(tO + (uint32_t)(t * 128 + cc), zero);
+                            }
 #pragma unroll
                             for (int k = 0; k < D; ++k) acc[k] *= a;
-                            l *= a;
-                        }
-                        m = mx;
-                        const float sub = ms * p.qscale;
-                        float sum[2] = {0.f, 0.f};
-#pragma unroll
-                        for (int cc = 0; cc < 64; cc += 32) {
-                            uint32_t x[32];
-                            tmem_ld32(tS + (uint32_t)cc, x);
-                            tmem_landed(x);
-                            if (part) mask_columns(x, lim - cc);
-#pragma unroll
-                            for (int q = 0; q < 32; q += 16) {
-                                uint32_t w[3][8];
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) {
-                                    float u = ex2(fmaf(__uint_as_float(x[q + 2 * k]), p.qscale, -sub));
-                                    float v = ex2(fmaf(__uint_as_float(x[q + 2 * k + 1]), p.qscale, -sub));
-                                    sum[0] += u;
-                                    sum[1] += v;
-#pragma unroll
-                                    for (int e = 0; e < 3; ++e) {
-                                        w[e][k] = pack_bf16(u, v);
-                                        u -= bf16lo(w[e][k]);
-                                        v -= bf16hi(w[e][k]);
-                                    }
-                                }
-#pragma unroll
-                                for (int e = 0; e < 3; ++e) tmem_st8(tS + (uint32_t)(C::part_col(e) + (cc + q) / 2), w[e]);
-                            }
-                        }
-                        l += sum[0] + sum[1];
-                    }
-                } else {
-                    wait(s_full(t), cnt & 1u);
-                    if (any) {
-                        uint32_t x0[64], x1[64];
-                        tmem_ld64(tS, x0);
-                        tmem_landed(x0);
-                        tmem_ld64(tS + 64u, x1);
-                        if (part) mask_columns(x0, lim);
-                        float mx = max_of(x0, m);
-                        tmem_landed(x1);
-                        if (part) mask_columns(x1, lim - 64);
-                        mx = max_of(x1, mx);
-                        const bool grow = (mx - m) * p.qscale > kRescale;
-                        if (__any_sync(0xffffffffu, grow)) {
-                            const float a = grow ? ex2((m - mx) * p.qscale) : 1.f;
-                            l *= a;
-                            if (i > 0) {
+                        } else if (i > 0) {
 #pragma unroll 1
                             for (int cc = 0; cc < D; cc += 32) {
                                 uint32_t o[32];
@@ -907,26 +883,96 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                                 for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
                                 tmem_st32(tO + (uint32_t)(t * 128 + cc), o);
                             }
+                        }
+                    };
+                    if (spread) {
+                        // this warp's quarter of the columns; P of the others is 0 in its rows
+                        constexpr int Q = KT / 4;
+                        const int w = warp & 3;
+                        uint32_t x[Q];
+                        tmem_load(tS + (uint32_t)(w * Q), x);
+                        tmem_landed(x);
+                        if (part) mask_columns(x, lim - w * Q);
+                        const float mx = max_of(x, m);
+                        const bool grow = (mx - m) * p.qscale > kRescale;  // false where both are -inf
+                        if (__any_sync(0xffffffffu, grow)) grow_to(mx, grow);
+                        const float sub = m == -INFINITY ? 0.f : m * p.qscale;
+                        if constexpr (F32OUT) {
+                            uint32_t q[3][8];
+                            l += parts16(x, p.qscale, sub, q);
+#pragma unroll
+                            for (int e = 0; e < 3; ++e) {
+                                const uint32_t zero[8] = {};
+#pragma unroll
+                                for (int v = 0; v < 4; ++v) {
+                                    if (v == w) tmem_st8(tS + (uint32_t)(C::part_col(e) + 8 * v), q[e]);
+                                    else tmem_st8(tS + (uint32_t)(C::part_col(e) + 8 * v), zero);
+                                }
                             }
-                            if (grow) m = mx;
-                        }
-                        {
-                            const float sub = m == -INFINITY ? 0.f : m * p.qscale;
-                            const uint64_t nsub2 = pack2(-sub, -sub);
+                        } else {
                             uint64_t sum[2] = {0, 0};
-                            uint32_t w[16];
-                            weights32(x0, qscale2, nsub2, w, sum);
-                            tmem_st16(tS, w);
-                            weights32(x0 + 32, qscale2, nsub2, w, sum);
-                            tmem_st16(tS + 16u, w);
-                            weights32(x1, qscale2, nsub2, w, sum);
-                            tmem_st16(tS + 32u, w);
-                            weights32(x1 + 32, qscale2, nsub2, w, sum);
-                            tmem_st16(tS + 48u, w);
-                            float a1, b1;
-                            unpack2(add2(sum[0], sum[1]), a1, b1);
-                            l += a1 + b1;
+                            uint32_t q[16];
+                            const uint32_t zero[16] = {};
+                            weights32(x, qscale2, pack2(-sub, -sub), q, sum);
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) {
+                                if (v == w) tmem_st16(tS + (uint32_t)(16 * v), q);
+                                else tmem_st16(tS + (uint32_t)(16 * v), zero);
+                            }
+                            float a, b;
+                            unpack2(add2(sum[0], sum[1]), a, b);
+                            l += a + b;
                         }
+                    } else if constexpr (F32OUT) {
+                        float mx = m;
+                        {
+                            uint32_t x[64];
+                            tmem_ld64(tS, x);
+                            tmem_landed(x);
+                            if (part) mask_columns(x, lim);
+                            mx = max_of(x, mx);
+                        }
+                        const bool grow = (mx - m) * p.qscale > kRescale;  // false where both are -inf
+                        if (__any_sync(0xffffffffu, grow)) grow_to(mx, grow);
+                        const float sub = m == -INFINITY ? 0.f : m * p.qscale;
+#pragma unroll 1
+                        for (int cc = 0; cc < 64; cc += 16) {
+                            uint32_t x[16], q[3][8];
+                            tmem_load(tS + (uint32_t)cc, x);
+                            tmem_landed(x);
+                            if (part) mask_columns(x, lim - cc);
+                            l += parts16(x, p.qscale, sub, q);
+                            // the third part goes over columns of S that have been read: 8 for 16
+#pragma unroll
+                            for (int e = 0; e < 3; ++e) tmem_st8(tS + (uint32_t)(C::part_col(e) + cc / 2), q[e]);
+                        }
+                    } else {
+                        uint32_t x0[64], x1[64];
+                        tmem_ld64(tS, x0);
+                        tmem_landed(x0);
+                        tmem_ld64(tS + 64u, x1);
+                        if (part) mask_columns(x0, lim);
+                        float mx = max_of(x0, m);
+                        tmem_landed(x1);
+                        if (part) mask_columns(x1, lim - 64);
+                        mx = max_of(x1, mx);
+                        const bool grow = (mx - m) * p.qscale > kRescale;  // false where both are -inf
+                        if (__any_sync(0xffffffffu, grow)) grow_to(mx, grow);
+                        const float sub = m == -INFINITY ? 0.f : m * p.qscale;
+                        const uint64_t nsub2 = pack2(-sub, -sub);
+                        uint64_t sum[2] = {0, 0};
+                        uint32_t w[16];
+                        weights32(x0, qscale2, nsub2, w, sum);
+                        tmem_st16(tS, w);
+                        weights32(x0 + 32, qscale2, nsub2, w, sum);
+                        tmem_st16(tS + 16u, w);
+                        weights32(x1, qscale2, nsub2, w, sum);
+                        tmem_st16(tS + 32u, w);
+                        weights32(x1 + 32, qscale2, nsub2, w, sum);
+                        tmem_st16(tS + 48u, w);
+                        float a, b;
+                        unpack2(add2(sum[0], sum[1]), a, b);
+                        l += a + b;
                     }
                 }
                 ++cnt;
@@ -970,7 +1016,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 }
             }
             // row of out / lse, or of this CTA's part of the item
-            const int64_t row = whole ? (int64_t)(g.row0 + ltok) * p.Hq + g.head * p.G + rhead
+            const int64_t row = whole ? (int64_t)(g.row0 + ltok) * p.Hq + g.head * p.G + hd
                                       : (int64_t)(2 * blockIdx.x + (g.begins ? 1 : 0)) * p.slot_rows + (parity ? r : t * 128 + r);
             float ca = 1.f, cb = 0.f;          // factors of O0 (or of this stream's O) and O1
             uint32_t oa = tO + (uint32_t)(t * 128);
@@ -1066,15 +1112,20 @@ __global__ void __launch_bounds__(256) k_packed_merge(const PackedParams p) {
     const SplitItem d = p.items[blockIdx.x];
     if (d.parts <= 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool two = d.tokens > p.TQ;
-    const int rows = d.tokens * p.G;
+    // an item whose rows each warp of a stream held: four parts of 32 rows to a CTA
+    const bool spread = d.tokens < 0;
+    const int tokens = spread ? -d.tokens : d.tokens, rows = tokens * p.G, parts = spread ? 4 * d.parts : d.parts;
+    const bool two = tokens > p.TQ;
     constexpr int E = D / 32;
     for (int i = blockIdx.y * 8 + warp; i < rows; i += gridDim.y * 8) {
         const int tok = i / p.G, h = i - tok * p.G;
         const int row = two && tok >= p.TQ ? 128 + (tok - p.TQ) * p.G + h : i;
-        auto at = [&](int k) { return (int64_t)(2 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * p.slot_rows + row; };
+        auto at = [&](int k) {
+            const int c = spread ? k >> 2 : k;
+            return (int64_t)(2 * (blockIdx.x + c) + (c == 0 ? 1 : 0)) * p.slot_rows + row + (spread ? (k & 3) * 32 : 0);
+        };
         float m = -INFINITY;
-        for (int k = lane; k < d.parts; k += 32) m = fmaxf(m, p.part_ml[at(k)].x);
+        for (int k = lane; k < parts; k += 32) m = fmaxf(m, p.part_ml[at(k)].x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float ms = m == -INFINITY ? 0.f : m;
@@ -1082,7 +1133,7 @@ __global__ void __launch_bounds__(256) k_packed_merge(const PackedParams p) {
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
-        for (int k = 0; k < d.parts; ++k) {
+        for (int k = 0; k < parts; ++k) {
             const float2 ml = p.part_ml[at(k)];
             const float w = ex2((ml.x - ms) * p.qscale);
             const float* o = p.part_o + at(k) * D + lane * E;
@@ -1122,7 +1173,7 @@ cudaError_t launch_t(const PackedParams& p, const PackedMaps& m, int grid, bool 
     using C = AttCfg<D, F32OUT>;
     cudaError_t e = cudaFuncSetAttribute(k_packed_att<D, F32OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_ex(k_packed_att<D, F32OUT>, dim3((unsigned)grid), dim3(kAttThreads), C::kSmem, st, true, m.q, m.k, m.v, p);
+    e = launch_ex(k_packed_att<D, F32OUT>, dim3((unsigned)grid), dim3(kAttThreads), C::kSmem, st, true, m.q, m.qs, m.k, m.v, p);
     if (e != cudaSuccess || !merge) return e;
     return launch_ex(k_packed_merge<D, F32OUT>, dim3((unsigned)grid, 4), dim3(256), 0, st, true, p);
 }

@@ -28,7 +28,7 @@ inline EncodeTiledFn encode_fn() {
 
 // Tensor maps of the packed attention: bf16, 4 dimensions, 128-byte swizzle.
 struct PackedMaps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, qs, k, v;  // qs: the queries in copies of TS tokens
 };
 cudaError_t launch_packed_att(const struct PackedParams& p, const PackedMaps& m, int d, bool f32_out, int grid,
                               bool merge, cudaStream_t st);
@@ -138,6 +138,15 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&v)[64]) {
           "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]), "=r"(v[56]), "=r"(v[57]),
           "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
         : "r"(taddr));
+}
+
+// Waits for this thread's TMEM loads; v's values are used after it.
+__device__ __forceinline__ void tmem_landed(uint32_t (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+          "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+        :
+        : "memory");
 }
 
 // Waits for this thread's TMEM loads; v's values are used after it.
