@@ -630,14 +630,12 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     const int page = page_n, row = row_n;
                     const int boxes = (min(KT, g.kend - j * KT) + (1 << lg) - 1) >> lg;
                     if (j + 1 < jend) where(j + 1, page_n, row_n);
+                    ok = !aborted();  // not between a free slot and its load
+                    if (!ok) break;
 #pragma unroll 1
                     for (int kv = 0; kv < 2; ++kv) {
                         const int s = n % S;
                         wait(empty(s), ((uint32_t)(n / S) & 1u) ^ 1u);
-                        if (aborted()) {
-                            ok = false;
-                            break;
-                        }
                         if (lane == 0) mbar_arrive_expect_tx(full(s), (uint32_t)((boxes << lg) * D * 2));
                         __syncwarp();
                         if (box < boxes && half < C::kHalves)
@@ -668,17 +666,16 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             const uint32_t k_lo = uniform(((s_ring & 0x3FFFFu) >> 4) | (1u << 16));
             const uint32_t v_lo = uniform(((s_ring & 0x3FFFFu) >> 4) | ((uint32_t)(C::kSpan >> 4) << 16));
             const uint32_t tm = uniform(tmem);
-            // S_t = Q K^T of the K tile in ring slot s
-            auto issue_s = [&](auto T, uint32_t qtile, uint32_t s) {
+            // S_t = Q K^T of the K tile in ring slot s, steps k0 to k1
+            auto issue_s = [&](auto T, uint32_t qtile, uint32_t s, int k0, int k1) {
                 constexpr uint32_t t = decltype(T)::value;
                 const uint32_t a = q_lo + qtile * (uint32_t)(C::kQTile >> 4), b = k_lo + s * (uint32_t)(C::kTile >> 4);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
+                for (int kk = k0; kk < k1; ++kk) {
                     const uint32_t h = (uint32_t)(kk >> 2), o = (uint32_t)(kk & 3) * 2u;
                     tc_mma(tm + t * 128u, sw128_desc_of(a + h * 1024u + o),
                            sw128_desc_of(b + h * (uint32_t)(C::kSpan >> 4) + o), kIdS, kk > 0 ? 1u : 0u);
                 }
-                tc_commit(s_full(t));
             };
             // O_t (+)= P_t V of the V tile in ring slot s
             auto issue_o = [&](auto T, uint32_t s, uint32_t acc) {
@@ -691,20 +688,17 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         tc_mma_ts(tm + 256u + t * 128u, tm + t * 128u + (uint32_t)(C::part_col(part) + kk * 8),
                                   sw128_desc_of(b + (uint32_t)kk * 128u), kIdO, part > 0 || kk > 0 ? 1u : acc);
             };
-            auto commit = [&](uint32_t bar) {
-                if (elect_one()) tc_commit(bar);
-                __syncwarp();
-            };
-            uint32_t slot = 0, round = 0;  // ring slot and parity of the next tile to be read
-            // the ring place d tiles on (d < S)
-            auto ahead = [&](uint32_t d, uint32_t& s, uint32_t& r) {
-                s = slot + d;
-                r = round;
-                if (s >= (uint32_t)S) {
-                    s -= (uint32_t)S;
-                    r ^= 1u;
+            // ring places: d tiles on (d < S)
+            struct Slot {
+                uint32_t s, r;
+                __device__ __forceinline__ Slot ahead(uint32_t d) const {
+                    const bool wrap = s + d >= (uint32_t)S;
+                    return Slot{wrap ? s + d - (uint32_t)S : s + d, wrap ? r ^ 1u : r};
                 }
             };
+            Slot at{0, 0};  // the next K tile; its V follows
+            auto landed = [&](const Slot& x) { return (bool)__all_sync(0xffffffffu, mbar_try_wait(full((int)x.s), x.r)); };
+            auto wait_slot = [&](const Slot& x) { wait(full((int)x.s), x.r); };
 #pragma unroll 1
             while (next_segment(nseg, g)) {
                 const int nt = (int)uniform((uint32_t)g.nt);
@@ -713,85 +707,134 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 // the O's of this one back: so neither side is ever two phases ahead, also
                 // where a stream has no tiles and nothing else holds its warps back.
                 const uint32_t free_ph = (uint32_t)nseg & 1u;
-                // Tiles i = 0 .. nt - 1 of the segment. Row tile 0 of two takes the first e0,
-                // row tile 1 all; with one row tile the streams take every other one. S of a
-                // stream's next tile is issued right behind P V of this one, which reads P where
-                // that S goes: the products run in the order of their issue. The queue of the
-                // tensor cores holds two or three products of 64 cycles: what is waited for
-                // between the products of a batch costs nothing, what is waited for before it
-                // leaves them idle, so only P is.
                 const bool parity = uniform((uint32_t)g.flags & 1u) != 0u;
                 const int e0 = (int)uniform((uint32_t)g.e0);
-                const int step = parity ? 2 : 1;
-                int k_ready = -1;  // last K tile that has been waited for
-                // K tile i, 2 (i - now) tiles ahead in the ring
-                auto wait_k = [&](int i, int now) {
-                    uint32_t s, r;
-                    ahead(2u * (uint32_t)(i - now), s, r);
-                    if (i > k_ready) {
-                        k_ready = i;
-                        wait(full(s), r);
-                    }
-                    return s;
-                };
-                // P V of stream t's tile i (i >= 0) and S of its next; `last`: nobody reads V(i)
-                // after it
-                auto advance = [&](auto T, int i, uint32_t sv, bool last) {
-                    constexpr int t = decltype(T)::value;
-                    const int ni = i < 0 ? (parity ? t : 0) : i + step;
-                    const bool more = ni < (t == 0 ? e0 : nt);
-                    if (i >= 0) {
-                        wait(p_full(t), (cnt >> t) & 1u);
-                        cnt ^= 1u << t;
-                        if (elect_one()) {
-                            issue_o(T, sv, F32OUT ? (uint32_t)(parity ? i >> 1 : i) & 1u : (i >= step ? 1u : 0u));
-                            if (F32OUT || !more) tc_commit(o_done(t));
-                            if (last) tc_commit(empty(sv));
-                        }
-                        __syncwarp();
-                    }
-                    uint32_t sk = 0;
-                    if (more) sk = wait_k(ni, max(i, 0));
-                    if (last && i >= 0 && i + 1 < nt) {
-                        uint32_t s, r;
-                        ahead(3, s, r);
-                        wait(full(s), r);
-                    }
-                    if (more && elect_one()) {
-                        issue_s(T, parity ? 0u : (uint32_t)t, sk);
-                        if (t == 1 || parity) {
-                            // S of tile ni for the last time: K(ni) is free, and Q after the last tile
-                            tc_commit(empty(sk));
-                            if (ni == nt - 1) tc_commit(q_empty);
-                        }
-                    }
-                    __syncwarp();
+                // Key tiles i = 0 .. nt - 1. S of a stream's next tile is issued right behind P V of
+                // this one, which reads P where that S goes: the products run in the order of
+                // their issue. The queue of the tensor cores holds two or three products of 64
+                // cycles, so they run dry wherever this warp spends more than that between two:
+                // the next tiles are looked for between the products of a batch (a look costs
+                // 100 cycles), and what is left before P V is the wait for P.
+                auto take_p = [&](int t) {
+                    wait(p_full(t), (cnt >> t) & 1u);
+                    cnt ^= 1u << t;
                 };
                 if (nt > 0) {
                     wait(q_full, (uint32_t)(nq & 1));
                     ++nq;
                 }
-                // first the S of both streams (i = -1), then the tiles
-#pragma unroll 1
-                for (int i = nt > 0 ? -1 : 0; i < nt; ++i) {
-                    uint32_t sv, rv;
-                    ahead(1, sv, rv);
-                    const bool even = (i & 1) == 0;
-                    if (i < 0 || (parity ? even : i < e0)) advance(Stream<0>{}, i, sv, parity);
-                    if (i < 0 || !parity || !even) advance(Stream<1>{}, i, sv, true);
-                    if (i < 0) {
-                        wait(full(sv), rv);
-                        wait(o_free(0), free_ph);
-                        wait(o_free(1), free_ph);
-                    } else {
-                        ahead(2, slot, round);
+                Slot v = at.ahead(1);
+                if (nt > 0 && !parity) {
+                    // two row tiles: row tile 0 takes the first e0 key tiles, row tile 1 all
+                    wait_slot(at);
+                    if (elect_one()) {
+                        if (e0 > 0) {
+                            issue_s(Stream<0>{}, 0, at.s, 0, D / 16);
+                            tc_commit(s_full(0));
+                        }
+                        issue_s(Stream<1>{}, 1, at.s, 0, D / 16);
+                        tc_commit(s_full(1));
+                        tc_commit(empty((int)at.s));
+                        if (nt == 1) tc_commit(q_empty);
                     }
-                }
-                if (nt == 0) {
+                    __syncwarp();
+                    wait(o_free(0), free_ph);
+                    wait(o_free(1), free_ph);
+                    bool v_ok = false, k_ok = false;
+                    Slot k = at.ahead(2);
+#pragma unroll 1
+                    for (int i = 0; i < nt; ++i) {
+                        const bool more = i + 1 < nt;
+                        if (!v_ok) wait_slot(v);
+                        if (i < e0) {
+                            take_p(0);
+                            if (elect_one()) {
+                                issue_o(Stream<0>{}, v.s, F32OUT ? (uint32_t)i & 1u : (i > 0 ? 1u : 0u));
+                                if (F32OUT || i + 1 == e0) tc_commit(o_done(0));
+                            }
+                            __syncwarp();
+                            if (i + 1 < e0) {
+                                if (!k_ok) wait_slot(k);
+                                k_ok = true;
+                                if (elect_one()) {
+                                    issue_s(Stream<0>{}, 0, k.s, 0, D / 16);
+                                    tc_commit(s_full(0));
+                                }
+                                __syncwarp();
+                            }
+                        }
+                        take_p(1);
+                        if (elect_one()) {
+                            issue_o(Stream<1>{}, v.s, F32OUT ? (uint32_t)i & 1u : (i > 0 ? 1u : 0u));
+                            if (F32OUT || !more) tc_commit(o_done(1));
+                            tc_commit(empty((int)v.s));
+                        }
+                        __syncwarp();
+                        if (more) {
+                            if (!k_ok) wait_slot(k);
+                            if (elect_one()) issue_s(Stream<1>{}, 1, k.s, 0, D / 32);
+                            __syncwarp();
+                            const Slot v1 = v.ahead(2), k1 = k.ahead(2);
+                            v_ok = landed(v1);
+                            if (elect_one()) {
+                                issue_s(Stream<1>{}, 1, k.s, D / 32, D / 16);
+                                tc_commit(s_full(1));
+                                tc_commit(empty((int)k.s));
+                                if (i + 2 == nt) tc_commit(q_empty);
+                            }
+                            __syncwarp();
+                            k_ok = i + 2 < nt && landed(k1);
+                            v = v1;
+                            k = k1;
+                        }
+                    }
+                } else if (nt > 0) {
+                    // one row tile: the streams take the key tiles in turn
+                    auto first = [&](auto T, const Slot& x, bool last) {
+                        constexpr int t = decltype(T)::value;
+                        wait_slot(x);
+                        if (elect_one()) {
+                            issue_s(T, 0, x.s, 0, D / 16);
+                            tc_commit(s_full(t));
+                            tc_commit(empty((int)x.s));
+                            if (last) tc_commit(q_empty);
+                        }
+                        __syncwarp();
+                    };
+                    first(Stream<0>{}, at, nt == 1);
+                    if (nt > 1) first(Stream<1>{}, at.ahead(2), nt == 2);
+                    wait(o_free(0), free_ph);
+                    wait(o_free(1), free_ph);
+                    Slot k = at.ahead(4);
+                    auto advance = [&](auto T, int i) {
+                        constexpr int t = decltype(T)::value;
+                        const bool more = i + 2 < nt;
+                        wait_slot(v);
+                        take_p(t);
+                        if (elect_one()) {
+                            issue_o(T, v.s, F32OUT ? (uint32_t)(i >> 1) & 1u : (i >= 2 ? 1u : 0u));
+                            if (F32OUT || !more) tc_commit(o_done(t));
+                            tc_commit(empty((int)v.s));
+                        }
+                        __syncwarp();
+                        if (more) first(T, k, i + 3 == nt);
+                        v = v.ahead(2);
+                        k = k.ahead(2);
+                    };
+#pragma unroll 1
+                    for (int i = 0; i < nt; i += 2) {
+                        advance(Stream<0>{}, i);
+                        if (i + 1 < nt) advance(Stream<1>{}, i + 1);
+                    }
+                } else {
                     wait(o_free(0), free_ph);
                     wait(o_free(1), free_ph);
                 }
-                commit(seg_done);
+                const uint32_t end = at.s + 2u * (uint32_t)nt;
+                at.r ^= (end / (uint32_t)S) & 1u;
+                at.s = end % (uint32_t)S;
+                if (elect_one()) tc_commit(seg_done);
+                __syncwarp();
             }
             if (lane == 0) {
                 if (*s_abort != 0) give_up();
