@@ -1146,21 +1146,27 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     }
 }
 
-// Joins the parts of every item that spans CTAs: grid (CTA in which an item may
-// begin, slices of its rows), one warp per row.
+// Joins the parts of every item that spans CTAs, in order: grid (CTA in which an item
+// may begin, slices of its rows). Latency is all it costs, so loads of several parts
+// and rows are in flight: a warp takes a row and four parts at a time; where each warp
+// of a stream left parts (32 rows at most, up to 600 parts), a CTA takes a row and its
+// eight warps share the parts.
+constexpr int kMergeSlices = 16;
 template <int D, bool F32OUT>
 __global__ void __launch_bounds__(256) k_packed_merge(const PackedParams p) {
+    constexpr int E = D / 32;
+    __shared__ float s_acc[8][D];
+    __shared__ float s_l[8];
     pdl_launch_dependents();
     pdl_wait();
     const SplitItem d = p.items[blockIdx.x];
     if (d.parts <= 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // an item whose rows each warp of a stream held: four parts of 32 rows to a CTA
     const bool spread = d.tokens < 0;
     const int tokens = spread ? -d.tokens : d.tokens, rows = tokens * p.G, parts = spread ? 4 * d.parts : d.parts;
     const bool two = tokens > p.TQ;
-    constexpr int E = D / 32;
-    for (int i = blockIdx.y * 8 + warp; i < rows; i += gridDim.y * 8) {
+    const int first = spread ? blockIdx.y : blockIdx.y * 8 + warp, step = spread ? kMergeSlices : kMergeSlices * 8;
+    for (int i = first; i < rows; i += step) {
         const int tok = i / p.G, h = i - tok * p.G;
         const int row = two && tok >= p.TQ ? 128 + (tok - p.TQ) * p.G + h : i;
         auto at = [&](int k) {
@@ -1175,39 +1181,63 @@ __global__ void __launch_bounds__(256) k_packed_merge(const PackedParams p) {
         float l = 0.f, acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-        for (int k = 0; k < parts; ++k) {
-            const float2 ml = p.part_ml[at(k)];
-            const float w = ex2((ml.x - ms) * p.qscale);
-            const float* o = p.part_o + at(k) * D + lane * E;
-            l = fmaf(ml.y, w, l);
-            float v[E];
-            if (E == 4) {
-                const float4 f = *reinterpret_cast<const float4*>(o);
-                v[0] = f.x;
-                v[1] = f.y;
-                v[E - 2] = f.z;
-                v[E - 1] = f.w;
-            } else {
-                const float2 f = *reinterpret_cast<const float2*>(o);
-                v[0] = f.x;
-                v[1] = f.y;
+        const int k0 = spread ? warp : 0, ks = spread ? 8 : 1;
+        for (int k = k0; k < parts; k += 4 * ks) {
+            float2 ml[4];
+            float v[4][E];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const bool in = k + u * ks < parts;
+                const int64_t a = at(in ? k + u * ks : k0);
+                ml[u] = in ? p.part_ml[a] : make_float2(-INFINITY, 0.f);
+                const float* o = p.part_o + a * D + lane * E;
+                if constexpr (E == 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(o);
+                    v[u][0] = f.x, v[u][1] = f.y, v[u][2] = f.z, v[u][3] = f.w;
+                } else {
+                    const float2 f = *reinterpret_cast<const float2*>(o);
+                    v[u][0] = f.x, v[u][1] = f.y;
+                }
             }
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(v[e], w, acc[e]);
-        }
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        const int64_t orow = (int64_t)(d.row0 + tok) * p.Hq + d.head * p.G + h;
-        if (F32OUT) {
-            float* o = reinterpret_cast<float*>(p.out) + orow * D + lane * E;
+            for (int u = 0; u < 4; ++u) {
+                const float w = ex2((ml[u].x - ms) * p.qscale);  // 0 behind the last part
+                l = fmaf(ml[u].y, w, l);
 #pragma unroll
-            for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(o + e) = make_float2(acc[e] * inv, acc[e + 1] * inv);
-        } else {
-            uint32_t* o = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * D + lane * E);
-#pragma unroll
-            for (int e = 0; e < E; e += 2) o[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(v[u][e], w, acc[e]);
+            }
         }
-        if (lane == 0) p.lse[orow] = l == 0.f ? -INFINITY : fmaf(m, p.qscale, log2f(l)) * 0.6931471805599453f;
+        if (spread) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+            if (lane == 0) s_l[warp] = l;
+            __syncthreads();
+            if (warp == 0) {
+                l = 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = 0.f;
+                for (int w = 0; w < 8; ++w) {
+                    l += s_l[w];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] += s_acc[w][lane * E + e];
+                }
+            }
+        }
+        if (!spread || warp == 0) {
+            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+            const int64_t orow = (int64_t)(d.row0 + tok) * p.Hq + d.head * p.G + h;
+            if (F32OUT) {
+                float* o = reinterpret_cast<float*>(p.out) + orow * D + lane * E;
+#pragma unroll
+                for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(o + e) = make_float2(acc[e] * inv, acc[e + 1] * inv);
+            } else {
+                uint32_t* o = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * D + lane * E);
+#pragma unroll
+                for (int e = 0; e < E; e += 2) o[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+            }
+            if (lane == 0) p.lse[orow] = l == 0.f ? -INFINITY : fmaf(m, p.qscale, log2f(l)) * 0.6931471805599453f;
+        }
+        if (spread) __syncthreads();
     }
 }
 
@@ -1218,7 +1248,7 @@ cudaError_t launch_t(const PackedParams& p, const PackedMaps& m, int grid, bool 
     if (e != cudaSuccess) return e;
     e = launch_ex(k_packed_att<D, F32OUT>, dim3((unsigned)grid), dim3(kAttThreads), C::kSmem, st, true, m.q, m.qs, m.k, m.v, p);
     if (e != cudaSuccess || !merge) return e;
-    return launch_ex(k_packed_merge<D, F32OUT>, dim3((unsigned)grid, 4), dim3(256), 0, st, true, p);
+    return launch_ex(k_packed_merge<D, F32OUT>, dim3((unsigned)grid, kMergeSlices), dim3(256), 0, st, true, p);
 }
 
 }  // namespace

@@ -250,8 +250,9 @@ def _raw_stream(device: int) -> int:
 def _device() -> int:
     global _device
     import torch
-    _device = torch.cuda.current_device
-    return _device()
+    device = torch.cuda.current_device()  # initialises CUDA
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return device
 
 
 def _stream(stream) -> int | None:
@@ -265,10 +266,10 @@ def _stream(stream) -> int | None:
 def _here(*tensors) -> list:
     """Addresses of the arguments (tensors, raw addresses or None); a tensor that is not
     on the current device, whose stream the call uses, is refused."""
-    out = []
+    device, out = _device(), []
     for t in tensors:
-        if t is not None and not isinstance(t, int):
-            if t.get_device() != _device():
+        if t is not None and t.__class__ is not int:
+            if t.get_device() != device:
                 raise ValueError(f"tensor on {t.device}: every argument must be on the current CUDA device")
             t = t.data_ptr()
         out.append(t)
