@@ -313,6 +313,7 @@ struct PackedParams {
     float2* part_ml;           // [2 grid][slot_rows] (m, l) of a part (workspace)
     float* part_o;             // [2 grid][slot_rows][d] unnormalised O of a part
     int slot_rows;
+    int split;                 // 0: items are not parted (their keys fit a few tiles)
     float qscale;              // log2(e) / sqrt(d)
 };
 

@@ -1392,6 +1392,7 @@ namespace {
 constexpr int64_t kMaxKeys = (int64_t)1 << 30;     // max_pages * page_size
 constexpr int64_t kMaxStride = (int64_t)1 << 36;   // elements; a tensor map holds strides below 2^40 bytes
 constexpr int kMaxGroup = 128;                     // query heads per KV head in a tile of 128 rows
+constexpr int kWholeTiles = 4;                     // items of no more key tiles are not parted
 
 ha_status check_tokens(const ha_tokens* t) {
     if (t == nullptr) return fail(HA_ERR_INVALID_ARG, "tokens is NULL");
@@ -1544,11 +1545,13 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
     if (!ok) return fail(HA_ERR_UNSUPPORTED, "the tensor-map encoder refused the layout of q, K or V");
     p.box_log2 = 0;
     while ((1 << p.box_log2) < box) ++p.box_log2;
-    // no more CTAs than the lengths can fill with a tile each, and no merge where an item is one tile
+    // No more CTAs than the lengths can fill with a tile each. Items of a few tiles are not
+    // parted, which saves the merge.
     const int64_t tiles = ceil_div(p.max_len, kt);
     const int64_t items = (ceil_div(t->total, 2 * L.tq) + t->n_seq) * t->h_kv;
     const int grid = (int)std::min<int64_t>(kSMs, items * tiles);
-    HA_LAUNCH(launch_packed_att(p, m, t->d, f32, grid, grid > 1 && tiles > 1, static_cast<cudaStream_t>(stream)),
+    p.split = tiles > kWholeTiles;
+    HA_LAUNCH(launch_packed_att(p, m, t->d, f32, grid, grid > 1 && p.split, static_cast<cudaStream_t>(stream)),
               "packed attention launch");
     return HA_OK;
 }

@@ -50,7 +50,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 9, kQWarp = 10, kPlanWarp = 11;
 // Registers of a softmax thread and of the others: 256 x 216 + 128 x 72 is what 384
 // threads are launched with (168 each).
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
-constexpr int kMinSpan = 2;           // fewest tiles of a CTA
+constexpr int kMinSpan = 1;           // fewest tiles of a CTA
 constexpr uint32_t kTmemCols = 512;   // S0, S1 (128 each; P overlays them), O0, O1
 constexpr int kItemCost = 2;           // tiles that an item's start and end cost beside its own
 constexpr int kSplitCost = 4;          // tiles that writing a part of an item and joining it cost
@@ -117,6 +117,11 @@ __device__ __forceinline__ unsigned long long floor_sum(uint32_t n, uint32_t m, 
         a = t;
     }
     return ans;
+}
+
+// a / b without the 64-bit division where a has 32 bits
+__device__ __forceinline__ unsigned long long div_short(unsigned long long a, unsigned b) {
+    return a >> 32 ? a / b : (unsigned long long)((unsigned)a / b);
 }
 
 // Keys that the first `upto` new tokens of the sequence see.
@@ -433,35 +438,45 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kPlanWarp) {
             // ---- this CTA's range of work, then its items in order
-            auto cost = [&](int s, bool report) {
-                return s < p.n_seq ? (unsigned long long)p.Hkv * head_cost<KT>(seq_info(p, s, report), t2) : 0ull;
+            // Sequences are taken 32 at a time, one to a lane; the first 32 stay in registers.
+            SeqInfo mine0{0, 0, 0}, i{0, 0, 0};
+            auto load = [&](int s, bool report) { return s < p.n_seq ? seq_info(p, s, report) : SeqInfo{0, 0, 0}; };
+            auto cost = [&](const SeqInfo& i) { return (unsigned long long)p.Hkv * head_cost<KT>(i, t2); };
+            auto info_of = [&](int s) {
+                if (s >= 32) return seq_info(p, s, false);
+                return SeqInfo{__shfl_sync(0xffffffffu, mine0.q0, s), __shfl_sync(0xffffffffu, mine0.nq, s),
+                               __shfl_sync(0xffffffffu, mine0.nk, s)};
             };
             unsigned long long U = 0, cost0 = 0;
 #pragma unroll 1
             for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
-                const unsigned long long c = cost(s0 + lane, blockIdx.x == 0);
-                if (s0 == 0) cost0 = c;
+                i = load(s0 + lane, blockIdx.x == 0);
+                const unsigned long long c = cost(i);
+                if (s0 == 0) {
+                    mine0 = i;
+                    cost0 = c;
+                }
                 U += c;
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) U += __shfl_xor_sync(0xffffffffu, U, o);
             // CTAs that work: as many as there are spans of kMinSpan tiles
-            const unsigned long long most = U / (kMinSpan + kItemCost);
+            const unsigned long long most = div_short(U, kMinSpan + kItemCost);
             const unsigned P = most < gridDim.x ? (most > 0 ? (unsigned)most : 1u) : gridDim.x;
             // a boundary close to an item's edge moves to it: within an eighth of a span, and
-            // within what parting the item would cost
-            const unsigned long long tol = min(U / P / 8, (unsigned long long)kSplitCost);
+            // within what parting the item would cost (always, where items are not parted)
+            const unsigned long long tol = p.split ? min(div_short(U, 8 * P), (unsigned long long)kSplitCost) : U;
             if (lane == 0) p.items[blockIdx.x].parts = 0;
             // the place of boundary c
             auto place = [&](unsigned c) {
                 Place a{U, 0, 0, 0, 0};
-                const unsigned long long b = c >= P ? U : U * c / P;
+                const unsigned long long b = c >= P ? U : div_short(U * c, P);
                 if (b == U) return a;
                 unsigned long long before = 0, incl = 0, mine = 0;
                 int s0 = 0;
 #pragma unroll 1
                 for (;; s0 += 32) {
-                    mine = s0 == 0 ? cost0 : cost(s0 + lane, false);
+                    mine = s0 == 0 ? cost0 : cost(load(s0 + lane, false));
                     incl = mine;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
@@ -474,10 +489,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 }
                 const int at = __ffs((int)__ballot_sync(0xffffffffu, b < before + incl)) - 1;
                 unsigned long long rem = b - before - __shfl_sync(0xffffffffu, incl - mine, at);
-                const unsigned long long uh = __shfl_sync(0xffffffffu, mine, at) / (unsigned)p.Hkv;
+                const unsigned long long uh = div_short(__shfl_sync(0xffffffffu, mine, at), (unsigned)p.Hkv);
                 a.s = s0 + at;
-                const SeqInfo i = seq_info(p, a.s, false);
-                a.head = (int)(rem / uh);
+                const SeqInfo i = info_of(a.s);
+                a.head = (int)(uh >> 32 ? rem / uh : div_short(rem, (unsigned)uh));
                 rem -= uh * a.head;
                 int lo = 0, hi = (i.nq + t2 - 1) / t2 - 1;  // the last item that begins at or before rem
 #pragma unroll 1
@@ -505,10 +520,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             const unsigned long long w1 = first_place.w < U ? place(blockIdx.x + 1).w : U;
             unsigned long long left = w1 - first_place.w;
             int s = first_place.s, head = first_place.head, qt = first_place.qt, j = first_place.j;
-            SeqInfo i{0, 0, 0};
             int nqt = 0, n = 0;
             if (left > 0) {
-                i = seq_info(p, s, false);
+                i = info_of(s);
                 nqt = (i.nq + t2 - 1) / t2;
             }
             bool more = left > 0, stop = false;
@@ -541,7 +555,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         if (j == 0 && je < len && lane == 0) {
                             const unsigned long long last = (w1 + (unsigned long long)(len - je) - tol) * P;
                             SplitItem d;
-                            d.parts = (int)((last + U - 1) / U) - (int)blockIdx.x;  // to the boundary at which it has ended
+                            d.parts = (int)(U >> 32 ? (last + U - 1) / U : div_short(last + U - 1, (unsigned)U)) - (int)blockIdx.x;  // to the boundary at which it has ended
                             d.row0 = o.row0;
                             d.head = head;
                             d.tokens = spread ? -o.tokens : o.tokens;
@@ -558,7 +572,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                                 do {
                                     ++s;
                                     if (s >= p.n_seq) left = 0;
-                                    else i = seq_info(p, s, false);
+                                    else i = info_of(s);
                                 } while (left > 0 && i.nq == 0);
                                 nqt = (i.nq + t2 - 1) / t2;
                             }
@@ -1093,31 +1107,41 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             if (any) {
                 const RowPair rows = pair_rows(whole ? reinterpret_cast<char*>(p.out) + row * (D * (F32OUT ? 4 : 2))
                                                      : reinterpret_cast<char*>(p.part_o) + row * (D * 4), valid, lane);
-#pragma unroll 1
-                for (int cc = col0; cc < col0 + cols; cc += 32) {
-                    uint32_t o[32];
+                // W columns of O (both streams' where there are two), scaled
+                auto take = [&](int cc, auto& o) {
+                    constexpr int W = sizeof(o) / 4;
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = 0u;
+                    for (int k = 0; k < W; ++k) o[k] = 0u;
                     if (have) {
-                        tmem_ld32(oa + (uint32_t)cc, o);
+                        tmem_load(oa + (uint32_t)cc, o);
                         tmem_landed(o);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * ca);
-                        if (both) {
-                            uint32_t o1[32];
-                            tmem_ld32(tO + 128u + (uint32_t)cc, o1);
-                            tmem_landed(o1);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                o[k] = __float_as_uint(fmaf(__uint_as_float(o1[k]), cb, __uint_as_float(o[k])));
-                        }
+                        for (int k = 0; k < W; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * ca);
                     }
-                    if (whole && !F32OUT) {
-                        uint32_t w[16];
+                    if (both) {
+                        uint32_t o1[W];
+                        tmem_load(tO + 128u + (uint32_t)cc, o1);
+                        tmem_landed(o1);
+#pragma unroll
+                        for (int k = 0; k < W; ++k)
+                            o[k] = __float_as_uint(fmaf(__uint_as_float(o1[k]), cb, __uint_as_float(o[k])));
+                    }
+                };
+                // (in short loops: run once for an item, their code is not in the cache)
+                if (!F32OUT && whole) {
+#pragma unroll 1
+                    for (int cc = col0; cc < col0 + cols; cc += 32) {
+                        uint32_t o[32], w[16];
+                        take(cc, o);
 #pragma unroll
                         for (int k = 0; k < 16; ++k) w[k] = pack_bf16(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
                         store_rows(w, rows, cc * 2, p.out_align32);
-                    } else {
+                    }
+                } else {
+#pragma unroll 1
+                    for (int cc = col0; cc < col0 + cols; cc += 16) {
+                        uint32_t o[16];
+                        take(cc, o);
                         store_rows(o, rows, cc * 4, !whole || p.out_align32);
                     }
                 }
