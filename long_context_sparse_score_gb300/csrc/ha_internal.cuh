@@ -305,6 +305,12 @@ struct PackedParams {
     int TS;                    // tokens whose rows fit 32 (0: G > 32)
     int page_size, n_pages, max_len;
     int box_log2;              // rows of a K/V copy: 2^box_log2
+    // How K and V tiles lie in shared memory and are addressed: 0: a half (64 dims) after the
+    // other, copies of one half, (dim, row, head, page). d = 128 in pages: the halves of
+    // 8 rows side by side, so that one copy takes both, by 8-row groups: 1: (group of the
+    // whole pool, head), for pages that follow each other like their tokens; 2: (group of
+    // a page, page x head), for heads that do.
+    int kv_fold;
     void* out;
     int out_align32;           // out starts on a 32-byte boundary
     float* lse;

@@ -1471,6 +1471,19 @@ bool encode_map(CUtensorMap* m, const void* base, int d, const int64_t (&extent)
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// K or V of d = 128 as 8-row groups of both 64-dim halves (PackedParams::kv_fold): dims (64, row,
+// half, group, outer).
+bool encode_fold(CUtensorMap* m, const void* base, int64_t row, int64_t groups, int64_t outer, int64_t outer_stride, int rows) {
+    const EncodeTiledFn enc = encode_fn();
+    if (enc == nullptr) return false;
+    const cuuint64_t dim[5] = {64u, 8u, 2u, (cuuint64_t)groups, (cuuint64_t)outer};
+    const cuuint64_t str[4] = {(cuuint64_t)row * 2u, 128u, (cuuint64_t)row * 16u, (cuuint64_t)(outer > 1 ? outer_stride : row) * 2u};
+    const cuuint32_t box[5] = {64u, 8u, 2u, (cuuint32_t)(rows / 8), 1u}, unit[5] = {1u, 1u, 1u, 1u, 1u};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dim, str, box, unit,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // prefill (cache null: K and V packed like q) and chunk
 ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q, const void* K, const void* V,
                            const int32_t* table, const int32_t* cu, const int32_t* seq_lens, void* out, float* lse,
@@ -1535,8 +1548,29 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
         p.n_pages = c->n_pages;
         p.max_len = c->max_pages * c->page_size;
         if (c->max_pages > 1 && (c->page_size & -c->page_size) < box) box = c->page_size & -c->page_size;
-        ok = ok && encode_map(&m.k, K, t->d, {c->page_size, t->h_kv, c->n_pages}, {c->k_sn, c->k_sh, c->k_sp}, box, 1) &&
-             encode_map(&m.v, V, t->d, {c->page_size, t->h_kv, c->n_pages}, {c->v_sn, c->v_sh, c->v_sp}, box, 1);
+        // strides of an extent of 1 say nothing
+        auto folds = [&](int64_t outer, int64_t n_outer, int64_t inner, int64_t n_inner) {
+            return n_outer == 1 || outer == inner * n_inner;
+        };
+        auto fold_of = [&](int64_t sp, int64_t sh, int64_t sn) {
+            if (t->d != 128 || c->page_size % 8 != 0) return 0;
+            if (folds(sp, c->n_pages, sn, c->page_size)) return 1;
+            return t->h_kv == 1 || folds(sp, c->n_pages, sh, t->h_kv) ? 2 : 0;
+        };
+        p.kv_fold = fold_of(c->k_sp, c->k_sh, c->k_sn);
+        if (fold_of(c->v_sp, c->v_sh, c->v_sn) != p.kv_fold) p.kv_fold = 0;
+        const int64_t groups = c->page_size / 8;
+        if (p.kv_fold == 1) {
+            ok = ok && encode_fold(&m.k, K, c->k_sn, groups * c->n_pages, t->h_kv, c->k_sh, box) &&
+                 encode_fold(&m.v, V, c->v_sn, groups * c->n_pages, t->h_kv, c->v_sh, box);
+        } else if (p.kv_fold == 2) {
+            const int64_t outer = (int64_t)t->h_kv * c->n_pages;
+            ok = ok && encode_fold(&m.k, K, c->k_sn, groups, outer, t->h_kv > 1 ? c->k_sh : c->k_sp, box) &&
+                 encode_fold(&m.v, V, c->v_sn, groups, outer, t->h_kv > 1 ? c->v_sh : c->v_sp, box);
+        } else {
+            ok = ok && encode_map(&m.k, K, t->d, {c->page_size, t->h_kv, c->n_pages}, {c->k_sn, c->k_sh, c->k_sp}, box, 1) &&
+                 encode_map(&m.v, V, t->d, {c->page_size, t->h_kv, c->n_pages}, {c->v_sn, c->v_sh, c->v_sp}, box, 1);
+        }
     } else {
         p.max_len = t->total;
         ok = ok && encode_map(&m.k, K, t->d, {t->total, t->h_kv, 1}, {t->k_st, t->k_sh, 0}, box, 1) &&

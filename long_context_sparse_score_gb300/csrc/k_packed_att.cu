@@ -57,13 +57,15 @@ constexpr int kSplitCost = 4;          // tiles that writing a part of an item a
 constexpr int kQueue = 4;              // segments that the scheduler is ahead
 constexpr float kRescale = 8.f;       // growth of the maximum (log2) that makes O be rescaled
 
-template <int D, bool F32OUT>
+// FOLD: the halves of a K/V tile lie side by side (PackedParams::kv_fold != 0)
+template <int D, bool F32OUT, bool FOLD>
 struct AttCfg {
     static constexpr int kKeys = F32OUT ? 64 : 128;      // keys per tile
     static constexpr int kHalves = D / 64;               // 128-byte swizzle spans of a row
     static constexpr int kQTile = 128 * D * 2;           // bytes of a Q tile
     static constexpr int kTile = kKeys * D * 2;          // bytes of a K or V tile
-    static constexpr int kSpan = kKeys * 128;            // bytes of one span of its rows
+    // its 8-row groups of one half lie kGroup bytes apart, its halves kSpan
+    static constexpr int kGroup = FOLD ? 2048 : 1024, kSpan = FOLD ? 1024 : kKeys * 128;
     static constexpr int kStages = 5 * 32768 / kTile;
     static constexpr int kParts = F32OUT ? 3 : 1;        // bf16 parts of P
     // First tensor memory column of a part: P takes the columns of S; three parts of 32
@@ -339,12 +341,12 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[32]) { tm
 
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-template <int D, bool F32OUT>
+template <int D, bool F32OUT, bool FOLD>
 __global__ void __launch_bounds__(kAttThreads, 1)
     k_packed_att(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQs,
                  const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const PackedParams p) {
-    using C = AttCfg<D, F32OUT>;
+    using C = AttCfg<D, F32OUT, FOLD>;
     constexpr int S = C::kStages, KT = C::kKeys;
     extern __shared__ __align__(1024) uint8_t s_raw[];
     const uint32_t base = smem_addr(s_raw);
@@ -612,9 +614,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             // before the CTA can exit: the products have read it, or at least it has landed
             if (lane == 0 && nq > 0) mbar_wait_drain(*s_abort == 0 ? q_empty : q_full, (uint32_t)(nq - 1) & 1u);
         } else if (warp == kLoadWarp) {
-            const int lg = p.box_log2;               // rows of a box: 2^lg
+            const int lg = p.box_log2;               // rows of a copy: 2^lg
             const int nbox = KT >> lg;
-            const int box = lane & (nbox - 1), half = lane / nbox;
+            // a copy takes one 64-dim half of its rows, or (pages, d = 128) both
+            const int box = lane & (nbox - 1), half = lane / nbox, halves = FOLD ? 1 : C::kHalves;
+            const uint32_t box_at = FOLD ? (uint32_t)(box << lg) * 256u : (uint32_t)(half * C::kSpan + (box << lg) * 128);
             int n = 0;
             bool ok = true;
 #pragma unroll 1
@@ -634,6 +638,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         if (page < 0 || page >= p.n_pages) {
                             flag_error(p.err, HA_DEVERR_INDEX);
                             page = p.n_pages;  // past the pool: the copy fills its rows with zeros
+                            row = 0;
                         }
                     }
                 };
@@ -641,20 +646,30 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 where(g.jb, page_n, row_n);
 #pragma unroll 1
                 for (int j = g.jb; ok && j < jend; ++j) {
-                    const int page = page_n, row = row_n;
                     const int boxes = (min(KT, g.kend - j * KT) + (1 << lg) - 1) >> lg;
+                    // coordinates behind the dims: (row, head, page), or 8-row groups (see PackedParams)
+                    int c1 = row_n, c2 = g.head, c3 = page_n;
+                    if (FOLD) {
+                        c1 = (p.kv_fold == 1 ? page_n * p.page_size + row_n : row_n) >> 3;
+                        if (p.kv_fold == 2) c2 = page_n < p.n_pages ? page_n * p.Hkv + g.head : p.n_pages * p.Hkv;
+                    }
                     if (j + 1 < jend) where(j + 1, page_n, row_n);
-                    ok = !aborted();  // not between a free slot and its load
-                    if (!ok) break;
 #pragma unroll 1
                     for (int kv = 0; kv < 2; ++kv) {
                         const int s = n % S;
                         wait(empty(s), ((uint32_t)(n / S) & 1u) ^ 1u);
+                        if (aborted()) {
+                            ok = false;
+                            break;
+                        }
                         if (lane == 0) mbar_arrive_expect_tx(full(s), (uint32_t)((boxes << lg) * D * 2));
                         __syncwarp();
-                        if (box < boxes && half < C::kHalves)
-                            tma_load_4d(s_ring + (uint32_t)(s * C::kTile + half * C::kSpan + (box << lg) * 128),
-                                        kv == 0 ? &tmK : &tmV, full(s), half * 64, row, g.head, page);
+                        if (box < boxes && half < halves) {
+                            const CUtensorMap* tm = kv == 0 ? &tmK : &tmV;
+                            const uint32_t dst = s_ring + (uint32_t)(s * C::kTile) + box_at;
+                            if (FOLD) tma_load_5d(dst, tm, full(s), 0, 0, 0, c1, c2);
+                            else tma_load_4d(dst, tm, full(s), half * 64, c1, c2, c3);
+                        }
                         ++n;
                     }
                 }
@@ -673,9 +688,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                                       ((128u >> 4) << 24);
             int nq = 0;
             uint32_t cnt = 0;  // bit t: parity of stream t's tiles so far
-            // Low halves of the descriptors: Q (K-major, leading offset unused), the first ring
-            // slot as K (the same) and as V, whose keys are the MMA's K dimension and the rows
-            // of the layout (MN-major): the next 64 dims lie kSpan bytes further, 16 keys 2048.
+            // Descriptors: Q (K-major, leading offset unused), the first ring slot as K (the same)
+            // and as V, whose keys are the MMA's K dimension and the rows of the layout (MN-major).
+            constexpr uint32_t kv_hi = sw128_desc_hi(C::kGroup);
             const uint32_t q_lo = uniform(((s_q & 0x3FFFFu) >> 4) | (1u << 16));
             const uint32_t k_lo = uniform(((s_ring & 0x3FFFFu) >> 4) | (1u << 16));
             const uint32_t v_lo = uniform(((s_ring & 0x3FFFFu) >> 4) | ((uint32_t)(C::kSpan >> 4) << 16));
@@ -687,8 +702,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 #pragma unroll
                 for (int kk = k0; kk < k1; ++kk) {
                     const uint32_t h = (uint32_t)(kk >> 2), o = (uint32_t)(kk & 3) * 2u;
-                    tc_mma(tm + t * 128u, sw128_desc_of(a + h * 1024u + o),
-                           sw128_desc_of(b + h * (uint32_t)(C::kSpan >> 4) + o), kIdS, kk > 0 ? 1u : 0u);
+                    tc_mma(tm + t * 128u, sw128_desc_of(a + h * 1024u + o, sw128_desc_hi(1024)),
+                           sw128_desc_of(b + h * (uint32_t)(C::kSpan >> 4) + o, kv_hi), kIdS, kk > 0 ? 1u : 0u);
                 }
             };
             // O_t (+)= P_t V of the V tile in ring slot s
@@ -700,7 +715,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 #pragma unroll
                     for (int kk = 0; kk < KT / 16; ++kk)
                         tc_mma_ts(tm + 256u + t * 128u, tm + t * 128u + (uint32_t)(C::part_col(part) + kk * 8),
-                                  sw128_desc_of(b + (uint32_t)kk * 128u), kIdO, part > 0 || kk > 0 ? 1u : acc);
+                                  sw128_desc_of(b + (uint32_t)kk * (uint32_t)(C::kGroup >> 3), kv_hi), kIdO, part > 0 || kk > 0 ? 1u : acc);
             };
             // ring places: d tiles on (d < S)
             struct Slot {
@@ -1037,11 +1052,12 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     const uint32_t k = ring + 2u * (uint32_t)(jlast - g.jb) + 1u, s = k % (uint32_t)S;
                     wait(full((int)s), (k / (uint32_t)S) & 1u);
                     const int rows = g.kend - jlast * KT, chunks = (KT - rows) * 8;
+                    uint8_t* tile = s_raw + 2 * C::kQTile + s * C::kTile;
 #pragma unroll 1
                     for (int e = r; e < chunks * C::kHalves; e += 128) {
-                        const int h = e >= chunks ? 1 : 0;
-                        *reinterpret_cast<uint4*>(s_raw + 2 * C::kQTile + s * C::kTile + h * C::kSpan + rows * 128 +
-                                                  (e - h * chunks) * 16) = make_uint4(0, 0, 0, 0);
+                        const int h = e >= chunks ? 1 : 0, c = e - h * chunks, y = rows + (c >> 3);
+                        *reinterpret_cast<uint4*>(tile + h * C::kSpan + (y >> 3) * C::kGroup + (y & 7) * 128 + (c & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
                     }
                     fence_async_shared();
                 }
@@ -1265,12 +1281,13 @@ __global__ void __launch_bounds__(256) k_packed_merge(const PackedParams p) {
     }
 }
 
-template <int D, bool F32OUT>
+template <int D, bool F32OUT, bool FOLD>
 cudaError_t launch_t(const PackedParams& p, const PackedMaps& m, int grid, bool merge, cudaStream_t st) {
-    using C = AttCfg<D, F32OUT>;
-    cudaError_t e = cudaFuncSetAttribute(k_packed_att<D, F32OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    using C = AttCfg<D, F32OUT, FOLD>;
+    cudaError_t e =
+        cudaFuncSetAttribute(k_packed_att<D, F32OUT, FOLD>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_ex(k_packed_att<D, F32OUT>, dim3((unsigned)grid), dim3(kAttThreads), C::kSmem, st, true, m.q, m.qs, m.k, m.v, p);
+    e = launch_ex(k_packed_att<D, F32OUT, FOLD>, dim3((unsigned)grid), dim3(kAttThreads), C::kSmem, st, true, m.q, m.qs, m.k, m.v, p);
     if (e != cudaSuccess || !merge) return e;
     return launch_ex(k_packed_merge<D, F32OUT>, dim3((unsigned)grid, kMergeSlices), dim3(256), 0, st, true, p);
 }
@@ -1281,8 +1298,9 @@ int packed_key_tile(bool f32_out) { return f32_out ? 64 : 128; }
 
 cudaError_t launch_packed_att(const PackedParams& p, const PackedMaps& m, int d, bool f32_out, int grid, bool merge,
                               cudaStream_t st) {
-    if (d == 128) return f32_out ? launch_t<128, true>(p, m, grid, merge, st) : launch_t<128, false>(p, m, grid, merge, st);
-    return f32_out ? launch_t<64, true>(p, m, grid, merge, st) : launch_t<64, false>(p, m, grid, merge, st);
+    if (d == 64) return f32_out ? launch_t<64, true, false>(p, m, grid, merge, st) : launch_t<64, false, false>(p, m, grid, merge, st);
+    if (p.kv_fold) return f32_out ? launch_t<128, true, true>(p, m, grid, merge, st) : launch_t<128, false, true>(p, m, grid, merge, st);
+    return f32_out ? launch_t<128, true, false>(p, m, grid, merge, st) : launch_t<128, false, false>(p, m, grid, merge, st);
 }
 
 }  // namespace ha

@@ -49,6 +49,15 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm,
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int c0, int c1,
+                                            int c2, int c3, int c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+        : "memory");
+}
+
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int c0, int c1) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
@@ -232,11 +241,10 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-// Descriptor from its halves: `lo` holds address and leading offset, the rest is the
-// 128-byte swizzle layout with 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t sw128_desc_of(uint32_t lo) {
-    return ((uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32) | lo;
-}
+// Shared-memory matrix descriptor in the 128-byte swizzle layout from its halves: the
+// low one holds address and leading offset, the high one the distance of the 8-row groups.
+__host__ __device__ constexpr uint32_t sw128_desc_hi(uint32_t group) { return (group >> 4) | (1u << 14) | (2u << 29); }
+__device__ __forceinline__ uint64_t sw128_desc_of(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
 
 // D (+)= A B with A (128 rows, two bf16 values of its K dimension per 32-bit column) in tensor memory.
 __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,

@@ -243,6 +243,31 @@ def test_chunk(H, case, out_dtype):
     assert torch.equal(again[0], out) and torch.equal(again[1], lse)  # the split's order is fixed
 
 
+@pytest.mark.parametrize("layout", ["kv-by-token", "kv-by-page", "padded-heads", "one-head"])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_chunk_pools_of_other_strides(H, layout, out_dtype):
+    """K and V as views of one pool, or of rows that lie apart."""
+    g = torch.Generator(device="cuda").manual_seed(27)
+    new, lens, Hkv, d, ps, pages_ = [1, 70, 3], [300, 200, 77], 2, 128, 32, 24
+    if layout == "kv-by-token":
+        pool = rand(g, pages_, ps, 2, Hkv, d)
+        K, V = pool[:, :, 0].permute(0, 2, 1, 3), pool[:, :, 1].permute(0, 2, 1, 3)
+    elif layout == "kv-by-page":
+        pool = rand(g, pages_, 2, Hkv, ps, d)
+        K, V = pool[:, 0], pool[:, 1]
+    elif layout == "padded-heads":
+        K, V = rand(g, pages_, Hkv, ps, d + 8)[..., :d], rand(g, pages_, Hkv, ps + 4, d)[:, :, :ps]
+    else:
+        Hkv = 1
+        K, V = rand(g, pages_, 2, ps, d)[:, :1], rand(g, pages_, 2, ps, d)[:, 1:]
+    table = torch.randperm(pages_, generator=g, device="cuda").to(torch.int32)[:24].view(3, 8).repeat(1, 2)
+    table[:, 8:] = table[:, :2].repeat(1, 4)  # pages may be read by several sequences and twice by one
+    q = rand(g, sum(new), 4, d)
+    out, lse, st = run_chunk(H, q, K, V, table, new, lens, Hkv, out_dtype)
+    assert st == (0, 0)
+    check_chunk(q, K, V, table, new, lens, out, lse, Hkv)
+
+
 def test_chunk_contiguous_cache_of_any_length(H):
     """One page per sequence: the cache [batch, h_kv, n_cap, d] of the decode step, n_cap odd."""
     g = torch.Generator(device="cuda").manual_seed(22)
