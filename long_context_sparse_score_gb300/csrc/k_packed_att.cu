@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 }
             };
             Slot at{0, 0};  // the next K tile; its V follows
-            auto landed = [&](const Slot& x) { return (bool)__all_sync(0xffffffffu, mbar_try_wait(full((int)x.s), x.r)); };
+            auto landed = [&](const Slot& x) { return (bool)__all_sync(0xffffffffu, mbar_test_wait(full((int)x.s), x.r)); };
             auto wait_slot = [&](const Slot& x) { wait(full((int)x.s), x.r); };
 #pragma unroll 1
             while (next_segment(nseg, g)) {
