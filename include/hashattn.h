@@ -666,7 +666,8 @@ ha_status hash_attn_packed_workspace_size(const ha_tokens* tokens, size_t* bytes
  * h_q / h_kv <= 128. V must be finite within a sequence (a weight of 0 multiplies
  * tokens that a row does not see); what lies outside it does not matter.
  * Errors: HA_ERR_INVALID_ARG, HA_ERR_UNSUPPORTED (an HA_F32 q, K or V; more than
- * 128 query heads per KV head; strides that a tensor map cannot hold),
+ * 128 query heads per KV head; strides that a tensor map cannot hold; work of
+ * 2^32 tiles or more: beyond a prompt of two million tokens with 32 heads),
  * HA_ERR_WORKSPACE before launch; HA_ERR_CUDA on a failed launch.
  */
 ha_status hash_attn_prefill(const ha_tokens* tokens, const void* q, const void* K, const void* V, const int32_t* cu,

@@ -1583,6 +1583,11 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
     // parted, which saves the merge.
     const int64_t tiles = ceil_div(p.max_len, kt);
     const int64_t items = (ceil_div(t->total, 2 * L.tq) + t->n_seq) * t->h_kv;
+    // the kernel counts the work in 32 bits (a prompt's items see half of its tiles on average)
+    const int64_t work = items * ((c != nullptr ? tiles : (tiles + 1) / 2) + 4);
+    if (work >= (int64_t)1 << 32)
+        return fail(HA_ERR_UNSUPPORTED, "too much for one call: up to %lld items of up to %lld key tiles (2^32 tiles in all)",
+                    (long long)items, (long long)tiles);
     const int grid = (int)std::min<int64_t>(kSMs, items * tiles);
     p.split = tiles > kWholeTiles;
     HA_LAUNCH(launch_packed_att(p, m, t->d, f32, grid, grid > 1 && p.split, static_cast<cudaStream_t>(stream)),

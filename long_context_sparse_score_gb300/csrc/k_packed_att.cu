@@ -98,16 +98,19 @@ __device__ __forceinline__ SeqInfo seq_info(const PackedParams& p, int s, bool r
     return i;
 }
 
-// sum over i < n of floor((a i + b) / m), m <= 128, a <= 256
-__device__ __forceinline__ unsigned long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
-    unsigned long long ans = 0;
+// sum over i < n of floor((a i + b) / m), m <= 128, a <= 256 (the host sees to it that all
+// tiles together are below 2^32)
+__device__ __forceinline__ uint32_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+    uint32_t ans = 0;
+#pragma unroll 1
     while (n != 0) {
         if (a >= m) {
-            ans += ((unsigned long long)n * (n - 1) >> 1) * (a / m);
+            const uint32_t pairs = n & 1u ? n * ((n - 1u) >> 1) : (n >> 1) * (n - 1u);
+            ans += pairs * (a / m);
             a %= m;
         }
         if (b >= m) {
-            ans += (unsigned long long)n * (b / m);
+            ans += n * (b / m);
             b %= m;
         }
         const uint32_t y = a * n + b;
@@ -119,11 +122,6 @@ __device__ __forceinline__ unsigned long long floor_sum(uint32_t n, uint32_t m, 
         a = t;
     }
     return ans;
-}
-
-// a / b without the 64-bit division where a has 32 bits
-__device__ __forceinline__ unsigned long long div_short(unsigned long long a, unsigned b) {
-    return a >> 32 ? a / b : (unsigned long long)((unsigned)a / b);
 }
 
 // Keys that the first `upto` new tokens of the sequence see.
@@ -140,11 +138,12 @@ __device__ __forceinline__ int key_tiles(int keys) {
 // Cost of the items 0 .. qt - 1 of one head, qt < the number of items: their tiles
 // (an item without keys counts one, so that its rows are written) and kItemCost each.
 template <int KT>
-__device__ unsigned long long cost_before(const SeqInfo& i, int t2, int qt) {
+__device__ __forceinline__ uint32_t cost_before(const SeqInfo& i, int t2, int qt) {
+    if (qt == 0) return 0;
     const int base = i.nk - i.nq;
     int z = 0;  // items that see no key
     if (base < 0) z = min(qt, (-base) / t2);
-    unsigned long long c = (unsigned long long)(unsigned)z + (unsigned long long)(unsigned)qt * kItemCost;
+    uint32_t c = (uint32_t)z + (uint32_t)qt * kItemCost;
     if (qt > z) c += floor_sum((uint32_t)(qt - z), KT, (uint32_t)t2, (uint32_t)(base + (z + 1) * t2 + KT - 1));
     return c;
 }
@@ -155,7 +154,7 @@ __device__ __forceinline__ int item_tiles(const SeqInfo& i, int t2, int qt) {
 }
 
 template <int KT>
-__device__ __forceinline__ unsigned long long head_cost(const SeqInfo& i, int t2) {
+__device__ __forceinline__ uint32_t head_cost(const SeqInfo& i, int t2) {
     if (i.nq == 0) return 0;
     const int last = (i.nq + t2 - 1) / t2 - 1;
     return cost_before<KT>(i, t2, last) + (unsigned)(item_tiles<KT>(i, t2, last) + kItemCost);
@@ -163,7 +162,7 @@ __device__ __forceinline__ unsigned long long head_cost(const SeqInfo& i, int t2
 
 // A place in the order of all work: tile j of item (s, head, qt), after w units.
 struct Place {
-    unsigned long long w;
+    uint32_t w;
     int s, head, qt, j;
 };
 
@@ -443,38 +442,38 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             // Sequences are taken 32 at a time, one to a lane; the first 32 stay in registers.
             SeqInfo mine0{0, 0, 0}, i{0, 0, 0};
             auto load = [&](int s, bool report) { return s < p.n_seq ? seq_info(p, s, report) : SeqInfo{0, 0, 0}; };
-            auto cost = [&](const SeqInfo& i) { return (unsigned long long)p.Hkv * head_cost<KT>(i, t2); };
+            auto cost = [&](const SeqInfo& i) { return (uint32_t)p.Hkv * head_cost<KT>(i, t2); };
             auto info_of = [&](int s) {
                 if (s >= 32) return seq_info(p, s, false);
                 return SeqInfo{__shfl_sync(0xffffffffu, mine0.q0, s), __shfl_sync(0xffffffffu, mine0.nq, s),
                                __shfl_sync(0xffffffffu, mine0.nk, s)};
             };
-            unsigned long long U = 0, cost0 = 0;
+            uint32_t U = 0, cost0 = 0;
 #pragma unroll 1
             for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
                 i = load(s0 + lane, blockIdx.x == 0);
-                const unsigned long long c = cost(i);
+                const uint32_t c = cost(i);
                 if (s0 == 0) {
                     mine0 = i;
                     cost0 = c;
                 }
                 U += c;
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) U += __shfl_xor_sync(0xffffffffu, U, o);
+            U = __reduce_add_sync(0xffffffffu, U);
             // CTAs that work: as many as there are spans of kMinSpan tiles
-            const unsigned long long most = div_short(U, kMinSpan + kItemCost);
-            const unsigned P = most < gridDim.x ? (most > 0 ? (unsigned)most : 1u) : gridDim.x;
+            const uint32_t P = min(max(U / (kMinSpan + kItemCost), 1u), gridDim.x);
+            const uint32_t span = U / P, over = U - span * P;  // boundary c: c U / P
+            auto boundary = [&](uint32_t c) { return span * c + over * c / P; };
             // a boundary close to an item's edge moves to it: within an eighth of a span, and
             // within what parting the item would cost (always, where items are not parted)
-            const unsigned long long tol = p.split ? min(div_short(U, 8 * P), (unsigned long long)kSplitCost) : U;
+            const uint32_t tol = p.split ? min(span / 8, (uint32_t)kSplitCost) : U;
             if (lane == 0) p.items[blockIdx.x].parts = 0;
             // the place of boundary c
-            auto place = [&](unsigned c) {
+            auto place = [&](uint32_t c) {
                 Place a{U, 0, 0, 0, 0};
-                const unsigned long long b = c >= P ? U : div_short(U * c, P);
-                if (b == U) return a;
-                unsigned long long before = 0, incl = 0, mine = 0;
+                if (c >= P || U == 0) return a;
+                const uint32_t b = boundary(c);
+                uint32_t before = 0, incl = 0, mine = 0;
                 int s0 = 0;
 #pragma unroll 1
                 for (;; s0 += 32) {
@@ -482,20 +481,22 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     incl = mine;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
-                        const unsigned long long v = __shfl_up_sync(0xffffffffu, incl, o);
+                        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
                         if (lane >= o) incl += v;
                     }
-                    const unsigned long long all = __shfl_sync(0xffffffffu, incl, 31);
+                    const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
                     if (b < before + all) break;
                     before += all;
                 }
                 const int at = __ffs((int)__ballot_sync(0xffffffffu, b < before + incl)) - 1;
-                unsigned long long rem = b - before - __shfl_sync(0xffffffffu, incl - mine, at);
-                const unsigned long long uh = div_short(__shfl_sync(0xffffffffu, mine, at), (unsigned)p.Hkv);
+                uint32_t rem = b - before - __shfl_sync(0xffffffffu, incl - mine, at);
                 a.s = s0 + at;
+                a.w = b;
+                if (rem == 0) return a;  // where a sequence begins
+                const uint32_t uh = __shfl_sync(0xffffffffu, mine, at) / (uint32_t)p.Hkv;
                 const SeqInfo i = info_of(a.s);
-                a.head = (int)(uh >> 32 ? rem / uh : div_short(rem, (unsigned)uh));
-                rem -= uh * a.head;
+                a.head = (int)(rem / uh);
+                rem -= uh * (uint32_t)a.head;
                 int lo = 0, hi = (i.nq + t2 - 1) / t2 - 1;  // the last item that begins at or before rem
 #pragma unroll 1
                 while (lo < hi) {
@@ -503,10 +504,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     if (cost_before<KT>(i, t2, mid) <= rem) lo = mid;
                     else hi = mid - 1;
                 }
-                const unsigned long long off = rem - cost_before<KT>(i, t2, lo);
+                const uint32_t off = rem - cost_before<KT>(i, t2, lo);
                 const int tiles = item_tiles<KT>(i, t2, lo);
-                const unsigned long long to_end = (unsigned long long)(tiles + kItemCost) - off;
-                a.w = b;
+                const uint32_t to_end = (uint32_t)(tiles + kItemCost) - off;
                 a.qt = lo;
                 a.j = (int)off - kItemCost;
                 if (off <= kItemCost || (off <= tol && off <= to_end)) {
@@ -519,8 +519,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 return a;
             };
             const Place first_place = place(blockIdx.x);
-            const unsigned long long w1 = first_place.w < U ? place(blockIdx.x + 1).w : U;
-            unsigned long long left = w1 - first_place.w;
+            const uint32_t w1 = first_place.w < U ? place(blockIdx.x + 1).w : U;
+            uint32_t left = w1 - first_place.w;
             int s = first_place.s, head = first_place.head, qt = first_place.qt, j = first_place.j;
             int nqt = 0, n = 0;
             if (left > 0) {
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 if (more) {
                     const int len = item_tiles<KT>(i, t2, qt);
                     if (j < len) {
-                        const unsigned long long rest = (unsigned long long)(len - j + (j == 0 ? kItemCost : 0));
+                        const uint32_t rest = (uint32_t)(len - j + (j == 0 ? kItemCost : 0));
                         const int je = rest <= left ? len : j + (int)left - (j == 0 ? kItemCost : 0);
                         left -= rest <= left ? rest : left;
                         o.jb = j;
@@ -555,9 +555,13 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         o.begins = j == 0;
                         // the item begins here and goes on in the next CTAs: what the merge needs
                         if (j == 0 && je < len && lane == 0) {
-                            const unsigned long long last = (w1 + (unsigned long long)(len - je) - tol) * P;
+                            // it ends at the first boundary that has reached it (within tol)
+                            const uint32_t last = w1 + (uint32_t)(len - je) - tol;
+                            uint32_t stop = min((uint32_t)((float)last / (float)U * (float)P), P);  // off by one at most
+                            while (stop > 0 && (stop == P ? U : boundary(stop)) >= last) --stop;
+                            while (stop < P && boundary(stop) < last) ++stop;
                             SplitItem d;
-                            d.parts = (int)(U >> 32 ? (last + U - 1) / U : div_short(last + U - 1, (unsigned)U)) - (int)blockIdx.x;  // to the boundary at which it has ended
+                            d.parts = (int)(stop - blockIdx.x);
                             d.row0 = o.row0;
                             d.head = head;
                             d.tokens = spread ? -o.tokens : o.tokens;
