@@ -1515,10 +1515,19 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
 
     const bool f32 = t->out_dtype == HA_F32;
     const int kt = packed_key_tile(f32);
+    const int max_len = c != nullptr ? c->max_pages * c->page_size : t->total;
+    const int64_t tiles = ceil_div(max_len, kt);
+    const int64_t items = (ceil_div(t->total, 2 * L.tq) + t->n_seq) * t->h_kv;
+    // the kernel counts the work in 32 bits (a prompt's items see half of its tiles on average)
+    const int64_t work = items * ((c != nullptr ? tiles : (tiles + 1) / 2) + 4);
+    if (work >= (int64_t)1 << 32)
+        return fail(HA_ERR_UNSUPPORTED, "too much for one call: up to %lld items of up to %lld key tiles (2^32 tiles in all)",
+                    (long long)items, (long long)tiles);
     PackedParams p{};
     p.cu = cu;
     p.n_seq = t->n_seq;
     p.total = t->total;
+    p.max_len = max_len;
     p.Hq = t->h_q;
     p.Hkv = t->h_kv;
     p.G = G;
@@ -1546,7 +1555,6 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
         p.table_st = c->table_st;
         p.page_size = c->page_size;
         p.n_pages = c->n_pages;
-        p.max_len = c->max_pages * c->page_size;
         if (c->max_pages > 1 && (c->page_size & -c->page_size) < box) box = c->page_size & -c->page_size;
         // strides of an extent of 1 say nothing
         auto folds = [&](int64_t outer, int64_t n_outer, int64_t inner, int64_t n_inner) {
@@ -1572,7 +1580,6 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
                  encode_map(&m.v, V, t->d, {c->page_size, t->h_kv, c->n_pages}, {c->v_sn, c->v_sh, c->v_sp}, box, 1);
         }
     } else {
-        p.max_len = t->total;
         ok = ok && encode_map(&m.k, K, t->d, {t->total, t->h_kv, 1}, {t->k_st, t->k_sh, 0}, box, 1) &&
              encode_map(&m.v, V, t->d, {t->total, t->h_kv, 1}, {t->v_st, t->v_sh, 0}, box, 1);
     }
@@ -1581,13 +1588,6 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
     while ((1 << p.box_log2) < box) ++p.box_log2;
     // No more CTAs than the lengths can fill with a tile each. Items of a few tiles are not
     // parted, which saves the merge.
-    const int64_t tiles = ceil_div(p.max_len, kt);
-    const int64_t items = (ceil_div(t->total, 2 * L.tq) + t->n_seq) * t->h_kv;
-    // the kernel counts the work in 32 bits (a prompt's items see half of its tiles on average)
-    const int64_t work = items * ((c != nullptr ? tiles : (tiles + 1) / 2) + 4);
-    if (work >= (int64_t)1 << 32)
-        return fail(HA_ERR_UNSUPPORTED, "too much for one call: up to %lld items of up to %lld key tiles (2^32 tiles in all)",
-                    (long long)items, (long long)tiles);
     const int grid = (int)std::min<int64_t>(kSMs, items * tiles);
     p.split = tiles > kWholeTiles;
     HA_LAUNCH(launch_packed_att(p, m, t->d, f32, grid, grid > 1 && p.split, static_cast<cudaStream_t>(stream)),

@@ -276,6 +276,20 @@ def _here(*tensors) -> list:
     return out
 
 
+_ITEM = (4, 2)  # bytes of an HA_F32, an HA_BF16
+
+
+def _whole(t, n: int, item: int, what: str) -> None:
+    """A contiguous tensor of n elements (raw addresses are the caller's word)."""
+    if t is not None and t.__class__ is not int and (t.numel() != n or t.element_size() != item or not t.is_contiguous()):
+        raise ValueError(f"{what} must be contiguous, with {n} elements of {item} bytes")
+
+
+def _int32s(t, n: int, what: str) -> None:
+    if t is not None and t.__class__ is not int and (t.element_size() != 4 or t.numel() < n or not t.is_contiguous()):
+        raise ValueError(f"{what} must be contiguous int32 with at least {n} elements")
+
+
 def _dtype_code(t) -> int:
     import torch
     if t.dtype == torch.float32:
@@ -583,6 +597,10 @@ def hash_attn_append(tokens, cache, q, k, v, page_table, cu, seq_lens, q_out, K,
                      dev_flags=None, stream=None) -> None:
     """Rotate the packed new tokens' q (into ``q_out``) and k by position and write k, v
     (and with ``W`` the keys' codes) into the paged cache; ``q`` and ``q_out`` may be None."""
+    _whole(q_out, tokens.total * tokens.h_q * tokens.d, _ITEM[tokens.dtype], "q_out")
+    _whole(W, tokens.h_kv * 32 * tokens.d, 4, "W")
+    _int32s(cu, tokens.n_seq + 1, "cu")
+    _int32s(seq_lens, tokens.n_seq, "seq_lens")
     a = _here(q, k, v, W, page_table, cu, seq_lens, q_out, K, V, k_sig, dev_flags)
     _check(lib().hash_attn_append(ctypes.byref(tokens), ctypes.byref(cache), None if rope is None else ctypes.byref(rope),
                                   *a, _stream(stream)))
@@ -596,12 +614,21 @@ def hash_attn_packed_workspace_size(tokens) -> int:
 
 def hash_attn_prefill(tokens, q, K, V, cu, out, lse, *, workspace, stream=None) -> None:
     """Causal attention over packed prompts; out [total, Hq, d], lse [total, Hq] contiguous."""
+    rows = tokens.total * tokens.h_q
+    _whole(out, rows * tokens.d, _ITEM[tokens.out_dtype], "out")
+    _whole(lse, rows, 4, "lse")
+    _int32s(cu, tokens.n_seq + 1, "cu")
     a = _here(q, K, V, cu, out, lse, workspace)
     _check(lib().hash_attn_prefill(ctypes.byref(tokens), *a, workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def hash_attn_chunk(tokens, cache, q, K, V, page_table, cu, seq_lens, out, lse, *, workspace, stream=None) -> None:
     """Attention of the packed new tokens over the paged cache (their keys are in it already)."""
+    rows = tokens.total * tokens.h_q
+    _whole(out, rows * tokens.d, _ITEM[tokens.out_dtype], "out")
+    _whole(lse, rows, 4, "lse")
+    _int32s(cu, tokens.n_seq + 1, "cu")
+    _int32s(seq_lens, tokens.n_seq, "seq_lens")
     a = _here(q, K, V, page_table, cu, seq_lens, out, lse, workspace)
     _check(lib().hash_attn_chunk(ctypes.byref(tokens), ctypes.byref(cache), *a,
                                  workspace.numel() * workspace.element_size(), _stream(stream)))

@@ -371,6 +371,108 @@ def test_large_pool_offsets(H):
     check_prefill(q, k, v, [130], out, lse, heads=[0, 7])
 
 
+def reference(q, keys, values, new, lens):
+    """Float64 on the GPU: out, lse, and what check_rows measures errors by, over all rows."""
+    T, Hq, d = q.shape
+    out, mag = torch.zeros(T, Hq, d, dtype=torch.float64, device="cuda"), torch.zeros(T, Hq, d, dtype=torch.float64, device="cuda")
+    lse = torch.full((T, Hq), -math.inf, dtype=torch.float64, device="cuda")
+    zmax = torch.zeros(T, Hq, dtype=torch.float64, device="cuda")
+    a = 0
+    for s, (nq, nk) in enumerate(zip(new, lens)):
+        if nq and nk:
+            K, V = keys(s).double(), values(s).double()  # [nk, Hkv, d]
+            x = q[a:a + nq].double().view(nq, K.shape[1], -1, d)
+            z = torch.einsum("ihgd,jhd->ihgj", x, K) / math.sqrt(d)
+            sees = torch.arange(nk, device="cuda") <= nk - nq + torch.arange(nq, device="cuda")[:, None]
+            z.masked_fill_(~sees[:, None, None], -math.inf)
+            l = torch.logsumexp(z, -1)
+            w = torch.exp(z - l.clamp(min=-1e300)[..., None])
+            out[a:a + nq] = torch.einsum("ihgj,jhd->ihgd", w, V).reshape(nq, Hq, d)
+            mag[a:a + nq] = torch.einsum("ihgj,jhd->ihgd", w, V.abs()).reshape(nq, Hq, d)
+            lse[a:a + nq] = l.reshape(nq, Hq)
+            zmax[a:a + nq] = (torch.einsum("ihgd,jhd->ihgj", x.abs(), K.abs()).amax(-1) / math.sqrt(d)).reshape(nq, Hq)
+        a += nq
+    flat = lambda t: t.reshape(-1, *t.shape[2:]).cpu().numpy()  # noqa: E731
+    return flat(out), flat(lse), flat(mag), flat(zmax), max(lens)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_shapes(H, seed):
+    """Seeded shapes over the whole range: heads, groups, dims, lengths, pages, both output types."""
+    import random
+    r = random.Random(1000 + seed)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    Hkv, G, d = r.choice([1, 2, 3, 5, 8]), r.choice([1, 2, 3, 4, 5, 6, 7, 8, 12, 16, 33, 64]), r.choice([64, 128])
+    n = r.choice([1, 2, 5, 17, 40])
+    most = r.choice([1, 4, 60, 400])
+    new = [r.randint(0, most) for _ in range(n)]
+    new[0] = max(1, new[0])
+    out_dtype = r.choice([torch.bfloat16, torch.float32])
+    q = rand(g, sum(new), Hkv * G, d)
+    if seed % 3 == 0:
+        k, v = rand(g, sum(new), Hkv, d), rand(g, sum(new), Hkv, d)
+        out, lse, st = run_prefill(H, q, k, v, new, out_dtype)
+        at = np.concatenate([[0], np.cumsum(new)])
+        ref = reference(q, lambda s: k[at[s]:at[s + 1]], lambda s: v[at[s]:at[s + 1]], new, new)
+    else:
+        lens = [max(0, a + r.randint(-3, r.choice([5, 900, 5000]))) for a in new]
+        K, V, table = pages(g, lens, ps := r.choice([16, 32, 48, 112, 256]), Hkv, d, r.choice(["token", "head"]))
+        out, lse, st = run_chunk(H, q, K, V, table, new, lens, Hkv, out_dtype)
+
+        def rows(X, s):
+            j = torch.arange(lens[s], device="cuda")
+            return X[table[s].long()[j // ps], :, j % ps]
+        ref = reference(q, lambda s: rows(K, s), lambda s: rows(V, s), new, lens)
+    assert st == (0, 0)
+    check_rows(out.flatten(0, 1), lse.flatten(), ref, out_dtype == torch.bfloat16, f"seed {seed}")
+
+
+@pytest.mark.parametrize("n", [33, 700, 2500])
+def test_many_sequences(H, n):
+    """More sequences than a warp, or than CTAs; some of them empty."""
+    g = torch.Generator(device="cuda").manual_seed(28)
+    rng = np.random.default_rng(n)
+    Hq, Hkv, d, ps = 4, 2, 64, 16
+    new = [int(x) for x in rng.choice([0, 1, 1, 1, 2], n)]
+    lens = [a + int(x) for a, x in zip(new, rng.integers(0, 60, n))]
+    K, V, table = pages(g, lens, ps, Hkv, d)
+    q = rand(g, sum(new), Hq, d)
+    out, lse, st = run_chunk(H, q, K, V, table, new, lens, Hkv)
+    assert st == (0, 0)
+
+    def rows(X, s):
+        j = torch.arange(lens[s], device="cuda")
+        return X[table[s].long()[j // ps], :, j % ps]
+    ref = reference(q, lambda s: rows(K, s), lambda s: rows(V, s), new, lens)
+    check_rows(out.flatten(0, 1), lse.flatten(), ref, True, f"{n} sequences")
+
+
+def test_two_streams_with_their_own_workspaces(H):
+    """Two calls at once."""
+    g = torch.Generator(device="cuda").manual_seed(29)
+    lens, new, Hkv, d = [3000, 2000], [1, 90], 2, 128
+    K, V, table = pages(g, lens, 64, Hkv, d)
+    q = rand(g, sum(new), 8, d)
+    want = run_chunk(H, q, K, V, table, new, lens, Hkv)[:2]
+    tok, cache = H.make_tokens(q, None, None, 2, h_kv=Hkv, out_dtype=torch.bfloat16), H.make_cache(K, V, table)
+    cu, lt = cumulative(new), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = []
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            ws = torch.zeros(H.hash_attn_packed_workspace_size(tok), dtype=torch.uint8, device="cuda")
+            outs = [(torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")) for _ in range(5)]
+            got.append((outs, ws))
+    for i in range(5):
+        for st, (outs, ws) in zip(streams, got):
+            H.hash_attn_chunk(tok, cache, q, K, V, table, cu, lt, *outs[i], workspace=ws, stream=st)
+    torch.cuda.synchronize()
+    for outs, _ in got:
+        for o, l in outs:
+            assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+
+
 # ---------------------------------------------------------------- append
 
 def inv_freq(rot, base=500000.0):

@@ -81,6 +81,11 @@ def test_prefill_and_chunk_refusals(ha):
         assert call(ws=None) == ha.HA_ERR_WORKSPACE
         assert call(ws=1024 + 16) == ha.HA_ERR_WORKSPACE
         assert call(ws_bytes=4096) == ha.HA_ERR_WORKSPACE
+    # more tiles than the kernel counts (a prompt of 16 M tokens; 2^20 sequences of 2^30 keys)
+    big = _tokens(ha, n_seq=1, total=1 << 24)
+    assert _prefill(ha, big) == ha.HA_ERR_UNSUPPORTED and "too much" in ha.last_error()
+    many = _cache(ha, page_size=1 << 10, max_pages=1 << 20, table_st=1 << 20)
+    assert _chunk(ha, _tokens(ha, n_seq=1 << 20, total=1 << 20), many) == ha.HA_ERR_UNSUPPORTED and "too much" in ha.last_error()
     assert _prefill(ha, None) == ha.HA_ERR_INVALID_ARG
     assert _prefill(ha, _tokens(ha, k_sh=100)) == ha.HA_ERR_INVALID_ARG
     assert _prefill(ha, _tokens(ha, total=0)) == ha.HA_OK                           # nothing to do
@@ -150,11 +155,39 @@ def test_binding_refuses_tensors_elsewhere(ha, monkeypatch):
     q, k = torch.zeros(5, 4, 64, dtype=torch.bfloat16), torch.zeros(5, 2, 64, dtype=torch.bfloat16)
     pool, table = torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16), torch.zeros(2, 4, dtype=torch.int32)
     t, c, i, f = ha.make_tokens(q, k, k, 2), ha.make_cache(pool, pool, table), torch.zeros(3, dtype=torch.int32), torch.zeros(5, 4)
+    out = torch.zeros(5, 4, 64)
     for call in (lambda: ha.hash_attn_append(t, c, q, k, k, table, i, i, q, pool, pool, stream=0),
-                 lambda: ha.hash_attn_prefill(t, q, k, k, i, f, f, workspace=f, stream=0),
-                 lambda: ha.hash_attn_chunk(t, c, q, pool, pool, table, i, i, f, f, workspace=f, stream=0)):
+                 lambda: ha.hash_attn_prefill(t, q, k, k, i, out, f, workspace=f, stream=0),
+                 lambda: ha.hash_attn_chunk(t, c, q, pool, pool, table, i, i, out, f, workspace=f, stream=0)):
         with pytest.raises(ValueError, match="current CUDA device"):
             call()
+
+
+def test_binding_refuses_outputs_that_do_not_fit(ha):
+    """Wrong size, type or strides of what a call writes (or of its bounds) would go past the end."""
+    import torch
+    q, k = torch.zeros(5, 4, 64, dtype=torch.bfloat16), torch.zeros(5, 2, 64, dtype=torch.bfloat16)
+    pool, table = torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16), torch.zeros(2, 4, dtype=torch.int32)
+    t, c = ha.make_tokens(q, k, k, 2), ha.make_cache(pool, pool, table)
+    cu, lens, out, lse = torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(5, 4, 64), torch.zeros(5, 4)
+
+    def prefill(cu=cu, out=out, lse=lse):
+        ha.hash_attn_prefill(t, q, k, k, cu, out, lse, workspace=lse, stream=0)
+
+    def chunk(cu=cu, lens=lens, out=out, lse=lse):
+        ha.hash_attn_chunk(t, c, q, pool, pool, table, cu, lens, out, lse, workspace=lse, stream=0)
+
+    def append(cu=cu, lens=lens, q_out=q, W=None):
+        ha.hash_attn_append(t, c, q, k, k, table, cu, lens, q_out, pool, pool, W=W, stream=0)
+
+    bad_out = [out[:4], out.bfloat16(), torch.zeros(5, 4, 128)[..., :64]]
+    for call, bad in [(prefill, dict(out=bad_out, lse=[lse[1:], lse.half()], cu=[cu[:2], cu.long()])),
+                      (chunk, dict(out=bad_out, lse=[lse[1:]], cu=[cu[:2]], lens=[lens[:1], lens.long()])),
+                      (append, dict(q_out=[q[:4], q.float()], cu=[cu[:2]], lens=[lens.long()], W=[torch.zeros(2, 32, 32)]))]:
+        for name, values in bad.items():
+            for v in values:
+                with pytest.raises(ValueError, match="must be contiguous"):
+                    call(**{name: v})
 
 
 # ---------------------------------------------------------------- the oracle
