@@ -660,6 +660,7 @@ ha_status hash_attn_packed_workspace_size(const ha_tokens* tokens, size_t* bytes
  *   q, K, V    packed (ha_tokens), HA_BF16
  *   cu         int32 [n_seq + 1] (device), 0 <= cu[s] <= cu[s + 1] <= total; a
  *              sequence that breaks this is skipped and flagged HA_DEVERR_SEQLEN
+ *              (all are, where the others then overlap: more than total rows)
  *   out        contiguous [total, h_q, d] of out_dtype, 16-byte aligned
  *   lse        float32 [total, h_q] (natural log)
  *   workspace  >= hash_attn_packed_workspace_size bytes, 256-byte aligned

@@ -1519,7 +1519,7 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
     const int64_t tiles = ceil_div(max_len, kt);
     const int64_t items = (ceil_div(t->total, 2 * L.tq) + t->n_seq) * t->h_kv;
     // the kernel counts the work in 32 bits (a prompt's items see half of its tiles on average)
-    const int64_t work = items * ((c != nullptr ? tiles : (tiles + 1) / 2) + 4);
+    const int64_t work = items * ((c != nullptr ? tiles : tiles / 2) + 8);
     if (work >= (int64_t)1 << 32)
         return fail(HA_ERR_UNSUPPORTED, "too much for one call: up to %lld items of up to %lld key tiles (2^32 tiles in all)",
                     (long long)items, (long long)tiles);
@@ -1562,6 +1562,7 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
         };
         auto fold_of = [&](int64_t sp, int64_t sh, int64_t sn) {
             if (t->d != 128 || c->page_size % 8 != 0) return 0;
+            if (((int64_t)c->n_pages + 1) * std::max(c->page_size, t->h_kv) > INT32_MAX) return 0;  // coordinates are 32 bits
             if (folds(sp, c->n_pages, sn, c->page_size)) return 1;
             return t->h_kv == 1 || folds(sp, c->n_pages, sh, t->h_kv) ? 2 : 0;
         };

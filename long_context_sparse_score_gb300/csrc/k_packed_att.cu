@@ -449,6 +449,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                                __shfl_sync(0xffffffffu, mine0.nk, s)};
             };
             uint32_t U = 0, cost0 = 0;
+            int rows = 0;  // of this lane's sequences, as far as it matters
 #pragma unroll 1
             for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
                 i = load(s0 + lane, blockIdx.x == 0);
@@ -458,8 +459,12 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     cost0 = c;
                 }
                 U += c;
+                rows = min(rows + i.nq, 1 << 25);
             }
             U = __reduce_add_sync(0xffffffffu, U);
+            // Bounds that go back (flagged above) can make the others overlap. Their work may
+            // not be what the host has bounded, so nothing is done then.
+            if (__reduce_add_sync(0xffffffffu, rows) > p.total) U = 0;
             // CTAs that work: as many as there are spans of kMinSpan tiles
             const uint32_t P = min(max(U / (kMinSpan + kItemCost), 1u), gridDim.x);
             const uint32_t span = U / P, over = U - span * P;  // boundary c: c U / P

@@ -473,6 +473,21 @@ def test_two_streams_with_their_own_workspaces(H):
             assert torch.equal(o, want[0]) and torch.equal(l, want[1])
 
 
+@pytest.mark.parametrize("n", [8, 1100])
+def test_bounds_that_go_back_and_forth(H, n):
+    """Every other sequence covers all rows: more work than the call can have, and than 32 bits count."""
+    g = torch.Generator(device="cuda").manual_seed(30)
+    total = 65536 if n > 8 else 300
+    q, k = rand(g, total, 128, 64), rand(g, total, 8, 64)
+    cu = torch.tensor([0, total] * (n // 2) + [0], dtype=torch.int32, device="cuda")
+    tok = H.make_tokens(q, k, k, n, out_dtype=torch.bfloat16)
+    out, lse = torch.full_like(q, 7.0), torch.full((total, 128), 7.0, device="cuda")
+    ws = torch.zeros(H.hash_attn_packed_workspace_size(tok), dtype=torch.uint8, device="cuda")
+    H.hash_attn_prefill(tok, q, k, k, cu, out, lse, workspace=ws, stream=torch.cuda.current_stream())
+    assert H.hash_attn_device_status(ws, torch.cuda.current_stream()) == (H.HA_ERR_DEVICE, H.HA_DEVERR_SEQLEN)
+    assert bool((out == 7).all()) and bool((lse == 7).all())
+
+
 # ---------------------------------------------------------------- append
 
 def inv_freq(rot, base=500000.0):
