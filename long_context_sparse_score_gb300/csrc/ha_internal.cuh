@@ -334,6 +334,7 @@ struct AppendParams {
     const int32_t* seq_lens;
     const int32_t* table;
     int64_t table_st;
+    float seqs_per_row;  // n_seq / total
     int n_seq, total, Hq, Hkv, d;
     int page_size, n_pages, max_len;
     const float* inv_freq;     // null: no rotation
