@@ -50,7 +50,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 9, kQWarp = 10, kPlanWarp = 11;
 // Registers of a softmax thread and of the others: 256 x 216 + 128 x 72 is what 384
 // threads are launched with (168 each).
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
-constexpr int kMinSpan = 1;           // fewest tiles of a CTA
+constexpr int kMinSpan = 2;           // least work of a CTA (a token over 700 keys, 2 KV heads: 14.8 us; with 3: 16.1)
 constexpr uint32_t kTmemCols = 512;   // S0, S1 (128 each; P overlays them), O0, O1
 constexpr int kItemCost = 2;           // tiles that an item's start and end cost beside its own
 constexpr int kSplitCost = 4;          // tiles that writing a part of an item and joining it cost
@@ -465,8 +465,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             // Bounds that go back (flagged above) can make the others overlap. Their work may
             // not be what the host has bounded, so nothing is done then.
             if (__reduce_add_sync(0xffffffffu, rows) > p.total) U = 0;
-            // CTAs that work: as many as there are spans of kMinSpan tiles
-            const uint32_t P = min(max(U / (kMinSpan + kItemCost), 1u), gridDim.x);
+            // CTAs that work: as many as there are spans of kMinSpan
+            const uint32_t P = min(max(U / kMinSpan, 1u), gridDim.x);
             const uint32_t span = U / P, over = U - span * P;  // boundary c: c U / P
             auto boundary = [&](uint32_t c) { return span * c + over * c / P; };
             // a boundary close to an item's edge moves to it: within an eighth of a span, and
@@ -1196,16 +1196,38 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 }
 
 // Joins the parts of every item that spans CTAs, in order: grid (CTA in which an item
-// may begin, slices of its rows). Latency is all it costs, so loads of several parts
-// and rows are in flight: a warp takes a row and four parts at a time; where each warp
-// of a stream left parts (32 rows at most, up to 600 parts), a CTA takes a row and its
-// eight warps share the parts.
+// may begin, slices of its rows), one pass with a running maximum. Latency is most of what
+// it costs, so loads of several parts and rows are in flight: a warp takes two rows and four
+// parts at a time; where each warp of a stream left parts (32 rows at most, up to 600
+// parts), a CTA takes a row and its eight warps share the parts.
 constexpr int kMergeSlices = 16;
+template <int D>
+struct Joined {
+    static constexpr int E = D / 32;
+    float m = -INFINITY, l = 0.f, acc[E] = {};
+    // n <= 4 parts more: their (m, l), and this lane's columns of their O
+    __device__ __forceinline__ void add(const float2 (&ml)[4], const float (&v)[4][E], float qscale) {
+        const float mx = fmaxf(fmaxf(fmaxf(m, ml[0].x), fmaxf(ml[1].x, ml[2].x)), ml[3].x);
+        const float ms = mx == -INFINITY ? 0.f : mx, a = ex2((m - ms) * qscale);
+        m = mx;
+        l *= a;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= a;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float w = ex2((ml[u].x - ms) * qscale);  // 0 behind the last part
+            l = fmaf(ml[u].y, w, l);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(v[u][e], w, acc[e]);
+        }
+    }
+};
+
 template <int D, bool F32OUT>
 __global__ void __launch_bounds__(256) k_packed_merge(const PackedParams p) {
     constexpr int E = D / 32;
     __shared__ float s_acc[8][D];
-    __shared__ float s_l[8];
+    __shared__ float2 s_ml[8];
     pdl_launch_dependents();
     pdl_wait();
     const SplitItem d = p.items[blockIdx.x];
@@ -1214,31 +1236,22 @@ __global__ void __launch_bounds__(256) k_packed_merge(const PackedParams p) {
     const bool spread = d.tokens < 0;
     const int tokens = spread ? -d.tokens : d.tokens, rows = tokens * p.G, parts = spread ? 4 * d.parts : d.parts;
     const bool two = tokens > p.TQ;
-    const int first = spread ? blockIdx.y : blockIdx.y * 8 + warp, step = spread ? kMergeSlices : kMergeSlices * 8;
-    for (int i = first; i < rows; i += step) {
-        const int tok = i / p.G, h = i - tok * p.G;
-        const int row = two && tok >= p.TQ ? 128 + (tok - p.TQ) * p.G + h : i;
-        auto at = [&](int k) {
-            const int c = spread ? k >> 2 : k;
-            return (int64_t)(2 * (blockIdx.x + c) + (c == 0 ? 1 : 0)) * p.slot_rows + row + (spread ? (k & 3) * 32 : 0);
-        };
-        float m = -INFINITY;
-        for (int k = lane; k < parts; k += 32) m = fmaxf(m, p.part_ml[at(k)].x);
+    // row i of the item in part k
+    auto at = [&](int i, int k) {
+        const int tok = i / p.G, row = two && tok >= p.TQ ? 128 + i - p.TQ * p.G : i, c = spread ? k >> 2 : k;
+        return (int64_t)(2 * (blockIdx.x + c) + (c == 0 ? 1 : 0)) * p.slot_rows + row + (spread ? (k & 3) * 32 : 0);
+    };
+    // parts k, k + ks, .. of row i (n of the four there are)
+    auto fetch = [&](int i, int k, int ks, float2 (&ml)[4], float (&v)[4][E]) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float ms = m == -INFINITY ? 0.f : m;
-        float l = 0.f, acc[E];
+        for (int u = 0; u < 4; ++u) {
+            const bool in = k + u * ks < parts;
+            ml[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        const int k0 = spread ? warp : 0, ks = spread ? 8 : 1;
-        for (int k = k0; k < parts; k += 4 * ks) {
-            float2 ml[4];
-            float v[4][E];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const bool in = k + u * ks < parts;
-                const int64_t a = at(in ? k + u * ks : k0);
-                ml[u] = in ? p.part_ml[a] : make_float2(-INFINITY, 0.f);
+            for (int e = 0; e < E; ++e) v[u][e] = 0.f;
+            if (in) {
+                const int64_t a = at(i, k + u * ks);
+                ml[u] = p.part_ml[a];
                 const float* o = p.part_o + a * D + lane * E;
                 if constexpr (E == 4) {
                     const float4 f = *reinterpret_cast<const float4*>(o);
@@ -1248,45 +1261,70 @@ __global__ void __launch_bounds__(256) k_packed_merge(const PackedParams p) {
                     v[u][0] = f.x, v[u][1] = f.y;
                 }
             }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float w = ex2((ml[u].x - ms) * p.qscale);  // 0 behind the last part
-                l = fmaf(ml[u].y, w, l);
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = fmaf(v[u][e], w, acc[e]);
-            }
         }
-        if (spread) {
+    };
+    auto finish = [&](int i, const Joined<D>& x) {
+        const int tok = i / p.G, h = i - tok * p.G;
+        const float inv = x.l > 0.f ? 1.f / x.l : (x.l == 0.f ? 0.f : x.l);
+        const int64_t orow = (int64_t)(d.row0 + tok) * p.Hq + d.head * p.G + h;
+        if (F32OUT) {
+            float* o = reinterpret_cast<float*>(p.out) + orow * D + lane * E;
 #pragma unroll
-            for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
-            if (lane == 0) s_l[warp] = l;
+            for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(o + e) = make_float2(x.acc[e] * inv, x.acc[e + 1] * inv);
+        } else {
+            uint32_t* o = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * D + lane * E);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) o[e / 2] = pack_bf16(x.acc[e] * inv, x.acc[e + 1] * inv);
+        }
+        if (lane == 0) p.lse[orow] = x.l == 0.f ? -INFINITY : fmaf(x.m, p.qscale, log2f(x.l)) * 0.6931471805599453f;
+    };
+    if (spread) {
+        for (int i = blockIdx.y; i < rows; i += kMergeSlices) {
+            Joined<D> x;
+            for (int k = warp; k < parts; k += 32) {
+                float2 ml[4];
+                float v[4][E];
+                fetch(i, k, 8, ml, v);
+                x.add(ml, v, p.qscale);
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = x.acc[e];
+            if (lane == 0) s_ml[warp] = make_float2(x.m, x.l);
             __syncthreads();
             if (warp == 0) {
-                l = 0.f;
+                Joined<D> y;
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = 0.f;
-                for (int w = 0; w < 8; ++w) {
-                    l += s_l[w];
+                for (int w = 0; w < 8; w += 4) {
+                    float2 ml[4];
+                    float v[4][E];
 #pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] += s_acc[w][lane * E + e];
+                    for (int u = 0; u < 4; ++u) {
+                        ml[u] = s_ml[w + u];
+#pragma unroll
+                        for (int e = 0; e < E; ++e) v[u][e] = s_acc[w + u][lane * E + e];
+                    }
+                    y.add(ml, v, p.qscale);
                 }
+                finish(i, y);
             }
+            __syncthreads();
         }
-        if (!spread || warp == 0) {
-            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-            const int64_t orow = (int64_t)(d.row0 + tok) * p.Hq + d.head * p.G + h;
-            if (F32OUT) {
-                float* o = reinterpret_cast<float*>(p.out) + orow * D + lane * E;
-#pragma unroll
-                for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(o + e) = make_float2(acc[e] * inv, acc[e + 1] * inv);
-            } else {
-                uint32_t* o = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * D + lane * E);
-#pragma unroll
-                for (int e = 0; e < E; e += 2) o[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+    } else {
+        constexpr int step = kMergeSlices * 8;
+        for (int i = blockIdx.y * 8 + warp; i < rows; i += 2 * step) {
+            const bool both = i + step < rows;
+            Joined<D> x, y;
+            for (int k = 0; k < parts; k += 4) {
+                float2 ml[4], ml2[4];
+                float v[4][E], v2[4][E];
+                fetch(i, k, 1, ml, v);
+                if (both) fetch(i + step, k, 1, ml2, v2);
+                x.add(ml, v, p.qscale);
+                if (both) y.add(ml2, v2, p.qscale);
             }
-            if (lane == 0) p.lse[orow] = l == 0.f ? -INFINITY : fmaf(m, p.qscale, log2f(l)) * 0.6931471805599453f;
+            finish(i, x);
+            if (both) finish(i + step, y);
         }
-        if (spread) __syncthreads();
     }
 }
 
