@@ -473,70 +473,89 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             // within what parting the item would cost (always, where items are not parted)
             const uint32_t tol = p.split ? min(span / 8, (uint32_t)kSplitCost) : U;
             if (lane == 0) p.items[blockIdx.x].parts = 0;
-            // the place of boundary c
-            auto place = [&](uint32_t c) {
-                Place a{U, 0, 0, 0, 0};
-                if (c >= P || U == 0) return a;
-                const uint32_t b = boundary(c);
-                uint32_t before = 0, incl = 0, mine = 0;
-                int s0 = 0;
+            // The places of this CTA's two boundaries at once, one to each half of the warp.
+            const int half = lane >> 4;
+            const uint32_t c = blockIdx.x + (uint32_t)half;
+            const bool inside = c < P && U != 0;
+            const uint32_t bnd = inside ? boundary(c) : U, b0 = __shfl_sync(0xffffffffu, bnd, 0), b1 = __shfl_sync(0xffffffffu, bnd, 16);
+            Place a{U, 0, 0, 0, 0};
+            SeqInfo ai{0, 0, 0};
+            uint32_t rem = 0, whole_seq = 1;
+            {
+                bool open = inside;
+                uint32_t before = 0;
 #pragma unroll 1
-                for (;; s0 += 32) {
-                    mine = s0 == 0 ? cost0 : cost(load(s0 + lane, false));
-                    incl = mine;
+                for (int s0 = 0; __any_sync(0xffffffffu, open); s0 += 32) {
+                    if (s0 > 0) i = load(s0 + lane, false);
+                    else i = mine0;
+                    const uint32_t mine = s0 == 0 ? cost0 : cost(i);
+                    uint32_t incl = mine;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
                         const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
                         if (lane >= o) incl += v;
                     }
-                    const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
-                    if (b < before + all) break;
-                    before += all;
+                    const uint32_t m0 = __ballot_sync(0xffffffffu, b0 < before + incl), m1 = __ballot_sync(0xffffffffu, b1 < before + incl);
+                    const uint32_t m = half ? m1 : m0;
+                    const int at = m != 0 ? __ffs((int)m) - 1 : 31;
+                    const uint32_t end = __shfl_sync(0xffffffffu, incl, at), own = __shfl_sync(0xffffffffu, mine, at);
+                    const SeqInfo ii{__shfl_sync(0xffffffffu, i.q0, at), __shfl_sync(0xffffffffu, i.nq, at), __shfl_sync(0xffffffffu, i.nk, at)};
+                    if (open && m != 0) {
+                        open = false;
+                        a.s = s0 + at;
+                        a.w = bnd;
+                        ai = ii;
+                        rem = bnd - before - (end - own);
+                        whole_seq = own;
+                    }
+                    before += __shfl_sync(0xffffffffu, incl, 31);
                 }
-                const int at = __ffs((int)__ballot_sync(0xffffffffu, b < before + incl)) - 1;
-                uint32_t rem = b - before - __shfl_sync(0xffffffffu, incl - mine, at);
-                a.s = s0 + at;
-                a.w = b;
-                if (rem == 0) return a;  // where a sequence begins
-                const uint32_t uh = __shfl_sync(0xffffffffu, mine, at) / (uint32_t)p.Hkv;
-                const SeqInfo i = info_of(a.s);
-                a.head = (int)(rem / uh);
+            }
+            {
+                const uint32_t uh = whole_seq / (uint32_t)p.Hkv;
+                if (inside) a.head = (int)(rem / uh);
                 rem -= uh * (uint32_t)a.head;
-                int lo = 0, hi = (i.nq + t2 - 1) / t2 - 1;  // the last item that begins at or before rem
+                // the last item that begins at or before rem, 16 of them a step
+                int lo = 0, n = inside ? (ai.nq + t2 - 1) / t2 : 1;
+                uint32_t begins = 0;
 #pragma unroll 1
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (cost_before<KT>(i, t2, mid) <= rem) lo = mid;
-                    else hi = mid - 1;
+                while (__any_sync(0xffffffffu, n > 1)) {
+                    const int step = (n + 15) >> 4, q = (lane & 15) * step;
+                    const uint32_t at = q < n ? cost_before<KT>(ai, t2, lo + q) : ~0u;
+                    const uint32_t m = __ballot_sync(0xffffffffu, at <= rem) >> (16 * half) & 0xffffu;
+                    const int k = 31 - __clz((int)(m | 1u));
+                    begins = __shfl_sync(0xffffffffu, at, 16 * half + k);
+                    lo += k * step;
+                    n = min(step, n - k * step);
                 }
-                const uint32_t off = rem - cost_before<KT>(i, t2, lo);
-                const int tiles = item_tiles<KT>(i, t2, lo);
+                const uint32_t off = rem - begins;
+                const int tiles = item_tiles<KT>(ai, t2, lo);
                 const uint32_t to_end = (uint32_t)(tiles + kItemCost) - off;
                 a.qt = lo;
-                a.j = (int)off - kItemCost;
-                if (off <= kItemCost || (off <= tol && off <= to_end)) {
-                    a.w -= off;
-                    a.j = 0;
-                } else if (to_end <= tol) {
-                    a.w += to_end;
-                    a.j = tiles;
+                a.j = max((int)off - kItemCost, 0);
+                if (inside) {
+                    if (off <= kItemCost || (off <= tol && off <= to_end)) {
+                        a.w -= off;
+                        a.j = 0;
+                    } else if (to_end <= tol) {
+                        a.w += to_end;
+                        a.j = tiles;
+                    }
                 }
-                return a;
-            };
-            const Place first_place = place(blockIdx.x);
-            const uint32_t w1 = first_place.w < U ? place(blockIdx.x + 1).w : U;
-            uint32_t left = w1 - first_place.w;
-            int s = first_place.s, head = first_place.head, qt = first_place.qt, j = first_place.j;
-            int nqt = 0, n = 0;
-            if (left > 0) {
-                i = info_of(s);
-                nqt = (i.nq + t2 - 1) / t2;
             }
+            const uint32_t w0 = __shfl_sync(0xffffffffu, a.w, 0), w1 = __shfl_sync(0xffffffffu, a.w, 16);
+            uint32_t left = w1 - w0;
+            int s = __shfl_sync(0xffffffffu, a.s, 0), head = __shfl_sync(0xffffffffu, a.head, 0);
+            int qt = __shfl_sync(0xffffffffu, a.qt, 0), j = __shfl_sync(0xffffffffu, a.j, 0), n = 0;
+            i = SeqInfo{__shfl_sync(0xffffffffu, ai.q0, 0), __shfl_sync(0xffffffffu, ai.nq, 0), __shfl_sync(0xffffffffu, ai.nk, 0)};
+            int nqt = (i.nq + t2 - 1) / t2;
             bool more = left > 0, stop = false;
 #pragma unroll 1
             while (!stop) {
                 Segment o{};
                 o.nt = -1;
+                bool goes_on = false;  // the item begins here and goes on in the next CTAs
+                uint32_t rest_after = 0;
                 if (more) {
                     const int len = item_tiles<KT>(i, t2, qt);
                     if (j < len) {
@@ -558,20 +577,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         o.s = s;
                         o.q0 = i.q0;
                         o.begins = j == 0;
-                        // the item begins here and goes on in the next CTAs: what the merge needs
-                        if (j == 0 && je < len && lane == 0) {
-                            // it ends at the first boundary that has reached it (within tol)
-                            const uint32_t last = w1 + (uint32_t)(len - je) - tol;
-                            uint32_t stop = min((uint32_t)((float)last / (float)U * (float)P), P);  // off by one at most
-                            while (stop > 0 && (stop == P ? U : boundary(stop)) >= last) --stop;
-                            while (stop < P && boundary(stop) < last) ++stop;
-                            SplitItem d;
-                            d.parts = (int)(stop - blockIdx.x);
-                            d.row0 = o.row0;
-                            d.head = head;
-                            d.tokens = spread ? -o.tokens : o.tokens;
-                            p.items[blockIdx.x] = d;
-                        }
+                        goes_on = j == 0 && je < len;
+                        rest_after = (uint32_t)(len - je);
                     }
                     // the next item
                     j = 0;
@@ -596,6 +603,20 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 if (lane == 0) {
                     s_seg[n % kQueue] = o;
                     mbar_arrive(seg_full(n % kQueue));
+                }
+                __syncwarp();
+                if (goes_on && lane == 0) {
+                    // what the merge needs: it ends at the first boundary that has reached it (within tol)
+                    const uint32_t last = w1 + rest_after - tol;
+                    uint32_t end = min((uint32_t)((float)last / (float)U * (float)P), P);  // off by one at most
+                    while (end > 0 && (end == P ? U : boundary(end)) >= last) --end;
+                    while (end < P && boundary(end) < last) ++end;
+                    SplitItem d;
+                    d.parts = (int)(end - blockIdx.x);
+                    d.row0 = o.row0;
+                    d.head = o.head;
+                    d.tokens = (o.flags & 4) != 0 ? -o.tokens : o.tokens;
+                    p.items[blockIdx.x] = d;
                 }
                 __syncwarp();
                 ++n;
