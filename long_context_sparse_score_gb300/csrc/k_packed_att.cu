@@ -656,7 +656,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 if (g.nt == 0) continue;
                 const int jend = g.jb + g.nt;
                 const int32_t* table = p.table != nullptr ? p.table + (int64_t)g.s * p.table_st : nullptr;
-                // page and row of this lane's box of tile j
+                // Page and row of this lane's box of tile j. The entry is looked at when the tile's
+                // turn comes, so that its load does not hold up the tile before.
                 auto where = [&](int j, int& page, int& row) {
                     const int key = j * KT + (box << lg);
                     page = 0;
@@ -665,11 +666,6 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         const int e = key / p.page_size;
                         row = key - e * p.page_size;
                         page = table[e];
-                        if (page < 0 || page >= p.n_pages) {
-                            flag_error(p.err, HA_DEVERR_INDEX);
-                            page = p.n_pages;  // past the pool: the copy fills its rows with zeros
-                            row = 0;
-                        }
                     }
                 };
                 int page_n, row_n;
@@ -678,12 +674,18 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 for (int j = g.jb; ok && j < jend; ++j) {
                     const int boxes = (min(KT, g.kend - j * KT) + (1 << lg) - 1) >> lg;
                     // coordinates behind the dims: (row, head, page), or 8-row groups (see PackedParams)
-                    int c1 = row_n, c2 = g.head, c3 = page_n;
-                    if (FOLD) {
-                        c1 = (p.kv_fold == 1 ? page_n * p.page_size + row_n : row_n) >> 3;
-                        if (p.kv_fold == 2) c2 = page_n < p.n_pages ? page_n * p.Hkv + g.head : p.n_pages * p.Hkv;
-                    }
+                    int page = page_n, row = row_n;
                     if (j + 1 < jend) where(j + 1, page_n, row_n);
+                    if (table != nullptr && (page < 0 || page >= p.n_pages)) {
+                        flag_error(p.err, HA_DEVERR_INDEX);
+                        page = p.n_pages;  // past the pool: the copy fills its rows with zeros
+                        row = 0;
+                    }
+                    int c1 = row, c2 = g.head, c3 = page;
+                    if (FOLD) {
+                        c1 = (p.kv_fold == 1 ? page * p.page_size + row : row) >> 3;
+                        if (p.kv_fold == 2) c2 = page < p.n_pages ? page * p.Hkv + g.head : p.n_pages * p.Hkv;
+                    }
 #pragma unroll 1
                     for (int kv = 0; kv < 2; ++kv) {
                         const int s = n % S;
