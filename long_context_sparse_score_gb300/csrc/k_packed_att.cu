@@ -40,6 +40,8 @@
 // hands out the items (its code would cost every other role the instruction cache). Waits are bounded: one
 // that gives up flags HA_DEVERR_TIMEOUT, stops the other roles, lets the copies
 // and products in flight land and frees the tensor memory before the CTA exits.
+#include <climits>
+
 #include "tc_common.cuh"
 
 namespace ha {
@@ -71,7 +73,12 @@ struct AttCfg {
     // First tensor memory column of a part: P takes the columns of S; three parts of 32
     // columns take the second half, beside S's 64, and S's first 32 once they are read.
     static constexpr __host__ __device__ int part_col(int i) { return !F32OUT || i == 2 ? 0 : 64 + 32 * i; }
-    static constexpr int kBars = 2 * kStages + 13 + 2 * kQueue;
+    // Places for S and P: one to a stream where O leaves no more room; else three that the
+    // products take in turn, so that S runs up to three products ahead of P V.
+    static constexpr int kPlaces = D == 64 ? 3 : 2;
+    static constexpr int kOCols = D == 64 ? 64 : 128;
+    static constexpr __host__ __device__ uint32_t place_col(uint32_t b) { return b < 2u ? b * 128u : 384u; }
+    static constexpr int kBars = 2 * kStages + 9 + 3 * kPlaces - 2 + 2 * kQueue;
     static constexpr int kSmem = 2 * kQTile + kStages * kTile + 2048 + 8 * kBars + 64 * kQueue + 16;
     static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
@@ -346,7 +353,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                  const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const PackedParams p) {
     using C = AttCfg<D, F32OUT, FOLD>;
-    constexpr int S = C::kStages, KT = C::kKeys;
+    constexpr int S = C::kStages, KT = C::kKeys, NB = C::kPlaces;
     extern __shared__ __align__(1024) uint8_t s_raw[];
     const uint32_t base = smem_addr(s_raw);
     const uint32_t s_q = base, s_ring = base + 2 * C::kQTile;
@@ -360,13 +367,14 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     auto full = [&](int s) { return bars + 8u * (uint32_t)s; };
     auto empty = [&](int s) { return bars + 8u * (uint32_t)(S + s); };
     auto bar_at = [&](int i) { return bars + 8u * (uint32_t)(2 * S + i); };
-    const uint32_t q_full = bar_at(0), q_empty = bar_at(1), x_bar = bar_at(10), done = bar_at(11), seg_done = bar_at(12);
-    auto s_full = [&](int t) { return bar_at(2 + t); };
-    auto p_full = [&](int t) { return bar_at(4 + t); };
-    auto o_done = [&](int t) { return bar_at(6 + t); };
-    auto o_free = [&](int t) { return bar_at(8 + t); };
-    auto seg_full = [&](int i) { return bar_at(13 + i); };
-    auto seg_read = [&](int i) { return bar_at(13 + kQueue + i); };
+    const uint32_t q_full = bar_at(0), q_empty = bar_at(1), x_bar = bar_at(4 + 3 * NB), done = bar_at(5 + 3 * NB), seg_done = bar_at(6 + 3 * NB);
+    // of a place (which is the stream's, where there are two); o_done: P V from it has finished
+    auto s_full = [&](int b) { return bar_at(2 + b); };
+    auto p_full = [&](int b) { return bar_at(2 + NB + b); };
+    auto o_done = [&](int b) { return bar_at(2 + 2 * NB + b); };
+    auto o_free = [&](int t) { return bar_at(2 + 3 * NB + t); };
+    auto seg_full = [&](int i) { return bar_at(7 + 3 * NB + i); };
+    auto seg_read = [&](int i) { return bar_at(7 + 3 * NB + kQueue + i); };
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if ((base & 1023u) != 0u) {  // the swizzle atoms need it; shared memory starts there
@@ -384,12 +392,12 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(s_full(t), 1);
-            mbar_init(p_full(t), 4);
-            mbar_init(o_done(t), 1);
-            mbar_init(o_free(t), 8);
+        for (int b = 0; b < NB; ++b) {
+            mbar_init(s_full(b), 1);
+            mbar_init(p_full(b), 4);
+            mbar_init(o_done(b), 1);
         }
+        for (int t = 0; t < 2; ++t) mbar_init(o_free(t), 8);
         mbar_init(x_bar, 8);
         mbar_init(done, 1);
         mbar_init(seg_done, 1);
@@ -720,6 +728,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                                       ((128u >> 4) << 24);
             int nq = 0;
             uint32_t cnt = 0;  // bit t: parity of stream t's tiles so far
+            uint32_t sb = 0, pb = 0, pph = 0;  // three places: that of the next S and P, and P's phase
             // Descriptors: Q (K-major, leading offset unused), the first ring slot as K (the same)
             // and as V, whose keys are the MMA's K dimension and the rows of the layout (MN-major).
             constexpr uint32_t kv_hi = sw128_desc_hi(C::kGroup);
@@ -727,26 +736,24 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             const uint32_t k_lo = uniform(((s_ring & 0x3FFFFu) >> 4) | (1u << 16));
             const uint32_t v_lo = uniform(((s_ring & 0x3FFFFu) >> 4) | ((uint32_t)(C::kSpan >> 4) << 16));
             const uint32_t tm = uniform(tmem);
-            // S_t = Q K^T of the K tile in ring slot s, steps k0 to k1
-            auto issue_s = [&](auto T, uint32_t qtile, uint32_t s, int k0, int k1) {
-                constexpr uint32_t t = decltype(T)::value;
+            // S at column col = Q K^T of the K tile in ring slot s, steps k0 to k1
+            auto issue_s = [&](uint32_t col, uint32_t qtile, uint32_t s, int k0, int k1) {
                 const uint32_t a = q_lo + qtile * (uint32_t)(C::kQTile >> 4), b = k_lo + s * (uint32_t)(C::kTile >> 4);
 #pragma unroll
                 for (int kk = k0; kk < k1; ++kk) {
                     const uint32_t h = (uint32_t)(kk >> 2), o = (uint32_t)(kk & 3) * 2u;
-                    tc_mma(tm + t * 128u, sw128_desc_of(a + h * 1024u + o, sw128_desc_hi(1024)),
+                    tc_mma(tm + col, sw128_desc_of(a + h * 1024u + o, sw128_desc_hi(1024)),
                            sw128_desc_of(b + h * (uint32_t)(C::kSpan >> 4) + o, kv_hi), kIdS, kk > 0 ? 1u : 0u);
                 }
             };
-            // O_t (+)= P_t V of the V tile in ring slot s
-            auto issue_o = [&](auto T, uint32_t s, uint32_t acc) {
-                constexpr uint32_t t = decltype(T)::value;
+            // O of stream t (+)= P V, P at column col, of the V tile in ring slot s
+            auto issue_o = [&](uint32_t t, uint32_t col, uint32_t s, uint32_t acc) {
                 const uint32_t b = v_lo + s * (uint32_t)(C::kTile >> 4);
 #pragma unroll
                 for (int part = 0; part < C::kParts; ++part)
 #pragma unroll
                     for (int kk = 0; kk < KT / 16; ++kk)
-                        tc_mma_ts(tm + 256u + t * 128u, tm + t * 128u + (uint32_t)(C::part_col(part) + kk * 8),
+                        tc_mma_ts(tm + 256u + t * (uint32_t)C::kOCols, tm + col + (uint32_t)(C::part_col(part) + kk * 8),
                                   sw128_desc_of(b + (uint32_t)kk * (uint32_t)(C::kGroup >> 3), kv_hi), kIdO, part > 0 || kk > 0 ? 1u : acc);
             };
             // ring places: d tiles on (d < S)
@@ -785,15 +792,62 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     ++nq;
                 }
                 Slot v = at.ahead(1);
-                if (nt > 0 && !parity) {
+                if (NB == 3 && nt > 0) {
+                    // Products k = 0 .. N - 1 in the order (key tile, stream), or (one row tile) the
+                    // key tiles in turn: S of k + 3 goes where P of k was, right behind its P V.
+                    const int N = parity ? nt : e0 + nt;
+                    // the last product of its key tile: row tile 1's
+                    auto second = [&](int k) { return parity || k >= 2 * e0 || (k & 1) != 0; };
+                    int ks = 0;  // the next S, its K tile
+                    Slot kt = at;
+                    bool k_in = false, v_in = false;
+                    auto next_s = [&]() {
+                        const bool last = second(ks);
+                        if (!k_in) wait_slot(kt);
+                        k_in = !last;
+                        if (elect_one()) {
+                            issue_s(C::place_col(sb), !parity && last ? 1u : 0u, kt.s, 0, D / 16);
+                            tc_commit(s_full((int)sb));
+                            if (last) tc_commit(empty((int)kt.s));
+                            if (ks + 1 == N) tc_commit(q_empty);
+                        }
+                        __syncwarp();
+                        if (last) kt = kt.ahead(2);
+                        sb = sb == 2u ? 0u : sb + 1u;
+                        ++ks;
+                    };
+                    while (ks < N && ks < 3) next_s();
+                    wait(o_free(0), free_ph);
+                    wait(o_free(1), free_ph);
+                    int begun = 0;  // per stream (bit t): O holds something; float32: half of a pair of tiles
+#pragma unroll 1
+                    for (int k = 0; k < N; ++k) {
+                        const bool last = second(k);
+                        const int t = parity ? k & 1 : (last ? 1 : 0);
+                        if (!v_in) wait_slot(v);
+                        v_in = !last;
+                        wait(p_full((int)pb), pph);
+                        if (elect_one()) {
+                            issue_o((uint32_t)t, C::place_col(pb), v.s, (uint32_t)(begun >> t) & 1u);
+                            tc_commit(o_done((int)pb));
+                            if (last) tc_commit(empty((int)v.s));
+                        }
+                        __syncwarp();
+                        begun = F32OUT ? begun ^ (1 << t) : begun | (1 << t);
+                        if (ks < N) next_s();
+                        if (last) v = v.ahead(2);
+                        pph ^= pb == 2u ? 1u : 0u;
+                        pb = pb == 2u ? 0u : pb + 1u;
+                    }
+                } else if (nt > 0 && !parity) {
                     // two row tiles: row tile 0 takes the first e0 key tiles, row tile 1 all
                     wait_slot(at);
                     if (elect_one()) {
                         if (e0 > 0) {
-                            issue_s(Stream<0>{}, 0, at.s, 0, D / 16);
+                            issue_s(0u, 0, at.s, 0, D / 16);
                             tc_commit(s_full(0));
                         }
-                        issue_s(Stream<1>{}, 1, at.s, 0, D / 16);
+                        issue_s(128u, 1, at.s, 0, D / 16);
                         tc_commit(s_full(1));
                         tc_commit(empty((int)at.s));
                         if (nt == 1) tc_commit(q_empty);
@@ -810,7 +864,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         if (i < e0) {
                             take_p(0);
                             if (elect_one()) {
-                                issue_o(Stream<0>{}, v.s, F32OUT ? (uint32_t)i & 1u : (i > 0 ? 1u : 0u));
+                                issue_o(0u, 0u, v.s, F32OUT ? (uint32_t)i & 1u : (i > 0 ? 1u : 0u));
                                 if (F32OUT || i + 1 == e0) tc_commit(o_done(0));
                             }
                             __syncwarp();
@@ -818,7 +872,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                                 if (!k_ok) wait_slot(k);
                                 k_ok = true;
                                 if (elect_one()) {
-                                    issue_s(Stream<0>{}, 0, k.s, 0, D / 16);
+                                    issue_s(0u, 0, k.s, 0, D / 16);
                                     tc_commit(s_full(0));
                                 }
                                 __syncwarp();
@@ -826,19 +880,19 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         }
                         take_p(1);
                         if (elect_one()) {
-                            issue_o(Stream<1>{}, v.s, F32OUT ? (uint32_t)i & 1u : (i > 0 ? 1u : 0u));
+                            issue_o(1u, 128u, v.s, F32OUT ? (uint32_t)i & 1u : (i > 0 ? 1u : 0u));
                             if (F32OUT || !more) tc_commit(o_done(1));
                             tc_commit(empty((int)v.s));
                         }
                         __syncwarp();
                         if (more) {
                             if (!k_ok) wait_slot(k);
-                            if (elect_one()) issue_s(Stream<1>{}, 1, k.s, 0, D / 32);
+                            if (elect_one()) issue_s(128u, 1, k.s, 0, D / 32);
                             __syncwarp();
                             const Slot v1 = v.ahead(2), k1 = k.ahead(2);
                             v_ok = landed(v1);
                             if (elect_one()) {
-                                issue_s(Stream<1>{}, 1, k.s, D / 32, D / 16);
+                                issue_s(128u, 1, k.s, D / 32, D / 16);
                                 tc_commit(s_full(1));
                                 tc_commit(empty((int)k.s));
                                 if (i + 2 == nt) tc_commit(q_empty);
@@ -855,7 +909,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         constexpr int t = decltype(T)::value;
                         wait_slot(x);
                         if (elect_one()) {
-                            issue_s(T, 0, x.s, 0, D / 16);
+                            issue_s(128u * t, 0, x.s, 0, D / 16);
                             tc_commit(s_full(t));
                             tc_commit(empty((int)x.s));
                             if (last) tc_commit(q_empty);
@@ -873,7 +927,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         wait_slot(v);
                         take_p(t);
                         if (elect_one()) {
-                            issue_o(T, v.s, F32OUT ? (uint32_t)(i >> 1) & 1u : (i >= 2 ? 1u : 0u));
+                            issue_o(t, 128u * t, v.s, F32OUT ? (uint32_t)(i >> 1) & 1u : (i >= 2 ? 1u : 0u));
                             if (F32OUT || !more) tc_commit(o_done(t));
                             tc_commit(empty((int)v.s));
                         }
@@ -908,18 +962,24 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int t = warp >> 2, r = tid & 127;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + lane_off + (uint32_t)(t * 128);
-        const uint32_t tO = tmem + lane_off + 256u;
+        uint32_t tS = tmem + lane_off + (uint32_t)(t * 128);
+        const uint32_t tO = tmem + lane_off + 256u, tOt = tO + (uint32_t)(t * C::kOCols);
         const int rtok = r / p.G, rhead = r - rtok * p.G, stok = lane / p.G, shead = lane - stok * p.G;
         const uint64_t qscale2 = pack2(p.qscale, p.qscale);
         uint32_t cnt = 0, odc[2] = {0, 0}, nx = 0, ring = 0;  // tiles, o_done's, exchanges, ring tiles so far
+        uint32_t kb = 0;                                      // three places: products so far
 #pragma unroll 1
         while (next_segment(nseg, g)) {
             const bool parity = (g.flags & 1) != 0, whole = (g.flags & 2) != 0, spread = (g.flags & 4) != 0;
             const int hd = spread ? shead : rhead;
             const int ltok = spread ? stok : (parity ? 0 : t * p.TQ) + rtok;  // token of this row within the item
             const bool valid = (spread ? stok < p.TS : rtok < p.TQ) && ltok < g.tokens;
-            const int kmax = valid ? min(g.nk, max(0, g.kfirst + ltok + 1)) : 0;
+            // Keys that this row sees, and the fewest of the warp's rows. With three places the
+            // softmax is what a tile waits for: no votes a tile, and rows of no token go unmasked
+            // (16,384 tokens, d 64: 1140 -> 1106 us; with two places and d 128 337 -> 341, float32
+            // 283 -> 300, so the votes stay there).
+            const int kmax = valid ? min(g.nk, max(0, g.kfirst + ltok + 1)) : (NB == 3 ? INT_MAX : 0);
+            const int kmin = __reduce_min_sync(0xffffffffu, kmax);
             const bool any = __any_sync(0xffffffffu, valid);
             const int st0 = parity ? (g.nt + 1) >> 1 : g.e0, st1 = parity ? g.nt >> 1 : g.nt;
             const int nt = t == 0 ? st0 : st1;
@@ -935,7 +995,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 #pragma unroll
                     for (int cc = 0; cc < D; cc += 32) {
                         uint32_t o[32];
-                        tmem_ld32(tO + (uint32_t)(t * 128 + cc), o);
+                        tmem_ld32(tOt + (uint32_t)cc, o);
                         tmem_landed(o);
 #pragma unroll
                         for (int k = 0; k < 32; ++k) acc[cc + k] += __uint_as_float(o[k]);
@@ -948,32 +1008,49 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             const int jlast = g.jb + g.nt - 1;
             const bool clears = g.kend < (jlast + 1) * KT && (t == 0 || parity || jlast >= g.jb + st0);
             int j = parity ? g.jb + t : g.jb;
+            // three places: the number of the product of this stream's tile i; whether it has
+            // finished P V (the place's earlier products have, where S of a later one is there)
+            auto product = [&](int tt, int i) { return kb + (uint32_t)(parity ? 2 * i + tt : (i < g.e0 ? 2 * i + tt : g.e0 + i)); };
+            auto wait_o = [&](uint32_t k) { wait(o_done((int)(k % 3u)), (k / 3u) & 1u); };
 #pragma unroll 1
             for (int i = 0; i < nt; ++i, j += jstep) {
                 const int lim = kmax - j * KT;  // columns of this tile the row sees
-                const bool part = __any_sync(0xffffffffu, lim < KT);
-                if (aborted()) break;
-                if constexpr (F32OUT) {
-                    // O holds two tiles at most (24 steps of the accumulator)
-                    if (i > 0 && (i & 1) == 0) {
+                const bool part = NB == 3 ? kmin - j * KT < KT : (bool)__any_sync(0xffffffffu, lim < KT);
+                if (NB == 2 && aborted()) break;
+                // O holds two tiles at most (24 steps of the accumulator)
+                bool take_o = F32OUT && i > 0 && (i & 1) == 0;
+                int place = t;
+                if constexpr (NB == 3) {
+                    const uint32_t k = product(t, i), b = k % 3u;
+                    place = (int)b;
+                    tS = tmem + lane_off + C::place_col(b);
+                    wait(s_full(place), (k / 3u) & 1u);
+                } else {
+                    if (take_o) {
                         wait(o_done(t), (cnt - 1u) & 1u);
                         if (any) add_o();
+                        take_o = false;
                     }
+                    wait(s_full(t), cnt & 1u);
                 }
-                wait(s_full(t), cnt & 1u);
                 if (any) {
-                    // The reference grows to mx: what was added up shrinks by a. S of this tile
-                    // came behind the products of the tiles before, so O holds those.
+                    // The reference grows to mx: what was added up shrinks by a. With two places S of
+                    // this tile came behind the products of the tiles before, so O holds those.
                     auto grow_to = [&](float mx, bool grow) {
+                        if (NB == 3 && i > 0) wait_o(product(t, i - 1));
                         const float a = grow ? ex2((m - mx) * p.qscale) : 1.f;  // 0 from -inf
                         l *= a;
                         if (grow) m = mx;
                         if constexpr (F32OUT) {
+                            if (take_o) {
+                                add_o();
+                                take_o = false;
+                            }
                             if ((i & 1) != 0) {
                                 add_o();
                                 const uint32_t zero[32] = {};
 #pragma unroll 1
-                                for (int cc = 0; cc < D; cc += 32) tmem_st32(tO + (uint32_t)(t * 128 + cc), zero);
+                                for (int cc = 0; cc < D; cc += 32) tmem_st32(tOt + (uint32_t)cc, zero);
                             }
 #pragma unroll
                             for (int k = 0; k < D; ++k) acc[k] *= a;
@@ -981,11 +1058,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 #pragma unroll 1
                             for (int cc = 0; cc < D; cc += 32) {
                                 uint32_t o[32];
-                                tmem_ld32(tO + (uint32_t)(t * 128 + cc), o);
+                                tmem_ld32(tOt + (uint32_t)cc, o);
                                 tmem_landed(o);
 #pragma unroll
                                 for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-                                tmem_st32(tO + (uint32_t)(t * 128 + cc), o);
+                                tmem_st32(tOt + (uint32_t)cc, o);
                             }
                         }
                     };
@@ -998,7 +1075,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         tmem_landed(x);
                         if (part) mask_columns(x, lim - w * Q);
                         const float mx = max_of(x, m);
-                        const bool grow = (mx - m) * p.qscale > kRescale;  // false where both are -inf
+                        const bool grow = (NB == 2 || valid) && (mx - m) * p.qscale > kRescale;  // false where both are -inf
                         if (__any_sync(0xffffffffu, grow)) grow_to(mx, grow);
                         const float sub = m == -INFINITY ? 0.f : m * p.qscale;
                         if constexpr (F32OUT) {
@@ -1036,7 +1113,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                             if (part) mask_columns(x, lim);
                             mx = max_of(x, mx);
                         }
-                        const bool grow = (mx - m) * p.qscale > kRescale;  // false where both are -inf
+                        const bool grow = (NB == 2 || valid) && (mx - m) * p.qscale > kRescale;  // false where both are -inf
                         if (__any_sync(0xffffffffu, grow)) grow_to(mx, grow);
                         const float sub = m == -INFINITY ? 0.f : m * p.qscale;
 #pragma unroll 1
@@ -1060,7 +1137,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         tmem_landed(x1);
                         if (part) mask_columns(x1, lim - 64);
                         mx = max_of(x1, mx);
-                        const bool grow = (mx - m) * p.qscale > kRescale;  // false where both are -inf
+                        const bool grow = (NB == 2 || valid) && (mx - m) * p.qscale > kRescale;  // false where both are -inf
                         if (__any_sync(0xffffffffu, grow)) grow_to(mx, grow);
                         const float sub = m == -INFINITY ? 0.f : m * p.qscale;
                         const uint64_t nsub2 = pack2(-sub, -sub);
@@ -1079,6 +1156,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         l += a + b;
                     }
                 }
+                if (NB == 3 && take_o) {  // before P V of this tile overwrites it
+                    wait_o(product(t, i - 1));
+                    if (any) add_o();
+                }
                 ++cnt;
                 if (clears && j == jlast) {
                     const uint32_t k = ring + 2u * (uint32_t)(jlast - g.jb) + 1u, s = k % (uint32_t)S;
@@ -1096,13 +1177,17 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(t));
+                if (lane == 0) mbar_arrive(p_full(place));
             }
             ring += 2u * (uint32_t)g.nt;
             // o_done: every tile with a float32 output, else a stream's last one
             odc[0] += F32OUT ? (uint32_t)st0 : (st0 > 0 ? 1u : 0u);
             odc[1] += F32OUT ? (uint32_t)st1 : (st1 > 0 ? 1u : 0u);
-            if (nt > 0) wait(o_done(t), (odc[t] - 1u) & 1u);
+            if (NB == 3) {
+                if (nt > 0) wait_o(product(t, nt - 1));
+            } else if (nt > 0) {
+                wait(o_done(t), (odc[t] - 1u) & 1u);
+            }
             if constexpr (F32OUT) {
                 // the whole O goes where the rest reads it
                 if (nt > 0) {
@@ -1113,7 +1198,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                             uint32_t o[32];
 #pragma unroll
                             for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(acc[cc + k]);
-                            tmem_st32(tO + (uint32_t)(t * 128 + cc), o);
+                            tmem_st32(tOt + (uint32_t)cc, o);
                         }
                         tmem_wait_st();
                     }
@@ -1124,13 +1209,16 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             const int64_t row = whole ? (int64_t)(g.row0 + ltok) * p.Hq + g.head * p.G + hd
                                       : (int64_t)(2 * blockIdx.x + (g.begins ? 1 : 0)) * p.slot_rows + (parity ? r : t * 128 + r);
             float ca = 1.f, cb = 0.f;          // factors of O0 (or of this stream's O) and O1
-            uint32_t oa = tO + (uint32_t)(t * 128);
+            uint32_t oa = tOt;
             int col0 = 0, cols = D;
             const bool have = parity ? st0 > 0 : nt > 0, both = parity && st1 > 0;
             if (parity) {
                 if (st0 > 0) {
                     // the other stream: all but its last product came before ours
-                    if (t == 1 || st1 > 0) wait(o_done(t ^ 1), (odc[t ^ 1] - 1u) & 1u);
+                    if (t == 1 || st1 > 0) {
+                        if (NB == 3) wait_o(product(t ^ 1, (t == 0 ? st1 : st0) - 1));
+                        else wait(o_done(t ^ 1), (odc[t ^ 1] - 1u) & 1u);
+                    }
                     s_ml[t * 128 + r] = make_float2(m, l);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(x_bar);
@@ -1168,7 +1256,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     }
                     if (both) {
                         uint32_t o1[W];
-                        tmem_load(tO + 128u + (uint32_t)cc, o1);
+                        tmem_load(tO + (uint32_t)(C::kOCols + cc), o1);
                         tmem_landed(o1);
 #pragma unroll
                         for (int k = 0; k < W; ++k)
@@ -1200,6 +1288,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         p.part_ml[row] = make_float2(m, l);
                 }
             }
+            kb += (uint32_t)(parity ? g.nt : g.e0 + g.nt);
             tc_fence_before();
             wait(seg_done, (uint32_t)(nseg - 1) & 1u);
             if (lane == 0) {
