@@ -1556,7 +1556,8 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
         p.page_size = c->page_size;
         p.n_pages = c->n_pages;
         if (c->max_pages > 1 && (c->page_size & -c->page_size) < box) box = c->page_size & -c->page_size;
-        // strides of an extent of 1 say nothing
+        // Both halves in one copy: 64 decodes over pages of 16 404 -> 345 us, over pages of 64
+        // 342 -> 333, of 128 the same. Strides of an extent of 1 say nothing.
         auto folds = [&](int64_t outer, int64_t n_outer, int64_t inner, int64_t n_inner) {
             return n_outer == 1 || outer == inner * n_inner;
         };
@@ -1588,7 +1589,8 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
     p.box_log2 = 0;
     while ((1 << p.box_log2) < box) ++p.box_log2;
     // No more CTAs than the lengths can fill with a tile each. Items of a few tiles are not
-    // parted, which saves the merge.
+    // parted, which saves the merge (a prompt of 300 tokens 18.4 -> 14.4 us, 64 decodes over
+    // up to 500 keys 39.9 -> 36.7, one over 500 keys 11.6 -> 12.1).
     const int grid = (int)std::min<int64_t>(kSMs, items * tiles);
     p.split = tiles > kWholeTiles;
     HA_LAUNCH(launch_packed_att(p, m, t->d, f32, grid, grid > 1 && p.split, static_cast<cudaStream_t>(stream)),
