@@ -1548,6 +1548,9 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
     int box = kt;
     bool ok = encode_map(&m.q, q, t->d, {G, t->total, t->h_kv}, {t->q_sh, t->q_st, G * t->q_sh}, G, L.tq);
     m.qs = m.q;
+    m.o = m.q;
+    const int64_t rs = (int64_t)t->h_q * t->d;  // out is contiguous
+    if (!f32) ok = ok && encode_map(&m.o, out, t->d, {G, t->total, t->h_kv}, {t->d, rs, (int64_t)G * t->d}, G, L.tq);
     if (p.TS > 0) ok = ok && encode_map(&m.qs, q, t->d, {G, t->total, t->h_kv}, {t->q_sh, t->q_st, G * t->q_sh}, G, p.TS);
     if (c != nullptr) {
         p.seq_lens = seq_lens;

@@ -28,7 +28,7 @@ inline EncodeTiledFn encode_fn() {
 
 // Tensor maps of the packed attention: bf16, 4 dimensions, 128-byte swizzle.
 struct PackedMaps {
-    CUtensorMap q, qs, k, v;  // qs: the queries in copies of TS tokens
+    CUtensorMap q, qs, k, v, o;  // qs: the queries in copies of TS tokens; o: bf16 output, as q
 };
 cudaError_t launch_packed_att(const struct PackedParams& p, const PackedMaps& m, int d, bool f32_out, int grid,
                               bool merge, cudaStream_t st);
@@ -39,6 +39,18 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
+
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* tm, uint32_t src, int c0, int c1, int c2, int c3) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(tm), "r"(c0),
+                 "r"(c1), "r"(c2), "r"(c3), "r"(src)
+                 : "memory");
+}
+// The stores that this thread issued have read shared memory; they are done.
+__device__ __forceinline__ void tma_store_read() {
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int c0, int c1,
                                             int c2, int c3) {
