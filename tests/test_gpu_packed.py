@@ -473,6 +473,79 @@ def test_two_streams_with_their_own_workspaces(H):
             assert torch.equal(o, want[0]) and torch.equal(l, want[1])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_a_row_tile_without_keys_beside_one_with(H, d, out_dtype):
+    """The first 44 of 64 tokens see no key (a row tile is 32 of them), then a sequence of whole tiles."""
+    g = torch.Generator(device="cuda").manual_seed(31)
+    new, lens, Hkv = [64, 128], [20, 150], 2
+    K, V, table = pages(g, lens, 16, Hkv, d)
+    q = rand(g, sum(new), 4 * Hkv, d)
+    out, lse, st = run_chunk(H, q, K, V, table, new, lens, Hkv, out_dtype)
+    assert st == (0, 0)
+    check_chunk(q, K, V, table, new, lens, out, lse, Hkv)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_output_on_any_16_bytes_keeps_its_neighbours(H, d, out_dtype):
+    """`out` 16 bytes off a 32-byte boundary: the same bits, and nothing written around it."""
+    g = torch.Generator(device="cuda").manual_seed(32)
+    new, Hq = [300, 33, 64], 6
+    q, k, v = (rand(g, sum(new), h, d) for h in (Hq, 2, 2))
+    want, want_lse, _ = run_prefill(H, q, k, v, new, out_dtype)
+    pad = 16 // want.element_size()
+    room = torch.full((want.numel() + 2 * pad,), 7.0, dtype=out_dtype, device="cuda")
+    out, lse = room[pad:-pad].view(want.shape), torch.empty_like(want_lse)
+    tok = H.make_tokens(q, k, v, len(new), out_dtype=out_dtype)
+    ws = torch.zeros(H.hash_attn_packed_workspace_size(tok), dtype=torch.uint8, device="cuda")
+    H.hash_attn_prefill(tok, q, k, v, cumulative(new), out, lse, workspace=ws)
+    assert H.hash_attn_device_status(ws) == (0, 0)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert bool((room[:pad] == 7).all()) and bool((room[-pad:] == 7).all())
+
+
+def test_captured_graphs_share_a_workspace(H):
+    """A prompt and a mixed batch captured into a graph each, replayed in turn with new inputs."""
+    g = torch.Generator(device="cuda").manual_seed(33)
+    Hkv, d, new, lens, prompts = 2, 128, [1, 80, 0, 200], [700, 80, 0, 2500], [500, 40]
+    K, V, table = pages(g, lens, 32, Hkv, d)
+    q, cu, lt = rand(g, sum(new), 8, d), cumulative(new), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    pq, pk, pv, pcu = rand(g, sum(prompts), 8, d), rand(g, sum(prompts), Hkv, d), rand(g, sum(prompts), Hkv, d), cumulative(prompts)
+    t0, t1 = H.make_tokens(q, None, None, len(new), h_kv=Hkv, out_dtype=q.dtype), H.make_tokens(pq, pk, pv, 2, out_dtype=q.dtype)
+    cache = H.make_cache(K, V, table)
+    ws = torch.zeros(max(map(H.hash_attn_packed_workspace_size, (t0, t1))), dtype=torch.uint8, device="cuda")
+    out, lse, pout, plse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda"), torch.empty_like(pq), torch.empty(pq.shape[:2], device="cuda")
+
+    def chunk():
+        H.hash_attn_chunk(t0, cache, q, K, V, table, cu, lt, out, lse, workspace=ws, stream=torch.cuda.current_stream())
+
+    def prompt():
+        H.hash_attn_prefill(t1, pq, pk, pv, pcu, pout, plse, workspace=ws, stream=torch.cuda.current_stream())
+
+    chunk(), prompt()
+    torch.cuda.synchronize()
+    graphs = []
+    for call in (chunk, prompt):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call()
+            call()
+    for seed in (1, 2):
+        q.copy_(rand(g.manual_seed(seed), *q.shape))
+        pk.copy_(rand(g, *pk.shape))
+        want = run_chunk(H, q, K, V, table, new, lens, Hkv)
+        want_p = run_prefill(H, pq, pk, pv, prompts)
+        for x in (out, lse, pout, plse):
+            x.fill_(NAN)
+        for _ in range(3):
+            for gr in graphs:
+                gr.replay()
+        assert H.hash_attn_device_status(ws) == (0, 0)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        assert torch.equal(pout, want_p[0]) and torch.equal(plse, want_p[1])
+
+
 @pytest.mark.parametrize("n", [8, 1100])
 def test_bounds_that_go_back_and_forth(H, n):
     """Every other sequence covers all rows: more work than the call can have, and than 32 bits count."""
