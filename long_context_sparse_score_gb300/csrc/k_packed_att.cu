@@ -579,6 +579,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             int qt = __shfl_sync(0xffffffffu, a.qt, 0), j = __shfl_sync(0xffffffffu, a.j, 0), n = 0;
             i = SeqInfo{__shfl_sync(0xffffffffu, ai.q0, 0), __shfl_sync(0xffffffffu, ai.nq, 0), __shfl_sync(0xffffffffu, ai.nk, 0)};
             int nqt = (i.nq + t2 - 1) / t2;
+            // The rest of an item that began in the CTA before comes last: all CTAs begin at a first
+            // key, so those with items of the same K and V read them together (4 x 512 tokens over
+            // 20,000 to 32,000 keys: 594 -> 574 us, under the power cap 672 -> 631).
+            Segment held;
+            held.nt = -1;
             bool more = left > 0, stop = false;
 #pragma unroll 1
             while (!stop) {
@@ -630,6 +635,13 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     }
                     more = left > 0;
                     if (o.nt < 0 && more) continue;  // the first place was an item's end
+                    if (o.jb > 0 && more) {
+                        held = o;
+                        continue;
+                    }
+                } else if (held.nt >= 0) {
+                    o = held;
+                    held.nt = -1;
                 }
                 wait(seg_read(n % kQueue), ((uint32_t)(n / kQueue) & 1u) ^ 1u);
                 if (lane == 0) {
