@@ -1528,6 +1528,7 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
     p.n_seq = t->n_seq;
     p.total = t->total;
     p.max_len = max_len;
+    p.split = tiles > kWholeTiles;
     p.Hq = t->h_q;
     p.Hkv = t->h_kv;
     p.G = G;
@@ -1550,8 +1551,8 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
     m.qs = m.q;
     m.o = m.q;
     const int64_t rs = (int64_t)t->h_q * t->d;  // out is contiguous
-    if (!f32) ok = ok && encode_map(&m.o, out, t->d, {G, t->total, t->h_kv}, {t->d, rs, (int64_t)G * t->d}, G, L.tq);
-    if (p.TS > 0) ok = ok && encode_map(&m.qs, q, t->d, {G, t->total, t->h_kv}, {t->q_sh, t->q_st, G * t->q_sh}, G, p.TS);
+    if (!f32 && t->d == 128) ok = ok && encode_map(&m.o, out, t->d, {G, t->total, t->h_kv}, {t->d, rs, (int64_t)G * t->d}, G, L.tq);
+    if (p.TS > 0 && p.split) ok = ok && encode_map(&m.qs, q, t->d, {G, t->total, t->h_kv}, {t->q_sh, t->q_st, G * t->q_sh}, G, p.TS);
     if (c != nullptr) {
         p.seq_lens = seq_lens;
         p.table = table;
@@ -1595,7 +1596,6 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
     // parted, which saves the merge (a prompt of 300 tokens 18.4 -> 14.4 us, 64 decodes over
     // up to 500 keys 39.9 -> 36.7, one over 500 keys 11.6 -> 12.1).
     const int grid = (int)std::min<int64_t>(kSMs, items * tiles);
-    p.split = tiles > kWholeTiles;
     HA_LAUNCH(launch_packed_att(p, m, t->d, f32, grid, grid > 1 && p.split, static_cast<cudaStream_t>(stream)),
               "packed attention launch");
     return HA_OK;
