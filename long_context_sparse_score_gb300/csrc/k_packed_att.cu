@@ -35,19 +35,20 @@
 // them, in order, so results do not depend on timing.
 //
 // Measured (graph replays; rates against cuBLAS's bf16 burst and a plain copy): a prompt of
-// 16,384 tokens, 32/8 heads of 128: 1.33-1.39 ms, 1.58-1.66 PFLOP/s, 83-87 %; 24 prompts of
-// 33 to 2,500: 338 us, 57 % (an item's start and end cost about 7,000 cycles of each CTA,
-// 2.4 tiles); 16,384 tokens at d 64: 1.11 ms, 52 % (bound by the softmax warps'
-// latency, not by a unit); decode of 64 sequences of 1,000 to 16,000 keys: 345 us, 6.4 TB/s,
-// 95 %; one token over 131,072 keys, float32 out: 118 us, 4.5 TB/s, 67 % (bound by the
-// products: three for P V).
+// 16,384 tokens, 32/8 heads of 128: 1.33 ms, 1.65 PFLOP/s, 86 % (1.43 ms at the power cap);
+// 24 prompts of 33 to 2,500: 330 us, 58 % (an item's start and end cost each CTA about
+// 6,000 cycles, two tiles); 16,384 tokens at d 64: 1.10 ms, 52 % (bound by the softmax
+// warps' latency, not by a unit); decode of 64 sequences of 1,000 to 16,000 keys: 345 us,
+// 6.4 TB/s, 95 %; one token over 131,072 keys, float32 out: 109 us, 4.9 TB/s, 73 % (bound by
+// the products: three for P V); 4 x 512 tokens over 20,000 to 32,000 keys: 574 us, 84 %.
 //
 // 12 warps: two softmax warpgroups (thread = row: a tcgen05.ld gives a thread
 // its whole row of S, no shuffles), one warp that issues the MMAs, one that loads K
-// and V by TMA (128-byte swizzle; a ring of tiles), one that loads Q, and one that
-// hands out the items (its code would cost every other role the instruction cache). Waits are bounded: one
-// that gives up flags HA_DEVERR_TIMEOUT, stops the other roles, lets the copies
-// and products in flight land and frees the tensor memory before the CTA exits.
+// and V by TMA (128-byte swizzle; a ring of tiles), one that loads Q and sends staged
+// rows off, and one that hands out the items (its code would cost every other role the
+// instruction cache). Waits are bounded: one that gives up flags HA_DEVERR_TIMEOUT, stops
+// the other roles, lets the copies and products in flight land and frees the tensor
+// memory before the CTA exits.
 #include <climits>
 
 #include "tc_common.cuh"
@@ -1419,8 +1420,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 // may begin, slices of its rows), one pass with a running maximum. Latency is most of what
 // it costs, so loads of several parts and rows are in flight: a warp takes two rows and four
 // parts at a time; where each warp of a stream left parts (32 rows at most, up to 600
-// parts), a CTA takes a row and its eight warps share the parts. 2.7 us behind a decode step, 7 to 10 us where every CTA
-// left two parts of 256 rows (40 MB through L2); with 8 or 32 slices the same within 2 %.
+// parts), a CTA takes a row and its eight warps share the parts. 2.7 us
+// behind a decode step, 7 to 10 us where every CTA left two parts of 256 rows (40 MB
+// through L2); with 8 or 32 slices the same within 2 %.
 constexpr int kMergeSlices = 16;
 template <int D>
 struct Joined {
