@@ -127,9 +127,9 @@ __global__ void __launch_bounds__(kAppWarps * 32) k_append(const AppendParams p)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();
     pdl_launch_dependents();  // the kernel that writes the codes may read everything but the cache
-    if (blockIdx.x == 0 && blockIdx.y == 0 && p.flags != nullptr) {
+    if (blockIdx.y == 0 && p.flags != nullptr) {
         // the sequences' bounds, once
-        for (int s = tid; s < p.n_seq; s += kAppWarps * 32) {
+        for (int s = blockIdx.x * kAppWarps * 32 + tid; s < p.n_seq; s += gridDim.x * kAppWarps * 32) {
             const int a = p.cu[s], b = p.cu[s + 1], nk = p.seq_lens[s];
             if (a < 0 || b < a || b > p.total || nk < 0 || nk > p.max_len) atomicOr(p.flags, HA_DEVERR_SEQLEN);
             else if (nk < b - a) atomicOr(p.flags, HA_DEVERR_INDEX);

@@ -290,6 +290,11 @@ def _int32s(t, n: int, what: str) -> None:
         raise ValueError(f"{what} must be contiguous int32 with at least {n} elements")
 
 
+def _rows_of_table(t, n: int) -> None:
+    if t is not None and t.__class__ is not int and t.shape[0] < n:
+        raise ValueError(f"page_table must have a row for each of the {n} sequences")
+
+
 def _dtype_code(t) -> int:
     import torch
     if t.dtype == torch.float32:
@@ -601,6 +606,7 @@ def hash_attn_append(tokens, cache, q, k, v, page_table, cu, seq_lens, q_out, K,
     _whole(W, tokens.h_kv * 32 * tokens.d, 4, "W")
     _int32s(cu, tokens.n_seq + 1, "cu")
     _int32s(seq_lens, tokens.n_seq, "seq_lens")
+    _rows_of_table(page_table, tokens.n_seq)
     a = _here(q, k, v, W, page_table, cu, seq_lens, q_out, K, V, k_sig, dev_flags)
     _check(lib().hash_attn_append(ctypes.byref(tokens), ctypes.byref(cache), None if rope is None else ctypes.byref(rope),
                                   *a, _stream(stream)))
@@ -629,6 +635,7 @@ def hash_attn_chunk(tokens, cache, q, K, V, page_table, cu, seq_lens, out, lse, 
     _whole(lse, rows, 4, "lse")
     _int32s(cu, tokens.n_seq + 1, "cu")
     _int32s(seq_lens, tokens.n_seq, "seq_lens")
+    _rows_of_table(page_table, tokens.n_seq)
     a = _here(q, K, V, page_table, cu, seq_lens, out, lse, workspace)
     _check(lib().hash_attn_chunk(ctypes.byref(tokens), ctypes.byref(cache), *a,
                                  workspace.numel() * workspace.element_size(), _stream(stream)))

@@ -648,6 +648,29 @@ def test_append(H, case):
     assert torch.equal(K1, K) and torch.equal(V1, V)
 
 
+@pytest.mark.parametrize("n,most", [(40, 3), (700, 2), (5000, 1)])
+def test_append_to_many_sequences(H, n, most):
+    """Sequences without new tokens among the others; every token at its place, nothing flagged."""
+    g = torch.Generator(device="cuda").manual_seed(34)
+    rng = np.random.default_rng(n)
+    new = [int(x) for x in rng.integers(0, most + 1, n)]
+    lens = [a + int(x) for a, x in zip(new, rng.integers(0, 70, n))]
+    Hkv, d, ps = 2, 64, 16
+    K, V, table = pages(g, lens, ps, Hkv, d, dirty=False)
+    k, v = rand(g, sum(new), Hkv, d), rand(g, sum(new), Hkv, d)
+    tok, flags = H.make_tokens(k, k, v, n), torch.zeros(1, dtype=torch.int32, device="cuda")
+    before = K.clone()
+    H.hash_attn_append(tok, H.make_cache(K, V, table), None, k, v, table, cumulative(new),
+                       torch.tensor(lens, dtype=torch.int32, device="cuda"), None, K, V, dev_flags=flags)
+    assert int(flags) == 0
+    seq = torch.tensor([s for s, a in enumerate(new) for _ in range(a)], device="cuda")
+    pos = torch.tensor([l - a + i for a, l in zip(new, lens) for i in range(a)], device="cuda")
+    page, row = table[seq, pos // ps].long(), pos % ps
+    assert torch.equal(K[page, :, row], k) and torch.equal(V[page, :, row], v)
+    before[page, :, row] = k
+    assert torch.equal(K, before)
+
+
 def test_append_far_positions(H):
     """Every position keeps its angle to 2^-21, up to the longest cache (2^30 tokens)."""
     d, ps = 64, 1 << 10

@@ -188,6 +188,10 @@ def test_binding_refuses_outputs_that_do_not_fit(ha):
             for v in values:
                 with pytest.raises(ValueError, match="must be contiguous"):
                     call(**{name: v})
+    table = table[:1]  # two sequences
+    for call in (chunk, append):
+        with pytest.raises(ValueError, match="a row for each"):
+            call()
 
 
 # ---------------------------------------------------------------- the oracle
