@@ -1345,6 +1345,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 fence_async_shared();
                 if (valid) p.lse[row] = l == 0.f ? -INFINITY : fmaf(m, p.qscale, log2f(l)) * 0.6931471805599453f;
             } else if (any) {
+                // one warp's rows: their stores are few, the exchange would be code to fetch
+                const bool few = parity && g.tokens <= p.TS;
                 const RowPair rows = pair_rows(whole ? reinterpret_cast<char*>(p.out) + row * (D * (F32OUT ? 4 : 2))
                                                      : reinterpret_cast<char*>(p.part_o) + row * (D * 4), valid, lane);
                 // W columns of O (both streams' where there are two), scaled
@@ -1375,7 +1377,14 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         take(cc, o);
 #pragma unroll
                         for (int k = 0; k < 16; ++k) w[k] = pack_bf16(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
-                        store_rows(w, rows, cc * 2, p.out_align32);
+                        if (few) {
+                            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.out) + row * (D * 2) + cc * 2);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (valid) dst[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                        } else {
+                            store_rows(w, rows, cc * 2, p.out_align32);
+                        }
                     }
                 } else {
 #pragma unroll 1
