@@ -32,6 +32,10 @@
  *  - `stream` is a cudaStream_t passed as void* (NULL = the legacy default
  *    stream). All work is enqueued on it; no call synchronises except
  *    hash_attn_device_status and hash_attn_workspace_init's caller-visible copy.
+ *    A call sees everything that earlier work on its stream wrote. Kernels start
+ *    ahead of their predecessors' ends (programmatic dependent launch), which
+ *    asks one thing of a caller's kernel that does the same: it executes
+ *    griddepcontrol.wait before griddepcontrol.launch_dependents.
  *  - Argument errors are found on the host and returned BEFORE anything is
  *    enqueued. Errors that only the device can see (a seq_len outside
  *    [0, n_cap], a per-sequence budget above the bound, an index outside
@@ -182,12 +186,13 @@ int32_t hash_attn_select_capacity(int32_t n_cap, int32_t m, int32_t n_sink, int3
  * builds each head's selection mask from the codes and attends over the union
  * of the group's rows (each row read once per group; K/V must then be finite,
  * since a row of one head's set is multiplied by weight 0 into the others').
- * The scan may start while the previous kernel in the stream drains: it waits
- * for it before writing workspace state. Otherwise the selection writes per-head
+ * The scan waits for the previous kernel in the stream before it reads an input;
+ * where that is the group kernel of the previous call on this workspace, it only
+ * waits for it before writing workspace state. Otherwise the selection writes per-head
  * lists (or sel_idx) and GATHER-ATT runs per query head. The dense path runs one
  * kernel: per GQA group on the same shapes (each row read once per group; its
- * copies may start while the previous kernel drains, its results are written
- * after it), else per query head.
+ * copies may start while the previous call's group kernel drains, like the scan's,
+ * its results are written after it), else per query head.
  * Errors: HA_ERR_INVALID_ARG, HA_ERR_UNSUPPORTED, HA_ERR_WORKSPACE before
  * launch; HA_ERR_CUDA on a failed launch.
  */

@@ -34,6 +34,7 @@ constexpr int kFusedRange = 8192;         // tokens per range of the fused selec
 // counters   uint32[heads]  split-K arrival counters of GATHER-ATT
 // score_cnt  uint32[batch*h_kv]          SCORE arrival counters
 // tot, ready                             fused selection totals and ready flags
+// busy       uint32[2]                    tag of the decode call that runs, its pairs done
 // scratch (its layout depends on the budget, the options and the path):
 // chunk_hist uint32[heads][nchunks][33]  SCORE histogram of every chunk
 // seg_cnt    int32 [heads][nseg]         selected tokens of every segment (one
@@ -64,6 +65,7 @@ struct Layout {
     size_t off_meta_tt = 0;             // fused: per (pair, head) int2 {t, total}
     size_t off_tot = 0;                 // fused: per (pair, head) 36-word distance histogram (zero at rest)
     size_t off_ready = 0;               // fused: per pair, shares-complete flag (zero at rest)
+    size_t off_busy = 0;                // {tag of the decode call that runs, its pairs done} (zero at rest)
     int64_t d_sp = 0;                   // fused: words per row of the distance buffer
     size_t total = 0;
 };
@@ -150,6 +152,7 @@ struct FusedSelParams {
     uint32_t* ready;         // [B * Hkv] or null: set to `epoch` once a pair's shares are
                              // written (k_group_att waits for that value and resets it)
     uint32_t epoch;          // nonzero tag of the call (a flag left by an earlier call differs)
+    uint32_t* busy;          // {tag of the call that runs, pairs done} (see earlier_call_runs) or null
     int32_t* list;           // [B * Hq][cap] selected tokens, ascending
     int cap;
     int32_t* cnt;            // [B * Hq]
@@ -377,8 +380,8 @@ cudaError_t launch_select(const SelectParams& p, int batch_hkv, cudaStream_t st,
 cudaError_t launch_select_fused(const FusedSelParams& p, int batch_hkv, cudaStream_t st);
 // k_sel_scan alone (the threshold metadata, no lists); write_dist = false leaves
 // out the packed distances (their consumer recomputes them from the codes);
-// pdl = true lets its counting overlap the previous kernel in the stream.
-cudaError_t launch_sel_scan(const FusedSelParams& p, int batch_hkv, cudaStream_t st, bool write_dist, bool pdl);
+// its counting may overlap the previous call's group kernel (inputs_are_there).
+cudaError_t launch_sel_scan(const FusedSelParams& p, int batch_hkv, cudaStream_t st, bool write_dist);
 cudaError_t launch_compact(const CompactParams& p, int heads, cudaStream_t st);
 cudaError_t launch_hist(const HistParams& p, int heads, cudaStream_t st);
 cudaError_t launch_gather(const GatherParams& p, int d, int kv_bf16, cudaStream_t st, bool pdl = false);
@@ -553,6 +556,32 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 // before touching the predecessor's outputs. launch_dependents lets the next
 // such kernel start early (it changes only when it may start, not what it sees).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// For the first kernel of a decode call, which waits (pdl_wait) before it reads an input unless
+// this is true. The kernel before it in the stream may be the one that writes the lengths, the
+// query, the codes or the rows (an append, a code map, the caller's own), so it has to have
+// completed, unless it is known to be an earlier decode call's group kernel, which writes none of
+// them. It is known where a call that began on this workspace has not ended (busy[0], see
+// mark_busy and mark_pair_done): a kernel between the two would have waited for that call's
+// before it let this one start. Nothing from before that call can be running either, for the same
+// reason. busy null: launched normally. (Decode calls with nothing between them, 16 x 131,072
+// tokens: 205.9 us a step, with a plain wait 209.8; one sequence of 32K tokens 18.9 and 22.0.)
+__device__ __forceinline__ bool earlier_call_runs(const uint32_t* busy) {
+    uint32_t a = 0u;
+    if (busy != nullptr) asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(a) : "l"(busy) : "memory");
+    return a != 0u;
+}
+// One thread of that kernel: the call with this tag has begun.
+__device__ __forceinline__ void mark_busy(uint32_t* busy, uint32_t tag) {
+    if (busy != nullptr) asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(busy), "r"(tag) : "memory");
+}
+// One thread, for each of the call's pairs at its end: with the last one the call has ended (the
+// next one may have begun, and put its own tag there). Pairs of two calls do not
+// mix: a group kernel ends its pairs when the call before has completed.
+__device__ __forceinline__ void mark_pair_done(uint32_t* busy, uint32_t tag, uint32_t pairs) {
+    if (busy == nullptr || atomicAdd(busy + 1, 1u) < pairs - 1u) return;
+    busy[1] = 0u;
+    atomicCAS(busy, tag, 0u);
+}
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }

@@ -497,6 +497,8 @@ ha_status decode_impl(const ha_shape* s, const void* q, const uint32_t* q_sig, c
             GroupAttParams ga{};
             ga.sel = dense_sel_params(s, v, seq_lens);
             ga.sel.kv_mul = kv_magic(kdiv);
+            ga.sel.busy = at<uint32_t>(ws, lay.off_busy);
+            ga.sel.epoch = next_call_tag();
             ga.att = gp;
             ga.nsplit = group_dense_splits(bhkv, s->n_cap);
             HA_LAUNCH(launch_group_dense(ga, s->d, bhkv, st, true), "GATHER-ATT launch");
@@ -517,11 +519,10 @@ ha_status decode_impl(const ha_shape* s, const void* q, const uint32_t* q_sig, c
         ga.sel.kv_mul = kv_magic(kdiv);
         ga.sel.ready = at<uint32_t>(ws, lay.off_ready);
         ga.sel.epoch = next_call_tag();
+        ga.sel.busy = at<uint32_t>(ws, lay.off_busy);
         ga.att = gp;
         ga.nsplit = group_splits((int64_t)bhkv * lay.nranges);
-        // the scan's counting may overlap the previous call's last kernel (not the
-        // map kernels, whose codes it reads)
-        HA_LAUNCH(launch_sel_scan(ga.sel, bhkv, st, false, map == nullptr), "SCORE+TOPK launch");
+        HA_LAUNCH(launch_sel_scan(ga.sel, bhkv, st, false), "SCORE+TOPK launch");
         HA_TRY(record(events, 1, st));
         HA_TRY(record(events, 2, st));
         HA_LAUNCH(launch_group_att(ga, s->d, bhkv, st, true), "GATHER-ATT launch");
@@ -739,6 +740,8 @@ Layout make_layout(const ha_shape& s, int64_t rows_cap, bool with_selection, int
     off = align_up(off + (size_t)pairs * 4 * 36 * 4, 256);
     L.off_ready = off;    // fused: per pair, shares-complete flag
     off = align_up(off + (size_t)pairs * 4, 256);
+    L.off_busy = off;     // {tag of the decode call that runs, its pairs done}
+    off = align_up(off + 8, 256);
     // scratch: written by every call before it reads it
     if (with_selection) {
         L.chunk = choose_chunk(pairs, s.n_cap);

@@ -126,7 +126,9 @@ template <typename TI, typename TC>
 __global__ void __launch_bounds__(kAppWarps * 32) k_append(const AppendParams p) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();
-    pdl_launch_dependents();  // the kernel that writes the codes may read everything but the cache
+    // The kernel that writes the codes may read everything but the cache ahead of its wait. Any other
+    // kernel of the library waits before it reads what an append may write.
+    pdl_launch_dependents();
     if (blockIdx.y == 0 && p.flags != nullptr) {
         // the sequences' bounds, once
         for (int s = blockIdx.x * kAppWarps * 32 + tid; s < p.n_seq; s += gridDim.x * kAppWarps * 32) {

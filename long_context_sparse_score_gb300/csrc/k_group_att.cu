@@ -168,6 +168,11 @@ __global__ void __launch_bounds__(32 * NW, GCfg<D, ST, NW>::MINB) k_group_att(co
     const int range = lin % p.nranges;
     const int g = lin / p.nranges;
     const int pair = b * p.Hkv + g;
+    // (behind the scan there is nothing to look for: it lets this grid start once it has looked)
+    if constexpr (DENSE) {
+        if (!earlier_call_runs(p.busy)) pdl_wait();
+        if (blockIdx.x == 0 && tid == 0) mark_busy(p.busy, p.epoch);
+    }
     const int n = checked_len(p.seq_lens, b, p.n_cap, p.err, range == 0 && g == 0 && split == 0 && tid == 0);
     // ranges past the sequence's end hold no rows: their CTAs leave at once, and
     // the pair's parts are those of the live ranges (range 0 always runs)
@@ -245,8 +250,8 @@ __global__ void __launch_bounds__(32 * NW, GCfg<D, ST, NW>::MINB) k_group_att(co
     // launch), so the flag comes; the wait is bounded all the same.
     __shared__ int s_go;
     if (DENSE) {
-        // nothing to wait for before the copies: the inputs are the caller's, and the
-        // partials and counters are written after the wait below
+        // nothing more to wait for before the copies: the partials and counters are written
+        // after the wait below
     } else if (p.ready != nullptr) {
         if (tid == 0) {
             int ok = 0;
@@ -634,7 +639,10 @@ __global__ void __launch_bounds__(32 * NW, GCfg<D, ST, NW>::MINB) k_group_att(co
         }
     }
     if (nlive == 1) {
-        if (tid == 0 && p.ready != nullptr) p.ready[pair] = 0u;
+        if (tid == 0) {
+            if (p.ready != nullptr) p.ready[pair] = 0u;
+            mark_pair_done(p.busy, p.epoch, (uint32_t)(p.B * p.Hkv));
+        }
         return;
     }
 
@@ -648,6 +656,8 @@ __global__ void __launch_bounds__(32 * NW, GCfg<D, ST, NW>::MINB) k_group_att(co
     __syncthreads();
     if (!s_last) return;
     __threadfence();
+    // (before the merge, which the two atomics would lengthen)
+    if (tid == kGT - 1) mark_pair_done(p.busy, p.epoch, (uint32_t)(p.B * p.Hkv));
     // Merge the pair's parts per head (Nectar Eq. (3.4)). One warp per head finds
     // the head's maximum over all parts, then, for blocks of up to kMB parts, each
     // part's weight 2^(m_r - M) once (in the ring's shared memory, free again), and

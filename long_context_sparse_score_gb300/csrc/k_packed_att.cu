@@ -432,8 +432,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         tmap_prefetch(&tmV);
     }
     if (warp == kMmaWarp) tmem_alloc(smem_addr(s_tmem), kTmemCols);
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();  // behind the wait, so that what the next kernel may find running is this one alone
 
     tc_fence_before();
     __syncthreads();
@@ -1463,8 +1463,8 @@ __global__ void __launch_bounds__(256) k_packed_merge(const PackedParams p) {
     constexpr int E = D / 32;
     __shared__ float s_acc[8][D];
     __shared__ float2 s_ml[8];
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
     const SplitItem d = p.items[blockIdx.x];
     if (d.parts <= 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -78,6 +78,11 @@ __global__ void __launch_bounds__(kSelThreads, WD ? 5 : 8) k_sel_scan(const Fuse
     // one KV head complete together (and a cache shared by the batch is read once)
     const int b = blockIdx.x % p.B, range = (blockIdx.x / p.B) % p.nranges, g = blockIdx.x / (p.B * p.nranges);
     const int pair = b * p.Hkv + g;
+    const bool ahead = earlier_call_runs(p.busy);
+    for (int x = tid; x < HA_NBINS * 2 * 32; x += NT) (&hist[0][0][0])[x] = 0u;
+    for (int x = tid; x < 3 * 4 * (HA_NBINS + 3); x += NT) (&s_h[0][0][0])[x] = 0u;
+    if (!ahead) pdl_wait();
+    if (blockIdx.x == 0 && tid == 0) mark_busy(p.busy, p.epoch);
     const int n = checked_len(p.seq_lens, b, p.n_cap, p.err, range == 0 && g == 0 && tid == 0);
     // ranges past the sequence's end hold no tokens: they leave at once, and the
     // pair's last CTA counts only the live ones (range 0 always runs)
@@ -93,9 +98,7 @@ __global__ void __launch_bounds__(kSelThreads, WD ? 5 : 8) k_sel_scan(const Fuse
     uint32_t qs[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) qs[e] = (e < nh) ? p.q_sig[head0 + e] : 0u;
-    for (int x = tid; x < HA_NBINS * 2 * 32; x += NT) (&hist[0][0][0])[x] = 0u;
-    for (int x = tid; x < 3 * 4 * (HA_NBINS + 3); x += NT) (&s_h[0][0][0])[x] = 0u;
-    pdl_launch_dependents();
+    pdl_launch_dependents();  // the next kernel reads the query ahead of this one's results
     __syncthreads();
 
     {
@@ -203,9 +206,8 @@ __global__ void __launch_bounds__(kSelThreads, WD ? 5 : 8) k_sel_scan(const Fuse
                 if (e < nh) atomicAdd(&s_h[which][e][(w >> (8 * e)) & 0xffu], 1u);
         }
     }
-    // Launched with programmatic dependent launch, everything above (reads of the
-    // codes, this CTA's shared memory) may overlap the previous kernel in the
-    // stream; everything below writes state that the previous call's kernels may
+    // Everything above (reads of the codes, this CTA's shared memory) may overlap the
+    // previous call's group kernel; everything below writes state that its kernels may
     // still read (published sums, totals, shares), so wait for it here (every
     // kernel of the library waits for its own predecessor before it completes, so
     // this orders the calls).
@@ -490,14 +492,14 @@ cudaError_t launch_select_fused(const FusedSelParams& p, int batch_hkv, cudaStre
     return launch_ex(k_sel_emit, grid, dim3(kSelThreads), 0, st, true, p);
 }
 
-cudaError_t launch_sel_scan(const FusedSelParams& p, int batch_hkv, cudaStream_t st, bool write_dist, bool pdl) {
+cudaError_t launch_sel_scan(const FusedSelParams& p, int batch_hkv, cudaStream_t st, bool write_dist) {
     const dim3 grid((unsigned)batch_hkv * (unsigned)p.nranges);
     if (p.G == 4) {
-        if (write_dist) return launch_ex(k_sel_scan<true, 4>, grid, dim3(kSelThreads), 0, st, pdl, p);
-        return launch_ex(k_sel_scan<false, 4>, grid, dim3(kSelThreads), 0, st, pdl, p);
+        if (write_dist) return launch_ex(k_sel_scan<true, 4>, grid, dim3(kSelThreads), 0, st, true, p);
+        return launch_ex(k_sel_scan<false, 4>, grid, dim3(kSelThreads), 0, st, true, p);
     }
-    if (write_dist) return launch_ex(k_sel_scan<true, 0>, grid, dim3(kSelThreads), 0, st, pdl, p);
-    return launch_ex(k_sel_scan<false, 0>, grid, dim3(kSelThreads), 0, st, pdl, p);
+    if (write_dist) return launch_ex(k_sel_scan<true, 0>, grid, dim3(kSelThreads), 0, st, true, p);
+    return launch_ex(k_sel_scan<false, 0>, grid, dim3(kSelThreads), 0, st, true, p);
 }
 
 }  // namespace ha
