@@ -51,6 +51,7 @@
 // memory before the CTA exits.
 #include <climits>
 
+#include "packed_order.h"
 #include "tc_common.cuh"
 
 namespace ha {
@@ -869,16 +870,15 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 }
                 Slot v = at.ahead(1);
                 if (NB == 3 && nt > 0) {
-                    // Products k = 0 .. N - 1 in the order (key tile, stream), or (one row tile) the
-                    // key tiles in turn: S of k + 3 goes where P of k was, right behind its P V.
-                    const int N = parity ? nt : e0 + nt;
-                    // the last product of its key tile: row tile 1's
-                    auto second = [&](int k) { return parity || k >= 2 * e0 || (k & 1) != 0; };
+                    // Products k = 0 .. N - 1 (see Products): S of k + 3 goes where P of k was, right
+                    // behind its P V.
+                    const Products order{e0, nt, parity};
+                    const int N = order.count();
                     int ks = 0;  // the next S, its K tile
                     Slot kt = at;
                     bool k_in = false, v_in = false;
                     auto next_s = [&]() {
-                        const bool last = second(ks);
+                        const bool last = order.last_of_tile(ks);
                         if (!k_in) wait_slot(kt);
                         k_in = !last;
                         if (elect_one()) {
@@ -898,8 +898,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     int begun = 0;  // per stream (bit t): O holds something; float32: half of a pair of tiles
 #pragma unroll 1
                     for (int k = 0; k < N; ++k) {
-                        const bool last = second(k);
-                        const int t = parity ? k & 1 : (last ? 1 : 0);
+                        const bool last = order.last_of_tile(k);
+                        const int t = order.stream(k, last);
                         if (!v_in) wait_slot(v);
                         v_in = !last;
                         wait(p_full((int)pb), pph);
@@ -1085,9 +1085,12 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             const int jlast = g.jb + g.nt - 1;
             const bool clears = g.kend < (jlast + 1) * KT && (t == 0 || parity || jlast >= g.jb + st0);
             int j = parity ? g.jb + t : g.jb;
-            // three places: the number of the product of this stream's tile i; whether it has
-            // finished P V (the place's earlier products have, where S of a later one is there)
-            auto product = [&](int tt, int i) { return kb + (uint32_t)(parity ? 2 * i + tt : (i < g.e0 ? 2 * i + tt : g.e0 + i)); };
+            // three places: the number of the product of a stream's tile i; whether it has finished
+            // P V. A barrier that has gone on by two phases looks like one that has not moved, so
+            // product k + 3 must not finish before a warp has found k: before a stream's last
+            // tile it comes behind a product that waits for the stream's P; behind it, see below.
+            const Products order{g.e0, g.nt, parity};
+            auto product = [&](int tt, int i) { return kb + (uint32_t)order.of(tt, i); };
             auto wait_o = [&](uint32_t k) { wait(o_done((int)(k % 3u)), (k / 3u) & 1u); };
 #pragma unroll 1
             for (int i = 0; i < nt; ++i, j += jstep) {
@@ -1264,7 +1267,13 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             odc[0] += F32OUT ? (uint32_t)st0 : (st0 > 0 ? 1u : 0u);
             odc[1] += F32OUT ? (uint32_t)st1 : (st1 > 0 ? 1u : 0u);
             if (NB == 3) {
-                if (nt > 0) wait_o(product(t, nt - 1));
+                // Nothing of row tile 0 holds back what comes behind its last product. Where a product
+                // of this segment uses that place again (128 tokens a row tile and tiles of 64
+                // keys: float32, one head per KV head), it waits for the segment's end instead;
+                // elsewhere the place's next product is one of the next segment, which
+                // waits for both streams' O.
+                if (F32OUT && order.lapped(t)) wait(seg_done, nd & 1u);
+                else if (nt > 0) wait_o(product(t, nt - 1));
             } else if (nt > 0) {
                 wait(o_done(t), (odc[t] - 1u) & 1u);
             }
@@ -1402,7 +1411,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         p.part_ml[row] = make_float2(m, l);
                 }
             }
-            kb += (uint32_t)(parity ? g.nt : g.e0 + g.nt);
+            kb += (uint32_t)order.count();
             if (put) {
                 ring += 2u;
                 __syncwarp();
