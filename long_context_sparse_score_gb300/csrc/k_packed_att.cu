@@ -94,6 +94,7 @@ struct AttCfg {
     // up to 500 tokens 152 -> 141. At d 64 there is half as much to write, and it cost (16,384
     // tokens 1106 -> 1151).
     static constexpr bool kStaged = !F32OUT && D == 128;
+    static_assert(!kStaged || kStages <= 5, "a staged item's second slot waits for the staged item before");
     static constexpr int kBars = (2 * kStages + 8 + 3 * kPlaces + 2 * kQueue + 1) & ~1;  // the segments behind them are read as vectors
     static constexpr int kSmem = 2 * kQTile + kStages * kTile + 2048 + 8 * kBars + 64 * kQueue + 16;
     static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -1330,9 +1331,14 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 cb *= inv;
             }
             const bool put = staged(g), box = put && (t == 0 || g.tokens == t2);
+            const uint32_t kput = ring + (uint32_t)t, sput = kput % (uint32_t)S;
+            // (Also without a box to put there: stream 1's slot comes at least five tiles behind
+            // the first slot of the staged item before, so it is free only once that item's rows
+            // have been sent, and staged_full cannot complete a second phase before the
+            // Q warp has found the first.)
+            if (put) wait(empty((int)sput), ((kput / (uint32_t)S) & 1u) ^ 1u);
             if (box) {
-                const uint32_t k = ring + (uint32_t)t, s = k % (uint32_t)S;
-                wait(empty((int)s), ((k / (uint32_t)S) & 1u) ^ 1u);
+                const uint32_t s = sput;
                 uint8_t* tile = s_raw + 2 * C::kQTile + s * C::kTile + r * 128;
 #pragma unroll 1
                 for (int cc = 0; cc < D; cc += 32) {

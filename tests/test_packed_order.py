@@ -93,3 +93,27 @@ def test_row_tiles_that_can_lap(G, keys):
     tq = 128 // G
     most = max(-(-(seen + x) // keys) - -(-seen // keys) for seen in range(1, 300) for x in range(tq + 1))
     assert (most > 1) == (keys == 64 and G == 1)
+
+
+# ---------------------------------------------------------------- rows that leave through the ring
+
+def second_phase_possible(stages, nt, full, all_wait):
+    """Staged item A's rows lie in ring slots 0 and 1 (of the tiles counted from there), the next
+    staged item has nt key tiles, and the warp that sends rows off has not looked at A's barrier yet,
+    so neither slot is free again. Can all eight warps arrive for the next item? ``full``: its second row
+    tile has a box to put; ``all_wait``: stream 1 waits for its slot without one too."""
+    tiles = range(2, 2 + 2 * nt)
+    if any(i >= stages and i - stages < 2 for i in tiles) or tiles[-1] >= stages + 2:
+        return False  # the loader stands before A's slots
+    waits = [tiles[-1] + 1] + ([tiles[-1] + 2] if full or all_wait else [])
+    return not any(0 <= i - stages < 2 for i in waits)
+
+
+def test_staged_rows_are_found_before_the_next_are_there():
+    for nt in range(1, 40):
+        for full in (False, True):
+            assert not second_phase_possible(5, nt, full, True)
+    # without the wait: a next item of one key tile whose second row tile is not full
+    assert [(nt, full) for nt in range(1, 40) for full in (False, True) if second_phase_possible(5, nt, full, False)] == [(1, False)]
+    # with a ring of more stages the wait would not hold it back
+    assert second_phase_possible(6, 1, True, True)
