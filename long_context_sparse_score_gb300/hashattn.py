@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from ._build import LIB_PATH
 
@@ -263,36 +264,71 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
-def _here(*tensors) -> list:
+def _here(device: int, *tensors) -> list:
     """Addresses of the arguments (tensors, raw addresses or None); a tensor that is not
     on the current device, whose stream the call uses, is refused."""
-    device, out = _device(), []
-    for t in tensors:
-        if t is not None and t.__class__ is not int:
-            if t.get_device() != device:
-                raise ValueError(f"tensor on {t.device}: every argument must be on the current CUDA device")
-            t = t.data_ptr()
-        out.append(t)
-    return out
+    return [t if t is None or t.__class__ is int else t.data_ptr() if t.get_device() == device else _elsewhere(t) for t in tensors]
 
 
-_ITEM = (4, 2)  # bytes of an HA_F32, an HA_BF16
+def _elsewhere(t):
+    raise ValueError(f"tensor on {t.device}: every argument must be on the current CUDA device")
 
 
-def _whole(t, n: int, item: int, what: str) -> None:
-    """A contiguous tensor of n elements (raw addresses are the caller's word)."""
-    if t is not None and t.__class__ is not int and (t.numel() != n or t.element_size() != item or not t.is_contiguous()):
-        raise ValueError(f"{what} must be contiguous, with {n} elements of {item} bytes")
+def _types() -> tuple:
+    """float32, torch's types of HA_F32 and HA_BF16, those of a 32-bit integer (kept once torch is there)."""
+    global _types
+    import torch
+    types = (torch.float32, (torch.float32, torch.bfloat16), (torch.int32, torch.uint32))
+    _types = lambda: types  # noqa: E731
+    return types
 
 
-def _int32s(t, n: int, what: str) -> None:
-    if t is not None and t.__class__ is not int and (t.element_size() != 4 or t.numel() < n or not t.is_contiguous()):
-        raise ValueError(f"{what} must be contiguous int32 with at least {n} elements")
+# What a call reads and writes goes by its descriptors, so a tensor that is smaller, or laid out
+# otherwise, than the one a descriptor was made from would be read or written past its end. The
+# checks below take a tensor as the descriptor tells of it; raw addresses are the caller's word.
+# A call first looks at everything in one expression (what is not a tensor ends it with an
+# AttributeError), and only where that fails at one thing after the other, to say what is wrong:
+# 1 us less of a call's 8 (the rest of the checks' 2 is torch's own, for shapes, strides and types).
+_fields_of_tokens = struct.Struct("8i6q").unpack_from
+_fields_of_cache = struct.Struct("4i9q").unpack_from
 
 
-def _rows_of_table(t, n: int) -> None:
-    if t is not None and t.__class__ is not int and t.shape[0] < n:
+def _whole(*specs) -> None:
+    """(tensor, elements, type, name): contiguous tensors."""
+    for t, n, dtype, what in specs:
+        if t is not None and t.__class__ is not int and (t.numel() != n or t.dtype is not dtype or not t.is_contiguous()):
+            raise ValueError(f"{what} must be contiguous, with {n} elements of {dtype}")
+
+
+def _int32s(*specs) -> None:
+    """(tensor, least elements, name): contiguous 32-bit integers."""
+    ints = _types()[2]
+    for t, n, what in specs:
+        if t is not None and t.__class__ is not int and (t.numel() < n or t.dtype not in ints or not t.is_contiguous()):
+            raise ValueError(f"{what} must be contiguous int32 with at least {n} elements")
+
+
+def _as_made(*specs) -> None:
+    """(tensor, shape, strides, type, name): tensors of this shape, type and strides (those of
+    extents over 1)."""
+    for t, shape, strides, dtype, what in specs:
+        if t is None or t.__class__ is int or (t.shape == shape and t.stride() == strides and t.dtype is dtype):
+            continue
+        if t.shape != shape or t.dtype is not dtype or (0 not in shape and any(
+                n > 1 and a != b for n, a, b in zip(shape, t.stride(), strides))):
+            raise ValueError(f"{what} is {tuple(t.shape)} of {t.dtype} with strides {t.stride()}: its descriptor was made "
+                             f"for {shape} of {dtype} with strides {strides}")
+
+
+def _table_as_made(t, n: int, pages: int, stride: int) -> None:
+    if t is None or t.__class__ is int:
+        return
+    rows, cols = t.shape
+    if rows < n:
         raise ValueError(f"page_table must have a row for each of the {n} sequences")
+    a, b = t.stride()
+    if cols < pages or (b != 1 and pages > 1) or (a != stride and n > 1) or t.dtype not in _types()[2]:
+        raise ValueError(f"page_table must be int32 with {pages} entries a row, its rows {stride} apart")
 
 
 def _dtype_code(t) -> int:
@@ -579,7 +615,8 @@ def make_cache(K, V, page_table, k_sig=None) -> HACache:
     c.dtype = _dtype_code(K)
     c.k_sp, c.k_sh, c.k_sn = _rows(K, "K", c.dtype, K.shape)[:3]
     c.v_sp, c.v_sh, c.v_sn = _rows(V, "V", c.dtype, K.shape)[:3]
-    if page_table.dim() != 2 or page_table.element_size() != 4 or page_table.stride(1) != 1 and page_table.shape[1] > 1:
+    if (page_table.dim() != 2 or page_table.element_size() != 4 or page_table.is_floating_point()
+            or page_table.stride(1) != 1 and page_table.shape[1] > 1):
         raise ValueError("page_table must be int32 [n_seq, max_pages] with contiguous rows")
     c.max_pages, c.table_st = page_table.shape[1], page_table.stride(0)
     if k_sig is not None:
@@ -590,8 +627,11 @@ def make_cache(K, V, page_table, k_sig=None) -> HACache:
 
 
 def rope(inv_freq, interleaved: bool = False) -> HARope:
-    """HARope over a float32 device tensor inv_freq [rot_dim / 2] (kept by the caller)."""
+    """HARope over a contiguous float32 device tensor inv_freq [rot_dim / 2] (which it keeps)."""
+    if inv_freq.dtype is not _types()[0] or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be contiguous float32")
     r = HARope()
+    r.tensor = inv_freq
     r.inv_freq = _ptr(inv_freq)
     r.rot_dim = 2 * inv_freq.numel()
     r.interleaved = 1 if interleaved else 0
@@ -602,14 +642,37 @@ def hash_attn_append(tokens, cache, q, k, v, page_table, cu, seq_lens, q_out, K,
                      dev_flags=None, stream=None) -> None:
     """Rotate the packed new tokens' q (into ``q_out``) and k by position and write k, v
     (and with ``W`` the keys' codes) into the paged cache; ``q`` and ``q_out`` may be None."""
-    _whole(q_out, tokens.total * tokens.h_q * tokens.d, _ITEM[tokens.dtype], "q_out")
-    _whole(W, tokens.h_kv * 32 * tokens.d, 4, "W")
-    _int32s(cu, tokens.n_seq + 1, "cu")
-    _int32s(seq_lens, tokens.n_seq, "seq_lens")
-    _rows_of_table(page_table, tokens.n_seq)
-    a = _here(q, k, v, W, page_table, cu, seq_lens, q_out, K, V, k_sig, dev_flags)
-    _check(lib().hash_attn_append(ctypes.byref(tokens), ctypes.byref(cache), None if rope is None else ctypes.byref(rope),
-                                  *a, _stream(stream)))
+    f32, types, ints = _types()
+    n, T, h_q, h_kv, d, dtype, _, _, q_st, q_sh, k_st, k_sh, v_st, v_sh = _fields_of_tokens(tokens)
+    pool, n_pages, size, pages, table_st, K_sp, K_sh, K_sn, V_sp, V_sh, V_sn, ks_sp, ks_sh = _fields_of_cache(cache)
+    dtype, pool, rows, cached = types[dtype], types[pool], (T, h_kv, d), (n_pages, h_kv, size, d)
+    try:
+        good = (q.shape == (T, h_q, d) and q.stride() == (q_st, q_sh, 1) and q.dtype is dtype
+                and k.shape == rows and k.stride() == (k_st, k_sh, 1) and k.dtype is dtype
+                and v.shape == rows and v.stride() == (v_st, v_sh, 1) and v.dtype is dtype
+                and K.shape == cached and K.stride() == (K_sp, K_sh, K_sn, 1) and K.dtype is pool
+                and V.shape == cached and V.stride() == (V_sp, V_sh, V_sn, 1) and V.dtype is pool
+                and page_table.shape == (n, pages) and page_table.stride() == (table_st, 1) and page_table.dtype in ints
+                and q_out.numel() == T * h_q * d and q_out.dtype is dtype and q_out.is_contiguous()
+                and cu.numel() == n + 1 and cu.dtype in ints and cu.is_contiguous()
+                and seq_lens.numel() == n and seq_lens.dtype in ints and seq_lens.is_contiguous()
+                and W is None and k_sig is None and dev_flags is None)
+    except AttributeError:
+        good = False
+    if not good:
+        _whole((q_out, T * h_q * d, dtype, "q_out"), (W, h_kv * 32 * d, f32, "W"))
+        _int32s((cu, n + 1, "cu"), (seq_lens, n, "seq_lens"), (dev_flags, 1, "dev_flags"))
+        _as_made((q, (T, h_q, d), (q_st, q_sh, 1), dtype, "q"), (k, rows, (k_st, k_sh, 1), dtype, "k"),
+                 (v, rows, (v_st, v_sh, 1), dtype, "v"), (K, cached, (K_sp, K_sh, K_sn, 1), pool, "K"),
+                 (V, cached, (V_sp, V_sh, V_sn, 1), pool, "V"))
+        _table_as_made(page_table, n, pages, table_st)
+        if k_sig is not None and k_sig.__class__ is not int:
+            _as_made((k_sig, cached[:3], (ks_sp, ks_sh, 1), k_sig.dtype if k_sig.dtype in ints else ints[0], "k_sig"))
+    device = _device()
+    a = _here(device, q, k, v, W, page_table, cu, seq_lens, q_out, K, V, k_sig, dev_flags)
+    if rope is not None:
+        _here(device, getattr(rope, "tensor", None))
+    _check(lib().hash_attn_append(tokens, cache, rope, *a, _raw_stream(device) if stream is None else _stream(stream)))
 
 
 def hash_attn_packed_workspace_size(tokens) -> int:
@@ -620,25 +683,56 @@ def hash_attn_packed_workspace_size(tokens) -> int:
 
 def hash_attn_prefill(tokens, q, K, V, cu, out, lse, *, workspace, stream=None) -> None:
     """Causal attention over packed prompts; out [total, Hq, d], lse [total, Hq] contiguous."""
-    rows = tokens.total * tokens.h_q
-    _whole(out, rows * tokens.d, _ITEM[tokens.out_dtype], "out")
-    _whole(lse, rows, 4, "lse")
-    _int32s(cu, tokens.n_seq + 1, "cu")
-    a = _here(q, K, V, cu, out, lse, workspace)
-    _check(lib().hash_attn_prefill(ctypes.byref(tokens), *a, workspace.numel() * workspace.element_size(), _stream(stream)))
+    f32, types, ints = _types()
+    n, T, h_q, h_kv, d, dtype, out_dtype, _, q_st, q_sh, k_st, k_sh, v_st, v_sh = _fields_of_tokens(tokens)
+    dtype, out_dtype, rows = types[dtype], types[out_dtype], (T, h_kv, d)
+    try:
+        good = (q.shape == (T, h_q, d) and q.stride() == (q_st, q_sh, 1) and q.dtype is dtype
+                and K.shape == rows and K.stride() == (k_st, k_sh, 1) and K.dtype is dtype
+                and V.shape == rows and V.stride() == (v_st, v_sh, 1) and V.dtype is dtype
+                and out.numel() == T * h_q * d and out.dtype is out_dtype and out.is_contiguous()
+                and lse.numel() == T * h_q and lse.dtype is f32 and lse.is_contiguous()
+                and cu.numel() == n + 1 and cu.dtype in ints and cu.is_contiguous())
+    except AttributeError:
+        good = False
+    if not good:
+        _whole((out, T * h_q * d, out_dtype, "out"), (lse, T * h_q, f32, "lse"))
+        _int32s((cu, n + 1, "cu"))
+        _as_made((q, (T, h_q, d), (q_st, q_sh, 1), dtype, "q"), (K, rows, (k_st, k_sh, 1), dtype, "K"),
+                 (V, rows, (v_st, v_sh, 1), dtype, "V"))
+    device = _device()
+    a = _here(device, q, K, V, cu, out, lse, workspace)
+    _check(lib().hash_attn_prefill(tokens, *a, workspace.numel() * workspace.element_size(),
+                                   _raw_stream(device) if stream is None else _stream(stream)))
 
 
 def hash_attn_chunk(tokens, cache, q, K, V, page_table, cu, seq_lens, out, lse, *, workspace, stream=None) -> None:
     """Attention of the packed new tokens over the paged cache (their keys are in it already)."""
-    rows = tokens.total * tokens.h_q
-    _whole(out, rows * tokens.d, _ITEM[tokens.out_dtype], "out")
-    _whole(lse, rows, 4, "lse")
-    _int32s(cu, tokens.n_seq + 1, "cu")
-    _int32s(seq_lens, tokens.n_seq, "seq_lens")
-    _rows_of_table(page_table, tokens.n_seq)
-    a = _here(q, K, V, page_table, cu, seq_lens, out, lse, workspace)
-    _check(lib().hash_attn_chunk(ctypes.byref(tokens), ctypes.byref(cache), *a,
-                                 workspace.numel() * workspace.element_size(), _stream(stream)))
+    f32, types, ints = _types()
+    n, T, h_q, h_kv, d, dtype, out_dtype, _, q_st, q_sh, _, _, _, _ = _fields_of_tokens(tokens)
+    pool, n_pages, size, pages, table_st, K_sp, K_sh, K_sn, V_sp, V_sh, V_sn, _, _ = _fields_of_cache(cache)
+    dtype, out_dtype, pool, cached = types[dtype], types[out_dtype], types[pool], (n_pages, h_kv, size, d)
+    try:
+        good = (q.shape == (T, h_q, d) and q.stride() == (q_st, q_sh, 1) and q.dtype is dtype
+                and K.shape == cached and K.stride() == (K_sp, K_sh, K_sn, 1) and K.dtype is pool
+                and V.shape == cached and V.stride() == (V_sp, V_sh, V_sn, 1) and V.dtype is pool
+                and page_table.shape == (n, pages) and page_table.stride() == (table_st, 1) and page_table.dtype in ints
+                and out.numel() == T * h_q * d and out.dtype is out_dtype and out.is_contiguous()
+                and lse.numel() == T * h_q and lse.dtype is f32 and lse.is_contiguous()
+                and cu.numel() == n + 1 and cu.dtype in ints and cu.is_contiguous()
+                and seq_lens.numel() == n and seq_lens.dtype in ints and seq_lens.is_contiguous())
+    except AttributeError:
+        good = False
+    if not good:
+        _whole((out, T * h_q * d, out_dtype, "out"), (lse, T * h_q, f32, "lse"))
+        _int32s((cu, n + 1, "cu"), (seq_lens, n, "seq_lens"))
+        _as_made((q, (T, h_q, d), (q_st, q_sh, 1), dtype, "q"), (K, cached, (K_sp, K_sh, K_sn, 1), pool, "K"),
+                 (V, cached, (V_sp, V_sh, V_sn, 1), pool, "V"))
+        _table_as_made(page_table, n, pages, table_st)
+    device = _device()
+    a = _here(device, q, K, V, page_table, cu, seq_lens, out, lse, workspace)
+    _check(lib().hash_attn_chunk(tokens, cache, *a, workspace.numel() * workspace.element_size(),
+                                 _raw_stream(device) if stream is None else _stream(stream)))
 
 
 def hash_attn_device_status(workspace, stream=None) -> tuple[int, int]:
