@@ -568,8 +568,8 @@ ha_status hash_attn_merge_n(const float* outs, int64_t out_seg_stride, const flo
  *
  * ha_tokens: the packed new tokens.
  *   n_seq      sequences (>= 1); total: rows of q, k, v, out, lse (0: the call does
- *              nothing). Rows that no sequence owns are neither read for a result
- *              nor written.
+ *              nothing, and their pointers, the workspace and strides are not looked
+ *              at). Rows that no sequence owns are neither read for a result nor written.
  *   h_q, h_kv, d   as ha_shape; h_q % h_kv == 0
  *   dtype      ha_dtype of q, k and v
  *   out_dtype  ha_dtype of out (prefill, chunk). HA_F32 results are float32

@@ -1498,15 +1498,17 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
         return fail(HA_ERR_UNSUPPORTED, "out_dtype must be HA_F32 or HA_BF16 (got %d)", t->out_dtype);
     const int G = t->h_q / t->h_kv;
     if (G > kMaxGroup) return fail(HA_ERR_UNSUPPORTED, "at most %d query heads per KV head (got %d)", kMaxGroup, G);
-    if (cu == nullptr || lse == nullptr || (c != nullptr && seq_lens == nullptr))
-        return fail(HA_ERR_INVALID_ARG, "cu, seq_lens and lse must not be NULL");
-    if (out == nullptr || !aligned16(out)) return fail(HA_ERR_INVALID_ARG, "out must not be NULL and must be 16-byte aligned");
-    HA_TRY(check_rows("q", q, t->dtype, t->d, {{t->total, t->q_st}, {t->h_q, t->q_sh}}));
+    if (cu == nullptr || (c != nullptr && seq_lens == nullptr)) return fail(HA_ERR_INVALID_ARG, "cu and seq_lens must not be NULL");
     if (c != nullptr) {
         HA_TRY(check_cache(c, t, K, V, table));
         if (c->max_pages > 1 && c->page_size % 16 != 0)
             return fail(HA_ERR_UNSUPPORTED, "page_size must be a multiple of 16 (got %d)", c->page_size);
-    } else {
+    }
+    if (t->total == 0) return HA_OK;  // rows of empty tensors may have no address
+    if (lse == nullptr) return fail(HA_ERR_INVALID_ARG, "lse must not be NULL");
+    if (out == nullptr || !aligned16(out)) return fail(HA_ERR_INVALID_ARG, "out must not be NULL and must be 16-byte aligned");
+    HA_TRY(check_rows("q", q, t->dtype, t->d, {{t->total, t->q_st}, {t->h_q, t->q_sh}}));
+    if (c == nullptr) {
         HA_TRY(check_rows("K", K, t->dtype, t->d, {{t->total, t->k_st}, {t->h_kv, t->k_sh}}));
         HA_TRY(check_rows("V", V, t->dtype, t->d, {{t->total, t->v_st}, {t->h_kv, t->v_sh}}));
     }
@@ -1514,7 +1516,6 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
     Layout ws{};
     ws.total = L.total;
     HA_TRY(check_ws(ws, workspace, ws_bytes));
-    if (t->total == 0) return HA_OK;
 
     const bool f32 = t->out_dtype == HA_F32;
     const int kt = packed_key_tile(f32);
@@ -1637,15 +1638,6 @@ extern "C" ha_status hash_attn_append(const ha_tokens* tokens, const ha_cache* c
     HA_TRY(check_tokens(t));
     HA_TRY(check_cache(c, t, K, V, table));
     if (cu == nullptr || seq_lens == nullptr) return fail(HA_ERR_INVALID_ARG, "cu and seq_lens must not be NULL");
-    HA_TRY(check_rows("k", k, t->dtype, t->d, {{t->total, t->k_st}, {t->h_kv, t->k_sh}}));
-    HA_TRY(check_rows("v", v, t->dtype, t->d, {{t->total, t->v_st}, {t->h_kv, t->v_sh}}));
-    if ((q == nullptr) != (q_out == nullptr)) return fail(HA_ERR_INVALID_ARG, "q and q_out must both be given or both be NULL");
-    if (q != nullptr) {
-        HA_TRY(check_rows("q", q, t->dtype, t->d, {{t->total, t->q_st}, {t->h_q, t->q_sh}}));
-        if (!aligned16(q_out)) return fail(HA_ERR_INVALID_ARG, "q_out must be 16-byte aligned");
-        const bool packed = (t->h_q == 1 || t->q_sh == t->d) && (t->total <= 1 || t->q_st == (int64_t)t->h_q * t->d);
-        if (q == q_out && !packed) return fail(HA_ERR_INVALID_ARG, "q_out may be q only if q is contiguous");
-    }
     if (rope != nullptr) {
         if (rope->inv_freq == nullptr) return fail(HA_ERR_INVALID_ARG, "rope->inv_freq is NULL");
         if (rope->rot_dim < 16 || rope->rot_dim > t->d || rope->rot_dim % 16 != 0)
@@ -1656,7 +1648,16 @@ extern "C" ha_status hash_attn_append(const ha_tokens* tokens, const ha_cache* c
     if ((W == nullptr) != (k_sig == nullptr)) return fail(HA_ERR_INVALID_ARG, "W and k_sig must both be given or both be NULL");
     if (W != nullptr && ((t->h_kv > 1 && c->ks_sh < c->page_size) || (c->n_pages > 1 && c->ks_sp < c->page_size)))
         return fail(HA_ERR_INVALID_ARG, "ks_sh and ks_sp must be at least page_size");
-    if (t->total == 0) return HA_OK;
+    if (t->total == 0) return HA_OK;  // rows of empty tensors may have no address
+    HA_TRY(check_rows("k", k, t->dtype, t->d, {{t->total, t->k_st}, {t->h_kv, t->k_sh}}));
+    HA_TRY(check_rows("v", v, t->dtype, t->d, {{t->total, t->v_st}, {t->h_kv, t->v_sh}}));
+    if ((q == nullptr) != (q_out == nullptr)) return fail(HA_ERR_INVALID_ARG, "q and q_out must both be given or both be NULL");
+    if (q != nullptr) {
+        HA_TRY(check_rows("q", q, t->dtype, t->d, {{t->total, t->q_st}, {t->h_q, t->q_sh}}));
+        if (!aligned16(q_out)) return fail(HA_ERR_INVALID_ARG, "q_out must be 16-byte aligned");
+        const bool packed = (t->h_q == 1 || t->q_sh == t->d) && (t->total <= 1 || t->q_st == (int64_t)t->h_q * t->d);
+        if (q == q_out && !packed) return fail(HA_ERR_INVALID_ARG, "q_out may be q only if q is contiguous");
+    }
     AppendParams p{};
     p.q = q;
     p.k = k;

@@ -165,3 +165,28 @@ def test_rope_takes_contiguous_float32_on_the_calls_device(calls, ha):
         calls.append(q=addr, k=addr, v=addr, table=addr, cu=addr, lens=addr, K=addr, V=addr, W=None, sig=None, q_out=addr, rope=r)
     at = ha.rope(torch.ones(D // 2)).tensor  # the struct keeps its tensor
     assert at.numel() == D // 2
+
+
+def test_a_call_without_rows_does_nothing(ha, monkeypatch):
+    """total = 0: empty tensors have no address, and nothing is asked of rows that are not there."""
+    import ctypes
+    monkeypatch.setattr(ha, "_device", lambda: -1)  # host tensors count as here: no kernel is started
+    q, k = bf(0, HQ, D), bf(0, HKV, D)
+    assert q.data_ptr() == 0
+    pool, table, cu, lens = bf(PAGES, HKV, PS, D), ints(N, 4), ints(N + 1), ints(N)
+    room = torch.zeros(1 << 12, dtype=torch.uint8)  # too small for a call with rows
+    for out_dtype in (torch.bfloat16, torch.float32):
+        tokens, cache = ha.make_tokens(q, k, k, N, out_dtype=out_dtype), ha.make_cache(pool, pool, table)
+        out, lse = torch.zeros(0, HQ, D, dtype=out_dtype), torch.zeros(0, HQ)
+        ha.hash_attn_append(tokens, cache, q, k, k, table, cu, lens, bf(0, HQ, D), pool, pool, stream=0)
+        ha.hash_attn_append(tokens, cache, None, k, k, table, cu, lens, None, pool, pool, stream=0)
+        ha.hash_attn_prefill(tokens, q, k, k, cu, out, lse, workspace=room, stream=0)
+        ha.hash_attn_chunk(tokens, cache, q, pool, pool, table, cu, lens, out, lse, workspace=room, stream=0)
+    L, t, c = ha.lib(), ctypes.byref(tokens), ctypes.byref(cache)
+    assert L.hash_attn_prefill(t, None, None, None, 512, None, None, None, 0, None) == ha.HA_OK
+    assert L.hash_attn_chunk(t, c, None, 512, 512, 512, 512, 512, None, None, None, 0, None) == ha.HA_OK
+    assert L.hash_attn_append(t, c, None, None, None, None, None, 512, 512, 512, None, 512, 512, None, None, None) == ha.HA_OK
+    # what is not rows is looked at all the same
+    assert L.hash_attn_prefill(t, None, None, None, None, None, None, None, 0, None) == ha.HA_ERR_INVALID_ARG
+    assert L.hash_attn_chunk(t, c, None, None, 512, 512, 512, 512, None, None, None, 0, None) == ha.HA_ERR_INVALID_ARG
+    assert L.hash_attn_append(t, c, None, None, None, None, None, None, 512, 512, None, 512, 512, None, None, None) == ha.HA_ERR_INVALID_ARG
