@@ -615,7 +615,9 @@ typedef struct {
  * interleaved = 1 (x[2 p], x[2 p + 1]); dims from rot_dim on stay as they are.
  *   inv_freq  float32 [rot_dim / 2], device, finite
  *   rot_dim   a multiple of 16, 16 <= rot_dim <= d
- * The angle is exact modulo a turn to 2^-31 of a half turn at every position.
+ * The angle is reduced modulo a turn before it is rounded: its error is at most
+ * 2^-25 + 2^-32 of a half turn, plus (|inv_freq[p]| + 2) * pos * 2^-64 half turns
+ * (2^-32 for frequencies up to 1 in the longest cache, 2^-18 for 65,504 there).
  */
 typedef struct {
     const float* inv_freq;

@@ -8,11 +8,12 @@
 // turns by the angle pos * inv_freq[p]; the other dims and the values are copied.
 //
 // The angle in turns, pos * inv_freq / 2 pi, is kept as a 64-bit fixed-point
-// fraction: inv_freq's 24-bit significand times 2^64 / 2 pi, shifted, is exact to
-// 2^-64 turns, and the product with pos wraps modulo one turn by itself. So a
-// position of millions loses nothing (in float32 the angle's error alone would
-// be pos * 2^-24), and neither double precision nor a range reduction is needed.
-// Rotations are computed in float32 and rounded once.
+// fraction: inv_freq's 24-bit significand times 2^64 / 2 pi, shifted, is off by less than
+// (|inv_freq| / 2 + 1) 2^-64 turns, and the product with pos wraps modulo one turn by
+// itself. So a position of millions loses next to nothing (in float32 the angle's error
+// alone would be pos * 2^-24), and neither double precision nor a range reduction is
+// needed. The angle is then rounded to float32 in half turns (2^-25 at most, near a whole
+// half turn). Rotations are computed in float32 and rounded once.
 //
 // Bound by memory: every row is read and written once (32,768 tokens of 32 query and
 // 8 KV heads of 128: 135 us, 6.0 TB/s, 88 % of a plain copy). A warp takes one token

@@ -1,5 +1,8 @@
 """Packed attention and append where a wait, a bound or a rounding is at its edge
 (tolerances as in test_gpu_packed unless a test derives its own)."""
+import math
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -43,3 +46,44 @@ def test_items_of_one_key_tile_with_a_part_of_a_second_row_tile(H):  # noqa: F81
         out, lse, st = P.run_prefill(H, q, k, v, new)
         assert st == (0, 0)
         P.check_rows(out.flatten(0, 1), lse.flatten(), ref, True, "prompts")
+
+
+def pi_scaled(bits):
+    """floor(pi 2^bits), nearly: Machin's formula in integers."""
+    one = 1 << (bits + 32)
+
+    def arctan_of_inverse(x):
+        term, n, sign, total = one // x, 3, -1, one // x
+        while term:
+            term //= x * x
+            total += sign * (term // n)
+            n, sign = n + 2, -sign
+        return total
+    return 4 * (4 * arctan_of_inverse(5) - arctan_of_inverse(239)) >> 32
+
+
+def test_every_pair_keeps_its_angle_at_every_position(H):  # noqa: F811
+    """cos and sin of pos inv_freq, each pair by itself, against the angle modulo a turn from whole
+    numbers. The angle is off by 2^-25 + 2^-32 + (|w| + 2) pos 2^-64 half turns at most, its cosine by pi
+    times that; sincospif adds 2 steps of a value below 1 (2^-23)."""
+    d, ps, bits = 64, 1 << 10, 256
+    pi = pi_scaled(bits)
+    assert abs(pi / 2 ** bits - math.pi) < 1e-15
+    x = torch.zeros(1, 1, d, device="cuda")
+    x[..., : d // 2] = 1.0  # a pair (1, 0) becomes (cos, sin)
+    K, V = torch.zeros(1, 1, ps, d, device="cuda"), torch.zeros(1, 1, ps, d, device="cuda")
+    table = torch.zeros(1, 1 << 20, dtype=torch.int32, device="cuda")
+    w = torch.cat([P.inv_freq(d)[:14], torch.tensor([1.0, 0.3333333, 0.99999994, 3.0, 1e-9, 1e-30, 1e-40, 0.0, -0.7, -1e-4, 65504.0],
+                                                    device="cuda"), P.inv_freq(d)[25:]])
+    ws = [Fraction(float(f)) for f in w.cpu()]
+    rng = np.random.default_rng(5)
+    for pos in [0, 1, 2, 12345, 1 << 20, (1 << 24) + 1, (1 << 30) - 1] + [int(p) for p in rng.integers(0, 1 << 30, 20)]:
+        q_out = torch.empty(1, 1, d, device="cuda")
+        P.run_append(H, x, x, x, table, [1], [pos + 1], q_out, K, V, H.rope(w))
+        got = q_out[0, 0].double().cpu().numpy()
+        for p, f in enumerate(ws):
+            half = f * pos * (1 << bits) / pi  # half turns
+            a = math.pi * float(half - 2 * round(half / 2))
+            tol = math.pi * (2.0 ** -25 + 2.0 ** -32 + (abs(float(f)) + 2) * pos * 2.0 ** -64) + 2.0 ** -23 + 1e-15
+            err = max(abs(got[p] - math.cos(a)), abs(got[p + d // 2] - math.sin(a)))
+            assert err <= tol, (pos, float(f), err, tol)
