@@ -87,3 +87,85 @@ def test_every_pair_keeps_its_angle_at_every_position(H):  # noqa: F811
             tol = math.pi * (2.0 ** -25 + 2.0 ** -32 + (abs(float(f)) + 2) * pos * 2.0 ** -64) + 2.0 ** -23 + 1e-15
             err = max(abs(got[p] - math.cos(a)), abs(got[p + d // 2] - math.sin(a)))
             assert err <= tol, (pos, float(f), err, tol)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_scores_in_the_thousands_that_are_exact(H, d, out_dtype):  # noqa: F811
+    """Scores S = 256 h + l of whole numbers: exact in float32, up to 65,535 / sqrt(d), growing from
+    tile to tile, so that O is rescaled again and again and nothing hides in the products' rounding.
+
+    With t = log2(e) S / sqrt(d) at its largest and u = 2^-24: a weight's exponent is x qscale - m qscale
+    with m qscale rounded (u t), which differs between the references m that the sums passed through (2 u t
+    between two of them); qscale itself and the product of each rescaling are rounded (u t each over
+    all of them), and the same once more where parts are joined: 8 u t in all. Then 2^-22 for an
+    exponential, twice, and 2 u for each of n terms."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    T, Hkv, lens, new = 700, 2, [3000, 700, 900], [1, 90, 3]
+    u = 2.0 ** -24
+
+    def keys(n):
+        k = torch.zeros(n, Hkv, d, device="cuda")
+        step = torch.randint(0, 2, (n // 64 + 1,), generator=g, device="cuda") * torch.randint(1, 9, (n // 64 + 1,), generator=g, device="cuda")
+        k[:, :, 0] = torch.cumsum(step, 0).clamp(max=255)[torch.arange(n, device="cuda") // 64][:, None]
+        k[:, :, 1] = torch.randint(0, 256, (n, Hkv), generator=g, device="cuda")
+        return k.bfloat16()
+
+    def queries(n):
+        q = torch.zeros(n, 4 * Hkv, d, device="cuda")
+        q[:, :, 0], q[:, :, 1] = 256.0, 1.0
+        return q.bfloat16()
+
+    def check(out, lse, ref, what):
+        ro, rl, mag, zmax, n = ref
+        t = zmax * math.log2(math.e)
+        E = math.log(2) * 8 * u * t + 2.0 ** -21 + 2 * u * (n + 16)
+        tol = 2 * E[:, None] * mag + 1e-30
+        if out_dtype == torch.bfloat16:
+            tol = tol + 2.0 ** -8 * mag * (1 + 2 * E[:, None]) + 2.0 ** -8 * np.abs(ro) * (1 + 2.0 ** -7)
+        err = np.abs(out.flatten(0, 1).double().cpu().numpy() - ro)
+        assert np.all(err <= tol), f"{what}: out off by {err.max():.3g}, worst ratio {(err / tol).max():.3g}"
+        el = np.abs(lse.flatten().double().cpu().numpy() - rl)
+        assert np.all(el <= E + 2.0 ** -22 * (1 + np.abs(rl))), f"{what}: lse off by {el.max():.3g}"
+
+    q, k, v = queries(T), keys(T), P.rand(g, T, Hkv, d)
+    out, lse, st = P.run_prefill(H, q, k, v, [T], out_dtype)
+    assert st == (0, 0)
+    check(out, lse, P.reference(q, lambda s: k, lambda s: v, [T], [T]), "prefill")
+
+    K, V, table = P.pages(g, lens, 16, Hkv, d)
+    seqs = [keys(n) for n in lens]
+    for s, n in enumerate(lens):
+        j = torch.arange(n, device="cuda")
+        K[table[s].long()[j // 16], :, j % 16] = seqs[s]
+    q = queries(sum(new))
+    out, lse, st = P.run_chunk(H, q, K, V, table, new, lens, Hkv, out_dtype)
+    assert st == (0, 0)
+
+    def values(s):
+        j = torch.arange(lens[s], device="cuda")
+        return V[table[s].long()[j // 16], :, j % 16]
+    check(out, lse, P.reference(q, lambda s: seqs[s], values, new, lens), "chunk")
+
+
+def test_an_infinity_in_v_stays_in_its_sequence_and_behind_its_key_tile(H):  # noqa: F811
+    """V has to be finite within a sequence. Where it is not, rows whose key tiles end before that
+    token, other sequences and other heads keep their values."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    new, Hkv, d = [640, 200], 2, 128
+    T = sum(new)
+    q, k, v = P.rand(g, T, 4 * Hkv, d), P.rand(g, T, Hkv, d), P.rand(g, T, Hkv, d)
+    for out_dtype, tile in ((torch.bfloat16, 128), (torch.float32, 64)):
+        want = P.run_prefill(H, q, k, v, new, out_dtype)
+        bad = v.clone()
+        bad[500, 0, 7] = float("inf")
+        out, lse, st = P.run_prefill(H, q, k, bad, new, out_dtype)
+        assert st == (0, 0) and torch.equal(lse, want[1])
+        first = 500 // tile * tile
+        # an item is 64 tokens, all of whose rows take the key tiles that its last token sees
+        first = first // 64 * 64
+        assert torch.equal(out[:first], want[0][:first]) and torch.equal(out[640:], want[0][640:])
+        assert torch.equal(out[:, 4:], want[0][:, 4:])
+        other = torch.arange(d, device="cuda") != 7
+        assert torch.equal(out[:640, :4][..., other], want[0][:640, :4][..., other])
+        assert not torch.isfinite(out[500:640, :4, 7]).any()
