@@ -96,7 +96,7 @@ struct AttCfg {
     static constexpr bool kStaged = !F32OUT && D == 128;
     static_assert(!kStaged || kStages <= 5, "a staged item's second slot waits for the staged item before");
     static constexpr int kBars = (2 * kStages + 8 + 3 * kPlaces + 2 * kQueue + 1) & ~1;  // the segments behind them are read as vectors
-    static constexpr int kSmem = 2 * kQTile + kStages * kTile + 2048 + 8 * kBars + 64 * kQueue + 16;
+    static constexpr int kSmem = 2 * kQTile + kStages * kTile + 2048 + 8 * kBars + 64 * kQueue + 16 + kKeys;
     static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
 
@@ -122,32 +122,6 @@ __device__ __forceinline__ SeqInfo seq_info(const PackedParams& p, int s, bool r
     return i;
 }
 
-// sum over i < n of floor((a i + b) / m), m <= 128, a <= 256 (the host sees to it that all
-// tiles together are below 2^32)
-__device__ __forceinline__ uint32_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
-    uint32_t ans = 0;
-#pragma unroll 1
-    while (n != 0) {
-        if (a >= m) {
-            const uint32_t pairs = n & 1u ? n * ((n - 1u) >> 1) : (n >> 1) * (n - 1u);
-            ans += pairs * (a / m);
-            a %= m;
-        }
-        if (b >= m) {
-            ans += n * (b / m);
-            b %= m;
-        }
-        const uint32_t y = a * n + b;
-        if (y < m) break;
-        n = y / m;
-        b = y - n * m;
-        const uint32_t t = m;
-        m = a;
-        a = t;
-    }
-    return ans;
-}
-
 // Keys that the first `upto` new tokens of the sequence see.
 __device__ __forceinline__ int keys_seen(const SeqInfo& i, int upto) {
     const int k = i.nk - i.nq + min(upto, i.nq);
@@ -162,13 +136,20 @@ __device__ __forceinline__ int key_tiles(int keys) {
 // Cost of the items 0 .. qt - 1 of one head, qt < the number of items: their tiles
 // (an item without keys counts one, so that its rows are written) and kItemCost each.
 template <int KT>
-__device__ __forceinline__ uint32_t cost_before(const SeqInfo& i, int t2, int qt) {
+struct Tiles {
+    static constexpr int kLog = KT == 64 ? 6 : 7;
+    TileSums<kLog> sums;
+    const uint16_t* before;  // (shared memory)
+};
+
+template <int KT>
+__device__ __forceinline__ uint32_t cost_before(const SeqInfo& i, int t2, int qt, const Tiles<KT>& tiles) {
     if (qt == 0) return 0;
     const int base = i.nk - i.nq;
     int z = 0;  // items that see no key
     if (base < 0) z = min(qt, (-base) / t2);
     uint32_t c = (uint32_t)z + (uint32_t)qt * kItemCost;
-    if (qt > z) c += floor_sum((uint32_t)(qt - z), KT, (uint32_t)t2, (uint32_t)(base + (z + 1) * t2 + KT - 1));
+    if (qt > z) c += tiles.sums.sum((uint32_t)(qt - z), (uint32_t)(base + (z + 1) * t2 + KT - 1), tiles.before);
     return c;
 }
 
@@ -178,10 +159,10 @@ __device__ __forceinline__ int item_tiles(const SeqInfo& i, int t2, int qt) {
 }
 
 template <int KT>
-__device__ __forceinline__ uint32_t head_cost(const SeqInfo& i, int t2) {
+__device__ __forceinline__ uint32_t head_cost(const SeqInfo& i, int t2, const Tiles<KT>& tiles) {
     if (i.nq == 0) return 0;
     const int last = (i.nq + t2 - 1) / t2 - 1;
-    return cost_before<KT>(i, t2, last) + (unsigned)(item_tiles<KT>(i, t2, last) + kItemCost);
+    return cost_before<KT>(i, t2, last, tiles) + (unsigned)(item_tiles<KT>(i, t2, last) + kItemCost);
 }
 
 // A place in the order of all work: tile j of item (s, head, qt), after w units.
@@ -384,6 +365,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     Segment* s_seg = reinterpret_cast<Segment*>(g_misc);              // [kQueue]
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(g_misc + kQueue * sizeof(Segment));
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+    uint16_t* s_before = reinterpret_cast<uint16_t*>(s_tmem + 4);     // [kKeys / 2] (TileSums)
     auto full = [&](int s) { return bars + 8u * (uint32_t)s; };
     auto empty = [&](int s) { return bars + 8u * (uint32_t)(S + s); };
     auto bar_at = [&](int i) { return bars + 8u * (uint32_t)(2 * S + i); };
@@ -434,6 +416,28 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         tmap_prefetch(&tmV);
     }
     if (warp == kMmaWarp) tmem_alloc(smem_addr(s_tmem), kTmemCols);
+    const int t2 = 2 * p.TQ;
+    const Tiles<KT> tiles{TileSums<Tiles<KT>::kLog>((uint32_t)t2), s_before};
+    if (warp == kPlanWarp) {
+        // sums of remainders, two a lane at most
+        constexpr int per = KT / 64;
+        uint32_t r[per], incl = 0;
+#pragma unroll
+        for (int u = 0; u < per; ++u) incl += r[u] = tiles.sums.remainder((uint32_t)(per * lane + u));
+        uint32_t at = incl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        at = incl - at;
+#pragma unroll
+        for (int u = 0; u < per; ++u) {
+            s_before[per * lane + u] = (uint16_t)at;
+            at += r[u];
+        }
+        __syncwarp();
+    }
     pdl_wait();
     pdl_launch_dependents();  // behind the wait, so that what the next kernel may find running is this one alone
 
@@ -441,7 +445,6 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    const int t2 = 2 * p.TQ;
 
     auto give_up = [&]() {
         flag_error(p.err, HA_DEVERR_TIMEOUT);
@@ -477,7 +480,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             // Sequences are taken 32 at a time, one to a lane; the first 32 stay in registers.
             SeqInfo mine0{0, 0, 0}, i{0, 0, 0};
             auto load = [&](int s, bool report) { return s < p.n_seq ? seq_info(p, s, report) : SeqInfo{0, 0, 0}; };
-            auto cost = [&](const SeqInfo& i) { return (uint32_t)p.Hkv * head_cost<KT>(i, t2); };
+            auto cost = [&](const SeqInfo& i) { return (uint32_t)p.Hkv * head_cost<KT>(i, t2, tiles); };
             auto info_of = [&](int s) {
                 if (s >= 32) return seq_info(p, s, false);
                 return SeqInfo{__shfl_sync(0xffffffffu, mine0.q0, s), __shfl_sync(0xffffffffu, mine0.nq, s),
@@ -556,7 +559,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 #pragma unroll 1
                 while (__any_sync(0xffffffffu, n > 1)) {
                     const int step = (n + 15) >> 4, q = (lane & 15) * step;
-                    const uint32_t at = q < n ? cost_before<KT>(ai, t2, lo + q) : ~0u;
+                    const uint32_t at = q < n ? cost_before<KT>(ai, t2, lo + q, tiles) : ~0u;
                     const uint32_t m = __ballot_sync(0xffffffffu, at <= rem) >> (16 * half) & 0xffffu;
                     const int k = 31 - __clz((int)(m | 1u));
                     begins = __shfl_sync(0xffffffffu, at, 16 * half + k);
@@ -564,8 +567,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     n = min(step, n - k * step);
                 }
                 const uint32_t off = rem - begins;
-                const int tiles = item_tiles<KT>(ai, t2, lo);
-                const uint32_t to_end = (uint32_t)(tiles + kItemCost) - off;
+                const int len = item_tiles<KT>(ai, t2, lo);
+                const uint32_t to_end = (uint32_t)(len + kItemCost) - off;
                 a.qt = lo;
                 a.j = max((int)off - kItemCost, 0);
                 if (inside) {
@@ -574,7 +577,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         a.j = 0;
                     } else if (to_end <= tol) {
                         a.w += to_end;
-                        a.j = tiles;
+                        a.j = len;
                     }
                 }
             }

@@ -117,3 +117,60 @@ def test_staged_rows_are_found_before_the_next_are_there():
     assert [(nt, full) for nt in range(1, 40) for full in (False, True) if second_phase_possible(5, nt, full, False)] == [(1, False)]
     # with a ring of more stages the wait would not hold it back
     assert second_phase_possible(6, 1, True, True)
+
+
+# ---------------------------------------------------------------- the work of a row of items
+
+TILE_SOURCE = """
+#include "packed_order.h"
+template <int K>
+static uint32_t sum(uint32_t a, uint32_t n, uint32_t b) {
+    const ha::TileSums<K> t(a);
+    uint16_t before[ha::TileSums<K>::kMost] = {};
+    uint32_t at = 0;
+    for (int x = 0; x < ha::TileSums<K>::kMost; ++x) {
+        before[x] = (uint16_t)at;
+        at += t.remainder((uint32_t)x);
+    }
+    return t.sum(n, b, before);
+}
+extern "C" uint32_t sum6(uint32_t a, uint32_t n, uint32_t b) { return sum<6>(a, n, b); }
+extern "C" uint32_t sum7(uint32_t a, uint32_t n, uint32_t b) { return sum<7>(a, n, b); }
+"""
+
+
+@pytest.fixture(scope="module")
+def sums(tmp_path_factory):
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("needs a host compiler")
+    d = tmp_path_factory.mktemp("sums")
+    src, lib = d / "sums.cpp", d / "libsums.so"
+    src.write_text(TILE_SOURCE)
+    subprocess.run([cxx, "-std=c++17", "-O1", "-Wall", "-Werror", "-shared", "-fPIC", "-I", CSRC, str(src), "-o", str(lib)], check=True)
+    L = ctypes.CDLL(str(lib))
+    for f in (L.sum6, L.sum7):
+        f.restype, f.argtypes = ctypes.c_uint32, [ctypes.c_uint32] * 3
+    return {64: L.sum6, 128: L.sum7}
+
+
+@pytest.mark.parametrize("keys", [64, 128])
+def test_key_tiles_of_a_row_of_items(sums, keys):
+    """For every number of heads a KV head has: sum over i < n of floor((a i + b) / keys)."""
+    f = sums[keys]
+    for a in sorted({2 * (128 // G) for G in range(1, 129)}):
+        for b in list(range(0, 3 * keys, 7)) + [keys - 1, keys, 12345, (1 << 20) + 77]:
+            total = 0
+            for n in range(1, 150):
+                total += (a * (n - 1) + b) // keys
+                assert f(a, n, b) == total % 2 ** 32, (a, n, b)
+    import random
+    r = random.Random(keys)
+    for _ in range(300):
+        a, n = 2 * (128 // r.randint(1, 128)), r.randint(1, 20000)
+        b = r.randrange(1 << r.randint(1, 30))
+        total = sum((a * i + b) // keys for i in range(n))
+        assert f(a, n, b) == total % 2 ** 32, (a, n, b)
+    # as many tokens as a call takes
+    n = (1 << 24) // 256
+    assert f(256, n, 1) == sum((256 * i + 1) // keys for i in range(n)) % 2 ** 32
