@@ -477,14 +477,20 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kPlanWarp) {
             // ---- this CTA's range of work, then its items in order
-            // Sequences are taken 32 at a time, one to a lane; the first 32 stay in registers.
-            SeqInfo mine0{0, 0, 0}, i{0, 0, 0};
+            // Sequences are taken 32 at a time, one to a lane; a batch stays in registers (the first,
+            // until the items are handed out).
+            SeqInfo batch{0, 0, 0}, i{0, 0, 0};
             auto load = [&](int s, bool report) { return s < p.n_seq ? seq_info(p, s, report) : SeqInfo{0, 0, 0}; };
             auto cost = [&](const SeqInfo& i) { return (uint32_t)p.Hkv * head_cost<KT>(i, t2, tiles); };
+            int batch0 = 0;  // the batch's first sequence
             auto info_of = [&](int s) {
-                if (s >= 32) return seq_info(p, s, false);
-                return SeqInfo{__shfl_sync(0xffffffffu, mine0.q0, s), __shfl_sync(0xffffffffu, mine0.nq, s),
-                               __shfl_sync(0xffffffffu, mine0.nk, s)};
+                if (s >= batch0 + 32) {
+                    batch0 = s;
+                    batch = load(s + lane, false);
+                }
+                const int at = s - batch0;
+                return SeqInfo{__shfl_sync(0xffffffffu, batch.q0, at), __shfl_sync(0xffffffffu, batch.nq, at),
+                               __shfl_sync(0xffffffffu, batch.nk, at)};
             };
             uint32_t U = 0, cost0 = 0;
             int rows = 0;  // of this lane's sequences, as far as it matters
@@ -493,7 +499,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 i = load(s0 + lane, blockIdx.x == 0);
                 const uint32_t c = cost(i);
                 if (s0 == 0) {
-                    mine0 = i;
+                    batch = i;
                     cost0 = c;
                 }
                 U += c;
@@ -525,7 +531,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 #pragma unroll 1
                 for (int s0 = 0; __any_sync(0xffffffffu, open); s0 += 32) {
                     if (s0 > 0) i = load(s0 + lane, false);
-                    else i = mine0;
+                    else i = batch;
                     const uint32_t mine = s0 == 0 ? cost0 : cost(i);
                     uint32_t incl = mine;
 #pragma unroll
@@ -632,11 +638,17 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         if (++head >= p.Hkv) {
                             head = 0;
                             if (left > 0) {
-                                do {
-                                    ++s;
-                                    if (s >= p.n_seq) left = 0;
-                                    else i = info_of(s);
-                                } while (left > 0 && i.nq == 0);
+                                ++s;
+                                if (s < p.n_seq) i = info_of(s);
+                                // Sequences without new tokens are passed by 32 at a time: one at a time (two
+                                // dependent loads each) a few hundred thousand outlast the others' waits.
+#pragma unroll 1
+                                while (s < p.n_seq && i.nq == 0) {
+                                    const uint32_t some = __ballot_sync(0xffffffffu, load(s + 1 + lane, false).nq > 0);
+                                    s += some != 0 ? __ffs((int)some) : 32;
+                                    if (some != 0) i = info_of(s);
+                                }
+                                if (s >= p.n_seq) left = 0;
                                 nqt = (i.nq + t2 - 1) / t2;
                             }
                         }

@@ -169,3 +169,42 @@ def test_an_infinity_in_v_stays_in_its_sequence_and_behind_its_key_tile(H):  # n
         other = torch.arange(d, device="cuda") != 7
         assert torch.equal(out[:640, :4][..., other], want[0][:640, :4][..., other])
         assert not torch.isfinite(out[500:640, :4, 7]).any()
+
+
+@pytest.mark.parametrize("n", [100, 5000, 1 << 20])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_few_sequences_among_many_without_new_tokens(H, d, n):  # noqa: F811
+    """The longest list of sequences, nearly all without new tokens (some of those have keys)."""
+    g = torch.Generator(device="cuda").manual_seed(n + d)
+    Hkv, ps, wide = 2, 128, 8
+    own = {0: (3, 500), 5: (1, 1), 6: (0, 300), n // 2 - 30: (70, 800), n // 2: (200, 200), n - 40: (0, 7), n - 1: (2, 1000)}
+    new, lens = torch.zeros(n, dtype=torch.int32), torch.zeros(n, dtype=torch.int32)
+    for s, (a, b) in own.items():
+        new[s], lens[s] = a, b
+    table = torch.full((n, wide), -1, dtype=torch.int32, device="cuda")
+    perm = torch.randperm(wide * len(own), generator=g, device="cuda").to(torch.int32)
+    for i, s in enumerate(own):
+        table[s] = perm[i * wide:(i + 1) * wide]
+    rows = [s for s, (a, _) in own.items() if a]
+    T, cu = int(new.sum()), torch.cat([torch.zeros(1, dtype=torch.int32), torch.cumsum(new, 0).int()]).cuda()
+    K, V = P.rand(g, wide * len(own), Hkv, ps, d), P.rand(g, wide * len(own), Hkv, ps, d)
+    q, k, v = P.rand(g, T, 8, d), P.rand(g, T, Hkv, d), P.rand(g, T, Hkv, d)
+    tok = H.make_tokens(q, k, v, n, out_dtype=torch.bfloat16)
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    H.hash_attn_append(tok, H.make_cache(K, V, table), None, k, v, table, cu, lens.cuda(), None, K, V, dev_flags=flags)
+    assert int(flags) == 0
+
+    def cached(X, s):
+        j = torch.arange(own[s][1], device="cuda")
+        return X[table[s].long()[j // ps], :, j % ps]
+    at = 0
+    for s in rows:
+        a, b = own[s]
+        assert torch.equal(cached(K, s)[b - a:], k[at:at + a]) and torch.equal(cached(V, s)[b - a:], v[at:at + a])
+        at += a
+    for out_dtype in (torch.bfloat16, torch.float32):
+        out, lse, st = P.run_chunk(H, q, K, V, table, new.tolist(), lens.tolist(), Hkv, out_dtype, cu=cu, lens_t=lens.cuda())
+        assert st == (0, 0), hex(st[1])
+        ref = P.reference(q, lambda i: cached(K, rows[i]), lambda i: cached(V, rows[i]), [own[s][0] for s in rows],
+                          [own[s][1] for s in rows])
+        P.check_rows(out.flatten(0, 1), lse.flatten(), ref, out_dtype == torch.bfloat16, f"{n} sequences")
