@@ -657,7 +657,8 @@ ha_status hash_attn_append(const ha_tokens* tokens, const ha_cache* cache, const
  * tokens (n_seq, total, h_q, h_kv, d are read). Its first word is the device error
  * word (hash_attn_workspace_init zeroes it, hash_attn_device_status reads it); the
  * rest needs no zeroing and carries nothing from call to call, so one workspace
- * sized for the largest total and head counts serves calls in turn.
+ * serves calls in turn, sized for the largest total, h_q / h_kv and d among them
+ * (the size grows with each of the three and depends on nothing else).
  */
 ha_status hash_attn_packed_workspace_size(const ha_tokens* tokens, size_t* bytes);
 

@@ -190,3 +190,22 @@ def test_a_call_without_rows_does_nothing(ha, monkeypatch):
     assert L.hash_attn_prefill(t, None, None, None, None, None, None, None, 0, None) == ha.HA_ERR_INVALID_ARG
     assert L.hash_attn_chunk(t, c, None, None, 512, 512, 512, 512, None, None, None, 0, None) == ha.HA_ERR_INVALID_ARG
     assert L.hash_attn_append(t, c, None, None, None, None, None, None, 512, 512, None, 512, 512, None, None, None) == ha.HA_ERR_INVALID_ARG
+
+
+def test_workspace_of_the_largest_total_group_and_head_dim_serves_all(ha):
+    """More heads alone are not more workspace: a group of four takes twice that of one, for the same total."""
+    def size(total, h_q, h_kv, d):
+        t = ha.HATokens()
+        t.n_seq, t.total, t.h_q, t.h_kv, t.d, t.dtype = 1, total, h_q, h_kv, d, ha.HA_BF16
+        return ha.hash_attn_packed_workspace_size(t)
+    assert size(100, 8, 2, 128) > size(100, 32, 32, 128)
+    totals, groups = [0, 1, 2, 9, 10, 32, 33, 64, 128, 129, 5000, 1 << 24], [1, 2, 3, 4, 8, 12, 16, 64, 128]
+    for d in (64, 128):
+        for G in groups:
+            for h_kv in (1, 8):
+                sizes = [size(t, G * h_kv, h_kv, d) for t in totals]
+                assert sizes == sorted(sizes) and sizes == [size(t, G, 1, d) for t in totals]
+                assert all(a >= b for a, b in zip(sizes, [size(t, 1, 1, 64) for t in totals]))
+        for t in totals:
+            sizes = [size(t, G, 1, d) for G in groups]
+            assert sizes == sorted(sizes)
