@@ -35,11 +35,11 @@
 // them, in order, so results do not depend on timing.
 //
 // Measured (graph replays; rates against cuBLAS's bf16 burst and a plain copy): a prompt of
-// 16,384 tokens, 32/8 heads of 128: 1.33 ms, 1.65 PFLOP/s, 86 % (1.43 ms at the power cap);
-// 24 prompts of 33 to 2,500: 330 us, 58 % (an item's start and end cost each CTA about
+// 16,384 tokens, 32/8 heads of 128: 1.33 to 1.37 ms, 1.65 PFLOP/s, 86 % (1.43 ms at the power cap);
+// 24 prompts of 33 to 2,500: 330 to 334 us, 58 % (an item's start and end cost each CTA about
 // 6,000 cycles, two tiles); 16,384 tokens at d 64: 1.10 ms, 52 % (bound by the softmax
 // warps' latency, not by a unit); decode of 64 sequences of 1,000 to 16,000 keys: 345 us,
-// 6.4 TB/s, 95 %; one token over 131,072 keys, float32 out: 109 us, 4.9 TB/s, 73 % (bound by
+// 6.4 TB/s, 95 %; one token over 131,072 keys, float32 out: 108 us, 5.0 TB/s, 73 % (bound by
 // the products: three for P V); 4 x 512 tokens over 20,000 to 32,000 keys: 574 us, 84 %.
 //
 // 12 warps: two softmax warpgroups (thread = row: a tcgen05.ld gives a thread

@@ -26,7 +26,8 @@ inline EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// Tensor maps of the packed attention: bf16, 4 dimensions, 128-byte swizzle.
+// Tensor maps of the packed attention: bf16, 128-byte swizzle, 4 dimensions (K and V of folded
+// pages: 5).
 struct PackedMaps {
     CUtensorMap q, qs, k, v, o;  // qs: the queries in copies of TS tokens; o: bf16 output, as q
 };
