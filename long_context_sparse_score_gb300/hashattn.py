@@ -142,6 +142,7 @@ class HACache(ctypes.Structure):
 class HARope(ctypes.Structure):
     """Mirror of ``ha_rope``."""
 
+    tensor = None  # inv_freq, where it came as one (see rope)
     _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
@@ -670,8 +671,8 @@ def hash_attn_append(tokens, cache, q, k, v, page_table, cu, seq_lens, q_out, K,
             _as_made((k_sig, cached[:3], (ks_sp, ks_sh, 1), k_sig.dtype if k_sig.dtype in ints else ints[0], "k_sig"))
     device = _device()
     a = _here(device, q, k, v, W, page_table, cu, seq_lens, q_out, K, V, k_sig, dev_flags)
-    if rope is not None:
-        _here(device, getattr(rope, "tensor", None))
+    if rope is not None and rope.tensor is not None and rope.tensor.get_device() != device:
+        _elsewhere(rope.tensor)
     _check(lib().hash_attn_append(tokens, cache, rope, *a, _raw_stream(device) if stream is None else _stream(stream)))
 
 

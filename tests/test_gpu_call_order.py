@@ -44,6 +44,8 @@ class Loop:
         sizes = [H.hash_attn_workspace_size(shape, m, 4, 8) for m in (self.m, cap)]
         self.ws = torch.empty(max(sizes), dtype=torch.uint8, device="cuda")
         H.hash_attn_workspace_init(self.ws)
+        self.ws2 = torch.empty_like(self.ws)
+        H.hash_attn_workspace_init(self.ws2)
         tok = H.make_tokens(*self.rows[0], B, out_dtype=torch.bfloat16)
         self.wp = torch.zeros(H.hash_attn_packed_workspace_size(tok), dtype=torch.uint8, device="cuda")
 
@@ -65,6 +67,7 @@ class Loop:
         q_sig = torch.zeros(B, Hq, dtype=torch.int32, device="cuda")
         outs = [(torch.full((B, Hq, d), float("nan"), device="cuda"), torch.full((B, Hq), float("nan"), device="cuda")) for _ in range(n)]
         couts = [(torch.empty_like(qo), torch.empty(qo.shape[:2], device="cuda")) for _ in range(n)]
+        douts = [tuple(torch.full_like(x, float("nan")) for x in o) for o in outs]
         sigs = []
         st = torch.cuda.current_stream()
         shape = H.make_shape(q, K, V, sig)
@@ -85,14 +88,18 @@ class Loop:
                 wait and st.synchronize()
                 H.hash_attn_chunk(tok, cache, qo, K, V, self.table, self.cu, lens, *couts[i], workspace=self.wp, stream=st)
             wait and st.synchronize()
+            if "both" in chain:  # two decode calls in turn, each with a workspace of its own
+                H.hash_attn_decode(shape, q, None, None, K, V, lens, None, self.cap, 4, 8, *douts[i], workspace=self.ws2, stream=st)
+                wait and st.synchronize()
             if "dense" in chain:
                 H.hash_attn_decode(shape, q, None, None, K, V, lens, None, self.cap, 4, 8, *outs[i], workspace=self.ws, stream=st)
             else:
                 H.hash_attn_decode(shape, q, q_sig if q_sigs is None else q_sigs[i], sig, K, V, lens, None, self.m, 4, 8, *outs[i],
                                    workspace=self.ws, stream=st)
             wait and st.synchronize()
-        assert H.hash_attn_device_status(self.ws)[0] == 0 and H.hash_attn_device_status(self.wp)[0] == 0
-        return [t for o in outs + (couts if "chunk" in chain else []) for t in o] + [K, V, sig], sigs
+        assert all(H.hash_attn_device_status(w)[0] == 0 for w in (self.ws, self.ws2, self.wp))
+        more = (couts if "chunk" in chain else []) + (douts if "both" in chain else [])
+        return [t for o in outs + more for t in o] + [K, V, sig], sigs
 
 
 CHAINS = {
@@ -102,6 +109,9 @@ CHAINS = {
     "append-codes-sparse": ("codes",),
     "append-chunk-sparse": ("codes", "chunk"),
     "append-keys-sparse": ("keys",),
+    "append-dense-sparse": ("codes", "both"),
+    "append-chunk-dense-sparse": ("codes", "chunk", "both"),
+    "append-dense-dense": ("both", "dense"),
 }
 
 
