@@ -29,12 +29,12 @@ constexpr int kFusedRange = 8192;         // tokens per range of the fused selec
 
 // ------------------------------------------------------------------ workspace
 //
-// [0, 256)                 error word (uint32) + padding
+// [0, 256)                 error word (uint32); at 128: tag of the decode call that runs, its pairs
+//                          done (uint32[2], zero between calls)
 // zero between calls (self-resetting), at offsets fixed by the shape:
 // counters   uint32[heads]  split-K arrival counters of GATHER-ATT
 // score_cnt  uint32[batch*h_kv]          SCORE arrival counters
 // tot, ready                             fused selection totals and ready flags
-// busy       uint32[2]                    tag of the decode call that runs, its pairs done
 // scratch (its layout depends on the budget, the options and the path):
 // chunk_hist uint32[heads][nchunks][33]  SCORE histogram of every chunk
 // seg_cnt    int32 [heads][nseg]         selected tokens of every segment (one

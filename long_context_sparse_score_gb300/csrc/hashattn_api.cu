@@ -725,8 +725,9 @@ Layout make_layout(const ha_shape& s, int64_t rows_cap, bool with_selection, int
     L.heads = s.batch * s.h_q;
     L.rows_cap = (int)rows_cap;
     choose_splits(L.heads, rows_cap, &L.splits, &L.rows_per_split);
-    size_t off = 256;  // error word + padding
+    size_t off = 256;  // error word, busy words, padding
     L.off_err = 0;
+    L.off_busy = 128;     // {tag of the decode call that runs, its pairs done}: at one place in every layout
     // What must be zero between calls comes first, at offsets that depend on the
     // shape alone: calls with other budgets, code widths or options, the dense
     // path and the entry points with given lists lay out the scratch after it
@@ -740,8 +741,6 @@ Layout make_layout(const ha_shape& s, int64_t rows_cap, bool with_selection, int
     off = align_up(off + (size_t)pairs * 4 * 36 * 4, 256);
     L.off_ready = off;    // fused: per pair, shares-complete flag
     off = align_up(off + (size_t)pairs * 4, 256);
-    L.off_busy = off;     // {tag of the decode call that runs, its pairs done}
-    off = align_up(off + 8, 256);
     // scratch: written by every call before it reads it
     if (with_selection) {
         L.chunk = choose_chunk(pairs, s.n_cap);
