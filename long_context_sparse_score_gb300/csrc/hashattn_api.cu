@@ -731,16 +731,18 @@ Layout make_layout(const ha_shape& s, int64_t rows_cap, bool with_selection, int
     // What must be zero between calls comes first, at offsets that depend on the
     // shape alone: calls with other budgets, code widths or options, the dense
     // path and the entry points with given lists lay out the scratch after it
-    // differently, so one workspace serves all of them in turn.
+    // differently, so one workspace serves all of them in turn. The decode runs with
+    // more than four query heads per KV head on virtual KV heads, the other entry points and wide
+    // codes on the real ones, so there is room for as many pairs as there are heads.
     const int64_t pairs = (int64_t)s.batch * s.h_kv;
     L.off_counter = off;  // GATHER-ATT split-K arrival counters, per head
     off = align_up(off + (size_t)L.heads * 4, 256);
     L.off_scnt = off;     // SCORE arrival counters, per (batch entry, KV head)
-    off = align_up(off + (size_t)pairs * 4, 256);
+    off = align_up(off + (size_t)L.heads * 4, 256);
     L.off_tot = off;      // fused: per (pair, head) 36-word distance histogram
-    off = align_up(off + (size_t)pairs * 4 * 36 * 4, 256);
+    off = align_up(off + (size_t)L.heads * 4 * 36 * 4, 256);
     L.off_ready = off;    // fused: per pair, shares-complete flag
-    off = align_up(off + (size_t)pairs * 4, 256);
+    off = align_up(off + (size_t)L.heads * 4, 256);
     // scratch: written by every call before it reads it
     if (with_selection) {
         L.chunk = choose_chunk(pairs, s.n_cap);
