@@ -564,7 +564,7 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 // mark_busy and mark_pair_done): a kernel between the two would have waited for that call's
 // before it let this one start. Nothing from before that call can be running either, for the same
 // reason. busy null: launched normally. (Decode calls with nothing between them, 16 x 131,072
-// tokens: 205.9 us a step, with a plain wait 209.8; one sequence of 32K tokens 18.9 and 22.0.)
+// tokens: 205.0 us a step, with a plain wait 209.8; one sequence of 32K tokens 18.9 and 22.0.)
 __device__ __forceinline__ bool earlier_call_runs(const uint32_t* busy) {
     uint32_t a = 0u;
     if (busy != nullptr) asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(a) : "l"(busy) : "memory");
