@@ -283,17 +283,20 @@ def _plain_plan(s):
     pushed = (place >= 0) & (place < back.shape[0])
     free = torch.where(pushed, torch.cat([back, back.new_zeros(1)])[place.clamp(0, back.shape[0])], s["free"])
     takes = (p1 - p0).clamp(min=0)
-    before = torch.cumsum(takes, 0) - takes
-    k = top - 1 - (before[:, None] + cols - p0[:, None])
-    got = torch.where(k >= 0, free[k.clamp(0, s["n_pages"] - 1)], -1)
-    table = torch.where((cols >= p0[:, None]) & (cols < p1[:, None]), got, table)
+    upto = torch.cumsum(takes, 0)
+    goes = (takes == 0) | (upto <= top)  # the others are stopped: their pages have run out
+    lens = torch.where(goes, lens, ~had)
+    k = top - 1 - ((upto - takes)[:, None] + cols - p0[:, None])
+    got = free[k.clamp(0, s["n_pages"] - 1)]
+    table = torch.where(goes[:, None] & (cols >= p0[:, None]) & (cols < p1[:, None]), got, table)
     t = torch.arange(s["total"], device="cuda")
     seq = (torch.searchsorted(cu, t, right=True) - 1).clamp(max=n - 1)
     pos = had[seq] + t - cu[seq]
     page = table[seq, (pos // ps).clamp(max=table.shape[1] - 1)].long()
-    slots = torch.where((t < cu[-1]) & (page >= 0), page * ps + pos % ps, -1)
+    slots = torch.where((t < cu[-1]) & goes[seq], page * ps + pos % ps, -1)
+    left = top - torch.where(upto <= top, upto, 0).amax()
     i = lambda x: x.to(torch.int32)  # noqa: E731
-    return {"table": i(table), "lens": i(lens), "cu": i(cu), "slots": i(slots), "free": i(free), "n_free": i((top - takes.sum()).clamp(min=0))}
+    return {"table": i(table), "lens": i(lens), "cu": i(cu), "slots": i(slots), "free": i(free), "n_free": i(left.reshape(1))}
 
 
 def _places(s):
@@ -432,22 +435,27 @@ def _exact_plan(case, s):
             for j in range(-(-had[i] // ps)):
                 stack[n_free] = table[i][j]
                 n_free += 1
-    cu, lens, slots = [0], [], []
+    cu, lens, slots, wanted, top = [0], [], [], 0, n_free
     for i, m in enumerate(new):
         cu.append(cu[-1] + max(m, 0))
         if m < 0:
             lens.append(0)
             continue
+        fresh = -(-(had[i] + m) // ps) - -(-had[i] // ps)
+        wanted += fresh
+        if fresh and wanted > top:  # those behind it that need pages are stopped as well
+            lens.append(-1 - had[i])
+            slots += [-1] * m
+            continue
         for pos in range(had[i], had[i] + m):
             if pos % ps == 0:
                 n_free -= 1
-                table[i][pos // ps] = stack[n_free] if n_free >= 0 else -1
-            page = table[i][pos // ps]
-            slots.append(-1 if page < 0 else page * ps + pos % ps)
+                table[i][pos // ps] = stack[n_free]
+            slots.append(table[i][pos // ps] * ps + pos % ps)
         lens.append(had[i] + m)
     slots += [-1] * (s["total"] - len(slots))
     ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
-    return {"table": ints(table), "lens": ints(lens), "cu": ints(cu), "slots": ints(slots), "free": ints(stack), "n_free": ints([max(n_free, 0)])}
+    return {"table": ints(table), "lens": ints(lens), "cu": ints(cu), "slots": ints(slots), "free": ints(stack), "n_free": ints([n_free])}
 
 
 def exact(case, seed):
