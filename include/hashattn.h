@@ -76,6 +76,7 @@ typedef enum { HA_F32 = 0, HA_BF16 = 1 } ha_dtype;
 #define HA_DEVERR_COUNT    0x8u  /* a given count outside [0, idx_cap]: clamped     */
 #define HA_DEVERR_TIMEOUT  0x10u /* a bounded pipeline wait gave up                 */
 #define HA_DEVERR_STATE    0x20u /* workspace counters were not in their reset state */
+#define HA_DEVERR_PAGES    0x40u /* the free pages ran out: the sequence is stopped     */
 
 /* Number of Hamming-distance bins of a 32-bit code (distances 0..32). */
 #define HA_NBINS 33
@@ -698,6 +699,102 @@ ha_status hash_attn_prefill(const ha_tokens* tokens, const void* q, const void* 
 ha_status hash_attn_chunk(const ha_tokens* tokens, const ha_cache* cache, const void* q, const void* K, const void* V,
                           const int32_t* table, const int32_t* cu, const int32_t* seq_lens, void* out, float* lse,
                           void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * ---- Around the packed calls: the page plan, several position axes, score options ----
+ *
+ * hash_attn_plan_pages makes what the packed calls read of a serving step (page table,
+ * cu, seq_lens) from the sequences' new lengths, on the device, so a step that is captured
+ * in a graph serves any lengths. hash_attn_append_axes is hash_attn_append with positions
+ * of several axes.
+ *
+ * ha_paging: a batch of sequences and the pool that holds their pages.
+ *   n_seq      sequences, in [1, 2^20]
+ *   total      rows that the packed buffers (and slots) have room for, in [0, 2^24]
+ *   n_pages, page_size, max_pages, table_st   as ha_cache (any page_size)
+ *   reserved   must be 0
+ */
+typedef struct {
+    int32_t n_seq, total;
+    int32_t n_pages, page_size, max_pages;
+    int32_t reserved;
+    int64_t table_st;
+} ha_paging;
+
+/*
+ * Plan one step. Sequence s has seq_lens[s] tokens and gets new_lens[s] more (0: none), or,
+ * with new_lens[s] below 0, ends. In this order:
+ *  - An ended sequence's pages (the first ceil(seq_lens[s] / page_size) entries of its
+ *    row) are put on the stack of free pages, sequence after sequence; its length is 0
+ *    and its row of the table stays as it is.
+ *  - Every page that the new tokens begin is taken from the top of the stack, sequence
+ *    after sequence and page after page, and entered in the table. Where the stack does
+ *    not hold all pages that a sequence needs, that sequence and the ones behind it that
+ *    need a page are stopped (HA_DEVERR_PAGES); so is one that would outgrow its row of
+ *    the table (HA_DEVERR_SEQLEN). Nothing of a stopped sequence changes but its length,
+ *    which becomes ~length (below 0; hash_attn_append and hash_attn_chunk pass its rows
+ *    by as those of a bad length). It stays stopped until the caller ends it, which
+ *    gives back its pages, or writes its length again.
+ *  - cu: the new tokens' rows, one sequence after the other, stopped ones among them (the
+ *    rows are the caller's layout). Their sum must not exceed total; otherwise nothing is
+ *    planned: cu is 0 throughout, and the lengths, the table and the free pages stay as they
+ *    are (HA_DEVERR_COUNT).
+ *   new_lens      int32 [n_seq]
+ *   seq_lens      int32 [n_seq]; lengths outside [0, max_pages * page_size] stay as they are, and
+ *                 so stopped (flagged HA_DEVERR_SEQLEN where tokens are to be added, or the
+ *                 length is above); an ended one of length ~n gives back the pages of n
+ *   seq_lens_out  int32 [n_seq], may be seq_lens itself
+ *   cu            int32 [n_seq + 1]
+ *   table         int32 rows of pages, as hash_attn_append; only the entries of pages taken
+ *                 are written, so one plan run twice from the same inputs gives the same
+ *   slots         int32 [total] or NULL: the place page * page_size + row of every packed token in
+ *                 the pool; -1 for a stopped sequence's rows and those behind the last
+ *                 sequence. Asks for n_pages * page_size < 2^31.
+ *   free_pages    int32 [n_pages], the stack: free_pages[0 .. n_free)
+ *   n_free, n_free_out   one int32 each, may be the same (an n_free outside [0, n_pages] is
+ *                 clamped and flagged HA_DEVERR_STATE)
+ *   dev_flags     optional device uint32; bits are OR-ed in: those above, HA_DEVERR_INDEX
+ *                 for a page outside [0, n_pages) (one given back is left out; one taken
+ *                 is entered as -1), HA_DEVERR_STATE where more pages come back than there
+ *                 are
+ * A page belongs to one sequence. No other buffers may overlap.
+ * Errors: HA_ERR_INVALID_ARG, HA_ERR_UNSUPPORTED (slots past 2^31) before anything is
+ * enqueued; HA_ERR_CUDA on a failed launch.
+ */
+ha_status hash_attn_plan_pages(const ha_paging* paging, const int32_t* new_lens, const int32_t* seq_lens,
+                               int32_t* seq_lens_out, int32_t* cu, int32_t* table, int32_t* slots, int32_t* free_pages,
+                               const int32_t* n_free, int32_t* n_free_out, uint32_t* dev_flags, void* stream);
+
+/*
+ * A rotation by several position axes (time, height and width of images and video, say):
+ * pair p of a row turns by positions[axis[p]] * inv_freq[p].
+ *   inv_freq, rot_dim, interleaved   as ha_rope (and its bound on the angle's error)
+ *   n_axes     in [1, 8]
+ *   axis       axis[p] < n_axes for p < rot_dim / 2 (host values: any order of the axes,
+ *              in blocks or in turn); the rest is not read
+ *   reserved   must be 0
+ */
+typedef struct {
+    const float* inv_freq;
+    int32_t rot_dim;
+    int32_t interleaved;
+    int32_t n_axes;
+    int32_t reserved;
+    uint8_t axis[64];
+} ha_rope_axes;
+
+/*
+ * hash_attn_append with a rotation by several axes.
+ *   rope        not NULL
+ *   positions   int32 device, any values: axis a of packed row t at positions[a * pos_st + t];
+ *               pos_st >= total for more than one axis. Where a token goes in the cache is
+ *               decided by seq_lens and cu alone.
+ *   the rest and the errors as hash_attn_append
+ */
+ha_status hash_attn_append_axes(const ha_tokens* tokens, const ha_cache* cache, const ha_rope_axes* rope,
+                                const int32_t* positions, int64_t pos_st, const void* q, const void* k, const void* v,
+                                const float* W, const int32_t* table, const int32_t* cu, const int32_t* seq_lens,
+                                void* q_out, void* K, void* V, uint32_t* k_sig, uint32_t* dev_flags, void* stream);
 
 /*
  * Synchronise `stream`, read and clear the workspace's device error word.

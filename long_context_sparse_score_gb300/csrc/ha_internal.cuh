@@ -342,11 +342,26 @@ struct AppendParams {
     int page_size, n_pages, max_len;
     const float* inv_freq;     // null: no rotation
     int rot, inter;
+    const int32_t* positions;  // [n_axes], pos_st apart: positions of the rows by axis, or null: by place
+    int64_t pos_st;
+    int n_axes;
+    uint32_t axes[8];          // axis of pair 8 i + k: bits 4 k of axes[i]
     const float* W;            // [Hkv][32][d] or null: no codes
     uint32_t* codes;
     int64_t c_sp, c_sh;
     uint32_t* flags;           // optional HA_DEVERR_* word
     int row_splits;            // CTAs that share a block of tokens (k_append)
+};
+
+// k_plan_pages: see hash_attn_plan_pages.
+struct PagesParams {
+    const int32_t *new_lens, *seq_lens;
+    int32_t *lens_out, *cu, *table, *slots, *free_pages;
+    const int32_t* n_free;
+    int32_t* n_free_out;
+    uint32_t* flags;
+    int64_t table_st;
+    int n_seq, total, n_pages, page_size, max_pages;
 };
 
 struct MergeNParams {
@@ -412,6 +427,7 @@ cudaError_t launch_select_wide(const WideParams& p, int batch_hkv, cudaStream_t 
 // Keys per tile of k_packed_att.
 int packed_key_tile(bool f32_out);
 cudaError_t launch_append(const AppendParams& p, bool in_bf16, bool cache_bf16, cudaStream_t st);
+cudaError_t launch_plan_pages(const PagesParams& p, cudaStream_t st);
 
 // Query-head groups per KV head: group g of k per KV head reads KV head g / k. The
 // kernels divide by a multiply-high with kv_magic(k) = ceil(2^32 / k), exact for

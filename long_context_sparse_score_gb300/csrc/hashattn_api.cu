@@ -1630,21 +1630,39 @@ extern "C" ha_status hash_attn_chunk(const ha_tokens* tokens, const ha_cache* ca
     return packed_attention(tokens, cache, q, K, V, table, cu, seq_lens, out, lse, workspace, ws_bytes, stream);
 }
 
-extern "C" ha_status hash_attn_append(const ha_tokens* tokens, const ha_cache* cache, const ha_rope* rope, const void* q,
-                                      const void* k, const void* v, const float* W, const int32_t* table, const int32_t* cu,
-                                      const int32_t* seq_lens, void* q_out, void* K, void* V, uint32_t* k_sig,
-                                      uint32_t* dev_flags, void* stream) {
+namespace ha {
+namespace {
+
+ha_status check_rope(const float* inv_freq, int rot_dim, int interleaved, int d) {
+    if (inv_freq == nullptr) return fail(HA_ERR_INVALID_ARG, "rope->inv_freq is NULL");
+    if (rot_dim < 16 || rot_dim > d || rot_dim % 16 != 0)
+        return fail(HA_ERR_INVALID_ARG, "rope->rot_dim must be a multiple of 16 in [16, d] (got %d)", rot_dim);
+    if (interleaved != 0 && interleaved != 1)
+        return fail(HA_ERR_INVALID_ARG, "rope->interleaved must be 0 or 1 (got %d)", interleaved);
+    return HA_OK;
+}
+
+// with positions of axes: `axes`; else `rope` or none
+ha_status append(const ha_tokens* tokens, const ha_cache* cache, const ha_rope* rope, const ha_rope_axes* axes,
+                 const int32_t* positions, int64_t pos_st, const void* q, const void* k, const void* v, const float* W,
+                 const int32_t* table, const int32_t* cu, const int32_t* seq_lens, void* q_out, void* K, void* V,
+                 uint32_t* k_sig, uint32_t* dev_flags, void* stream) {
     const ha_tokens* t = tokens;
     const ha_cache* c = cache;
     HA_TRY(check_tokens(t));
     HA_TRY(check_cache(c, t, K, V, table));
     if (cu == nullptr || seq_lens == nullptr) return fail(HA_ERR_INVALID_ARG, "cu and seq_lens must not be NULL");
-    if (rope != nullptr) {
-        if (rope->inv_freq == nullptr) return fail(HA_ERR_INVALID_ARG, "rope->inv_freq is NULL");
-        if (rope->rot_dim < 16 || rope->rot_dim > t->d || rope->rot_dim % 16 != 0)
-            return fail(HA_ERR_INVALID_ARG, "rope->rot_dim must be a multiple of 16 in [16, d] (got %d)", rope->rot_dim);
-        if (rope->interleaved != 0 && rope->interleaved != 1)
-            return fail(HA_ERR_INVALID_ARG, "rope->interleaved must be 0 or 1 (got %d)", rope->interleaved);
+    if (rope != nullptr) HA_TRY(check_rope(rope->inv_freq, rope->rot_dim, rope->interleaved, t->d));
+    if (axes != nullptr) {
+        HA_TRY(check_rope(axes->inv_freq, axes->rot_dim, axes->interleaved, t->d));
+        if (axes->n_axes < 1 || axes->n_axes > 8) return fail(HA_ERR_INVALID_ARG, "rope->n_axes must be in [1, 8] (got %d)", axes->n_axes);
+        if (axes->reserved != 0) return fail(HA_ERR_INVALID_ARG, "ha_rope_axes.reserved must be zero");
+        for (int i = 0; i < axes->rot_dim / 2; ++i)
+            if (axes->axis[i] >= axes->n_axes)
+                return fail(HA_ERR_INVALID_ARG, "rope->axis[%d] must be below n_axes (got %d)", i, (int)axes->axis[i]);
+        if (axes->n_axes > 1 && (pos_st < t->total || pos_st > kMaxStride))
+            return fail(HA_ERR_INVALID_ARG, "pos_st must be in [total, 2^36] (got %lld)", (long long)pos_st);
+        if (positions == nullptr && t->total > 0) return fail(HA_ERR_INVALID_ARG, "positions is NULL");
     }
     if ((W == nullptr) != (k_sig == nullptr)) return fail(HA_ERR_INVALID_ARG, "W and k_sig must both be given or both be NULL");
     if (W != nullptr && ((t->h_kv > 1 && c->ks_sh < c->page_size) || (c->n_pages > 1 && c->ks_sp < c->page_size)))
@@ -1695,11 +1713,80 @@ extern "C" ha_status hash_attn_append(const ha_tokens* tokens, const ha_cache* c
         p.rot = rope->rot_dim;
         p.inter = rope->interleaved;
     }
+    if (axes != nullptr) {
+        p.inv_freq = axes->inv_freq;
+        p.rot = axes->rot_dim;
+        p.inter = axes->interleaved;
+        p.positions = positions;
+        p.pos_st = pos_st;
+        p.n_axes = axes->n_axes;
+        for (int i = 0; i < axes->rot_dim / 2; ++i) p.axes[i / 8] |= (uint32_t)axes->axis[i] << (4 * (i % 8));
+    }
     p.W = W;
     p.codes = k_sig;
     p.c_sp = c->ks_sp;
     p.c_sh = c->ks_sh;
     p.flags = dev_flags;
     HA_LAUNCH(launch_append(p, t->dtype == HA_BF16, c->dtype == HA_BF16, static_cast<cudaStream_t>(stream)), "append launch");
+    return HA_OK;
+}
+
+}  // namespace
+}  // namespace ha
+
+extern "C" ha_status hash_attn_append(const ha_tokens* tokens, const ha_cache* cache, const ha_rope* rope, const void* q,
+                                      const void* k, const void* v, const float* W, const int32_t* table, const int32_t* cu,
+                                      const int32_t* seq_lens, void* q_out, void* K, void* V, uint32_t* k_sig,
+                                      uint32_t* dev_flags, void* stream) {
+    return append(tokens, cache, rope, nullptr, nullptr, 0, q, k, v, W, table, cu, seq_lens, q_out, K, V, k_sig, dev_flags, stream);
+}
+
+extern "C" ha_status hash_attn_append_axes(const ha_tokens* tokens, const ha_cache* cache, const ha_rope_axes* rope,
+                                           const int32_t* positions, int64_t pos_st, const void* q, const void* k,
+                                           const void* v, const float* W, const int32_t* table, const int32_t* cu,
+                                           const int32_t* seq_lens, void* q_out, void* K, void* V, uint32_t* k_sig,
+                                           uint32_t* dev_flags, void* stream) {
+    if (rope == nullptr) return fail(HA_ERR_INVALID_ARG, "rope is NULL");
+    return append(tokens, cache, nullptr, rope, positions, pos_st, q, k, v, W, table, cu, seq_lens, q_out, K, V, k_sig, dev_flags, stream);
+}
+
+extern "C" ha_status hash_attn_plan_pages(const ha_paging* paging, const int32_t* new_lens, const int32_t* seq_lens,
+                                          int32_t* seq_lens_out, int32_t* cu, int32_t* table, int32_t* slots,
+                                          int32_t* free_pages, const int32_t* n_free, int32_t* n_free_out,
+                                          uint32_t* dev_flags, void* stream) {
+    const ha_paging* g = paging;
+    if (g == nullptr) return fail(HA_ERR_INVALID_ARG, "paging is NULL");
+    if (g->n_seq < 1 || g->n_seq > (1 << 20)) return fail(HA_ERR_INVALID_ARG, "n_seq must be in [1, 2^20] (got %d)", g->n_seq);
+    if (g->total < 0 || g->total > kMaxCap)
+        return fail(HA_ERR_INVALID_ARG, "total must be in [0, %lld] (got %d)", (long long)kMaxCap, g->total);
+    if (g->n_pages < 1 || g->page_size < 1 || g->max_pages < 1 || (int64_t)g->max_pages * g->page_size > kMaxKeys)
+        return fail(HA_ERR_INVALID_ARG, "n_pages, page_size and max_pages must be >= 1 and max_pages * page_size <= 2^30 (got %d, %d, %d)",
+                    g->n_pages, g->page_size, g->max_pages);
+    if (g->reserved != 0) return fail(HA_ERR_INVALID_ARG, "ha_paging.reserved must be zero");
+    if (g->n_seq > 1 && g->table_st < g->max_pages)
+        return fail(HA_ERR_INVALID_ARG, "table_st (%lld) must be at least max_pages (%d)", (long long)g->table_st, g->max_pages);
+    if (new_lens == nullptr || seq_lens == nullptr || seq_lens_out == nullptr || cu == nullptr || table == nullptr ||
+        free_pages == nullptr || n_free == nullptr || n_free_out == nullptr)
+        return fail(HA_ERR_INVALID_ARG, "new_lens, seq_lens, seq_lens_out, cu, table, free_pages, n_free and n_free_out must not be NULL");
+    if (slots != nullptr && (int64_t)g->n_pages * g->page_size > INT32_MAX)
+        return fail(HA_ERR_UNSUPPORTED, "slots are 32 bits: n_pages * page_size must be below 2^31");
+    PagesParams p{};
+    p.new_lens = new_lens;
+    p.seq_lens = seq_lens;
+    p.lens_out = seq_lens_out;
+    p.cu = cu;
+    p.table = table;
+    p.slots = g->total > 0 ? slots : nullptr;
+    p.free_pages = free_pages;
+    p.n_free = n_free;
+    p.n_free_out = n_free_out;
+    p.flags = dev_flags;
+    p.table_st = g->table_st;
+    p.n_seq = g->n_seq;
+    p.total = g->total;
+    p.n_pages = g->n_pages;
+    p.page_size = g->page_size;
+    p.max_pages = g->max_pages;
+    HA_LAUNCH(launch_plan_pages(p, static_cast<cudaStream_t>(stream)), "page plan launch");
     return HA_OK;
 }

@@ -5,7 +5,10 @@
 // sits at position pos = nk - nq + i, in row pos % page_size of page
 // table[s][pos / page_size]. Its queries and keys are rotated: pair p of the
 // first `rot` dims, (x_p, x_{p + rot/2}) or, interleaved, (x_{2p}, x_{2p+1}),
-// turns by the angle pos * inv_freq[p]; the other dims and the values are copied.
+// turns by the angle pos * inv_freq[p]; the other dims and the values are copied. With
+// several axes (AXES) the angle is positions[axis[p]] * inv_freq[p] instead: a lane holds
+// one axis' position and the others take it from there, so it costs one load a warp,
+// beside those of the place.
 //
 // The angle in turns, pos * inv_freq / 2 pi, is kept as a 64-bit fixed-point
 // fraction: inv_freq's 24-bit significand times 2^64 / 2 pi, shifted, is off by less than
@@ -123,7 +126,7 @@ struct Vec8<float> {
     }
 };
 
-template <typename TI, typename TC>
+template <typename TI, typename TC, bool AXES>
 __global__ void __launch_bounds__(kAppWarps * 32) k_append(const AppendParams p) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();
@@ -169,6 +172,8 @@ __global__ void __launch_bounds__(kAppWarps * 32) k_append(const AppendParams p)
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[k] = p.inv_freq[8 * i + k];
     }
+    // the token's position on axis `lane`
+    const int on_axis = AXES && lane < p.n_axes ? p.positions[lane * p.pos_st + t] : 0;
     const TokenPlace at = place_of(p, t);
     if (at.pos < 0) return;
     const int entry = at.pos / p.page_size, prow = at.pos - entry * p.page_size;
@@ -176,7 +181,14 @@ __global__ void __launch_bounds__(kAppWarps * 32) k_append(const AppendParams p)
     const bool good = page >= 0 && page < p.n_pages;
     if (!good && lane == 0 && p.flags != nullptr) atomicOr(p.flags, HA_DEVERR_INDEX);
     float c[8], sn[8];
-    if (turns) {
+    if constexpr (AXES) {
+        const uint32_t axes = p.axes[i];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int pos = __shfl_sync(0xffffffffu, on_axis, (int)(axes >> (4 * k) & 15u));
+            if (turns) turn(turn_step(f[k]), pos, c[k], sn[k]);
+        }
+    } else if (turns) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) turn(turn_step(f[k]), at.pos, c[k], sn[k]);
     }
@@ -342,7 +354,7 @@ cudaError_t launch_append_t(const AppendParams& p, cudaStream_t st) {
         attr[1].val.sharedMemCarveout = cudaSharedmemCarveoutMaxShared;
         cfg.numAttrs = 2;
     }
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_append<TI, TC>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, p.positions != nullptr ? k_append<TI, TC, true> : k_append<TI, TC, false>, p);
     if (e != cudaSuccess || p.W == nullptr) return e;
     // Few keys: one a lane, as long as there is an SM for each CTA of 32 of them.
     // d 128, 8 heads, one key a lane / four: 64 tokens 6.4 / 8.7 us, 256: 6.6 / 10.1, 1024: 12.3 / 10.8.

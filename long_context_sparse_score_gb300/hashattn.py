@@ -31,6 +31,7 @@ HA_DEVERR_INDEX = 0x4
 HA_DEVERR_COUNT = 0x8
 HA_DEVERR_TIMEOUT = 0x10
 HA_DEVERR_STATE = 0x20
+HA_DEVERR_PAGES = 0x40
 
 HA_NBINS = 33
 HA_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -46,6 +47,7 @@ EXPORTED = [
     "hash_attn_encode_keys_mlp", "hash_attn_decode_mapped", "hash_attn_topk_exact_workspace_size",
     "hash_attn_topk_exact", "hash_attn_topk_exact_timed", "hash_attn_recall",
     "hash_attn_append", "hash_attn_packed_workspace_size", "hash_attn_prefill", "hash_attn_chunk",
+    "hash_attn_plan_pages", "hash_attn_append_axes",
     "hash_attn_device_status",
     "hash_attn_status_string", "hash_attn_last_error",
 ]
@@ -146,6 +148,22 @@ class HARope(ctypes.Structure):
     _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
+class HARopeAxes(ctypes.Structure):
+    """Mirror of ``ha_rope_axes``."""
+
+    tensor = None  # inv_freq, where it came as one (see rope_axes)
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("reserved", ctypes.c_int32), ("axis", ctypes.c_uint8 * 64)]
+
+
+class HAPaging(ctypes.Structure):
+    """Mirror of ``ha_paging``."""
+
+    _fields_ = [("n_seq", ctypes.c_int32), ("total", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("table_st", ctypes.c_int64)]
+
+
 class HashAttnError(RuntimeError):
     def __init__(self, status: int, detail: str):
         super().__init__(f"{status_string(status)} ({status}): {detail}")
@@ -204,6 +222,8 @@ def lib() -> ctypes.CDLL:
     L.hash_attn_recall.argtypes = [_P, _P, _I32, _P, _P, _I32, _I32, _P, _P]
     TP, CP = ctypes.POINTER(HATokens), ctypes.POINTER(HACache)
     L.hash_attn_append.argtypes = [TP, CP, ctypes.POINTER(HARope)] + [_P] * 13
+    L.hash_attn_append_axes.argtypes = [TP, CP, ctypes.POINTER(HARopeAxes), _P, ctypes.c_int64] + [_P] * 13
+    L.hash_attn_plan_pages.argtypes = [ctypes.POINTER(HAPaging)] + [_P] * 11
     L.hash_attn_packed_workspace_size.argtypes = [TP, ctypes.POINTER(_SZ)]
     L.hash_attn_prefill.argtypes = [TP] + [_P] * 7 + [_SZ, _P]
     L.hash_attn_chunk.argtypes = [TP, CP] + [_P] * 9 + [_SZ, _P]
@@ -639,10 +659,7 @@ def rope(inv_freq, interleaved: bool = False) -> HARope:
     return r
 
 
-def hash_attn_append(tokens, cache, q, k, v, page_table, cu, seq_lens, q_out, K, V, *, rope=None, W=None, k_sig=None,
-                     dev_flags=None, stream=None) -> None:
-    """Rotate the packed new tokens' q (into ``q_out``) and k by position and write k, v
-    (and with ``W`` the keys' codes) into the paged cache; ``q`` and ``q_out`` may be None."""
+def _append_checked(tokens, cache, q, k, v, page_table, cu, seq_lens, q_out, K, V, W, k_sig, dev_flags) -> None:
     f32, types, ints = _types()
     n, T, h_q, h_kv, d, dtype, _, _, q_st, q_sh, k_st, k_sh, v_st, v_sh = _fields_of_tokens(tokens)
     pool, n_pages, size, pages, table_st, K_sp, K_sh, K_sn, V_sp, V_sh, V_sn, ks_sp, ks_sh = _fields_of_cache(cache)
@@ -669,11 +686,93 @@ def hash_attn_append(tokens, cache, q, k, v, page_table, cu, seq_lens, q_out, K,
         _table_as_made(page_table, n, pages, table_st)
         if k_sig is not None and k_sig.__class__ is not int:
             _as_made((k_sig, cached[:3], (ks_sp, ks_sh, 1), k_sig.dtype if k_sig.dtype in ints else ints[0], "k_sig"))
+
+
+def hash_attn_append(tokens, cache, q, k, v, page_table, cu, seq_lens, q_out, K, V, *, rope=None, W=None, k_sig=None,
+                     dev_flags=None, stream=None) -> None:
+    """Rotate the packed new tokens' q (into ``q_out``) and k by position and write k, v
+    (and with ``W`` the keys' codes) into the paged cache; ``q`` and ``q_out`` may be None."""
+    _append_checked(tokens, cache, q, k, v, page_table, cu, seq_lens, q_out, K, V, W, k_sig, dev_flags)
     device = _device()
     a = _here(device, q, k, v, W, page_table, cu, seq_lens, q_out, K, V, k_sig, dev_flags)
     if rope is not None and rope.tensor is not None and rope.tensor.get_device() != device:
         _elsewhere(rope.tensor)
     _check(lib().hash_attn_append(tokens, cache, rope, *a, _raw_stream(device) if stream is None else _stream(stream)))
+
+
+def rope_axes(inv_freq, axis, interleaved: bool = False) -> HARopeAxes:
+    """HARopeAxes over a contiguous float32 device tensor inv_freq [rot_dim / 2] (which it keeps);
+    ``axis``: the axis of every pair (whole numbers from 0)."""
+    if inv_freq.dtype is not _types()[0] or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be contiguous float32")
+    axis = [int(a) for a in axis]
+    if len(axis) != inv_freq.numel() or not axis or min(axis) < 0 or max(axis) > 7 or len(axis) > 64:
+        raise ValueError(f"axis must give each of the {inv_freq.numel()} pairs (64 at most) one of 8 axes")
+    r = HARopeAxes()
+    r.tensor = inv_freq
+    r.inv_freq = _ptr(inv_freq)
+    r.rot_dim = 2 * len(axis)
+    r.interleaved = 1 if interleaved else 0
+    r.n_axes = max(axis) + 1
+    r.axis[:len(axis)] = axis
+    return r
+
+
+def hash_attn_append_axes(tokens, cache, q, k, v, page_table, cu, seq_lens, positions, q_out, K, V, *, rope, W=None, k_sig=None,
+                          dev_flags=None, stream=None) -> None:
+    """hash_attn_append with rotations by several axes: ``rope`` from ``rope_axes``, ``positions``
+    int32 [n_axes, total] (rows contiguous; more axes than the rope has are not read)."""
+    _append_checked(tokens, cache, q, k, v, page_table, cu, seq_lens, q_out, K, V, W, k_sig, dev_flags)
+    pos_st = tokens.total
+    if positions.__class__ is not int:
+        axes, rows = positions.shape
+        pos_st = positions.stride(0)
+        if (axes < rope.n_axes or rows != tokens.total or positions.dtype is not _types()[2][0] or (positions.stride(1) != 1 and rows > 1)
+                or (pos_st < rows and axes > 1)):
+            raise ValueError(f"positions must be int32 [{rope.n_axes}, {tokens.total}] with contiguous rows")
+    device = _device()
+    a = _here(device, q, k, v, W, page_table, cu, seq_lens, q_out, K, V, k_sig, dev_flags, positions)
+    if rope.tensor is not None and rope.tensor.get_device() != device:
+        _elsewhere(rope.tensor)
+    _check(lib().hash_attn_append_axes(tokens, cache, rope, a[12], pos_st, *a[:12], _raw_stream(device) if stream is None else _stream(stream)))
+
+
+def make_paging(page_table, n_pages: int, page_size: int, total: int) -> HAPaging:
+    """ha_paging of sequences whose pages are in ``page_table`` int32 [n_seq, max_pages], out of a pool
+    of ``n_pages``; ``total``: rows that the packed buffers have room for."""
+    if page_table.dim() != 2 or page_table.dtype not in _types()[2] or page_table.stride(1) != 1 and page_table.shape[1] > 1:
+        raise ValueError("page_table must be int32 [n_seq, max_pages] with contiguous rows")
+    p = HAPaging()
+    p.n_seq, p.max_pages = page_table.shape
+    p.total, p.n_pages, p.page_size = int(total), int(n_pages), int(page_size)
+    p.table_st = page_table.stride(0)
+    return p
+
+
+def hash_attn_plan_pages(paging, new_lens, seq_lens, seq_lens_out, cu, page_table, free_pages, n_free, n_free_out, *, slots=None,
+                         dev_flags=None, stream=None) -> None:
+    """Plan a step's pages: ``seq_lens_out`` and ``n_free_out`` may be ``seq_lens`` and ``n_free``; the table
+    and the stack of free pages are updated in place (a plan changes neither if run again)."""
+    ints, n, pages = _types()[2], paging.n_seq, paging.max_pages
+    try:
+        good = (new_lens.numel() == n and new_lens.dtype in ints and new_lens.is_contiguous()
+                and seq_lens.numel() == n and seq_lens.dtype in ints and seq_lens.is_contiguous()
+                and seq_lens_out.numel() == n and seq_lens_out.dtype in ints and seq_lens_out.is_contiguous()
+                and cu.numel() == n + 1 and cu.dtype in ints and cu.is_contiguous()
+                and page_table.shape == (n, pages) and page_table.stride() == (paging.table_st, 1) and page_table.dtype in ints
+                and free_pages.numel() == paging.n_pages and free_pages.dtype in ints and free_pages.is_contiguous()
+                and n_free.numel() == 1 and n_free.dtype in ints and n_free_out.numel() == 1 and n_free_out.dtype in ints
+                and slots.numel() == paging.total and slots.dtype in ints and slots.is_contiguous() and dev_flags is None)
+    except AttributeError:
+        good = False
+    if not good:
+        _int32s((new_lens, n, "new_lens"), (seq_lens, n, "seq_lens"), (seq_lens_out, n, "seq_lens_out"), (cu, n + 1, "cu"),
+                (free_pages, paging.n_pages, "free_pages"), (n_free, 1, "n_free"), (n_free_out, 1, "n_free_out"),
+                (slots, paging.total, "slots"), (dev_flags, 1, "dev_flags"))
+        _table_as_made(page_table, n, pages, paging.table_st)
+    device = _device()
+    a = _here(device, new_lens, seq_lens, seq_lens_out, cu, page_table, slots, free_pages, n_free, n_free_out, dev_flags)
+    _check(lib().hash_attn_plan_pages(paging, *a, _raw_stream(device) if stream is None else _stream(stream)))
 
 
 def hash_attn_packed_workspace_size(tokens) -> int:
