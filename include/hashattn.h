@@ -797,6 +797,53 @@ ha_status hash_attn_append_axes(const ha_tokens* tokens, const ha_cache* cache, 
                                 void* q_out, void* K, void* V, uint32_t* k_sig, uint32_t* dev_flags, void* stream);
 
 /*
+ * Score options of prefill and chunk (zero-initialise and set what is needed). With z = <q, k_j> and
+ * pos the token's position among its sequence's keys (seq_lens[s] - nq + i, a prompt's i), a
+ * token's score of key j is
+ *   cap(scale z) - slopes[h] |pos - j|,   cap(z) = softcap tanh(z / softcap), or z without a cap,
+ * and the token sees the keys
+ *   max(first[s], pos - window + 1) <= j < max(pos + 1, prefix[s]),   0 <= j < nk.
+ * A token that sees none gives out = 0, lse = -inf.
+ *   scale    0: 1 / sqrt(d); else in [2^-60, 2^60]
+ *   softcap  0: none; else in [2^-60, 2^60], with scale / softcap in [2^-60, 2^60]
+ *   window   0: none; else a token sees itself and the window - 1 keys before it (and what a prefix
+ *            shows it behind it)
+ *   slopes   float32 [h_q] (device, finite, any sign), or NULL: no bias
+ *   prefix   int32 [n_seq] (device), or NULL: keys below prefix[s] are seen by every token of the
+ *            sequence, later ones too (an image, an instruction; prefix[s] = nk: attention both ways)
+ *   first    int32 [n_seq] (device), or NULL: the sequence's first key (what lies before it is
+ *            padding, or another document: tokens of several documents in one sequence are
+ *            given as several sequences that share a row of the table)
+ *   reserved must be 0
+ * prefix and first are clamped to [0, nk]. Pages whose keys no token of the sequence sees are not
+ * read: their table entries and contents may be anything.
+ */
+typedef struct {
+    float scale;
+    float softcap;
+    int32_t window;
+    int32_t reserved;
+    const float* slopes;
+    const int32_t* prefix;
+    const int32_t* first;
+} ha_score_opts;
+
+/*
+ * hash_attn_prefill and hash_attn_chunk with score options (opts may be NULL: the calls without).
+ * Workspace, layouts, limits and errors are the same, and HA_ERR_INVALID_ARG for options outside
+ * their ranges. V must be finite for the keys that a token of the sequence sees, K and V may hold
+ * anything elsewhere. slopes with a bias that outweighs float32 (slope x distance above 2^24) leave
+ * the nearest keys' weights exact and round the others'.
+ */
+ha_status hash_attn_prefill_ex(const ha_tokens* tokens, const ha_score_opts* opts, const void* q, const void* K,
+                               const void* V, const int32_t* cu, void* out, float* lse, void* workspace, size_t ws_bytes,
+                               void* stream);
+ha_status hash_attn_chunk_ex(const ha_tokens* tokens, const ha_cache* cache, const ha_score_opts* opts, const void* q,
+                             const void* K, const void* V, const int32_t* table, const int32_t* cu,
+                             const int32_t* seq_lens, void* out, float* lse, void* workspace, size_t ws_bytes,
+                             void* stream);
+
+/*
  * Synchronise `stream`, read and clear the workspace's device error word.
  * Returns HA_OK, HA_ERR_TIMEOUT (timeout flag set) or HA_ERR_DEVICE (any other
  * flag); *flags (optional) receives the raw HA_DEVERR_* bits.

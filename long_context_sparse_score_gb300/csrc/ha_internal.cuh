@@ -326,6 +326,26 @@ struct PackedParams {
     float qscale;              // log2(e) / sqrt(d)
 };
 
+// The same with score options (ha_score_opts). Where scores are shaped (capped or biased) the softmax
+// takes them in units of log2 e, and qscale is 1.
+struct PackedParamsEx : PackedParams {
+    const int32_t* prefix;     // [n_seq] or null
+    const int32_t* first;      // [n_seq] or null
+    const float* slopes;       // [Hq] or null
+    int window;                // 0: none
+    int shaped;
+    float scale;               // scale of the scores x log2(e)
+    float cap;                 // cap x log2(e), 0: none
+    float twice;               // 2 log2(e) scale / cap: e^{2 u} = 2^{twice x}
+    float fit;                 // |x| up to which tanh is the polynomial
+    float unit;                // scale / cap: u of a product x is unit x
+    float poly[7];             // cap tanh(u) = u (poly[0] + poly[1] u^2 + ..)
+    // Capped scores lie within +-cap, so where 2^{2 cap} fits a float's range a constant reference
+    // serves as the softmax's maximum: no maximum is looked for, and nothing is rescaled.
+    int fixed_ref;
+    float ref;
+};
+
 // k_append: rotation of queries and keys, keys and values into the cache.
 struct AppendParams {
     const void *q, *k, *v;     // q may be null

@@ -1488,8 +1488,49 @@ bool encode_fold(CUtensorMap* m, const void* base, int64_t row, int64_t groups, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// tanh(u) / u for |u| <= 1 as a polynomial of u^2, fitted in relative error (Chebyshev nodes,
+// weights moved until the error is even): degree 5 to 5.9e-7, degree 6 to 5.0e-8.
+constexpr double kTanh5[7] = {0.9999994136, -0.3332904237, 0.1328143379, -0.05160567156, 0.01674311229, -0.003067059224, 0.0};
+constexpr double kTanh6[7] = {0.9999999502, -0.3333283915, 0.1332520406, -0.0534570289, 0.02028997915, -0.006203377978, 0.00104102226};
+
+ha_status check_opts(const ha_score_opts* o) {
+    auto in_range = [](double x) { return x >= std::ldexp(1.0, -60) && x <= std::ldexp(1.0, 60); };  // false for NaN
+    if (o->scale != 0.f && !in_range(o->scale)) return fail(HA_ERR_INVALID_ARG, "opts->scale must be 0 or in [2^-60, 2^60] (got %g)", o->scale);
+    if (o->softcap != 0.f && !in_range(o->softcap))
+        return fail(HA_ERR_INVALID_ARG, "opts->softcap must be 0 or in [2^-60, 2^60] (got %g)", o->softcap);
+    if (o->softcap != 0.f && o->scale != 0.f && !in_range((double)o->scale / o->softcap))
+        return fail(HA_ERR_INVALID_ARG, "opts->scale / opts->softcap must be in [2^-60, 2^60] (got %g, %g)", o->scale, o->softcap);
+    if (o->window < 0) return fail(HA_ERR_INVALID_ARG, "opts->window must be at least 0 (got %d)", o->window);
+    if (o->reserved != 0) return fail(HA_ERR_INVALID_ARG, "ha_score_opts.reserved must be zero");
+    return HA_OK;
+}
+
+void set_opts(PackedParamsEx& p, const ha_score_opts* o, int d, bool f32) {
+    const double log2e = 1.4426950408889634, scale = o->scale != 0.f ? (double)o->scale : 1.0 / std::sqrt((double)d);
+    p.prefix = o->prefix;
+    p.first = o->first;
+    p.slopes = o->slopes;
+    p.window = o->window < p.max_len ? o->window : 0;  // one that reaches over all keys is none
+    p.scale = (float)(scale * log2e);
+    p.qscale = p.scale;
+    p.shaped = o->softcap != 0.f || o->slopes != nullptr;
+    if (p.shaped) p.qscale = 1.f;
+    if (o->softcap != 0.f) {
+        const double cap = o->softcap;
+        p.cap = (float)(cap * log2e);
+        p.unit = (float)(scale / cap);
+        p.twice = (float)(2.0 * log2e * scale / cap);
+        p.fit = (float)(cap / scale);
+        for (int i = 0; i < 7; ++i) p.poly[i] = (float)((f32 ? kTanh6[i] : kTanh5[i]) * cap * log2e);
+        // Weights from 2^24 (sums of 2^24 of them, times V, stay in range) down to what keeps a float's
+        // (or, of three bf16 parts, the last one's) full precision.
+        p.ref = p.cap - 24.f;
+        p.fixed_ref = o->slopes == nullptr && 2.f * p.cap - 24.f <= (f32 ? 100.f : 122.f);
+    }
+}
+
 // prefill (cache null: K and V packed like q) and chunk
-ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q, const void* K, const void* V,
+ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const ha_score_opts* opts, const void* q, const void* K, const void* V,
                            const int32_t* table, const int32_t* cu, const int32_t* seq_lens, void* out, float* lse,
                            void* workspace, size_t ws_bytes, void* stream) {
     HA_TRY(check_tokens(t));
@@ -1499,6 +1540,7 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
         return fail(HA_ERR_UNSUPPORTED, "out_dtype must be HA_F32 or HA_BF16 (got %d)", t->out_dtype);
     const int G = t->h_q / t->h_kv;
     if (G > kMaxGroup) return fail(HA_ERR_UNSUPPORTED, "at most %d query heads per KV head (got %d)", kMaxGroup, G);
+    if (opts != nullptr) HA_TRY(check_opts(opts));
     if (cu == nullptr || (c != nullptr && seq_lens == nullptr)) return fail(HA_ERR_INVALID_ARG, "cu and seq_lens must not be NULL");
     if (c != nullptr) {
         HA_TRY(check_cache(c, t, K, V, table));
@@ -1524,11 +1566,12 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
     const int64_t tiles = ceil_div(max_len, kt);
     const int64_t items = (ceil_div(t->total, 2 * L.tq) + t->n_seq) * t->h_kv;
     // the kernel counts the work in 32 bits (a prompt's items see half of its tiles on average)
-    const int64_t work = items * ((c != nullptr ? tiles : tiles / 2) + 8);
+    const bool half = c == nullptr && (opts == nullptr || opts->prefix == nullptr);
+    const int64_t work = items * ((half ? tiles / 2 : tiles) + 8);
     if (work >= (int64_t)1 << 32)
         return fail(HA_ERR_UNSUPPORTED, "too much for one call: up to %lld items of up to %lld key tiles (2^32 tiles in all)",
                     (long long)items, (long long)tiles);
-    PackedParams p{};
+    PackedParamsEx p{};
     p.cu = cu;
     p.n_seq = t->n_seq;
     p.total = t->total;
@@ -1601,8 +1644,13 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const void* q,
     // parted, which saves the merge (a prompt of 300 tokens 18.4 -> 14.4 us, 64 decodes over
     // up to 500 keys 39.9 -> 36.7, one over 500 keys 11.6 -> 12.1).
     const int grid = (int)std::min<int64_t>(kSMs, items * tiles);
-    HA_LAUNCH(launch_packed_att(p, m, t->d, f32, grid, grid > 1 && p.split, static_cast<cudaStream_t>(stream)),
-              "packed attention launch");
+    const bool merge = grid > 1 && p.split;
+    if (opts == nullptr) {
+        HA_LAUNCH(launch_packed_att(p, m, t->d, f32, grid, merge, static_cast<cudaStream_t>(stream)), "packed attention launch");
+    } else {
+        set_opts(p, opts, t->d, f32);
+        HA_LAUNCH(launch_packed_att_ex(p, m, t->d, f32, grid, merge, static_cast<cudaStream_t>(stream)), "packed attention launch");
+    }
     return HA_OK;
 }
 
@@ -1620,14 +1668,28 @@ extern "C" ha_status hash_attn_packed_workspace_size(const ha_tokens* tokens, si
 
 extern "C" ha_status hash_attn_prefill(const ha_tokens* tokens, const void* q, const void* K, const void* V, const int32_t* cu,
                                        void* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
-    return packed_attention(tokens, nullptr, q, K, V, nullptr, cu, nullptr, out, lse, workspace, ws_bytes, stream);
+    return packed_attention(tokens, nullptr, nullptr, q, K, V, nullptr, cu, nullptr, out, lse, workspace, ws_bytes, stream);
 }
 
 extern "C" ha_status hash_attn_chunk(const ha_tokens* tokens, const ha_cache* cache, const void* q, const void* K, const void* V,
                                      const int32_t* table, const int32_t* cu, const int32_t* seq_lens, void* out, float* lse,
                                      void* workspace, size_t ws_bytes, void* stream) {
     if (cache == nullptr) return fail(HA_ERR_INVALID_ARG, "cache is NULL");
-    return packed_attention(tokens, cache, q, K, V, table, cu, seq_lens, out, lse, workspace, ws_bytes, stream);
+    return packed_attention(tokens, cache, nullptr, q, K, V, table, cu, seq_lens, out, lse, workspace, ws_bytes, stream);
+}
+
+extern "C" ha_status hash_attn_prefill_ex(const ha_tokens* tokens, const ha_score_opts* opts, const void* q, const void* K,
+                                          const void* V, const int32_t* cu, void* out, float* lse, void* workspace,
+                                          size_t ws_bytes, void* stream) {
+    return packed_attention(tokens, nullptr, opts, q, K, V, nullptr, cu, nullptr, out, lse, workspace, ws_bytes, stream);
+}
+
+extern "C" ha_status hash_attn_chunk_ex(const ha_tokens* tokens, const ha_cache* cache, const ha_score_opts* opts, const void* q,
+                                        const void* K, const void* V, const int32_t* table, const int32_t* cu,
+                                        const int32_t* seq_lens, void* out, float* lse, void* workspace, size_t ws_bytes,
+                                        void* stream) {
+    if (cache == nullptr) return fail(HA_ERR_INVALID_ARG, "cache is NULL");
+    return packed_attention(tokens, cache, opts, q, K, V, table, cu, seq_lens, out, lse, workspace, ws_bytes, stream);
 }
 
 namespace ha {

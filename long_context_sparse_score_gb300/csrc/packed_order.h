@@ -41,6 +41,45 @@ struct TileSums {
     }
 };
 
+// The keys and key tiles (2^K keys) of a row of items under score options: t2 new tokens to an item;
+// token t of nq, whose position is base + t, sees the keys max(first, base + t + 1 - window) <= j <
+// max(base + t + 1, prefix) below nk = base + nq (window 0: none; first and prefix lie within [0, nk]).
+// Both ends grow with the item, each from where it leaves a constant, so the work of a row of items
+// is two constants and two sums in closed form.
+template <int K>
+struct MaskedItems {
+    int base, nq, first, prefix, window, t2;
+    HA_HD static int least(int a, int b) { return a < b ? a : b; }
+    HA_HD static int most(int a, int b) { return a > b ? a : b; }
+    HA_HD static int tiles_of(int keys) { return (keys + (1 << K) - 1) >> K; }
+    // end of the keys that the first `upto` tokens see
+    HA_HD int end(int upto) const { return most(base + least(upto, nq), prefix); }
+    // the first key that token t sees, if it sees any
+    HA_HD int begin(int t) const { return window > 0 ? most(first, base + t + 1 - window) : first; }
+    // An item's first tile (0 where it sees no key) and its tiles (then 1, so that its rows are written).
+    HA_HD bool none(int qt) const { return begin(qt * t2) >= end((qt + 1) * t2); }
+    HA_HD int begin_tile(int qt) const { return none(qt) ? 0 : begin(qt * t2) >> K; }
+    HA_HD int tiles(int qt) const { return none(qt) ? 1 : tiles_of(end((qt + 1) * t2)) - (begin(qt * t2) >> K); }
+    // tiles of the items 0 .. qt - 1, all of t2 tokens
+    HA_HD uint32_t tiles_before(int qt, const TileSums<K>& sums, const uint16_t* before) const {
+        if (qt == 0) return 0;
+        // items 0 .. z - 1 see no key: they end at or before `first`
+        const int z = prefix > first || base > first ? 0 : least(qt, (first - base) / t2);
+        // items z .. e - 1 end with the prefix
+        const int e = base > prefix ? z : least(qt, most(z, (prefix - base) / t2));
+        uint32_t c = (uint32_t)z + (uint32_t)(e - z) * (uint32_t)tiles_of(prefix);
+        if (qt > e) c += sums.sum((uint32_t)(qt - e), (uint32_t)(base + (e + 1) * t2 + (1 << K) - 1), before);
+        // items z .. b - 1 begin at `first`
+        int b = qt;
+        if (window > 0) {
+            const int w = base + 1 - window;
+            b = w > first ? z : least(qt, most(z, (first - w) / t2 + 1));
+            if (qt > b) c -= sums.sum((uint32_t)(qt - b), (uint32_t)(w + b * t2), before);
+        }
+        return c - (uint32_t)(b - z) * (uint32_t)(first >> K);
+    }
+};
+
 // The order of the products of a segment whose S and P have three places (head dim 64): which stream
 // and key tile product k belongs to, for the warp that issues them and the warps that wait for them.
 // One row tile: the key tiles in turn, even ones stream 0's. Two: key tile by key tile, row

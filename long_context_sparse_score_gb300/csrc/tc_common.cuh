@@ -33,6 +33,8 @@ struct PackedMaps {
 };
 cudaError_t launch_packed_att(const struct PackedParams& p, const PackedMaps& m, int d, bool f32_out, int grid,
                               bool merge, cudaStream_t st);
+cudaError_t launch_packed_att_ex(const struct PackedParamsEx& p, const PackedMaps& m, int d, bool f32_out, int grid,
+                                 bool merge, cudaStream_t st);
 
 // Shared-memory matrix descriptor of a K-major operand in the 128-byte swizzle
 // layout that TMA writes: rows of 128 bytes, 8-row groups 1024 bytes apart.

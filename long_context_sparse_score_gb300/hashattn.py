@@ -47,7 +47,7 @@ EXPORTED = [
     "hash_attn_encode_keys_mlp", "hash_attn_decode_mapped", "hash_attn_topk_exact_workspace_size",
     "hash_attn_topk_exact", "hash_attn_topk_exact_timed", "hash_attn_recall",
     "hash_attn_append", "hash_attn_packed_workspace_size", "hash_attn_prefill", "hash_attn_chunk",
-    "hash_attn_plan_pages", "hash_attn_append_axes",
+    "hash_attn_plan_pages", "hash_attn_append_axes", "hash_attn_prefill_ex", "hash_attn_chunk_ex",
     "hash_attn_device_status",
     "hash_attn_status_string", "hash_attn_last_error",
 ]
@@ -156,6 +156,14 @@ class HARopeAxes(ctypes.Structure):
                 ("n_axes", ctypes.c_int32), ("reserved", ctypes.c_int32), ("axis", ctypes.c_uint8 * 64)]
 
 
+class HAScoreOpts(ctypes.Structure):
+    """Mirror of ``ha_score_opts``."""
+
+    tensors = None  # slopes, prefix and first, where any of them came as a tensor (see score_opts)
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("slopes", ctypes.c_void_p), ("prefix", ctypes.c_void_p), ("first", ctypes.c_void_p)]
+
+
 class HAPaging(ctypes.Structure):
     """Mirror of ``ha_paging``."""
 
@@ -227,6 +235,9 @@ def lib() -> ctypes.CDLL:
     L.hash_attn_packed_workspace_size.argtypes = [TP, ctypes.POINTER(_SZ)]
     L.hash_attn_prefill.argtypes = [TP] + [_P] * 7 + [_SZ, _P]
     L.hash_attn_chunk.argtypes = [TP, CP] + [_P] * 9 + [_SZ, _P]
+    XP = ctypes.POINTER(HAScoreOpts)
+    L.hash_attn_prefill_ex.argtypes = [TP, XP] + [_P] * 7 + [_SZ, _P]
+    L.hash_attn_chunk_ex.argtypes = [TP, CP, XP] + [_P] * 9 + [_SZ, _P]
     L.hash_attn_device_status.argtypes = [_P, _P, ctypes.POINTER(ctypes.c_uint32)]
     L.hash_attn_status_string.argtypes = [_I32]
     L.hash_attn_status_string.restype = ctypes.c_char_p
@@ -781,8 +792,7 @@ def hash_attn_packed_workspace_size(tokens) -> int:
     return out.value
 
 
-def hash_attn_prefill(tokens, q, K, V, cu, out, lse, *, workspace, stream=None) -> None:
-    """Causal attention over packed prompts; out [total, Hq, d], lse [total, Hq] contiguous."""
+def _prefill_checked(tokens, q, K, V, cu, out, lse) -> None:
     f32, types, ints = _types()
     n, T, h_q, h_kv, d, dtype, out_dtype, _, q_st, q_sh, k_st, k_sh, v_st, v_sh = _fields_of_tokens(tokens)
     dtype, out_dtype, rows = types[dtype], types[out_dtype], (T, h_kv, d)
@@ -800,14 +810,18 @@ def hash_attn_prefill(tokens, q, K, V, cu, out, lse, *, workspace, stream=None) 
         _int32s((cu, n + 1, "cu"))
         _as_made((q, (T, h_q, d), (q_st, q_sh, 1), dtype, "q"), (K, rows, (k_st, k_sh, 1), dtype, "K"),
                  (V, rows, (v_st, v_sh, 1), dtype, "V"))
+
+
+def hash_attn_prefill(tokens, q, K, V, cu, out, lse, *, workspace, stream=None) -> None:
+    """Causal attention over packed prompts; out [total, Hq, d], lse [total, Hq] contiguous."""
+    _prefill_checked(tokens, q, K, V, cu, out, lse)
     device = _device()
     a = _here(device, q, K, V, cu, out, lse, workspace)
     _check(lib().hash_attn_prefill(tokens, *a, workspace.numel() * workspace.element_size(),
                                    _raw_stream(device) if stream is None else _stream(stream)))
 
 
-def hash_attn_chunk(tokens, cache, q, K, V, page_table, cu, seq_lens, out, lse, *, workspace, stream=None) -> None:
-    """Attention of the packed new tokens over the paged cache (their keys are in it already)."""
+def _chunk_checked(tokens, cache, q, K, V, page_table, cu, seq_lens, out, lse) -> None:
     f32, types, ints = _types()
     n, T, h_q, h_kv, d, dtype, out_dtype, _, q_st, q_sh, _, _, _, _ = _fields_of_tokens(tokens)
     pool, n_pages, size, pages, table_st, K_sp, K_sh, K_sn, V_sp, V_sh, V_sn, _, _ = _fields_of_cache(cache)
@@ -829,10 +843,57 @@ def hash_attn_chunk(tokens, cache, q, K, V, page_table, cu, seq_lens, out, lse, 
         _as_made((q, (T, h_q, d), (q_st, q_sh, 1), dtype, "q"), (K, cached, (K_sp, K_sh, K_sn, 1), pool, "K"),
                  (V, cached, (V_sp, V_sh, V_sn, 1), pool, "V"))
         _table_as_made(page_table, n, pages, table_st)
+
+
+def hash_attn_chunk(tokens, cache, q, K, V, page_table, cu, seq_lens, out, lse, *, workspace, stream=None) -> None:
+    """Attention of the packed new tokens over the paged cache (their keys are in it already)."""
+    _chunk_checked(tokens, cache, q, K, V, page_table, cu, seq_lens, out, lse)
     device = _device()
     a = _here(device, q, K, V, page_table, cu, seq_lens, out, lse, workspace)
     _check(lib().hash_attn_chunk(tokens, cache, *a, workspace.numel() * workspace.element_size(),
                                  _raw_stream(device) if stream is None else _stream(stream)))
+
+
+def score_opts(*, scale: float = 0.0, softcap: float = 0.0, window: int = 0, slopes=None, prefix=None, first=None) -> HAScoreOpts:
+    """HAScoreOpts: scores scale z (0: 1 / sqrt(d)), capped to softcap tanh(z / softcap), less
+    slopes[h] times the distance; a sliding ``window``; keys below prefix[s] seen by every token of sequence s,
+    keys before first[s] by none. ``slopes`` float32 [h_q], ``prefix`` and ``first`` int32 [n_seq], contiguous device
+    tensors (which it keeps), raw addresses or None."""
+    o = HAScoreOpts()
+    o.scale, o.softcap, o.window = scale, softcap, int(window)
+    o.slopes, o.prefix, o.first = (_ptr(t) for t in (slopes, prefix, first))
+    tensors = tuple(None if t.__class__ is int else t for t in (slopes, prefix, first))
+    o.tensors = tensors if any(t is not None for t in tensors) else None
+    return o
+
+
+def _opts_checked(opts, tokens, device) -> None:
+    slopes, prefix, first = opts.tensors
+    _whole((slopes, tokens.h_q, _types()[0], "slopes"))
+    _int32s((prefix, tokens.n_seq, "prefix"), (first, tokens.n_seq, "first"))
+    _here(device, slopes, prefix, first)
+
+
+def hash_attn_prefill_ex(tokens, opts, q, K, V, cu, out, lse, *, workspace, stream=None) -> None:
+    """hash_attn_prefill with score options (``score_opts``; None: without)."""
+    _prefill_checked(tokens, q, K, V, cu, out, lse)
+    device = _device()
+    if opts is not None and opts.tensors is not None:
+        _opts_checked(opts, tokens, device)
+    a = _here(device, q, K, V, cu, out, lse, workspace)
+    _check(lib().hash_attn_prefill_ex(tokens, opts, *a, workspace.numel() * workspace.element_size(),
+                                      _raw_stream(device) if stream is None else _stream(stream)))
+
+
+def hash_attn_chunk_ex(tokens, cache, opts, q, K, V, page_table, cu, seq_lens, out, lse, *, workspace, stream=None) -> None:
+    """hash_attn_chunk with score options (``score_opts``; None: without)."""
+    _chunk_checked(tokens, cache, q, K, V, page_table, cu, seq_lens, out, lse)
+    device = _device()
+    if opts is not None and opts.tensors is not None:
+        _opts_checked(opts, tokens, device)
+    a = _here(device, q, K, V, page_table, cu, seq_lens, out, lse, workspace)
+    _check(lib().hash_attn_chunk_ex(tokens, cache, opts, *a, workspace.numel() * workspace.element_size(),
+                                    _raw_stream(device) if stream is None else _stream(stream)))
 
 
 def hash_attn_device_status(workspace, stream=None) -> tuple[int, int]:

@@ -83,3 +83,41 @@ def rotate_axes(x, positions, axis, inv_freq, interleaved=False):
         u, v = x[..., i].copy(), x[..., j].copy()
         x[..., i], x[..., j] = u * math.cos(a) - v * math.sin(a), u * math.sin(a) + v * math.cos(a)
     return x
+
+
+def attention(q, K, V, *, scale=None, cap=0.0, slope=0.0, window=0, prefix=0, first=0):
+    """New tokens q [nq, d] (the last of the sequence) over keys K, V [nk, d] with score options: (out [nq, d],
+    lse [nq], tol [nq, d], tol_lse [nq], mag [nq, d]). mag = sum_j p_j |v_j|; tol bounds the error of a
+    computation in float32 (see below), before weights or results are rounded to fewer bits.
+
+    A score z sums d exact products (d steps of 2^-23 relative to sum_k |q_k K_jk| scale, if the adder
+    truncates); cap tanh(z / cap) costs 2^-20 cap (the polynomial 8e-7, its value less the softmax's
+    reference 2^-23 of up to 3 cap more); the bias, formed from the distance of up to 128 columns away, 2^-21 of
+    itself; the exponential 2^-22 and the sums 2^-23 a term. A weight's relative error e_j moves
+    out by p_j e_j (|v_j| + |out|) and lse by p_j e_j."""
+    q, K, V = (np.asarray(x, dtype=np.float64) for x in (q, K, V))
+    (nq, d), nk = q.shape, K.shape[0]
+    scale = 1 / math.sqrt(d) if scale is None else scale
+    out, tol, mag = np.zeros((nq, d)), np.zeros((nq, d)), np.zeros((nq, d))
+    lse, tol_lse = np.full(nq, -math.inf), np.zeros(nq)
+    for i in range(nq):
+        pos = nk - nq + i
+        lo = max(0, first, pos - window + 1 if window else 0)
+        hi = min(nk, max(pos + 1, prefix))
+        if lo >= hi:
+            continue
+        k, v = K[lo:hi], V[lo:hi]
+        z = k @ q[i] * scale
+        if cap:
+            z = cap * np.tanh(z / cap)
+        dist = np.abs(pos - np.arange(lo, hi))
+        z = z - slope * dist
+        top = z.max()
+        w = np.exp(z - top)
+        e = 2.0 ** -23 * ((d + 4) * scale * (np.abs(k) @ np.abs(q[i])) + (hi - lo) + 16) + 2.0 ** -20 * cap + 2.0 ** -21 * abs(slope) * (dist + 128)
+        p = w / w.sum()
+        out[i], mag[i] = p @ v, p @ np.abs(v)
+        lse[i] = top + math.log(w.sum())
+        tol_lse[i] = p @ e + 2.0 ** -22 * (1 + abs(lse[i]) + 2 * cap)
+        tol[i] = (p * e) @ np.abs(v) + (p @ e) * mag[i]
+    return out, lse, tol, tol_lse, mag
