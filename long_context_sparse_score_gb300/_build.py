@@ -19,7 +19,8 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libhashattn.so")
 
 SOURCES = ["hashattn_api.cu", "k_select.cu", "k_select_fused.cu", "k_gather_att.cu", "k_group_att.cu", "k_merge.cu", "k_encode.cu", "k_exact.cu",
-           "k_exact_tc.cu", "k_wide.cu", "k_packed_att.cu", "k_packed_att_ex.cu", "k_append.cu", "k_pages.cu"]
+           "k_exact_tc.cu", "k_wide.cu", "k_packed_att.cu", "k_packed_att_masked.cu", "k_packed_att_capped.cu",
+           "k_packed_att_shaped.cu", "k_append.cu", "k_pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -337,13 +337,14 @@ struct PackedParamsEx : PackedParams {
     float scale;               // scale of the scores x log2(e)
     float cap;                 // cap x log2(e), 0: none
     float twice;               // 2 log2(e) scale / cap: e^{2 u} = 2^{twice x}
-    float fit;                 // |x| up to which tanh is the polynomial
     float unit;                // scale / cap: u of a product x is unit x
-    float poly[7];             // cap tanh(u) = u (poly[0] + poly[1] u^2 + ..)
-    // Capped scores lie within +-cap, so where 2^{2 cap} fits a float's range a constant reference
-    // serves as the softmax's maximum: no maximum is looked for, and nothing is rescaled.
+    // cap tanh(u) log2(e) for |x| <= fit[i]: poly[0] and poly[1] are of x, poly[2] is of u
+    float fit[3];
+    float poly[3][7];
+    // Capped scores lie within +-cap, so where 2^{2 cap} fits a float's range a row keeps the reference
+    // that its first keys give (within these bounds): no maximum is looked for, and nothing is rescaled.
     int fixed_ref;
-    float ref;
+    float ref_low, ref_high;
 };
 
 // k_append: rotation of queries and keys, keys and values into the cache.

@@ -1488,12 +1488,21 @@ bool encode_fold(CUtensorMap* m, const void* base, int64_t row, int64_t groups, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// tanh(u) / u for |u| <= 1 as a polynomial of u^2, fitted in relative error (Chebyshev nodes,
-// weights moved until the error is even): degree 5 to 5.9e-7, degree 6 to 5.0e-8.
-constexpr double kTanh5[7] = {0.9999994136, -0.3332904237, 0.1328143379, -0.05160567156, 0.01674311229, -0.003067059224, 0.0};
-constexpr double kTanh6[7] = {0.9999999502, -0.3333283915, 0.1332520406, -0.0534570289, 0.02028997915, -0.006203377978, 0.00104102226};
+// tanh(u) / u as polynomials of u^2, fitted in relative error (at Chebyshev nodes, weights moved until
+// the error is even): for bf16 weights, and for float32 results.
+constexpr double kCapTo16[3] = {0.25, 0.5, 1.0}, kCapTo32[3] = {0.5, 0.75, 1.0};
+constexpr double kTanh16[3][7] = {
+    {0.9999996043, -0.3332190822, 0.1284161342},  // degree 2 up to 0.25: 4.0e-07
+    {0.9999994558, -0.3332631793, 0.1319029658, -0.04440222556},  // degree 3 up to 0.5: 5.4e-07
+    {0.9999994136, -0.3332904237, 0.1328143384, -0.05160567292, 0.01674311383, -0.003067059836},  // degree 5 up to 1: 5.9e-07
+};
+constexpr double kTanh32[3][7] = {
+    {0.9999999869, -0.3333306939, 0.1332477932, -0.05298607518, 0.01713500641},  // degree 4 up to 0.5: 1.3e-08
+    {0.999999971, -0.3333295888, 0.1332540601, -0.05334442995, 0.0195829078, -0.004716256975},  // degree 5 up to 0.75: 2.9e-08
+    {0.9999999502, -0.3333283915, 0.1332520407, -0.05345702927, 0.02028997985, -0.006203378602, 0.001041022467},  // degree 6 up to 1: 5.0e-08
+};
 
-ha_status check_opts(const ha_score_opts* o) {
+ha_status check_score_opts(const ha_score_opts* o) {
     auto in_range = [](double x) { return x >= std::ldexp(1.0, -60) && x <= std::ldexp(1.0, 60); };  // false for NaN
     if (o->scale != 0.f && !in_range(o->scale)) return fail(HA_ERR_INVALID_ARG, "opts->scale must be 0 or in [2^-60, 2^60] (got %g)", o->scale);
     if (o->softcap != 0.f && !in_range(o->softcap))
@@ -1520,12 +1529,18 @@ void set_opts(PackedParamsEx& p, const ha_score_opts* o, int d, bool f32) {
         p.cap = (float)(cap * log2e);
         p.unit = (float)(scale / cap);
         p.twice = (float)(2.0 * log2e * scale / cap);
-        p.fit = (float)(cap / scale);
-        for (int i = 0; i < 7; ++i) p.poly[i] = (float)((f32 ? kTanh6[i] : kTanh5[i]) * cap * log2e);
-        // Weights from 2^24 (sums of 2^24 of them, times V, stay in range) down to what keeps a float's
-        // (or, of three bf16 parts, the last one's) full precision.
-        p.ref = p.cap - 24.f;
-        p.fixed_ref = o->slopes == nullptr && 2.f * p.cap - 24.f <= (f32 ? 100.f : 122.f);
+        // Polynomials of x itself save a product; their terms (up to x^10) have to be normal numbers.
+        const bool plain = scale / cap >= std::ldexp(1.0, f32 ? -11 : -16) && scale / cap <= std::ldexp(1.0, 11);
+        for (int i = 0; i < 3; ++i) {
+            p.fit[i] = plain || i == 2 ? (float)((f32 ? kCapTo32 : kCapTo16)[i] * cap / scale) : -1.f;
+            for (int k = 0; k < 7; ++k)
+                p.poly[i][k] = (float)((f32 ? kTanh32 : kTanh16)[i][k] * cap * log2e * (i < 2 ? std::pow(scale / cap, 2 * k + 1) : 1.0));
+        }
+        // Weights up to 2^80 (sums of 2^24 of them, times V, stay in range) and down to what keeps a
+        // float's (or, of three bf16 parts, the last one's) full precision.
+        p.ref_low = p.cap - 80.f;
+        p.ref_high = (f32 ? 100.f : 122.f) - p.cap;
+        p.fixed_ref = o->slopes == nullptr && p.ref_low <= p.ref_high;
     }
 }
 
@@ -1540,7 +1555,7 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const ha_score
         return fail(HA_ERR_UNSUPPORTED, "out_dtype must be HA_F32 or HA_BF16 (got %d)", t->out_dtype);
     const int G = t->h_q / t->h_kv;
     if (G > kMaxGroup) return fail(HA_ERR_UNSUPPORTED, "at most %d query heads per KV head (got %d)", kMaxGroup, G);
-    if (opts != nullptr) HA_TRY(check_opts(opts));
+    if (opts != nullptr) HA_TRY(check_score_opts(opts));
     if (cu == nullptr || (c != nullptr && seq_lens == nullptr)) return fail(HA_ERR_INVALID_ARG, "cu and seq_lens must not be NULL");
     if (c != nullptr) {
         HA_TRY(check_cache(c, t, K, V, table));
@@ -1649,7 +1664,8 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const ha_score
         HA_LAUNCH(launch_packed_att(p, m, t->d, f32, grid, merge, static_cast<cudaStream_t>(stream)), "packed attention launch");
     } else {
         set_opts(p, opts, t->d, f32);
-        HA_LAUNCH(launch_packed_att_ex(p, m, t->d, f32, grid, merge, static_cast<cudaStream_t>(stream)), "packed attention launch");
+        const auto launch = !p.shaped ? launch_packed_att_masked : (p.fixed_ref ? launch_packed_att_capped : launch_packed_att_shaped);
+        HA_LAUNCH(launch(p, m, t->d, f32, grid, merge, static_cast<cudaStream_t>(stream)), "packed attention launch");
     }
     return HA_OK;
 }

@@ -306,14 +306,22 @@ __device__ __forceinline__ float max_of(const uint32_t (&x)[N], float a) {
 
 // The weights 2^{x qscale - sub} of 32 columns as bf16 pairs in w; their float32 sum is
 // added to sum, and mt takes part in the columns' maximum.
+// PLAIN: the weights 2^x.
+template <bool PLAIN = false>
 __device__ __forceinline__ void weights32(const uint32_t* x, uint64_t qscale2, uint64_t nsub2, uint32_t (&w)[16],
                                           uint64_t (&sum)[2]) {
 #pragma unroll
     for (int q = 0; q < 16; q += 4) {
         float e[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            unpack2(fma2(pack2(__uint_as_float(x[2 * (q + k)]), __uint_as_float(x[2 * (q + k) + 1])), qscale2, nsub2), e[2 * k], e[2 * k + 1]);
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (PLAIN) {
+                e[2 * k] = __uint_as_float(x[2 * (q + k)]);
+                e[2 * k + 1] = __uint_as_float(x[2 * (q + k) + 1]);
+            } else {
+                unpack2(fma2(pack2(__uint_as_float(x[2 * (q + k)]), __uint_as_float(x[2 * (q + k) + 1])), qscale2, nsub2), e[2 * k], e[2 * k + 1]);
+            }
+        }
 #pragma unroll
         for (int k = 0; k < 8; ++k) e[k] = ex2(e[k]);
 #pragma unroll
@@ -380,12 +388,15 @@ __device__ __forceinline__ void store_rows(const uint32_t (&w)[N], const RowPair
 
 // The weights 2^{x qscale - sub} of 16 columns as three bf16 parts each (pairs in q); returns
 // their float32 sum.
-__device__ __forceinline__ float parts16(const uint32_t (&x)[16], float qscale, float sub, uint32_t (&q)[3][8]) {
+// PLAIN: of the weights 2^x.
+template <int N, bool PLAIN = false>
+__device__ __forceinline__ float parts16(const uint32_t (&x)[N], float qscale, float sub, uint32_t (&q)[3][8]) {
+    static_assert(N == 16, "three parts of 16 columns");
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        float u = ex2(fmaf(__uint_as_float(x[2 * k]), qscale, -sub));
-        float v = ex2(fmaf(__uint_as_float(x[2 * k + 1]), qscale, -sub));
+        float u = ex2(PLAIN ? __uint_as_float(x[2 * k]) : fmaf(__uint_as_float(x[2 * k]), qscale, -sub));
+        float v = ex2(PLAIN ? __uint_as_float(x[2 * k + 1]) : fmaf(__uint_as_float(x[2 * k + 1]), qscale, -sub));
         s0 += u;
         s1 += v;
 #pragma unroll
@@ -418,31 +429,56 @@ __device__ __forceinline__ float magnitude(const uint32_t (&x)[N]) {
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// Products x = <q, k_j> of consecutive columns as what the softmax takes, in units of log2 e:
-// the score x scale, or capped cap tanh(x scale / cap), less slope times the distance. `from`:
-// the first column's key less the row's position (below 0: the key lies before it).
-// tanh u is u P(u^2) up to |u| = 1, two columns an instruction, which takes no exponential and no
-// reciprocal and is as exact for small scores; where a column of the warp is larger,
-// 1 - 2 / (1 + e^{2 u}), off by 2^-22 cap at most. P is fitted in relative error: degree DEG 5 to 6e-7
-// (bf16 weights have 4e-3), degree 6 to 5e-8 (a rounding of float32).
-template <int DEG, int N>
-__device__ __forceinline__ void shape_scores(uint32_t (&x)[N], const PackedParamsEx& p, float slope, float from, bool both_sides) {
-    const float row = both_sides ? 0.f : slope * from;  // the bias at the first column
-    if (p.cap != 0.f) {
-        if (!__any_sync(0xffffffffu, magnitude(x) > p.fit)) {
-            const uint64_t r2 = pack2(row, row), unit = pack2(p.unit, p.unit);
+// x = f(x) of pairs of columns.
+template <int N, typename F>
+__device__ __forceinline__ void each_pair(uint32_t (&x)[N], F&& f) {
 #pragma unroll
-            for (int k = 0; k < N; k += 2) {
-                const uint64_t v = mul2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), unit);
-                const uint64_t u = mul2(v, v);
-                uint64_t c = pack2(p.poly[DEG], p.poly[DEG]);
+    for (int k = 0; k < N; k += 2) {
+        float a, b;
+        unpack2(f(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]))), a, b);
+        x[k] = __float_as_uint(a);
+        x[k + 1] = __float_as_uint(b);
+    }
+}
+// v (c[0] + c[1] v^2 + .. + c[DEG] v^{2 DEG}) + plus
+template <int DEG>
+__device__ __forceinline__ uint64_t odd_poly(uint64_t v, const float (&c)[7], uint64_t plus) {
+    const uint64_t u = mul2(v, v);
+    uint64_t y = pack2(c[DEG], c[DEG]);
 #pragma unroll
-                for (int i = DEG - 1; i >= 0; --i) c = fma2(c, u, pack2(p.poly[i], p.poly[i]));
-                float a, b;
-                unpack2(fma2(v, c, r2), a, b);
-                x[k] = __float_as_uint(a);
-                x[k + 1] = __float_as_uint(b);
-            }
+    for (int i = DEG - 1; i >= 0; --i) y = fma2(y, u, pack2(c[i], c[i]));
+    return fma2(v, y, plus);
+}
+
+// Degrees of the polynomials for tanh(u) / u (PackedParamsEx::fit and poly).
+template <bool F32OUT>
+struct CapDegrees {
+    static constexpr int low = F32OUT ? 4 : 2, mid = F32OUT ? 5 : 3, high = F32OUT ? 6 : 5;
+};
+
+// Products x = <q, k_j> of consecutive columns as what the softmax takes the power of 2 of: the score
+// (x scale, or capped cap tanh(x scale / cap)) less slope times the distance, times log2 e, less
+// sub. `from`: the first column's key less the row's position (below 0: the key lies before it).
+//
+// The products of a float32 multiply and add are what a tile waits for (a pair of columns in one
+// instruction takes as long as two), so tanh u is u P(u^2) with no more terms than the warp's
+// largest |u| asks for, and no exponential or reciprocal: P is fitted in relative error, to
+// 5.4e-7 at most (bf16 weights: they are rounded to 4e-3) or 5.0e-8 (float32 results: half a
+// rounding). Beyond |u| = 1 it is 1 - 2 / (1 + e^{2 u}), off by 2^-22 cap at most.
+template <bool F32OUT, bool BIAS, int N>
+__device__ __forceinline__ void shape_scores(uint32_t (&x)[N], const PackedParamsEx& p, float slope, float from, bool both_sides, float sub) {
+    using Deg = CapDegrees<F32OUT>;
+    const float row = BIAS && !both_sides ? fmaf(slope, from, -sub) : -sub;
+    const uint64_t row2 = pack2(row, row);
+    if (!BIAS || p.cap != 0.f) {
+        const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(magnitude(x))));
+        if (top <= p.fit[0]) {
+            each_pair(x, [&](uint64_t v) { return odd_poly<Deg::low>(v, p.poly[0], row2); });
+        } else if (top <= p.fit[1]) {
+            each_pair(x, [&](uint64_t v) { return odd_poly<Deg::mid>(v, p.poly[1], row2); });
+        } else if (top <= p.fit[2]) {
+            const uint64_t unit = pack2(p.unit, p.unit);
+            each_pair(x, [&](uint64_t v) { return odd_poly<Deg::high>(mul2(v, unit), p.poly[2], row2); });
         } else {
 #pragma unroll
             for (int k = 0; k < N; ++k) {
@@ -453,32 +489,16 @@ __device__ __forceinline__ void shape_scores(uint32_t (&x)[N], const PackedParam
             }
         }
     } else {
-        const uint64_t s2 = pack2(p.scale, p.scale), r2 = pack2(row, row);
-#pragma unroll
-        for (int k = 0; k < N; k += 2) {
-            float a, b;
-            unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), s2, r2), a, b);
-            x[k] = __float_as_uint(a);
-            x[k + 1] = __float_as_uint(b);
-        }
+        const uint64_t s2 = pack2(p.scale, p.scale);
+        each_pair(x, [&](uint64_t v) { return fma2(v, s2, row2); });
     }
-    if (p.slopes != nullptr) {
+    if (BIAS && p.slopes != nullptr) {
         if (!both_sides) {
-            const uint64_t sl = pack2(slope, slope), two = pack2(2.f, 2.f);
-            uint64_t c = pack2(0.f, 1.f);
 #pragma unroll
-            for (int k = 0; k < N; k += 2) {
-                float a, b;
-                unpack2(fma2(sl, c, pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]))), a, b);
-                x[k] = __float_as_uint(a);
-                x[k + 1] = __float_as_uint(b);
-                c = add2(c, two);
-            }
-        } else {
-            // keys on both sides of the row's position
+            for (int k = 1; k < N; ++k) x[k] = __float_as_uint(fmaf(slope, (float)k, __uint_as_float(x[k])));
+        } else {  // keys on both sides of the row's position
 #pragma unroll
-            for (int k = 0; k < N; ++k)
-                x[k] = __float_as_uint(fmaf(-slope, fabsf(from + (float)k), __uint_as_float(x[k])));
+            for (int k = 0; k < N; ++k) x[k] = __float_as_uint(fmaf(-slope, fabsf(from + (float)k), __uint_as_float(x[k])));
         }
     }
 }
@@ -486,14 +506,31 @@ __device__ __forceinline__ void shape_scores(uint32_t (&x)[N], const PackedParam
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[16]) { tmem_ld16(addr, x); }
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[32]) { tmem_ld32(addr, x); }
 
+// a times the pairs of bf16 in 8 columns of tensor memory.
+__device__ __forceinline__ void scale_pairs8(uint32_t addr, float a) {
+    uint32_t w[8];
+    tmem_ld8(addr, w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = pack_bf16(bf16lo(w[k]) * a, bf16hi(w[k]) * a);
+    tmem_st8(addr, w);
+}
+
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-template <int D, bool F32OUT, bool FOLD, bool EX>
+// What the softmax takes the scores as: they are scaled (kPlain: no options at all; kMasked: masks
+// alone), capped with a reference that stays (kCapped), or shaped in any way (kShaped).
+enum Mode { kPlain = 0, kMasked = 1, kCapped = 2, kShaped = 3 };
+
+template <int D, bool F32OUT, bool FOLD, int MODE>
 __global__ void __launch_bounds__(kAttThreads, 1)
     k_packed_att(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQs,
                  const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const __grid_constant__ CUtensorMap tmO,
-                 const Params<EX> p) {
+                 const Params<(MODE != kPlain)> p) {
+    constexpr bool EX = MODE != kPlain, shaped = MODE >= kCapped, fixed = MODE == kCapped;
+    // Biased scores grow towards the row's own position, so key tiles are taken from the last one
+    // back: the reference is found in the first, instead of moving (and O being rescaled) in most.
+    constexpr bool BACK = MODE == kShaped;
     using C = AttCfg<D, F32OUT, FOLD>;
     constexpr int S = C::kStages, KT = C::kKeys, NB = C::kPlaces;
     extern __shared__ __align__(1024) uint8_t s_raw[];
@@ -768,7 +805,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         o.nt = none ? 0 : max(0, min(je, key_tiles<KT>(o.kend) - begin) - j);
                         o.tokens = min(t2, i.nq - qt * t2);
                         const bool one = o.tokens <= p.TQ;
-                        o.e0 = one || none ? o.nt : max(0, min(je, key_tiles<KT>(keys_seen(i, qt * t2 + p.TQ)) - begin) - j);
+                        // (from the last tile back, row tile 0 takes all, too: the ones that it sees come last)
+                        o.e0 = one || none || BACK ? o.nt : max(0, min(je, key_tiles<KT>(keys_seen(i, qt * t2 + p.TQ)) - begin) - j);
                         // (spread: a token over 131,072 keys 118 us, without 137; whole items have
                         // other warps' rows to fill the time, and no merge to add up the quarters)
                         const bool whole = j == 0 && je == len, spread = !whole && o.tokens <= p.TS;
@@ -922,13 +960,14 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     }
                 };
                 int page_n, row_n;
-                where(g.jb, page_n, row_n);
+                where(BACK ? jend - 1 : g.jb, page_n, row_n);
 #pragma unroll 1
-                for (int j = g.jb; ok && j < jend; ++j) {
+                for (int i = g.jb; ok && i < jend; ++i) {
+                    const int j = BACK ? g.jb + jend - 1 - i : i;
                     const int boxes = (min(KT, g.kend - j * KT) + (1 << lg) - 1) >> lg;
                     // coordinates behind the dims: (row, head, page), or 8-row groups (see PackedParams)
                     int page = page_n, row = row_n;
-                    if (j + 1 < jend) where(j + 1, page_n, row_n);
+                    if (i + 1 < jend) where(BACK ? j - 1 : j + 1, page_n, row_n);
                     if (table != nullptr && (page < 0 || page >= p.n_pages)) {
                         if (!EX || page != p.n_pages) flag_error(p.err, HA_DEVERR_INDEX);
                         page = p.n_pages;  // past the pool: the copy fills its rows with zeros
@@ -1217,11 +1256,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         const uint32_t tO = tmem + lane_off + 256u, tOt = tO + (uint32_t)(t * C::kOCols);
         const int rtok = r / p.G, rhead = r - rtok * p.G, stok = lane / p.G, shead = lane - stok * p.G;
         const uint64_t qscale2 = pack2(p.qscale, p.qscale);
-        bool ref_fixed = false;
-        float ref_of_cap = 0.f;
-        if constexpr (EX) {
-            ref_fixed = p.fixed_ref != 0;
-            ref_of_cap = p.ref;
+        float ref_low = 0.f, ref_high = 0.f;
+        if constexpr (fixed) {
+            ref_low = p.ref_low;
+            ref_high = p.ref_high;
         }
         uint32_t cnt = 0, odc[2] = {0, 0}, nx = 0, ring = 0;  // tiles, o_done's, exchanges, ring tiles so far
         uint32_t nd = 0;                                      // segments done
@@ -1244,17 +1282,15 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             if constexpr (EX) {
                 if (valid) {
                     klow = p.window > 0 ? max(g.first, g.kfirst + ltok + 1 - p.window) : g.first;
-                    if (p.slopes != nullptr) slope = p.slopes[g.head * p.G + hd] * 1.4426950408889634f;
+                    if (MODE == kShaped && p.slopes != nullptr) slope = p.slopes[g.head * p.G + hd] * 1.4426950408889634f;
                 }
                 klast = __reduce_max_sync(0xffffffffu, klow);
             }
-            // the scores of columns col, col + 1, .. of key tile j, and their masks
-            auto shape = [&](auto& x, int j, int col) {
-                if constexpr (EX) {
-                    if (p.shaped) {
-                        const int from = j * KT + col - (g.kfirst + ltok);
-                        shape_scores<F32OUT ? 6 : 5>(x, p, slope, (float)from, g.prefix > g.kfirst + 1 && (j + 1) * KT - 1 > g.kfirst);
-                    }
+            // shaped scores less sub of columns col, col + 1, .. of key tile j, and masks
+            auto shape = [&](auto& x, int j, int col, float sub) {
+                if constexpr (shaped) {
+                    const int from = j * KT + col - (g.kfirst + ltok);
+                    shape_scores<F32OUT, MODE == kShaped>(x, p, slope, (float)from, g.prefix > g.kfirst + 1 && (j + 1) * KT - 1 > g.kfirst, sub);
                 }
             };
             auto mask = [&](auto& x, int lim, int j, int col) {
@@ -1263,12 +1299,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     if (klast > j * KT) mask_before(x, klow - j * KT - col);
                 }
             };
-            const bool fixed = EX && ref_fixed;
             const bool any = __any_sync(0xffffffffu, valid);
             const int st0 = parity ? (g.nt + 1) >> 1 : g.e0, st1 = parity ? g.nt >> 1 : g.nt;
             const int nt = t == 0 ? st0 : st1;
-            const int jstep = parity ? 2 : 1;
-            float m = fixed ? ref_of_cap : -INFINITY, l = 0.f;
+            const int jstep = (parity ? 2 : 1) * (BACK ? -1 : 1);
+            float m = fixed ? ref_low : -INFINITY, l = 0.f;
             float acc[F32OUT ? D : 1];  // float32 output: O is added up here, tile by tile
             if constexpr (F32OUT) {
 #pragma unroll
@@ -1293,7 +1328,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             const bool clears = g.kend < (jlast + 1) * KT && (t == 0 || parity || jlast >= g.jb + st0);
             // (the same before the first key that the item sees)
             const bool clears_low = EX && g.begins != 0 && g.kbegin > g.jb * KT && (t == 0 || parity || st0 == 0);
-            int j = parity ? g.jb + t : g.jb;
+            int j = BACK ? jlast - (parity ? t : 0) : (parity ? g.jb + t : g.jb);
             // three places: the number of the product of a stream's tile i; whether it has finished
             // P V. A barrier that has gone on by two phases looks like one that has not moved, so
             // product k + 3 must not finish before a warp has found k: before a stream's last
@@ -1354,6 +1389,30 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                                 tmem_st32(tOt + (uint32_t)cc, o);
                             }
                         }
+                        return a;
+                    };
+                    // Shaped scores come less the reference as it is. It moves where their maximum `top` (less it
+                    // as well) asks for that; a constant one is set where a row sees its first keys.
+                    // Returns by how much, with what is to be scaled meanwhile done by scale(a).
+                    const bool looks = !fixed || (bool)__any_sync(0xffffffffu, l == 0.f && lim > 0 && klow < (j + 1) * KT);
+                    bool none = l == 0.f;
+                    auto settle = [&](float top, auto&& scale) {
+                        const float sub = m == -INFINITY ? 0.f : m;
+                        bool moves = top != -INFINITY && (fixed ? none : m == -INFINITY || top > kRescale);
+                        if (NB == 3) moves = moves && valid;
+                        none = none && top == -INFINITY;
+                        if (!__any_sync(0xffffffffu, moves)) return 0.f;
+                        // (a whole power of two further: weights that are there already are scaled exactly)
+                        const float to = fixed ? fminf(fmaxf(sub + top, ref_low), ref_high) : sub + ceilf(top);
+                        if constexpr (fixed) {
+                            if (moves) m = to;
+                        } else {
+                            scale(grow_to(to, moves));
+                        }
+                        return moves ? sub - to : 0.f;
+                    };
+                    auto shift = [&](auto& x, float by) {
+                        each_pair(x, [&](uint64_t v) { return add2(v, pack2(by, by)); });
                     };
                     if (spread) {
                         // this warp's quarter of the columns; P of the others is 0 in its rows
@@ -1362,17 +1421,23 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         uint32_t x[Q];
                         tmem_load(tS + (uint32_t)(w * Q), x);
                         tmem_landed(x);
-                        shape(x, j, w * Q);
-                        if (part) mask(x, lim, j, w * Q);
-                        if (!fixed) {
+                        if constexpr (shaped) {
+                            shape(x, j, w * Q, m == -INFINITY ? 0.f : m);
+                            if (part) mask(x, lim, j, w * Q);
+                            if (looks) {
+                                const float by = settle(max_of(x, -INFINITY), [](float) {});
+                                if (__any_sync(0xffffffffu, by != 0.f)) shift(x, by);
+                            }
+                        } else {
+                            if (part) mask(x, lim, j, w * Q);
                             const float mx = max_of(x, m);
                             const bool grow = (NB == 2 || valid) && (mx - m) * p.qscale > kRescale;  // false where both are -inf
                             if (__any_sync(0xffffffffu, grow)) grow_to(mx, grow);
                         }
-                        const float sub = m == -INFINITY ? 0.f : m * p.qscale;
+                        const float sub = shaped || m == -INFINITY ? 0.f : m * p.qscale;
                         if constexpr (F32OUT) {
                             uint32_t q[3][8];
-                            l += parts16(x, p.qscale, sub, q);
+                            l += parts16<16, shaped>(x, p.qscale, sub, q);
 #pragma unroll
                             for (int e = 0; e < 3; ++e) {
                                 const uint32_t zero[8] = {};
@@ -1386,7 +1451,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                             uint64_t sum[2] = {0, 0};
                             uint32_t q[16];
                             const uint32_t zero[16] = {};
-                            weights32(x, qscale2, pack2(-sub, -sub), q, sum);
+                            weights32<shaped>(x, qscale2, pack2(-sub, -sub), q, sum);
 #pragma unroll
                             for (int v = 0; v < 4; ++v) {
                                 if (v == w) tmem_st16(tS + (uint32_t)(16 * v), q);
@@ -1397,61 +1462,92 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                             l += a + b;
                         }
                     } else if constexpr (F32OUT) {
-                        if (!fixed) {
+                        if constexpr (!shaped) {
                             float mx = m;
                             {
                                 uint32_t x[64];
                                 tmem_ld64(tS, x);
                                 tmem_landed(x);
-                                shape(x, j, 0);
                                 if (part) mask(x, lim, j, 0);
                                 mx = max_of(x, mx);
                             }
                             const bool grow = (NB == 2 || valid) && (mx - m) * p.qscale > kRescale;  // false where both are -inf
                             if (__any_sync(0xffffffffu, grow)) grow_to(mx, grow);
                         }
-                        const float sub = m == -INFINITY ? 0.f : m * p.qscale;
+                        float sub = m == -INFINITY ? 0.f : m * p.qscale;
 #pragma unroll 1
                         for (int cc = 0; cc < 64; cc += 16) {
                             uint32_t x[16], q[3][8];
                             tmem_load(tS + (uint32_t)cc, x);
                             tmem_landed(x);
-                            shape(x, j, cc);
-                            if (part) mask(x, lim, j, cc);
-                            l += parts16(x, p.qscale, sub, q);
+                            if constexpr (shaped) {
+                                shape(x, j, cc, m == -INFINITY ? 0.f : m);
+                                if (part) mask(x, lim, j, cc);
+                                if (looks) {
+                                    const float by = settle(max_of(x, -INFINITY), [&](float a) {
+                                        tmem_wait_st();
+#pragma unroll 1
+                                        for (int c = 0; c < cc / 2; c += 8)
+#pragma unroll
+                                            for (int e = 0; e < 3; ++e) scale_pairs8(tS + (uint32_t)(C::part_col(e) + c), a);
+                                    });
+                                    if (__any_sync(0xffffffffu, by != 0.f)) shift(x, by);
+                                }
+                            } else if (part) {
+                                mask(x, lim, j, cc);
+                            }
+                            l += parts16<16, shaped>(x, p.qscale, sub, q);
                             // the third part goes over columns of S that have been read: 8 for 16
 #pragma unroll
                             for (int e = 0; e < 3; ++e) tmem_st8(tS + (uint32_t)(C::part_col(e) + cc / 2), q[e]);
                         }
                     } else {
-                        uint32_t x0[64], x1[64];
+                        uint64_t sum[2] = {0, 0};
+                        uint32_t x0[64], x1[64], w[16];
                         tmem_ld64(tS, x0);
                         tmem_landed(x0);
                         tmem_ld64(tS + 64u, x1);
-                        shape(x0, j, 0);
-                        if (part) mask(x0, lim, j, 0);
-                        float mx = m;
-                        if (!fixed) mx = max_of(x0, m);
-                        tmem_landed(x1);
-                        shape(x1, j, 64);
-                        if (part) mask(x1, lim, j, 64);
-                        if (!fixed) {
+                        if constexpr (shaped) {
+                            const float sub = m == -INFINITY ? 0.f : m;
+                            shape(x0, j, 0, sub);
+                            if (part) mask(x0, lim, j, 0);
+                            tmem_landed(x1);
+                            shape(x1, j, 64, sub);
+                            if (part) mask(x1, lim, j, 64);
+                            if (looks) {
+                                const float by = settle(max_of(x1, max_of(x0, -INFINITY)), [](float) {});
+                                if (__any_sync(0xffffffffu, by != 0.f)) {
+                                    shift(x0, by);
+                                    shift(x1, by);
+                                }
+                            }
+                            weights32<true>(x0, 0, 0, w, sum);
+                            tmem_st16(tS, w);
+                            weights32<true>(x0 + 32, 0, 0, w, sum);
+                            tmem_st16(tS + 16u, w);
+                            weights32<true>(x1, 0, 0, w, sum);
+                            tmem_st16(tS + 32u, w);
+                            weights32<true>(x1 + 32, 0, 0, w, sum);
+                            tmem_st16(tS + 48u, w);
+                        } else {
+                            if (part) mask(x0, lim, j, 0);
+                            float mx = max_of(x0, m);
+                            tmem_landed(x1);
+                            if (part) mask(x1, lim, j, 64);
                             mx = max_of(x1, mx);
                             const bool grow = (NB == 2 || valid) && (mx - m) * p.qscale > kRescale;  // false where both are -inf
                             if (__any_sync(0xffffffffu, grow)) grow_to(mx, grow);
+                            const float sub = m == -INFINITY ? 0.f : m * p.qscale;
+                            const uint64_t nsub2 = pack2(-sub, -sub);
+                            weights32(x0, qscale2, nsub2, w, sum);
+                            tmem_st16(tS, w);
+                            weights32(x0 + 32, qscale2, nsub2, w, sum);
+                            tmem_st16(tS + 16u, w);
+                            weights32(x1, qscale2, nsub2, w, sum);
+                            tmem_st16(tS + 32u, w);
+                            weights32(x1 + 32, qscale2, nsub2, w, sum);
+                            tmem_st16(tS + 48u, w);
                         }
-                        const float sub = m == -INFINITY ? 0.f : m * p.qscale;
-                        const uint64_t nsub2 = pack2(-sub, -sub);
-                        uint64_t sum[2] = {0, 0};
-                        uint32_t w[16];
-                        weights32(x0, qscale2, nsub2, w, sum);
-                        tmem_st16(tS, w);
-                        weights32(x0 + 32, qscale2, nsub2, w, sum);
-                        tmem_st16(tS + 16u, w);
-                        weights32(x1, qscale2, nsub2, w, sum);
-                        tmem_st16(tS + 32u, w);
-                        weights32(x1 + 32, qscale2, nsub2, w, sum);
-                        tmem_st16(tS + 48u, w);
                         float a, b;
                         unpack2(add2(sum[0], sum[1]), a, b);
                         l += a + b;
@@ -1464,7 +1560,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 ++cnt;
                 const bool low = EX && clears_low && j == g.jb;
                 if ((clears && j == jlast) || low) {
-                    const uint32_t k = ring + 2u * (uint32_t)(j - g.jb) + 1u, s = k % (uint32_t)S;
+                    const uint32_t k = ring + 2u * (uint32_t)(BACK ? jlast - j : j - g.jb) + 1u, s = k % (uint32_t)S;
                     wait(full((int)s), (k / (uint32_t)S) & 1u);
                     uint8_t* tile = s_raw + 2 * C::kQTile + s * C::kTile;
                     // rows [0, n0) and [rows, KT)
@@ -1801,22 +1897,22 @@ __global__ void __launch_bounds__(256) k_packed_merge(const PackedParams p) {
     }
 }
 
-template <int D, bool F32OUT, bool FOLD, bool EX>
-cudaError_t launch_t(const Params<EX>& p, const PackedMaps& m, int grid, bool merge, cudaStream_t st) {
+template <int D, bool F32OUT, bool FOLD, int MODE>
+cudaError_t launch_t(const Params<(MODE != kPlain)>& p, const PackedMaps& m, int grid, bool merge, cudaStream_t st) {
     using C = AttCfg<D, F32OUT, FOLD>;
     cudaError_t e =
-        cudaFuncSetAttribute(k_packed_att<D, F32OUT, FOLD, EX>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        cudaFuncSetAttribute(k_packed_att<D, F32OUT, FOLD, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_ex(k_packed_att<D, F32OUT, FOLD, EX>, dim3((unsigned)grid), dim3(kAttThreads), C::kSmem, st, true, m.q, m.qs, m.k, m.v, m.o, p);
+    e = launch_ex(k_packed_att<D, F32OUT, FOLD, MODE>, dim3((unsigned)grid), dim3(kAttThreads), C::kSmem, st, true, m.q, m.qs, m.k, m.v, m.o, p);
     if (e != cudaSuccess || !merge) return e;
     return launch_ex(k_packed_merge<D, F32OUT>, dim3((unsigned)grid, kMergeSlices), dim3(256), 0, st, true, static_cast<const PackedParams&>(p));
 }
 
-template <bool EX>
-cudaError_t launch(const Params<EX>& p, const PackedMaps& m, int d, bool f32_out, int grid, bool merge, cudaStream_t st) {
-    if (d == 64) return f32_out ? launch_t<64, true, false, EX>(p, m, grid, merge, st) : launch_t<64, false, false, EX>(p, m, grid, merge, st);
-    if (p.kv_fold) return f32_out ? launch_t<128, true, true, EX>(p, m, grid, merge, st) : launch_t<128, false, true, EX>(p, m, grid, merge, st);
-    return f32_out ? launch_t<128, true, false, EX>(p, m, grid, merge, st) : launch_t<128, false, false, EX>(p, m, grid, merge, st);
+template <int MODE>
+cudaError_t launch(const Params<(MODE != kPlain)>& p, const PackedMaps& m, int d, bool f32_out, int grid, bool merge, cudaStream_t st) {
+    if (d == 64) return f32_out ? launch_t<64, true, false, MODE>(p, m, grid, merge, st) : launch_t<64, false, false, MODE>(p, m, grid, merge, st);
+    if (p.kv_fold) return f32_out ? launch_t<128, true, true, MODE>(p, m, grid, merge, st) : launch_t<128, false, true, MODE>(p, m, grid, merge, st);
+    return f32_out ? launch_t<128, true, false, MODE>(p, m, grid, merge, st) : launch_t<128, false, false, MODE>(p, m, grid, merge, st);
 }
 
 }  // namespace

@@ -33,8 +33,12 @@ struct PackedMaps {
 };
 cudaError_t launch_packed_att(const struct PackedParams& p, const PackedMaps& m, int d, bool f32_out, int grid,
                               bool merge, cudaStream_t st);
-cudaError_t launch_packed_att_ex(const struct PackedParamsEx& p, const PackedMaps& m, int d, bool f32_out, int grid,
-                                 bool merge, cudaStream_t st);
+cudaError_t launch_packed_att_masked(const struct PackedParamsEx& p, const PackedMaps& m, int d, bool f32_out, int grid,
+                                     bool merge, cudaStream_t st);
+cudaError_t launch_packed_att_capped(const struct PackedParamsEx& p, const PackedMaps& m, int d, bool f32_out, int grid,
+                                     bool merge, cudaStream_t st);
+cudaError_t launch_packed_att_shaped(const struct PackedParamsEx& p, const PackedMaps& m, int d, bool f32_out, int grid,
+                                     bool merge, cudaStream_t st);
 
 // Shared-memory matrix descriptor of a K-major operand in the 128-byte swizzle
 // layout that TMA writes: rows of 128 bytes, 8-row groups 1024 bytes apart.
@@ -125,6 +129,17 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* v) {
 }
 
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// 8 consecutive 32-bit columns of this thread's TMEM lane, landed.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
+                 :
+                 : "memory");
+}
 
 // 32 consecutive 32-bit columns of this thread's TMEM lane; not to be touched before
 // tmem_landed(v).
