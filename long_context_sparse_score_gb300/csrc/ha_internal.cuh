@@ -338,9 +338,9 @@ struct PackedParamsEx : PackedParams {
     float cap;                 // cap x log2(e), 0: none
     float twice;               // 2 log2(e) scale / cap: e^{2 u} = 2^{twice x}
     float unit;                // scale / cap: u of a product x is unit x
-    // cap tanh(u) log2(e) for |x| <= fit[i]: poly[0] and poly[1] are of x, poly[2] is of u
-    float fit[3];
-    float poly[3][7];
+    // cap tanh(u) log2(e) for |x| <= fit[i]: poly[0] is of x, poly[1] of u
+    float fit[2];
+    float poly[2][7];
     // Capped scores lie within +-cap, so where 2^{2 cap} fits a float's range a row keeps the reference
     // that its first keys give (within these bounds): no maximum is looked for, and nothing is rescaled.
     int fixed_ref;

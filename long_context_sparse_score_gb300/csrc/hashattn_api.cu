@@ -1490,15 +1490,13 @@ bool encode_fold(CUtensorMap* m, const void* base, int64_t row, int64_t groups, 
 
 // tanh(u) / u as polynomials of u^2, fitted in relative error (at Chebyshev nodes, weights moved until
 // the error is even): for bf16 weights, and for float32 results.
-constexpr double kCapTo16[3] = {0.25, 0.5, 1.0}, kCapTo32[3] = {0.5, 0.75, 1.0};
-constexpr double kTanh16[3][7] = {
-    {0.9999996043, -0.3332190822, 0.1284161342},  // degree 2 up to 0.25: 4.0e-07
+constexpr double kCapTo[2] = {0.5, 1.0};
+constexpr double kTanh16[2][7] = {
     {0.9999994558, -0.3332631793, 0.1319029658, -0.04440222556},  // degree 3 up to 0.5: 5.4e-07
     {0.9999994136, -0.3332904237, 0.1328143384, -0.05160567292, 0.01674311383, -0.003067059836},  // degree 5 up to 1: 5.9e-07
 };
-constexpr double kTanh32[3][7] = {
+constexpr double kTanh32[2][7] = {
     {0.9999999869, -0.3333306939, 0.1332477932, -0.05298607518, 0.01713500641},  // degree 4 up to 0.5: 1.3e-08
-    {0.999999971, -0.3333295888, 0.1332540601, -0.05334442995, 0.0195829078, -0.004716256975},  // degree 5 up to 0.75: 2.9e-08
     {0.9999999502, -0.3333283915, 0.1332520407, -0.05345702927, 0.02028997985, -0.006203378602, 0.001041022467},  // degree 6 up to 1: 5.0e-08
 };
 
@@ -1529,12 +1527,12 @@ void set_opts(PackedParamsEx& p, const ha_score_opts* o, int d, bool f32) {
         p.cap = (float)(cap * log2e);
         p.unit = (float)(scale / cap);
         p.twice = (float)(2.0 * log2e * scale / cap);
-        // Polynomials of x itself save a product; their terms (up to x^10) have to be normal numbers.
-        const bool plain = scale / cap >= std::ldexp(1.0, f32 ? -11 : -16) && scale / cap <= std::ldexp(1.0, 11);
-        for (int i = 0; i < 3; ++i) {
-            p.fit[i] = plain || i == 2 ? (float)((f32 ? kCapTo32 : kCapTo16)[i] * cap / scale) : -1.f;
+        // A polynomial of x itself saves a product; its terms (up to x^9) have to be normal numbers.
+        const bool plain = scale / cap >= std::ldexp(1.0, f32 ? -12 : -15) && scale / cap <= std::ldexp(1.0, 12);
+        for (int i = 0; i < 2; ++i) {
+            p.fit[i] = plain || i == 1 ? (float)(kCapTo[i] * cap / scale) : -1.f;
             for (int k = 0; k < 7; ++k)
-                p.poly[i][k] = (float)((f32 ? kTanh32 : kTanh16)[i][k] * cap * log2e * (i < 2 ? std::pow(scale / cap, 2 * k + 1) : 1.0));
+                p.poly[i][k] = (float)((f32 ? kTanh32 : kTanh16)[i][k] * cap * log2e * (i == 0 ? std::pow(scale / cap, 2 * k + 1) : 1.0));
         }
         // Weights up to 2^80 (sums of 2^24 of them, times V, stay in range) and down to what keeps a
         // float's (or, of three bf16 parts, the last one's) full precision.

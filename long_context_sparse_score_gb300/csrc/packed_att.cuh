@@ -453,7 +453,7 @@ __device__ __forceinline__ uint64_t odd_poly(uint64_t v, const float (&c)[7], ui
 // Degrees of the polynomials for tanh(u) / u (PackedParamsEx::fit and poly).
 template <bool F32OUT>
 struct CapDegrees {
-    static constexpr int low = F32OUT ? 4 : 2, mid = F32OUT ? 5 : 3, high = F32OUT ? 6 : 5;
+    static constexpr int low = F32OUT ? 4 : 3, high = F32OUT ? 6 : 5;
 };
 
 // Products x = <q, k_j> of consecutive columns as what the softmax takes the power of 2 of: the score
@@ -475,10 +475,8 @@ __device__ __forceinline__ void shape_scores(uint32_t (&x)[N], const PackedParam
         if (top <= p.fit[0]) {
             each_pair(x, [&](uint64_t v) { return odd_poly<Deg::low>(v, p.poly[0], row2); });
         } else if (top <= p.fit[1]) {
-            each_pair(x, [&](uint64_t v) { return odd_poly<Deg::mid>(v, p.poly[1], row2); });
-        } else if (top <= p.fit[2]) {
             const uint64_t unit = pack2(p.unit, p.unit);
-            each_pair(x, [&](uint64_t v) { return odd_poly<Deg::high>(mul2(v, unit), p.poly[2], row2); });
+            each_pair(x, [&](uint64_t v) { return odd_poly<Deg::high>(mul2(v, unit), p.poly[1], row2); });
         } else {
 #pragma unroll
             for (int k = 0; k < N; ++k) {
@@ -505,6 +503,51 @@ __device__ __forceinline__ void shape_scores(uint32_t (&x)[N], const PackedParam
 
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[16]) { tmem_ld16(addr, x); }
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[32]) { tmem_ld32(addr, x); }
+
+// The weights of a tile of 128 columns of capped scores: cap tanh() as the polynomial c of x, less
+// the reference (minus: -m twice), for |x| <= fit. Returns the columns done: those before
+// the first 32 that hold a larger product of any of the warp's rows.
+__device__ __forceinline__ int capped_tile(uint32_t tS, const float (&c)[7], float fit, uint64_t minus, uint64_t (&sum)[2]) {
+    uint32_t x[32], y[2][32], w[16];
+    bool large[2];
+    auto begin = [&](uint32_t (&to)[32]) {  // x to its scores; are any too large?
+#pragma unroll
+        for (int k = 0; k < 32; ++k) to[k] = x[k];
+        each_pair(to, [&](uint64_t v) { return odd_poly<3>(v, c, minus); });
+        return magnitude(x) > fit;
+    };
+    tmem_ld32(tS, x);
+    tmem_landed(x);
+    large[0] = (bool)__any_sync(0xffffffffu, begin(y[0]));
+    tmem_ld32(tS + 32u, x);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        uint32_t (&now)[32] = y[h & 1], (&next)[32] = y[(h & 1) ^ 1];
+        uint64_t s[2] = {0, 0};
+        if (h < 3) tmem_landed(x);
+        float big = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            const float a = ex2(__uint_as_float(now[k])), b = ex2(__uint_as_float(now[k + 1]));
+            if (h < 3) {
+                float u, v;
+                unpack2(odd_poly<3>(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c, minus), u, v);
+                next[k] = __float_as_uint(u);
+                next[k + 1] = __float_as_uint(v);
+                big = fmaxf(fmaxf(big, fabsf(__uint_as_float(x[k]))), fabsf(__uint_as_float(x[k + 1])));
+            }
+            w[k >> 1] = pack_bf16(a, b);
+            s[(k >> 1) & 1] = add2(s[(k >> 1) & 1], pack2(a, b));
+        }
+        if (h < 2) tmem_ld32(tS + (uint32_t)(64 + 32 * h), x);
+        if (large[h & 1]) return 32 * h;
+        if (h < 3) large[(h & 1) ^ 1] = (bool)__any_sync(0xffffffffu, big > fit);
+        sum[0] = add2(sum[0], s[0]);
+        sum[1] = add2(sum[1], s[1]);
+        tmem_st16(tS + (uint32_t)(16 * h), w);
+    }
+    return 128;
+}
 
 // a times the pairs of bf16 in 8 columns of tensor memory.
 __device__ __forceinline__ void scale_pairs8(uint32_t addr, float a) {
@@ -1503,7 +1546,28 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         }
                     } else {
                         uint64_t sum[2] = {0, 0};
-                        uint32_t x0[64], x1[64], w[16];
+                        uint32_t w[16];
+                        if constexpr (fixed) {
+                            // 32 columns at a time, the exponentials of some between the polynomials of the next,
+                            // as long as all are seen and small enough for the polynomial
+                            int cc = 0;
+                            if (!part && !looks) cc = capped_tile(tS, p.poly[0], p.fit[0], pack2(-m, -m), sum);
+#pragma unroll 1
+                            for (; cc < 128; cc += 32) {
+                                uint32_t x[32];
+                                tmem_ld32(tS + (uint32_t)cc, x);
+                                tmem_landed(x);
+                                shape(x, j, cc, m);
+                                if (part) mask(x, lim, j, cc);
+                                if (looks) {
+                                    const float by = settle(max_of(x, -INFINITY), [](float) {});
+                                    if (__any_sync(0xffffffffu, by != 0.f)) shift(x, by);
+                                }
+                                weights32<true>(x, 0, 0, w, sum);
+                                tmem_st16(tS + (uint32_t)(cc >> 1), w);
+                            }
+                        } else {
+                        uint32_t x0[64], x1[64];
                         tmem_ld64(tS, x0);
                         tmem_landed(x0);
                         tmem_ld64(tS + 64u, x1);
@@ -1547,6 +1611,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                             tmem_st16(tS + 32u, w);
                             weights32(x1 + 32, qscale2, nsub2, w, sum);
                             tmem_st16(tS + 48u, w);
+                        }
                         }
                         float a, b;
                         unpack2(add2(sum[0], sum[1]), a, b);
