@@ -73,6 +73,9 @@ constexpr uint32_t kTmemCols = 512;   // S0, S1 (128 each; P overlays them), O0,
 constexpr int kItemCost = 2, kSplitCost = 4;
 constexpr int kQueue = 4;              // segments that the scheduler is ahead
 constexpr float kRescale = 8.f;       // growth of the maximum (log2) that makes O be rescaled
+// The same for shaped scores, where it sends a tile's rest the slow way: weights up to 2^40 cost no more
+// range or precision than up to 2^8.
+constexpr float kShapedRescale = 40.f;
 
 // FOLD: the halves of a K/V tile lie side by side (PackedParams::kv_fold != 0)
 template <int D, bool F32OUT, bool FOLD>
@@ -504,44 +507,71 @@ __device__ __forceinline__ void shape_scores(uint32_t (&x)[N], const PackedParam
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[16]) { tmem_ld16(addr, x); }
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[32]) { tmem_ld32(addr, x); }
 
-// The weights of a tile of 128 columns of capped scores: cap tanh() as the polynomial c of x, less
-// the reference (minus: -m twice), for |x| <= fit. Returns the columns done: those before
-// the first 32 that hold a larger product of any of the warp's rows.
-__device__ __forceinline__ int capped_tile(uint32_t tS, const float (&c)[7], float fit, uint64_t minus, uint64_t (&sum)[2]) {
+// The weights of a tile of 128 columns of shaped scores, all seen, keys on one side: 32 columns at a
+// time, the exponentials of some between the products of the next, so that neither unit waits for
+// the other. Score k of the tile, less the reference: cap tanh() as a polynomial of x (CAP), or x scale;
+// plus row, plus slope k (BIAS). Returns the columns done: those before the first 32 where a product of any
+// of the warp's rows is too large for the polynomial (CAP), or a score more than kShapedRescale above the
+// reference (BIAS).
+template <bool CAP, bool BIAS>
+__device__ __forceinline__ int fast_tile(uint32_t tS, const PackedParamsEx& p, float row, float slope, bool valid, uint64_t (&sum)[2]) {
     uint32_t x[32], y[2][32], w[16];
-    bool large[2];
-    auto begin = [&](uint32_t (&to)[32]) {  // x to its scores; are any too large?
-#pragma unroll
-        for (int k = 0; k < 32; ++k) to[k] = x[k];
-        each_pair(to, [&](uint64_t v) { return odd_poly<3>(v, c, minus); });
-        return magnitude(x) > fit;
+    bool stop[2];
+    const uint64_t scale = pack2(p.scale, p.scale);
+    auto score = [&](int k, uint64_t row2, float& a, float& b) {  // columns k and k + 1 of the 32 in x
+        const uint64_t v = pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+        if constexpr (CAP) unpack2(odd_poly<CapDegrees<false>::low>(v, p.poly[0], row2), a, b);
+        else unpack2(fma2(v, scale, row2), a, b);
+        if constexpr (BIAS) {
+            a = fmaf(slope, (float)k, a);
+            b = fmaf(slope, (float)(k + 1), b);
+        }
+    };
+    auto larger = [&](int k, float a, float b, float& big, float& top) {
+        if constexpr (CAP) big = fmaxf(fmaxf(big, fabsf(__uint_as_float(x[k]))), fabsf(__uint_as_float(x[k + 1])));
+        if constexpr (BIAS) top = fmaxf(fmaxf(top, a), b);
+    };
+    auto stops = [&](float big, float top) {
+        return (bool)__any_sync(0xffffffffu, (CAP && big > p.fit[0]) || (BIAS && top > kShapedRescale && valid));
     };
     tmem_ld32(tS, x);
     tmem_landed(x);
-    large[0] = (bool)__any_sync(0xffffffffu, begin(y[0]));
+    {
+        float big[2] = {0.f, 0.f}, top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            float a, b;
+            score(k, pack2(row, row), a, b);
+            larger(k, a, b, big[(k >> 1) & 1], top[(k >> 1) & 1]);
+            y[0][k] = __float_as_uint(a);
+            y[0][k + 1] = __float_as_uint(b);
+        }
+        stop[0] = stops(fmaxf(big[0], big[1]), fmaxf(top[0], top[1]));
+    }
     tmem_ld32(tS + 32u, x);
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
         uint32_t (&now)[32] = y[h & 1], (&next)[32] = y[(h & 1) ^ 1];
         uint64_t s[2] = {0, 0};
+        float big[2] = {0.f, 0.f}, top[2] = {-INFINITY, -INFINITY};
+        const float r = BIAS ? fmaf(slope, (float)(32 * (h + 1)), row) : row;
         if (h < 3) tmem_landed(x);
-        float big = 0.f;
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
             const float a = ex2(__uint_as_float(now[k])), b = ex2(__uint_as_float(now[k + 1]));
             if (h < 3) {
                 float u, v;
-                unpack2(odd_poly<3>(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c, minus), u, v);
+                score(k, pack2(r, r), u, v);
+                larger(k, u, v, big[(k >> 1) & 1], top[(k >> 1) & 1]);
                 next[k] = __float_as_uint(u);
                 next[k + 1] = __float_as_uint(v);
-                big = fmaxf(fmaxf(big, fabsf(__uint_as_float(x[k]))), fabsf(__uint_as_float(x[k + 1])));
             }
             w[k >> 1] = pack_bf16(a, b);
             s[(k >> 1) & 1] = add2(s[(k >> 1) & 1], pack2(a, b));
         }
         if (h < 2) tmem_ld32(tS + (uint32_t)(64 + 32 * h), x);
-        if (large[h & 1]) return 32 * h;
-        if (h < 3) large[(h & 1) ^ 1] = (bool)__any_sync(0xffffffffu, big > fit);
+        if (stop[h & 1]) return 32 * h;
+        if (h < 3) stop[(h & 1) ^ 1] = stops(fmaxf(big[0], big[1]), fmaxf(top[0], top[1]));
         sum[0] = add2(sum[0], s[0]);
         sum[1] = add2(sum[1], s[1]);
         tmem_st16(tS + (uint32_t)(16 * h), w);
@@ -989,17 +1019,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     const int key = j * KT + (box << lg);
                     page = 0;
                     row = g.q0 + key;
-                    // (what lies before the first key seen may have been given away: its entries are not
-                    // looked at, and its rows become zeros)
-                    const bool gone = EX && key + (1 << lg) <= g.kbegin;
-                    if (EX && table != nullptr && gone) {
-                        row = 0;
-                        page = p.n_pages;
-                    } else if (table != nullptr && key < g.kend) {
+                    if (table != nullptr && key < g.kend) {
                         const int e = key / p.page_size;
                         row = key - e * p.page_size;
                         page = table[e];
-                        if (EX && page == p.n_pages) page = -1;
                     }
                 };
                 int page_n, row_n;
@@ -1011,8 +1034,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     // coordinates behind the dims: (row, head, page), or 8-row groups (see PackedParams)
                     int page = page_n, row = row_n;
                     if (i + 1 < jend) where(BACK ? j - 1 : j + 1, page_n, row_n);
-                    if (table != nullptr && (page < 0 || page >= p.n_pages)) {
-                        if (!EX || page != p.n_pages) flag_error(p.err, HA_DEVERR_INDEX);
+                    // what lies before the item's first key may have been given away: its entries say nothing
+                    const bool gone = EX && j == g.jb && j * KT + ((box + 1) << lg) <= g.kbegin;
+                    if (table != nullptr && (page < 0 || page >= p.n_pages || gone)) {
+                        if (!gone) flag_error(p.err, HA_DEVERR_INDEX);
                         page = p.n_pages;  // past the pool: the copy fills its rows with zeros
                         row = 0;
                     }
@@ -1317,7 +1342,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             // softmax is what a tile waits for: no votes a tile, and rows of no token go unmasked
             // (16,384 tokens, d 64: 1140 -> 1106 us; with two places and d 128 337 -> 341, float32
             // 283 -> 300, so the votes stay there).
-            const int kmax = valid ? min(g.nk, max(EX ? g.prefix : 0, g.kfirst + ltok + 1)) : (NB == 3 ? INT_MAX : 0);
+            const int kmax = valid ? min(g.nk, max(EX ? g.prefix : 0, g.kfirst + ltok + 1)) : (NB == 3 || shaped ? INT_MAX : 0);
             const int kmin = __reduce_min_sync(0xffffffffu, kmax);
             // with score options: the row's first key, the last of the warp's; its position; its slope
             int klow = 0, klast = 0;
@@ -1437,12 +1462,12 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     // Shaped scores come less the reference as it is. It moves where their maximum `top` (less it
                     // as well) asks for that; a constant one is set where a row sees its first keys.
                     // Returns by how much, with what is to be scaled meanwhile done by scale(a).
-                    const bool looks = !fixed || (bool)__any_sync(0xffffffffu, l == 0.f && lim > 0 && klow < (j + 1) * KT);
+                    const bool looks = !fixed || (bool)__any_sync(0xffffffffu, valid && l == 0.f && lim > 0 && klow < (j + 1) * KT);
                     bool none = l == 0.f;
                     auto settle = [&](float top, auto&& scale) {
                         const float sub = m == -INFINITY ? 0.f : m;
-                        bool moves = top != -INFINITY && (fixed ? none : m == -INFINITY || top > kRescale);
-                        if (NB == 3) moves = moves && valid;
+                        bool moves = top != -INFINITY && (fixed ? none : m == -INFINITY || top > kShapedRescale);
+                        moves = moves && valid;
                         none = none && top == -INFINITY;
                         if (!__any_sync(0xffffffffu, moves)) return 0.f;
                         // (a whole power of two further: weights that are there already are scaled exactly)
@@ -1547,53 +1572,43 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     } else {
                         uint64_t sum[2] = {0, 0};
                         uint32_t w[16];
-                        if constexpr (fixed) {
-                            // 32 columns at a time, the exponentials of some between the polynomials of the next,
-                            // as long as all are seen and small enough for the polynomial
+                        if constexpr (shaped) {
                             int cc = 0;
-                            if (!part && !looks) cc = capped_tile(tS, p.poly[0], p.fit[0], pack2(-m, -m), sum);
+                            const float to_row = (float)(j * KT - (g.kfirst + ltok));
+                            const bool both = MODE == kShaped && g.prefix > g.kfirst + 1 && (j + 1) * KT - 1 > g.kfirst;
+                            if constexpr (fixed) {
+                                if (!part && !looks) cc = fast_tile<true, false>(tS, p, -m, 0.f, valid, sum);
+                            } else if (!part && !both && !__any_sync(0xffffffffu, valid && m == -INFINITY)) {
+                                const float row = fmaf(slope, to_row, valid ? -m : 0.f);
+                                if (p.cap != 0.f) cc = fast_tile<true, true>(tS, p, row, slope, valid, sum);
+                                else cc = fast_tile<false, true>(tS, p, row, slope, valid, sum);
+                            }
+                            // the rest, in any case
 #pragma unroll 1
                             for (; cc < 128; cc += 32) {
                                 uint32_t x[32];
                                 tmem_ld32(tS + (uint32_t)cc, x);
                                 tmem_landed(x);
-                                shape(x, j, cc, m);
+                                shape(x, j, cc, m == -INFINITY ? 0.f : m);
                                 if (part) mask(x, lim, j, cc);
                                 if (looks) {
-                                    const float by = settle(max_of(x, -INFINITY), [](float) {});
+                                    const float by = settle(max_of(x, -INFINITY), [&](float a) {
+                                        sum[0] = mul2(sum[0], pack2(a, a));
+                                        sum[1] = mul2(sum[1], pack2(a, a));
+                                        tmem_wait_st();
+#pragma unroll 1
+                                        for (int c = 0; c < cc / 2; c += 8) scale_pairs8(tS + (uint32_t)c, a);
+                                    });
                                     if (__any_sync(0xffffffffu, by != 0.f)) shift(x, by);
                                 }
                                 weights32<true>(x, 0, 0, w, sum);
                                 tmem_st16(tS + (uint32_t)(cc >> 1), w);
                             }
                         } else {
-                        uint32_t x0[64], x1[64];
-                        tmem_ld64(tS, x0);
-                        tmem_landed(x0);
-                        tmem_ld64(tS + 64u, x1);
-                        if constexpr (shaped) {
-                            const float sub = m == -INFINITY ? 0.f : m;
-                            shape(x0, j, 0, sub);
-                            if (part) mask(x0, lim, j, 0);
-                            tmem_landed(x1);
-                            shape(x1, j, 64, sub);
-                            if (part) mask(x1, lim, j, 64);
-                            if (looks) {
-                                const float by = settle(max_of(x1, max_of(x0, -INFINITY)), [](float) {});
-                                if (__any_sync(0xffffffffu, by != 0.f)) {
-                                    shift(x0, by);
-                                    shift(x1, by);
-                                }
-                            }
-                            weights32<true>(x0, 0, 0, w, sum);
-                            tmem_st16(tS, w);
-                            weights32<true>(x0 + 32, 0, 0, w, sum);
-                            tmem_st16(tS + 16u, w);
-                            weights32<true>(x1, 0, 0, w, sum);
-                            tmem_st16(tS + 32u, w);
-                            weights32<true>(x1 + 32, 0, 0, w, sum);
-                            tmem_st16(tS + 48u, w);
-                        } else {
+                            uint32_t x0[64], x1[64];
+                            tmem_ld64(tS, x0);
+                            tmem_landed(x0);
+                            tmem_ld64(tS + 64u, x1);
                             if (part) mask(x0, lim, j, 0);
                             float mx = max_of(x0, m);
                             tmem_landed(x1);
@@ -1611,7 +1626,6 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                             tmem_st16(tS + 32u, w);
                             weights32(x1 + 32, qscale2, nsub2, w, sum);
                             tmem_st16(tS + 48u, w);
-                        }
                         }
                         float a, b;
                         unpack2(add2(sum[0], sum[1]), a, b);
