@@ -24,32 +24,51 @@ namespace {
 constexpr int kMostThreads = 1024, kCluster = 8;
 constexpr int kUnit = 256;    // rows that a warp writes at a time
 constexpr int kDirect = 8;    // rows of a sequence that its own thread writes
+// A sum of rows that stays here is more than any buffer holds.
+constexpr uint32_t kManyRows = 1u << 26;
 
 struct PagesRecord {  // what the warps need of a sequence with many rows
     int row0, nq, had, tb, unit0;  // had -1: it is stopped
 };
-
-struct Sums {
-    long long rows;
-    uint32_t takes, back;
+struct Ended {  // an ended sequence: its table's row, its pages, its place among the pages given back
+    int s, pages;
+    uint32_t at;
 };
 
-__device__ __forceinline__ uint32_t warp_incl(uint32_t x, int lane) {
+// What is summed over the sequences: new rows (up to kManyRows), pages taken, pages given back, units.
+struct Sums {
+    uint32_t rows, takes, back, units;
+    __device__ __forceinline__ void add(const Sums& o) {
+        rows = min(rows + o.rows, kManyRows);
+        takes += o.takes;
+        back += o.back;
+        units += o.units;
+    }
+};
+__device__ __forceinline__ Sums from_lane(const Sums& x, int l) {
+    return Sums{__shfl_sync(0xffffffffu, x.rows, l), __shfl_sync(0xffffffffu, x.takes, l), __shfl_sync(0xffffffffu, x.back, l),
+                __shfl_sync(0xffffffffu, x.units, l)};
+}
+__device__ __forceinline__ Sums scan_warp(Sums x, int lane) {  // inclusive
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += v;
+        const Sums v{__shfl_up_sync(0xffffffffu, x.rows, o), __shfl_up_sync(0xffffffffu, x.takes, o),
+                     __shfl_up_sync(0xffffffffu, x.back, o), __shfl_up_sync(0xffffffffu, x.units, o)};
+        if (lane >= o) x.add(v);
     }
     return x;
 }
 
 __global__ void __launch_bounds__(kMostThreads) k_plan_pages(const PagesParams p) {
     __shared__ PagesRecord s_rec[kMostThreads];
-    __shared__ uint32_t s_warp[4][32];
-    __shared__ Sums s_sums, s_warp_sums[32];
+    __shared__ Ended s_ended[kMostThreads];
+    __shared__ uint32_t s_back[kMostThreads];  // by thread: pages its ended sequence gives back
+    __shared__ Sums s_warp[32], s_sums;
+    __shared__ int s_n_ended;
     const cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    if (tid == 0) s_n_ended = 0;
     pdl_wait();
     pdl_launch_dependents();
 
@@ -62,36 +81,38 @@ __global__ void __launch_bounds__(kMostThreads) k_plan_pages(const PagesParams p
 
     uint32_t flags = 0;
     int n_free = *p.n_free;
-    if (n_free < 0 || n_free > p.n_pages) {
-        flags |= HA_DEVERR_STATE;
-        n_free = n_free < 0 ? 0 : p.n_pages;
-    }
 
     // Sequence of this thread in a tile. state 0: none; 1: it goes on; 2: it ends; 3: it is stopped
     struct Mine {
         int s, had, nq, p0, state;
         uint32_t takes, back;
     } x;
-    // Walks the entries of the warp's ended sequences, 32 at a time; put(place, page) for each that is a page.
-    auto walk = [&](auto&& put) {
-        uint32_t ended = __ballot_sync(0xffffffffu, x.state == 2 && x.p0 > 0);
-        while (ended != 0) {
-            const int l = __ffs((int)ended) - 1;
-            ended &= ended - 1;
-            const int pages = __shfl_sync(0xffffffffu, x.p0, l);
-            const int32_t* row = p.table + (int64_t)__shfl_sync(0xffffffffu, x.s, l) * p.table_st;
-            uint32_t n = 0;
-            for (int j = lane; j - lane < pages; j += 32) {
-                const int page = j < pages ? row[j] : -1;
-                const uint32_t m = __ballot_sync(0xffffffffu, page >= 0 && page < p.n_pages);
-                if (j < pages && (page < 0 || page >= p.n_pages)) flags |= HA_DEVERR_INDEX;
-                put(l, n + (uint32_t)__popc((int)(m & ((1u << lane) - 1u))), page, (m >> lane) & 1u);
+    auto page_ok = [&](int page) { return page >= 0 && page < p.n_pages; };
+    // Entries of an ended sequence, 8 a lane at a time; put(place, page) for each that is a page. Returns their number.
+    auto walk = [&](const Ended& e, auto&& put) {
+        const int32_t* row = p.table + (int64_t)e.s * p.table_st;
+        uint32_t n = 0;
+        for (int j0 = 0; j0 < e.pages; j0 += 256) {
+            int page[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int j = j0 + 32 * u + lane;
+                page[u] = j < e.pages ? row[j] : -1;
+                if (j < e.pages && !page_ok(page[u])) flags |= HA_DEVERR_INDEX;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const uint32_t m = __ballot_sync(0xffffffffu, page_ok(page[u]));
+                if ((m >> lane) & 1u) put(n + (uint32_t)__popc((int)(m & ((1u << lane) - 1u))), page[u]);
                 n += (uint32_t)__popc((int)m);
             }
-            if (lane == l) x.back = n;
         }
+        return n;
     };
+    // The tile's sequences; those that end are listed, and all warps count their pages.
+    int listed = -1;  // this thread's place in s_ended
     auto look = [&](int tile) {
+        listed = -1;
         const int s = s_begin + tile * (int)blockDim.x + tid;
         x = Mine{s, 0, 0, 0, 0, 0u, 0u};
         if (s < s_end) {
@@ -111,50 +132,68 @@ __global__ void __launch_bounds__(kMostThreads) k_plan_pages(const PagesParams p
                 x.takes = (uint32_t)(t / p.page_size + (t % p.page_size != 0 ? 1 : 0) - x.p0);
             }
         }
-        walk([](int, uint32_t, int, uint32_t) {});
+        if (!__syncthreads_or(x.state == 2 && x.p0 > 0)) return;
+        int at = -1;
+        if (x.state == 2 && x.p0 > 0) {
+            at = atomicAdd(&s_n_ended, 1);  // (their order does not matter: each has its place)
+            s_ended[at] = Ended{s, x.p0, 0u};
+        }
+        __syncthreads();
+        for (int i = warp; i < s_n_ended; i += warps) {
+            const uint32_t n = walk(s_ended[i], [](uint32_t, int) {});
+            if (lane == 0) s_back[i] = n;
+        }
+        __syncthreads();
+        if (at >= 0) x.back = s_back[at];
+        listed = at;
+    };
+    auto sums_of = [&]() {
+        return Sums{(uint32_t)min(x.nq, (int)kManyRows), x.takes, x.back, x.nq > kDirect ? (uint32_t)(x.nq - 1) / kUnit + 1u : 0u};
+    };
+    // Exclusive sums over the CTA's threads; total: all of them.
+    auto scan = [&](Sums& total) {
+        const Sums own = sums_of(), incl = scan_warp(own, lane);
+        if (lane == 31) s_warp[warp] = incl;
+        __syncthreads();
+        const Sums upto = scan_warp(lane < warps ? s_warp[lane] : Sums{0u, 0u, 0u, 0u}, lane);
+        total = from_lane(upto, 31);
+        Sums before = from_lane(upto, max(warp - 1, 0));
+        if (warp == 0) before = Sums{0u, 0u, 0u, 0u};
+        const Sums prev{__shfl_up_sync(0xffffffffu, incl.rows, 1), __shfl_up_sync(0xffffffffu, incl.takes, 1),
+                        __shfl_up_sync(0xffffffffu, incl.back, 1), __shfl_up_sync(0xffffffffu, incl.units, 1)};
+        if (lane > 0) before.add(prev);
+        __syncthreads();  // s_warp is free again
+        return before;
     };
 
     // ---- the sums, and those of the CTAs before
-    Sums mine{0, 0u, 0u};
+    Sums mine{0u, 0u, 0u, 0u}, mine_before{0u, 0u, 0u, 0u};
     for (int tile = 0; tile < n_tiles; ++tile) {
+        if (tile > 0) {
+            __syncthreads();
+            if (tid == 0) s_n_ended = 0;
+            __syncthreads();
+        }
         look(tile);
-        mine.rows += x.nq;
-        mine.takes += x.takes;
-        mine.back += x.back;
+        Sums t;
+        mine_before = scan(t);
+        mine.add(t);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine.rows += __shfl_xor_sync(0xffffffffu, mine.rows, o);
-    mine.takes = __reduce_add_sync(0xffffffffu, mine.takes);
-    mine.back = __reduce_add_sync(0xffffffffu, mine.back);
-    if (lane == 0) s_warp_sums[warp] = mine;
-    __syncthreads();
-    if (tid == 0) {
-        Sums sum{0, 0u, 0u};
-        for (int w = 0; w < warps; ++w) {
-            sum.rows += s_warp_sums[w].rows;
-            sum.takes += s_warp_sums[w].takes;
-            sum.back += s_warp_sums[w].back;
-        }
-        s_sums = sum;
+    if (tid == 0) s_sums = mine;
+    if (C > 1) cluster.sync();  // every input has been read, too: outputs may lie where inputs did
+    else __syncthreads();
+    if (n_free < 0 || n_free > p.n_pages) {
+        flags |= HA_DEVERR_STATE;
+        n_free = n_free < 0 ? 0 : p.n_pages;
     }
-    cluster.sync();  // every input has been read, too: outputs may lie where inputs did
-    Sums before{0, 0u, 0u}, total{0, 0u, 0u};
-    if (all) {
-        total = s_sums;
-    } else {
-        for (int r = 0; r < C; ++r) {
-            const Sums v = *cluster.map_shared_rank(&s_sums, r);
-            if (r < rank) {
-                before.rows += v.rows;
-                before.takes += v.takes;
-                before.back += v.back;
-            }
-            total.rows += v.rows;
-            total.takes += v.takes;
-            total.back += v.back;
-        }
+    Sums before{0u, 0u, 0u, 0u}, total = mine;
+    if (!all) {
+        const Sums v = lane < C ? *cluster.map_shared_rank(&s_sums, lane) : Sums{0u, 0u, 0u, 0u};
+        const Sums incl = scan_warp(v, lane);
+        total = from_lane(incl, 31);
+        if (rank > 0) before = from_lane(incl, rank - 1);
     }
-    const bool over = total.rows > p.total;  // then nothing is planned
+    const bool over = total.rows > (uint32_t)p.total;  // then nothing is planned
     uint32_t top = over ? (uint32_t)n_free : (uint32_t)n_free + min(total.back, (uint32_t)p.n_pages);
     if (top > (uint32_t)p.n_pages) {  // a page given back twice
         flags |= HA_DEVERR_STATE;
@@ -163,48 +202,55 @@ __global__ void __launch_bounds__(kMostThreads) k_plan_pages(const PagesParams p
     if (over) flags |= HA_DEVERR_COUNT;
     // which of several CTAs writes what belongs to sequence s
     auto writes = [&](int s) { return !all || s % C == rank; };
-
-    // exclusive sum over the CTA's threads; `at` moves on by the CTA's sum
-    auto scan = [&](int slot, uint32_t v, uint32_t& at) {
-        const uint32_t incl = warp_incl(v, lane);
-        if (lane == 31) s_warp[slot][warp] = incl;
+    auto reload = [&](int tile) {  // of several tiles
         __syncthreads();
-        uint32_t w = lane < warps ? s_warp[slot][lane] : 0u;
-        w = warp_incl(w, lane);
-        const uint32_t base = warp > 0 ? __shfl_sync(0xffffffffu, w, warp - 1) : 0u;
-        const uint32_t r = at + base + incl - v;
-        at += __shfl_sync(0xffffffffu, w, 31);
-        return r;
+        if (tid == 0) s_n_ended = 0;
+        __syncthreads();
+        look(tile);
+        Sums t;
+        mine_before = scan(t);
+        return t;
     };
 
     // ---- pages that come back
-    if (!over && total.back != 0) {
-        uint32_t at = before.back;
-        for (int tile = 0; tile < n_tiles; ++tile) {
-            if (n_tiles > 1) look(tile);
-            const uint32_t fb = scan(0, x.back, at);
-            walk([&](int l, uint32_t k, int page, uint32_t good) {
-                const uint32_t i = (uint32_t)n_free + __shfl_sync(0xffffffffu, fb, l) + k;
-                const int s = __shfl_sync(0xffffffffu, x.s, l);
-                if (good && i < (uint32_t)p.n_pages && writes(s)) p.free_pages[i] = page;
-            });
+    if (total.back != 0) {
+        Sums at = before;
+        for (int tile = 0; !over && tile < n_tiles; ++tile) {
+            Sums t = mine;
+            if (n_tiles > 1) t = reload(tile);
+            if (listed >= 0) s_ended[listed].at = at.back + mine_before.back;
             __syncthreads();
+            for (int i = warp; i < s_n_ended; i += warps) {
+                const Ended e = s_ended[i];
+                if (!writes(e.s)) continue;
+                walk(e, [&](uint32_t k, int page) {
+                    const uint32_t to = (uint32_t)n_free + e.at + k;
+                    if (to < (uint32_t)p.n_pages) p.free_pages[to] = page;
+                });
+            }
+            at.add(t);
         }
     }
-    cluster.sync();  // (nobody reads another CTA's sums any more, either)
+    // what was given back is there; nobody reads another CTA's sums any more
+    if (C > 1 && (total.back != 0 || !all)) cluster.sync();
+    else __syncthreads();
 
     // ---- lengths, bounds, tables, slots
-    uint32_t at_rows = over ? 0u : (uint32_t)before.rows, at_takes = before.takes;
+    auto pop = [&](uint32_t k) {  // (below top, as the sequence fits)
+        const int page = __ldcg(p.free_pages + (top - 1u - k));
+        if (page_ok(page)) return page;
+        flags |= HA_DEVERR_INDEX;
+        return -1;
+    };
+    Sums at = before;
     for (int tile = 0; tile < n_tiles; ++tile) {
-        if (n_tiles > 1) look(tile);
-        const uint32_t row0 = scan(1, over ? 0u : (uint32_t)x.nq, at_rows), tb = scan(2, x.takes, at_takes);
+        Sums t = mine;
+        if (n_tiles > 1) t = reload(tile);
+        const uint32_t row0 = over ? 0u : at.rows + mine_before.rows, tb = at.takes + mine_before.takes;
         if (over) x.nq = 0;
         const bool fits = x.takes == 0u || tb + x.takes <= top;
         const bool goes = x.state == 1 && fits;
-        const bool units = x.nq > kDirect;
-        uint32_t n_units = 0;
-        const uint32_t unit0 = scan(3, units ? (uint32_t)(x.nq + kUnit - 1) / kUnit : 0u, n_units);
-        s_rec[tid] = PagesRecord{(int)row0, x.nq, goes ? x.had : -1, (int)tb, (int)unit0};
+        s_rec[tid] = PagesRecord{(int)row0, x.nq, goes ? x.had : -1, (int)tb, (int)mine_before.units};
         if (x.state != 0 && writes(x.s)) {
             p.cu[x.s] = (int)row0;
             if (x.s == p.n_seq - 1) p.cu[p.n_seq] = (int)row0 + x.nq;
@@ -219,26 +265,23 @@ __global__ void __launch_bounds__(kMostThreads) k_plan_pages(const PagesParams p
                 }
             }
             p.lens_out[x.s] = len;
-        }
-        auto pop = [&](uint32_t k) {  // (below top, as the sequence fits)
-            const int page = __ldcg(p.free_pages + (top - 1u - k));
-            if (page >= 0 && page < p.n_pages) return page;
-            flags |= HA_DEVERR_INDEX;
-            return -1;
-        };
-        // few rows: by their sequence's thread
-        if (x.state != 0 && !over && !units && x.nq > 0 && writes(x.s)) {
-            int32_t* row = p.table + (int64_t)x.s * p.table_st;
-            int pg = x.had / p.page_size, r = x.had - pg * p.page_size, page = -1;
-            if (goes && r != 0) page = row[pg];
-            for (int i = 0; i < x.nq; ++i) {
-                if (goes && r == 0) row[pg] = page = pop(tb + (uint32_t)(pg - x.p0));
-                if (p.slots != nullptr) p.slots[row0 + (uint32_t)i] = goes && page >= 0 && page < p.n_pages ? page * p.page_size + r : -1;
-                if (++r == p.page_size) r = 0, ++pg;
+            // few rows: by their sequence's thread
+            if (x.nq > 0 && x.nq <= kDirect) {
+                int32_t* row = p.table + (int64_t)x.s * p.table_st;
+                int pg = x.had / p.page_size, r = x.had - pg * p.page_size, page = -1;
+                if (goes && r != 0) page = row[pg];
+                for (int i = 0; i < x.nq; ++i) {
+                    if (goes && r == 0) row[pg] = page = pop(tb + (uint32_t)(pg - x.p0));
+                    if (p.slots != nullptr) p.slots[row0 + (uint32_t)i] = goes && page_ok(page) ? page * p.page_size + r : -1;
+                    if (++r == p.page_size) r = 0, ++pg;
+                }
             }
         }
         __syncthreads();
-        // many: by the warps, kUnit rows at a time
+        // many: by the warps, kUnit rows at a time (32 rows on are so many pages and rows on: the one
+        // division of a row would be most of what it costs)
+        const int step_pages = 32 / p.page_size, step_rows = 32 - step_pages * p.page_size;
+        const uint32_t n_units = over ? 0u : t.units;
         for (uint32_t u = (uint32_t)(all ? warp * C + rank : warp); u < n_units; u += (uint32_t)(all ? warps * C : warps)) {
             int lo = 0, hi = (int)blockDim.x - 1;  // the last record that begins at or before u: it has units
             while (lo < hi) {
@@ -254,28 +297,39 @@ __global__ void __launch_bounds__(kMostThreads) k_plan_pages(const PagesParams p
                 continue;
             }
             int32_t* row = p.table + (int64_t)(s_begin + tile * (int)blockDim.x + lo) * p.table_st;
-            const int p0 = (rec.had + p.page_size - 1) / p.page_size;
-            // pages that begin in these rows
-            const int b0 = rec.had + i0, b1 = rec.had + i1;
-            for (int j = (b0 + p.page_size - 1) / p.page_size + lane; (int64_t)j * p.page_size < b1; j += 32)
-                row[j] = pop((uint32_t)(rec.tb + j - p0));
-            if (p.slots == nullptr) continue;
+            const int p0 = (rec.had + p.page_size - 1) / p.page_size, b0 = rec.had + i0, b1 = rec.had + i1;
+            // 32 of the unit's pages at a time, one to a lane, and the rows in them
+            const int pg1 = (b1 - 1) / p.page_size;
+            for (int pg0 = b0 / p.page_size; pg0 <= pg1; pg0 += 32) {
+                const int pg = pg0 + lane;
+                int page = -1;
+                if (pg <= pg1) {
+                    page = pg >= p0 ? pop((uint32_t)(rec.tb + pg - p0)) : row[pg];
+                    if (pg >= p0 && (int64_t)pg * p.page_size >= b0) row[pg] = page;  // it begins here
+                }
+                if (p.slots == nullptr) continue;
+                const int r0 = max(b0, pg0 * p.page_size);
+                const int r1 = (int)min((int64_t)b1, ((int64_t)pg0 + 32) * p.page_size);
+                int e = (r0 + lane) / p.page_size, off = r0 + lane - e * p.page_size;  // of this lane's row
 #pragma unroll 4
-            for (int i = i0 + lane; i < i1; i += 32) {
-                const int pos = rec.had + i, pg = pos / p.page_size;
-                const int page = pg >= p0 ? pop((uint32_t)(rec.tb + pg - p0)) : row[pg];
-                p.slots[rec.row0 + i] = page >= 0 && page < p.n_pages ? page * p.page_size + (pos - pg * p.page_size) : -1;
+                for (int q0 = r0; q0 < r1; q0 += 32) {
+                    const int of = __shfl_sync(0xffffffffu, page, min(e - pg0, 31)), pos = q0 + lane;
+                    if (pos < r1) p.slots[rec.row0 + (pos - rec.had)] = page_ok(of) ? of * p.page_size + off : -1;
+                    e += step_pages;
+                    off += step_rows;
+                    if (off >= p.page_size) off -= p.page_size, ++e;
+                }
             }
         }
-        __syncthreads();
+        at.add(t);
     }
     if (rank == 0 && tid == 0) {
         if (over) *p.n_free_out = n_free;
         else if (total.takes <= top) *p.n_free_out = (int)(top - total.takes);
     }
     if (p.slots != nullptr) {
-        const int64_t rows = over ? 0 : total.rows;
-        for (int64_t t = rows + rank * (int64_t)blockDim.x + tid; t < p.total; t += (int64_t)C * blockDim.x) p.slots[t] = -1;
+        const int rows = over ? 0 : (int)total.rows;
+        for (int t = rows + rank * (int)blockDim.x + tid; t < p.total; t += C * (int)blockDim.x) p.slots[t] = -1;
     }
     flags = __reduce_or_sync(0xffffffffu, flags);
     if (lane == 0 && flags != 0u) flag_error(p.flags, flags);
