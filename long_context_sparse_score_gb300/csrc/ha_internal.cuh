@@ -10,6 +10,7 @@
 #include <utility>
 
 #include "hashattn.h"
+#include "packed_order.h"
 
 namespace ha {
 
@@ -333,6 +334,7 @@ struct PackedParamsEx : PackedParams {
     const int32_t* first;      // [n_seq] or null
     const float* slopes;       // [Hq] or null
     int window;                // 0: none
+    Quotient per_item;         // by 2 TQ
     int shaped;
     float scale;               // scale of the scores x log2(e)
     float cap;                 // cap x log2(e), 0: none

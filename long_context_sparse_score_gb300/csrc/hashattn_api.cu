@@ -1518,6 +1518,7 @@ void set_opts(PackedParamsEx& p, const ha_score_opts* o, int d, bool f32) {
     p.first = o->first;
     p.slopes = o->slopes;
     p.window = o->window < p.max_len ? o->window : 0;  // one that reaches over all keys is none
+    p.per_item = Quotient::of(2u * (uint32_t)p.TQ);
     p.scale = (float)(scale * log2e);
     p.qscale = p.scale;
     p.shaped = o->softcap != 0.f || o->slopes != nullptr;
@@ -1658,10 +1659,11 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const ha_score
     // up to 500 keys 39.9 -> 36.7, one over 500 keys 11.6 -> 12.1).
     const int grid = (int)std::min<int64_t>(kSMs, items * tiles);
     const bool merge = grid > 1 && p.split;
-    if (opts == nullptr) {
+    if (opts != nullptr) set_opts(p, opts, t->d, f32);
+    const bool masked = p.window > 0 || p.prefix != nullptr || p.first != nullptr;
+    if (!p.shaped && !masked) {
         HA_LAUNCH(launch_packed_att(p, m, t->d, f32, grid, merge, static_cast<cudaStream_t>(stream)), "packed attention launch");
     } else {
-        set_opts(p, opts, t->d, f32);
         const auto launch = !p.shaped ? launch_packed_att_masked : (p.fixed_ref ? launch_packed_att_capped : launch_packed_att_shaped);
         HA_LAUNCH(launch(p, m, t->d, f32, grid, merge, static_cast<cudaStream_t>(stream)), "packed attention launch");
     }

@@ -171,6 +171,11 @@ __device__ __forceinline__ int key_tiles(int keys) {
 
 // Cost of the items 0 .. qt - 1 of one head, qt < the number of items: their tiles
 // (an item without keys counts one, so that its rows are written) and kItemCost each.
+struct Window {  // what the work of an item takes from the options, beside its sequence
+    int keys;
+    Quotient per;
+};
+
 template <int KT>
 struct Tiles {
     static constexpr int kLog = KT == 64 ? 6 : 7;
@@ -179,7 +184,7 @@ struct Tiles {
 };
 
 template <int KT>
-__device__ __forceinline__ uint32_t cost_before(const SeqInfo& i, int, int t2, int qt, const Tiles<KT>& tiles) {
+__device__ __forceinline__ uint32_t cost_before(const SeqInfo& i, const Window&, int t2, int qt, const Tiles<KT>& tiles) {
     if (qt == 0) return 0;
     const int base = i.nk - i.nq;
     int z = 0;  // items that see no key
@@ -190,26 +195,26 @@ __device__ __forceinline__ uint32_t cost_before(const SeqInfo& i, int, int t2, i
 }
 
 template <int KT>
-__device__ __forceinline__ int item_tiles(const SeqInfo& i, int, int t2, int qt) {
+__device__ __forceinline__ int item_tiles(const SeqInfo& i, const Window&, int t2, int qt) {
     return max(1, key_tiles<KT>(keys_seen(i, (qt + 1) * t2)));
 }
 
 // With score options.
 template <int KT>
-__device__ __forceinline__ MaskedItems<Tiles<KT>::kLog> masked(const SeqInfoEx& i, int window, int t2) {
-    return MaskedItems<Tiles<KT>::kLog>{i.nk - i.nq, i.nq, i.first, i.prefix, window, t2};
+__device__ __forceinline__ MaskedItems<Tiles<KT>::kLog> masked(const SeqInfoEx& i, const Window& window, int t2) {
+    return MaskedItems<Tiles<KT>::kLog>{i.nk - i.nq, i.nq, i.first, i.prefix, window.keys, t2, window.per};
 }
 template <int KT>
-__device__ __forceinline__ uint32_t cost_before(const SeqInfoEx& i, int window, int t2, int qt, const Tiles<KT>& tiles) {
+__device__ __forceinline__ uint32_t cost_before(const SeqInfoEx& i, const Window& window, int t2, int qt, const Tiles<KT>& tiles) {
     return masked<KT>(i, window, t2).tiles_before(qt, tiles.sums, tiles.before) + (uint32_t)qt * kItemCost;
 }
 template <int KT>
-__device__ __forceinline__ int item_tiles(const SeqInfoEx& i, int window, int t2, int qt) {
+__device__ __forceinline__ int item_tiles(const SeqInfoEx& i, const Window& window, int t2, int qt) {
     return masked<KT>(i, window, t2).tiles(qt);
 }
 
 template <int KT, typename I>
-__device__ __forceinline__ uint32_t head_cost(const I& i, int window, int t2, const Tiles<KT>& tiles) {
+__device__ __forceinline__ uint32_t head_cost(const I& i, const Window& window, int t2, const Tiles<KT>& tiles) {
     if (i.nq == 0) return 0;
     const int last = (i.nq + t2 - 1) / t2 - 1;
     return cost_before<KT>(i, window, t2, last, tiles) + (unsigned)(item_tiles<KT>(i, window, t2, last) + kItemCost);
@@ -507,74 +512,98 @@ __device__ __forceinline__ void shape_scores(uint32_t (&x)[N], const PackedParam
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[16]) { tmem_ld16(addr, x); }
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[32]) { tmem_ld32(addr, x); }
 
-// The weights of a tile of 128 columns of shaped scores, all seen, keys on one side: 32 columns at a
-// time, the exponentials of some between the products of the next, so that neither unit waits for
-// the other. Score k of the tile, less the reference: cap tanh() as a polynomial of x (CAP), or x scale;
-// plus row, plus slope k (BIAS). Returns the columns done: those before the first 32 where a product of any
-// of the warp's rows is too large for the polynomial (CAP), or a score more than kShapedRescale above the
-// reference (BIAS).
-template <bool CAP, bool BIAS>
-__device__ __forceinline__ int fast_tile(uint32_t tS, const PackedParamsEx& p, float row, float slope, bool valid, uint64_t (&sum)[2]) {
-    uint32_t x[32], y[2][32], w[16];
+// The weights of a tile of 128 columns of capped scores, all seen, less the reference (row2: -m twice).
+// The polynomials of 32 columns stand between the exponentials of the 32 before, so that neither unit
+// waits for the other: 16,384 tokens 1,605 us; one after the other in a loop 1,937 (it is the shorter code
+// for the instruction cache, and better for short prompts: 64 of 300 tokens 153 and 146 us). Returns the
+// columns done: those before the first 32 where a product of any of the warp's rows is too large
+// for the polynomial.
+__device__ __forceinline__ int capped_tile(uint32_t tS, const PackedParamsEx& p, uint64_t row2, uint64_t (&sum)[2]) {
+    uint32_t x[32] = {}, y[2][32], w[16];
     bool stop[2];
-    const uint64_t scale = pack2(p.scale, p.scale);
-    auto score = [&](int k, uint64_t row2, float& a, float& b) {  // columns k and k + 1 of the 32 in x
-        const uint64_t v = pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-        if constexpr (CAP) unpack2(odd_poly<CapDegrees<false>::low>(v, p.poly[0], row2), a, b);
-        else unpack2(fma2(v, scale, row2), a, b);
-        if constexpr (BIAS) {
-            a = fmaf(slope, (float)k, a);
-            b = fmaf(slope, (float)(k + 1), b);
-        }
-    };
-    auto larger = [&](int k, float a, float b, float& big, float& top) {
-        if constexpr (CAP) big = fmaxf(fmaxf(big, fabsf(__uint_as_float(x[k]))), fabsf(__uint_as_float(x[k + 1])));
-        if constexpr (BIAS) top = fmaxf(fmaxf(top, a), b);
-    };
-    auto stops = [&](float big, float top) {
-        return (bool)__any_sync(0xffffffffu, (CAP && big > p.fit[0]) || (BIAS && top > kShapedRescale && valid));
+    // the scores of columns k and k + 1 of x; big grows to their products
+    auto score = [&](int k, uint32_t (&to)[32], float& big) {
+        float a, b;
+        unpack2(odd_poly<CapDegrees<false>::low>(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), p.poly[0], row2), a, b);
+        big = fmaxf(fmaxf(big, fabsf(__uint_as_float(x[k]))), fabsf(__uint_as_float(x[k + 1])));
+        to[k] = __float_as_uint(a);
+        to[k + 1] = __float_as_uint(b);
     };
     tmem_ld32(tS, x);
     tmem_landed(x);
     {
-        float big[2] = {0.f, 0.f}, top[2] = {-INFINITY, -INFINITY};
+        float big[2] = {0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-            float a, b;
-            score(k, pack2(row, row), a, b);
-            larger(k, a, b, big[(k >> 1) & 1], top[(k >> 1) & 1]);
-            y[0][k] = __float_as_uint(a);
-            y[0][k + 1] = __float_as_uint(b);
-        }
-        stop[0] = stops(fmaxf(big[0], big[1]), fmaxf(top[0], top[1]));
+        for (int k = 0; k < 32; k += 2) score(k, y[0], big[(k >> 1) & 1]);
+        stop[0] = (bool)__any_sync(0xffffffffu, fmaxf(big[0], big[1]) > p.fit[0]);
     }
     tmem_ld32(tS + 32u, x);
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
         uint32_t (&now)[32] = y[h & 1], (&next)[32] = y[(h & 1) ^ 1];
         uint64_t s[2] = {0, 0};
-        float big[2] = {0.f, 0.f}, top[2] = {-INFINITY, -INFINITY};
-        const float r = BIAS ? fmaf(slope, (float)(32 * (h + 1)), row) : row;
+        float big[2] = {0.f, 0.f};
         if (h < 3) tmem_landed(x);
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
             const float a = ex2(__uint_as_float(now[k])), b = ex2(__uint_as_float(now[k + 1]));
-            if (h < 3) {
-                float u, v;
-                score(k, pack2(r, r), u, v);
-                larger(k, u, v, big[(k >> 1) & 1], top[(k >> 1) & 1]);
-                next[k] = __float_as_uint(u);
-                next[k + 1] = __float_as_uint(v);
-            }
+            if (h < 3) score(k, next, big[(k >> 1) & 1]);
             w[k >> 1] = pack_bf16(a, b);
             s[(k >> 1) & 1] = add2(s[(k >> 1) & 1], pack2(a, b));
         }
         if (h < 2) tmem_ld32(tS + (uint32_t)(64 + 32 * h), x);
         if (stop[h & 1]) return 32 * h;
-        if (h < 3) stop[(h & 1) ^ 1] = stops(fmaxf(big[0], big[1]), fmaxf(top[0], top[1]));
+        if (h < 3) stop[(h & 1) ^ 1] = (bool)__any_sync(0xffffffffu, fmaxf(big[0], big[1]) > p.fit[0]);
         sum[0] = add2(sum[0], s[0]);
         sum[1] = add2(sum[1], s[1]);
         tmem_st16(tS + (uint32_t)(16 * h), w);
+    }
+    return 128;
+}
+
+// The same of biased scores, keys on one side of the rows: score k of the tile is x scale (CAP: the
+// polynomial) + row + slope k. Also stops where a score is more than kShapedRescale above the reference.
+// In a loop: 24 prompts of 33 to 2,500 tokens 387 us, as above 413; 4,096 tokens 139 and 135.
+template <bool CAP>
+__device__ __forceinline__ int biased_tile(uint32_t tS, const PackedParamsEx& p, float row, float slope, bool valid, uint64_t (&sum)[2]) {
+    uint32_t x[32], w[16];
+    const uint64_t scale = pack2(p.scale, p.scale);
+    tmem_ld32(tS, x);
+#pragma unroll 1
+    for (int c0 = 0; c0 < 128; c0 += 32) {
+        uint64_t s[2] = {0, 0};
+        float y[32], big[2] = {0.f, 0.f}, top[2] = {-INFINITY, -INFINITY};
+        const float r = fmaf(slope, (float)c0, row);
+        const uint64_t row2 = pack2(r, r);
+        tmem_landed(x);
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            const uint64_t v = pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+            float a, b;
+            if constexpr (CAP) unpack2(odd_poly<CapDegrees<false>::low>(v, p.poly[0], row2), a, b);
+            else unpack2(fma2(v, scale, row2), a, b);
+            y[k] = fmaf(slope, (float)k, a);
+            y[k + 1] = fmaf(slope, (float)(k + 1), b);
+            const int u = (k >> 1) & 1;
+            if constexpr (CAP) big[u] = fmaxf(fmaxf(big[u], fabsf(__uint_as_float(x[k]))), fabsf(__uint_as_float(x[k + 1])));
+            top[u] = fmaxf(fmaxf(top[u], y[k]), y[k + 1]);
+        }
+        if (c0 < 96) tmem_ld32(tS + (uint32_t)(c0 + 32), x);
+        const bool stop = (bool)__any_sync(0xffffffffu, (CAP && fmaxf(big[0], big[1]) > p.fit[0]) ||
+                                                            (valid && fmaxf(top[0], top[1]) > kShapedRescale));
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            const float a = ex2(y[k]), b = ex2(y[k + 1]);
+            w[k >> 1] = pack_bf16(a, b);
+            s[(k >> 1) & 1] = add2(s[(k >> 1) & 1], pack2(a, b));
+        }
+        if (stop) {
+            tmem_landed(x);
+            return c0;
+        }
+        sum[0] = add2(sum[0], s[0]);
+        sum[1] = add2(sum[1], s[1]);
+        tmem_st16(tS + (uint32_t)(c0 >> 1), w);
     }
     return 128;
 }
@@ -668,8 +697,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     }
     if (warp == kMmaWarp) tmem_alloc(smem_addr(s_tmem), kTmemCols);
     const int t2 = 2 * p.TQ;
-    int window = 0;
-    if constexpr (EX) window = p.window;
+    Window window{};
+    if constexpr (EX) window = Window{p.window, p.per_item};
     const Tiles<KT> tiles{TileSums<Tiles<KT>::kLog>((uint32_t)t2), s_before};
     if (warp == kPlanWarp) {
         // sums of remainders, two a lane at most
@@ -1344,15 +1373,14 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             // 283 -> 300, so the votes stay there).
             const int kmax = valid ? min(g.nk, max(EX ? g.prefix : 0, g.kfirst + ltok + 1)) : (NB == 3 || shaped ? INT_MAX : 0);
             const int kmin = __reduce_min_sync(0xffffffffu, kmax);
-            // with score options: the row's first key, the last of the warp's; its position; its slope
-            int klow = 0, klast = 0;
+            // with score options: the first key of the item's last token, and of this row; the row's slope
+            const int klast = EX ? (window.keys > 0 ? max(g.first, g.kfirst + g.tokens - window.keys) : g.first) : 0;
+            auto first_key = [&]() {
+                return !valid ? 0 : window.keys > 0 ? max(g.first, g.kfirst + ltok + 1 - window.keys) : g.first;
+            };
             float slope = 0.f;
-            if constexpr (EX) {
-                if (valid) {
-                    klow = p.window > 0 ? max(g.first, g.kfirst + ltok + 1 - p.window) : g.first;
-                    if (MODE == kShaped && p.slopes != nullptr) slope = p.slopes[g.head * p.G + hd] * 1.4426950408889634f;
-                }
-                klast = __reduce_max_sync(0xffffffffu, klow);
+            if constexpr (MODE == kShaped) {
+                if (valid && p.slopes != nullptr) slope = p.slopes[g.head * p.G + hd] * 1.4426950408889634f;
             }
             // shaped scores less sub of columns col, col + 1, .. of key tile j, and masks
             auto shape = [&](auto& x, int j, int col, float sub) {
@@ -1363,8 +1391,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             };
             auto mask = [&](auto& x, int lim, int j, int col) {
                 mask_columns(x, lim - col);
-                if constexpr (EX) {
-                    if (klast > j * KT) mask_before(x, klow - j * KT - col);
+                if constexpr (shaped) {
+                    if (klast > j * KT) mask_before(x, first_key() - j * KT - col);
                 }
             };
             const bool any = __any_sync(0xffffffffu, valid);
@@ -1407,7 +1435,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 #pragma unroll 1
             for (int i = 0; i < nt; ++i, j += jstep) {
                 const int lim = kmax - j * KT;  // columns of this tile the row sees
-                const bool part = (NB == 3 ? kmin - j * KT < KT : (bool)__any_sync(0xffffffffu, lim < KT)) || (EX && klast > j * KT);
+                const bool part = (NB == 3 ? kmin - j * KT < KT : (bool)__any_sync(0xffffffffu, lim < KT)) || (shaped && klast > j * KT);
                 if (NB == 2 && aborted()) break;
                 // O holds two tiles at most (24 steps of the accumulator)
                 bool take_o = F32OUT && i > 0 && (i & 1) == 0;
@@ -1424,6 +1452,22 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         take_o = false;
                     }
                     wait(s_full(t), cnt & 1u);
+                }
+                if constexpr (MODE == kMasked) {
+                    // Scores that are only scaled are masked where they lie: in an item's first tiles alone, so in
+                    // a loop that is short rather than in the code of all tiles.
+                    if (any && klast > j * KT) {
+                        const int low = first_key() - j * KT;
+#pragma unroll 1
+                        for (int cc = 0; cc < KT; cc += 16) {
+                            uint32_t x[16];
+                            tmem_ld16(tS + (uint32_t)cc, x);
+                            tmem_landed(x);
+                            mask_before(x, low - cc);
+                            tmem_st16(tS + (uint32_t)cc, x);
+                        }
+                        tmem_wait_st();
+                    }
                 }
                 if (any) {
                     // The reference grows to mx: what was added up shrinks by a. With two places S of
@@ -1462,7 +1506,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     // Shaped scores come less the reference as it is. It moves where their maximum `top` (less it
                     // as well) asks for that; a constant one is set where a row sees its first keys.
                     // Returns by how much, with what is to be scaled meanwhile done by scale(a).
-                    const bool looks = !fixed || (bool)__any_sync(0xffffffffu, valid && l == 0.f && lim > 0 && klow < (j + 1) * KT);
+                    const bool looks = !fixed || (bool)__any_sync(0xffffffffu, valid && l == 0.f && lim > 0 && first_key() < (j + 1) * KT);
                     bool none = l == 0.f;
                     auto settle = [&](float top, auto&& scale) {
                         const float sub = m == -INFINITY ? 0.f : m;
@@ -1577,11 +1621,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                             const float to_row = (float)(j * KT - (g.kfirst + ltok));
                             const bool both = MODE == kShaped && g.prefix > g.kfirst + 1 && (j + 1) * KT - 1 > g.kfirst;
                             if constexpr (fixed) {
-                                if (!part && !looks) cc = fast_tile<true, false>(tS, p, -m, 0.f, valid, sum);
+                                if (!part && !looks) cc = capped_tile(tS, p, pack2(-m, -m), sum);
                             } else if (!part && !both && !__any_sync(0xffffffffu, valid && m == -INFINITY)) {
                                 const float row = fmaf(slope, to_row, valid ? -m : 0.f);
-                                if (p.cap != 0.f) cc = fast_tile<true, true>(tS, p, row, slope, valid, sum);
-                                else cc = fast_tile<false, true>(tS, p, row, slope, valid, sum);
+                                cc = p.cap != 0.f ? biased_tile<true>(tS, p, row, slope, valid, sum) : biased_tile<false>(tS, p, row, slope, valid, sum);
                             }
                             // the rest, in any case
 #pragma unroll 1

@@ -41,6 +41,21 @@ struct TileSums {
     }
 };
 
+// n / d for 0 <= n < 2^31 and d >= 1 as a product: with 2^k < d <= 2^(k + 1) and m = ceil(2^(32 + k) / d),
+// m d exceeds 2^(32 + k) by less than d, so m n / 2^(32 + k) exceeds n / d by less than 1 / d.
+struct Quotient {
+    uint32_t m;
+    int k;  // -1: d is 1
+    static Quotient of(uint32_t d) {
+        int k = -1;
+        while (((uint64_t)1 << (k + 1)) < d) ++k;
+        return Quotient{k < 0 ? 0u : (uint32_t)((((uint64_t)1 << (32 + k)) + d - 1u) / d), k};
+    }
+    HA_HD int operator()(int n) const {
+        return k < 0 ? n : (int)((uint32_t)((uint64_t)(uint32_t)n * m >> 32) >> k);
+    }
+};
+
 // The keys and key tiles (2^K keys) of a row of items under score options: t2 new tokens to an item;
 // token t of nq, whose position is base + t, sees the keys max(first, base + t + 1 - window) <= j <
 // max(base + t + 1, prefix) below nk = base + nq (window 0: none; first and prefix lie within [0, nk]).
@@ -49,6 +64,7 @@ struct TileSums {
 template <int K>
 struct MaskedItems {
     int base, nq, first, prefix, window, t2;
+    Quotient per;  // by t2
     HA_HD static int least(int a, int b) { return a < b ? a : b; }
     HA_HD static int most(int a, int b) { return a > b ? a : b; }
     HA_HD static int tiles_of(int keys) { return (keys + (1 << K) - 1) >> K; }
@@ -64,16 +80,16 @@ struct MaskedItems {
     HA_HD uint32_t tiles_before(int qt, const TileSums<K>& sums, const uint16_t* before) const {
         if (qt == 0) return 0;
         // items 0 .. z - 1 see no key: they end at or before `first`
-        const int z = prefix > first || base > first ? 0 : least(qt, (first - base) / t2);
+        const int z = prefix > first || base > first ? 0 : least(qt, per(first - base));
         // items z .. e - 1 end with the prefix
-        const int e = base > prefix ? z : least(qt, most(z, (prefix - base) / t2));
+        const int e = base > prefix ? z : least(qt, most(z, per(prefix - base)));
         uint32_t c = (uint32_t)z + (uint32_t)(e - z) * (uint32_t)tiles_of(prefix);
         if (qt > e) c += sums.sum((uint32_t)(qt - e), (uint32_t)(base + (e + 1) * t2 + (1 << K) - 1), before);
         // items z .. b - 1 begin at `first`
         int b = qt;
         if (window > 0) {
             const int w = base + 1 - window;
-            b = w > first ? z : least(qt, most(z, (first - w) / t2 + 1));
+            b = w > first ? z : least(qt, most(z, per(first - w) + 1));
             if (qt > b) c -= sums.sum((uint32_t)(qt - b), (uint32_t)(w + b * t2), before);
         }
         return c - (uint32_t)(b - z) * (uint32_t)(first >> K);

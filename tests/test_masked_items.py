@@ -20,17 +20,19 @@ static uint32_t before(int base, int nq, int first, int prefix, int window, int 
         b[x] = (uint16_t)at;
         at += t.remainder((uint32_t)x);
     }
-    return ha::MaskedItems<K>{base, nq, first, prefix, window, t2}.tiles_before(qt, t, b);
+    return ha::MaskedItems<K>{base, nq, first, prefix, window, t2, ha::Quotient::of((uint32_t)t2)}.tiles_before(qt, t, b);
 }
 #define ARGS int base, int nq, int first, int prefix, int window, int t2, int qt
-#define PASS base, nq, first, prefix, window, t2
+#define PASS base, nq, first, prefix, window, t2, ha::Quotient::of((uint32_t)t2)
+#define PLAIN base, nq, first, prefix, window, t2
 extern "C" {
-uint32_t before6(ARGS) { return before<6>(PASS, qt); }
-uint32_t before7(ARGS) { return before<7>(PASS, qt); }
+uint32_t before6(ARGS) { return before<6>(PLAIN, qt); }
+uint32_t before7(ARGS) { return before<7>(PLAIN, qt); }
 int tiles6(ARGS) { return ha::MaskedItems<6>{PASS}.tiles(qt); }
 int tiles7(ARGS) { return ha::MaskedItems<7>{PASS}.tiles(qt); }
 int begin6(ARGS) { return ha::MaskedItems<6>{PASS}.begin_tile(qt); }
 int begin7(ARGS) { return ha::MaskedItems<7>{PASS}.begin_tile(qt); }
+int quotient(int n, int d) { return ha::Quotient::of((uint32_t)d)(n); }
 }
 """
 
@@ -113,3 +115,11 @@ def test_tiles_of_items_of_long_caches(lib, log2):
             if qt + 1 < n_items:
                 a, b = getattr(lib, f"before{log2}")(*c, qt), getattr(lib, f"before{log2}")(*c, qt + 1)
                 assert (b - a) % (1 << 32) == tiles, (c, qt)
+
+
+def test_quotients(lib):
+    r = random.Random(4)
+    for d in [*range(1, 300), 1 << 20, (1 << 20) + 1, (1 << 31) - 1]:
+        for n in [0, 1, d - 1, d, d + 1, (1 << 31) - 1, (1 << 31) - 2, (1 << 30) + 7] + [k * d + e for k in r.sample(range(1, max(2, (1 << 31) // d - 1)), min(6, max(1, (1 << 31) // d - 3))) for e in (-1, 0)]:
+            if 0 <= n < 1 << 31:
+                assert lib.quotient(n, d) == n // d, (n, d)
