@@ -347,6 +347,7 @@ struct PackedParamsEx : PackedParams {
     // that its first keys give (within these bounds): no maximum is looked for, and nothing is rescaled.
     int fixed_ref;
     float ref_low, ref_high;
+    int long_items;            // see fast_tile
 };
 
 // k_append: rotation of queries and keys, keys and values into the cache.

@@ -512,95 +512,54 @@ __device__ __forceinline__ void shape_scores(uint32_t (&x)[N], const PackedParam
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[16]) { tmem_ld16(addr, x); }
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[32]) { tmem_ld32(addr, x); }
 
-// The weights of a tile of 128 columns of capped scores, all seen, less the reference (row2: -m twice).
-// The polynomials of 32 columns stand between the exponentials of the 32 before, so that neither unit
-// waits for the other: 16,384 tokens 1,605 us; one after the other in a loop 1,937 (it is the shorter code
-// for the instruction cache, and better for short prompts: 64 of 300 tokens 153 and 146 us). Returns the
-// columns done: those before the first 32 where a product of any of the warp's rows is too large
-// for the polynomial.
-__device__ __forceinline__ int capped_tile(uint32_t tS, const PackedParamsEx& p, uint64_t row2, uint64_t (&sum)[2]) {
-    uint32_t x[32] = {}, y[2][32], w[16];
-    bool stop[2];
-    // the scores of columns k and k + 1 of x; big grows to their products
-    auto score = [&](int k, uint32_t (&to)[32], float& big) {
-        float a, b;
-        unpack2(odd_poly<CapDegrees<false>::low>(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), p.poly[0], row2), a, b);
-        big = fmaxf(fmaxf(big, fabsf(__uint_as_float(x[k]))), fabsf(__uint_as_float(x[k + 1])));
-        to[k] = __float_as_uint(a);
-        to[k + 1] = __float_as_uint(b);
-    };
-    tmem_ld32(tS, x);
-    tmem_landed(x);
-    {
-        float big[2] = {0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) score(k, y[0], big[(k >> 1) & 1]);
-        stop[0] = (bool)__any_sync(0xffffffffu, fmaxf(big[0], big[1]) > p.fit[0]);
-    }
-    tmem_ld32(tS + 32u, x);
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-        uint32_t (&now)[32] = y[h & 1], (&next)[32] = y[(h & 1) ^ 1];
-        uint64_t s[2] = {0, 0};
-        float big[2] = {0.f, 0.f};
-        if (h < 3) tmem_landed(x);
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-            const float a = ex2(__uint_as_float(now[k])), b = ex2(__uint_as_float(now[k + 1]));
-            if (h < 3) score(k, next, big[(k >> 1) & 1]);
-            w[k >> 1] = pack_bf16(a, b);
-            s[(k >> 1) & 1] = add2(s[(k >> 1) & 1], pack2(a, b));
-        }
-        if (h < 2) tmem_ld32(tS + (uint32_t)(64 + 32 * h), x);
-        if (stop[h & 1]) return 32 * h;
-        if (h < 3) stop[(h & 1) ^ 1] = (bool)__any_sync(0xffffffffu, fmaxf(big[0], big[1]) > p.fit[0]);
-        sum[0] = add2(sum[0], s[0]);
-        sum[1] = add2(sum[1], s[1]);
-        tmem_st16(tS + (uint32_t)(16 * h), w);
-    }
-    return 128;
-}
-
-// The same of biased scores, keys on one side of the rows: score k of the tile is x scale (CAP: the
-// polynomial) + row + slope k. Also stops where a score is more than kShapedRescale above the reference.
-// In a loop: 24 prompts of 33 to 2,500 tokens 387 us, as above 413; 4,096 tokens 139 and 135.
-template <bool CAP>
-__device__ __forceinline__ int biased_tile(uint32_t tS, const PackedParamsEx& p, float row, float slope, bool valid, uint64_t (&sum)[2]) {
-    uint32_t x[32], w[16];
+// The weights of a tile of 128 columns of shaped scores, all seen, keys on one side of the rows: score k
+// of the tile, less the reference, is x scale (CAP: the polynomial) + row, and with BIAS + slope k.
+// Returns the columns done: those before the first 32 where a product of any of the warp's rows is too
+// large for the polynomial, or (BIAS) a score more than kShapedRescale above the reference.
+//
+// 32 columns at a time in a loop: what bounds short prompts is the instruction cache, which the item's
+// first and last tiles share with this code. UNROLL 4 lets the exponentials of 32 columns run under the
+// multiplications of the next (in a kernel of its own: beside the loop it is no faster). Capped scores, loop / unrolled: 24 prompts of 1,000 tokens 267 / 288 us, 8 of
+// 2,048 286 / 282, 4 of 4,096 493 / 481, one of 16,384 1,730 / 1,657; at d 64 the loop is the faster at any
+// length (223 / 245, 235 / 245, 403 / 410, 1,384 / 1,383), and for biased ones at d 128 up to 4,096 tokens
+// (24 of 1,000: 260 / 292, 4 of 4,096: 477 / 477).
+template <bool CAP, bool BIAS, int UNROLL>
+__device__ __forceinline__ int fast_tile(uint32_t tS, const PackedParamsEx& p, float row, float slope, bool valid, uint64_t (&sum)[2]) {
     const uint64_t scale = pack2(p.scale, p.scale);
-    tmem_ld32(tS, x);
-#pragma unroll 1
+#pragma unroll UNROLL
     for (int c0 = 0; c0 < 128; c0 += 32) {
+        uint32_t x[32], w[16];
         uint64_t s[2] = {0, 0};
         float y[32], big[2] = {0.f, 0.f}, top[2] = {-INFINITY, -INFINITY};
-        const float r = fmaf(slope, (float)c0, row);
+        const float r = BIAS ? fmaf(slope, (float)c0, row) : row;
         const uint64_t row2 = pack2(r, r);
+        tmem_ld32(tS + (uint32_t)c0, x);
         tmem_landed(x);
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
             const uint64_t v = pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-            float a, b;
-            if constexpr (CAP) unpack2(odd_poly<CapDegrees<false>::low>(v, p.poly[0], row2), a, b);
-            else unpack2(fma2(v, scale, row2), a, b);
-            y[k] = fmaf(slope, (float)k, a);
-            y[k + 1] = fmaf(slope, (float)(k + 1), b);
             const int u = (k >> 1) & 1;
-            if constexpr (CAP) big[u] = fmaxf(fmaxf(big[u], fabsf(__uint_as_float(x[k]))), fabsf(__uint_as_float(x[k + 1])));
-            top[u] = fmaxf(fmaxf(top[u], y[k]), y[k + 1]);
+            if constexpr (CAP) {
+                unpack2(odd_poly<CapDegrees<false>::low>(v, p.poly[0], row2), y[k], y[k + 1]);
+                big[u] = fmaxf(fmaxf(big[u], fabsf(__uint_as_float(x[k]))), fabsf(__uint_as_float(x[k + 1])));
+            } else {
+                unpack2(fma2(v, scale, row2), y[k], y[k + 1]);
+            }
+            if constexpr (BIAS) {
+                y[k] = fmaf(slope, (float)k, y[k]);
+                y[k + 1] = fmaf(slope, (float)(k + 1), y[k + 1]);
+                top[u] = fmaxf(fmaxf(top[u], y[k]), y[k + 1]);
+            }
         }
-        if (c0 < 96) tmem_ld32(tS + (uint32_t)(c0 + 32), x);
         const bool stop = (bool)__any_sync(0xffffffffu, (CAP && fmaxf(big[0], big[1]) > p.fit[0]) ||
-                                                            (valid && fmaxf(top[0], top[1]) > kShapedRescale));
+                                                            (BIAS && valid && fmaxf(top[0], top[1]) > kShapedRescale));
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
             const float a = ex2(y[k]), b = ex2(y[k + 1]);
             w[k >> 1] = pack_bf16(a, b);
             s[(k >> 1) & 1] = add2(s[(k >> 1) & 1], pack2(a, b));
         }
-        if (stop) {
-            tmem_landed(x);
-            return c0;
-        }
+        if (stop) return c0;
         sum[0] = add2(sum[0], s[0]);
         sum[1] = add2(sum[1], s[1]);
         tmem_st16(tS + (uint32_t)(c0 >> 1), w);
@@ -620,8 +579,9 @@ __device__ __forceinline__ void scale_pairs8(uint32_t addr, float a) {
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // What the softmax takes the scores as: they are scaled (kPlain: no options at all; kMasked: masks
-// alone), capped with a reference that stays (kCapped), or shaped in any way (kShaped).
-enum Mode { kPlain = 0, kMasked = 1, kCapped = 2, kShaped = 3 };
+// alone), capped with a reference that stays (kCapped; kCappedLong: of long items, see fast_tile), or
+// shaped in any way (kShaped).
+enum Mode { kPlain = 0, kMasked = 1, kCapped = 2, kCappedLong = 3, kShaped = 4 };
 
 template <int D, bool F32OUT, bool FOLD, int MODE>
 __global__ void __launch_bounds__(kAttThreads, 1)
@@ -629,7 +589,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                  const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const __grid_constant__ CUtensorMap tmO,
                  const Params<(MODE != kPlain)> p) {
-    constexpr bool EX = MODE != kPlain, shaped = MODE >= kCapped, fixed = MODE == kCapped;
+    constexpr bool EX = MODE != kPlain, shaped = MODE >= kCapped, fixed = MODE == kCapped || MODE == kCappedLong;
     // Biased scores grow towards the row's own position, so key tiles are taken from the last one
     // back: the reference is found in the first, instead of moving (and O being rescaled) in most.
     constexpr bool BACK = MODE == kShaped;
@@ -1514,8 +1474,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         moves = moves && valid;
                         none = none && top == -INFINITY;
                         if (!__any_sync(0xffffffffu, moves)) return 0.f;
-                        // (a whole power of two further: weights that are there already are scaled exactly)
-                        const float to = fixed ? fminf(fmaxf(sub + top, ref_low), ref_high) : sub + ceilf(top);
+                        const float to = fixed ? fminf(fmaxf(sub + top, ref_low), ref_high) : sub + top;
                         if constexpr (fixed) {
                             if (moves) m = to;
                         } else {
@@ -1621,10 +1580,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                             const float to_row = (float)(j * KT - (g.kfirst + ltok));
                             const bool both = MODE == kShaped && g.prefix > g.kfirst + 1 && (j + 1) * KT - 1 > g.kfirst;
                             if constexpr (fixed) {
-                                if (!part && !looks) cc = capped_tile(tS, p, pack2(-m, -m), sum);
+                                if (!part && !looks) cc = fast_tile<true, false, MODE == kCappedLong ? 4 : 1>(tS, p, -m, 0.f, valid, sum);
                             } else if (!part && !both && !__any_sync(0xffffffffu, valid && m == -INFINITY)) {
                                 const float row = fmaf(slope, to_row, valid ? -m : 0.f);
-                                cc = p.cap != 0.f ? biased_tile<true>(tS, p, row, slope, valid, sum) : biased_tile<false>(tS, p, row, slope, valid, sum);
+                                cc = p.cap != 0.f ? fast_tile<true, true, 1>(tS, p, row, slope, valid, sum)
+                                                  : fast_tile<false, true, 1>(tS, p, row, slope, valid, sum);
                             }
                             // the rest, in any case
 #pragma unroll 1
@@ -2035,6 +1995,11 @@ cudaError_t launch(const Params<(MODE != kPlain)>& p, const PackedMaps& m, int d
     if (d == 64) return f32_out ? launch_t<64, true, false, MODE>(p, m, grid, merge, st) : launch_t<64, false, false, MODE>(p, m, grid, merge, st);
     if (p.kv_fold) return f32_out ? launch_t<128, true, true, MODE>(p, m, grid, merge, st) : launch_t<128, false, true, MODE>(p, m, grid, merge, st);
     return f32_out ? launch_t<128, true, false, MODE>(p, m, grid, merge, st) : launch_t<128, false, false, MODE>(p, m, grid, merge, st);
+}
+// For d = 128 and bf16 outputs.
+template <int MODE>
+cudaError_t launch_128(const Params<(MODE != kPlain)>& p, const PackedMaps& m, int grid, bool merge, cudaStream_t st) {
+    return p.kv_fold ? launch_t<128, false, true, MODE>(p, m, grid, merge, st) : launch_t<128, false, false, MODE>(p, m, grid, merge, st);
 }
 
 }  // namespace
