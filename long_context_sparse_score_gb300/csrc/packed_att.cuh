@@ -567,6 +567,47 @@ __device__ __forceinline__ int fast_tile(uint32_t tS, const PackedParamsEx& p, f
     return 128;
 }
 
+// The same for tiles of 64 columns and weights of three bf16 parts, 16 columns at a time.
+template <bool CAP, bool BIAS>
+__device__ __forceinline__ int fast_parts(uint32_t tS, const uint32_t (&part_at)[3], const PackedParamsEx& p, float row, float slope, bool valid,
+                                          float& l) {
+    const uint64_t scale = pack2(p.scale, p.scale);
+#pragma unroll 1
+    for (int c0 = 0; c0 < 64; c0 += 16) {
+        uint32_t x[16], q[3][8];
+        float big = 0.f, top = -INFINITY;
+        const float r = BIAS ? fmaf(slope, (float)c0, row) : row;
+        const uint64_t row2 = pack2(r, r);
+        tmem_ld16(tS + (uint32_t)c0, x);
+        tmem_landed(x);
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+            float a = __uint_as_float(x[k]), b = __uint_as_float(x[k + 1]);
+            const uint64_t v = pack2(a, b);
+            if constexpr (CAP) {
+                big = fmaxf(fmaxf(big, fabsf(a)), fabsf(b));
+                unpack2(odd_poly<CapDegrees<true>::low>(v, p.poly[0], row2), a, b);
+            } else {
+                unpack2(fma2(v, scale, row2), a, b);
+            }
+            if constexpr (BIAS) {
+                a = fmaf(slope, (float)k, a);
+                b = fmaf(slope, (float)(k + 1), b);
+                top = fmaxf(fmaxf(top, a), b);
+            }
+            x[k] = __float_as_uint(a);
+            x[k + 1] = __float_as_uint(b);
+        }
+        const bool stop = (bool)__any_sync(0xffffffffu, (CAP && big > p.fit[0]) || (BIAS && valid && top > kShapedRescale));
+        const float more = parts16<16, true>(x, 0.f, 0.f, q);
+        if (stop) return c0;
+        l += more;
+#pragma unroll
+        for (int e = 0; e < 3; ++e) tmem_st8(tS + part_at[e] + (uint32_t)(c0 >> 1), q[e]);
+    }
+    return 64;
+}
+
 // a times the pairs of bf16 in 8 columns of tensor memory.
 __device__ __forceinline__ void scale_pairs8(uint32_t addr, float a) {
     uint32_t w[8];
@@ -1482,6 +1523,13 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         }
                         return moves ? sub - to : 0.f;
                     };
+                    // biased scores: whether the tile's keys all lie on one side of the rows, which have seen keys;
+                    // a row's bias at the tile's first column, less the reference
+                    auto fast_ok = [&](bool part) {
+                        return !part && !(g.prefix > g.kfirst + 1 && (j + 1) * KT - 1 > g.kfirst) &&
+                               !__any_sync(0xffffffffu, valid && m == -INFINITY);
+                    };
+                    auto fast_row = [&]() { return fmaf(slope, (float)(j * KT - (g.kfirst + ltok)), m == -INFINITY ? 0.f : -m); };
                     auto shift = [&](auto& x, float by) {
                         each_pair(x, [&](uint64_t v) { return add2(v, pack2(by, by)); });
                     };
@@ -1546,8 +1594,19 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                             if (__any_sync(0xffffffffu, grow)) grow_to(mx, grow);
                         }
                         float sub = m == -INFINITY ? 0.f : m * p.qscale;
+                        int cc = 0;
+                        if constexpr (shaped) {
+                            const uint32_t part_at[3] = {(uint32_t)C::part_col(0), (uint32_t)C::part_col(1), (uint32_t)C::part_col(2)};
+                            if constexpr (fixed) {
+                                if (!part && !looks) cc = fast_parts<true, false>(tS, part_at, p, -m, 0.f, valid, l);
+                            } else if (fast_ok(part)) {
+                                const float row = fast_row();
+                                cc = p.cap != 0.f ? fast_parts<true, true>(tS, part_at, p, row, slope, valid, l)
+                                                  : fast_parts<false, true>(tS, part_at, p, row, slope, valid, l);
+                            }
+                        }
 #pragma unroll 1
-                        for (int cc = 0; cc < 64; cc += 16) {
+                        for (; cc < 64; cc += 16) {
                             uint32_t x[16], q[3][8];
                             tmem_load(tS + (uint32_t)cc, x);
                             tmem_landed(x);
@@ -1577,12 +1636,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         uint32_t w[16];
                         if constexpr (shaped) {
                             int cc = 0;
-                            const float to_row = (float)(j * KT - (g.kfirst + ltok));
-                            const bool both = MODE == kShaped && g.prefix > g.kfirst + 1 && (j + 1) * KT - 1 > g.kfirst;
                             if constexpr (fixed) {
                                 if (!part && !looks) cc = fast_tile<true, false, MODE == kCappedLong ? 4 : 1>(tS, p, -m, 0.f, valid, sum);
-                            } else if (!part && !both && !__any_sync(0xffffffffu, valid && m == -INFINITY)) {
-                                const float row = fmaf(slope, to_row, valid ? -m : 0.f);
+                            } else if (fast_ok(part)) {
+                                const float row = fast_row();
                                 cc = p.cap != 0.f ? fast_tile<true, true, 1>(tS, p, row, slope, valid, sum)
                                                   : fast_tile<false, true, 1>(tS, p, row, slope, valid, sum);
                             }
