@@ -831,7 +831,8 @@ typedef struct {
 /*
  * hash_attn_prefill and hash_attn_chunk with score options (opts may be NULL: the calls without).
  * Workspace, layouts, limits and errors are the same, and HA_ERR_INVALID_ARG for options outside
- * their ranges. V must be finite for the keys that a token of the sequence sees, K and V may hold
+ * their ranges. V must be finite for the keys that a token of the sequence sees (with a softcap,
+ * below 2^20 in magnitude: weights are kept up to 2^80 until a row's end), K and V may hold
  * anything elsewhere. slopes with a bias that outweighs float32 (slope x distance above 2^24) leave
  * the nearest keys' weights exact and round the others'.
  */

@@ -262,6 +262,43 @@ def test_bias_that_leaves_only_far_keys(H):
         check_prefill(q, k, v, [n], opts, out, lse)
 
 
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("cap", [30.0, 50.0])
+def test_weights_over_the_whole_range_of_the_cap(H, cap, out_dtype):
+    """The first keys' scores saturate at -cap, the last ones' at +cap (or the other way round), with large values: from
+    the smallest weights to the largest, none is lost and no sum overflows."""
+    g = torch.Generator(device="cuda").manual_seed(35)
+    n, d = 400, 128
+    q, v = rand(g, n, 1, d).abs() + 1, rand(g, n, 1, d, scale=2.0 ** 17)
+    k = torch.full((n, 1, d), 500.0, device="cuda").bfloat16()
+    k[:200] = -500.0
+    for keys in (k, k.flip(0)):
+        out, lse = prefill(H, q, keys, v, [n], Opts(cap=cap), out_dtype)
+        qh, kh, vh = (x.double().cpu().numpy()[:, 0] for x in (q, keys, v))
+        ref = SO.attention(qh, kh, vh, cap=cap)
+        E = 2.0 ** -20 * cap + 2.0 ** -23 * (n + 16) + 2.0 ** -19  # (the cap is flat: the scores' own error does not matter)
+        check_rows(out[:, 0], lse[:, 0], (ref[0], ref[1], 2 * E * ref[4], np.full(n, E + 2.0 ** -22 * (1 + 3 * cap)), ref[4]), f"cap {cap}")
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("cap,scale", [(1e-3, None), (1e6, None), (2.0 ** 60, None), (2.0 ** -30, 2.0 ** -40), (2.0 ** 40, 2.0 ** -20), (3.0, 2.0 ** -30), (60.0, 1.0)])
+def test_caps_and_scales_of_any_size(H, cap, scale, out_dtype):
+    g = torch.Generator(device="cuda").manual_seed(36)
+    n, d = 200, 64
+    q, k, v = rand(g, n, 2, d), rand(g, n, 1, d), rand(g, n, 1, d)
+    opts = Opts(cap=cap, scale=scale)
+    out, lse = prefill(H, q, k, v, [n], opts, out_dtype)
+    qh, kh, vh = (x.double().cpu().numpy() for x in (q, k, v))
+    for h in range(2):
+        ref = SO.attention(qh[:, h], kh[:, 0], vh[:, 0], **opts.of(0, h))
+        if cap > 1e5:  # a score's share of the cap's error goes by the score, not by the cap: 2^-20 of its magnitude
+            plain = SO.attention(qh[:, h], kh[:, 0], vh[:, 0], scale=scale)
+            z = (np.abs(qh[:, h]) @ np.abs(kh[:, 0]).T).max(1) * (scale or d ** -0.5)
+            tol = plain[2] + 2.0 ** -19 * z[:, None] * plain[4]
+            ref = (ref[0], ref[1], tol, plain[3] + 2.0 ** -20 * z, ref[4])
+        check_rows(out[:, h], lse[:, h], ref, f"cap {cap} head {h}")
+
+
 # ---------------------------------------------------------------- chunks
 
 CHUNK = [
@@ -322,6 +359,24 @@ def test_bad_pages_that_are_seen_are_flagged(H):
         K2, V2 = torch.cat([K, torch.zeros_like(K[:1])]), torch.cat([V, torch.zeros_like(V[:1])])
         t[0, 4] = K.shape[0]
         check_chunk(q, K2, V2, t, [1], [100], opts, out, lse)
+
+
+def test_device_errors(H):
+    """Bad and stopped lengths count as empty of keys, bad bounds are skipped, whatever the options say."""
+    g = torch.Generator(device="cuda").manual_seed(49)
+    lens, d = [64, 64, 64], 64
+    K, V, table = pages(g, [1, 1, 1], lens, 16, 1, d, "token", Opts())
+    q = rand(g, 3, 2, d)
+    for o in (Opts(window=5, prefix=[64, 64, 64]), Opts(cap=50.0, first=[3, 60, 70]), Opts(cap=50.0, slopes=[0.1, 0.2], prefix=[9, 9, 9])):
+        out, lse = chunk(H, q, K, V, table, [1, 1, 1], [64, 65, -65], 1, o, status=(H.HA_ERR_DEVICE, H.HA_DEVERR_SEQLEN))
+        check_chunk(q[:1], K, V, table, [1], [64], o, out[:1], lse[:1])
+        assert torch.all(out[1:] == 0) and torch.all(torch.isneginf(lse[1:]))
+        tok, cache = H.make_tokens(q, None, None, 3, h_kv=1, out_dtype=torch.bfloat16), H.make_cache(K, V, table)
+        ws, out, lse = workspace(H, tok), torch.full_like(q, NAN), torch.full((3, 2), NAN, device="cuda")
+        H.hash_attn_chunk_ex(tok, cache, o.made(H), q, K, V, table, ints([0, 1, 9, 3]), ints(lens), out, lse, workspace=ws)
+        assert H.hash_attn_device_status(ws) == (H.HA_ERR_DEVICE, H.HA_DEVERR_SEQLEN)
+        check_chunk(q[:1], K, V, table, [1], [64], o, out[:1], lse[:1])
+        assert torch.isnan(out[1:]).all()
 
 
 def test_documents_of_one_sequence(H):
@@ -507,3 +562,57 @@ def test_serving_run(H):
             a += m
         assert torch.isnan(out[T:]).all()
     assert lens.tolist() == [51, 36, 3] and n_free.item() == n_pages - 4 - 3 - 1
+
+
+def test_a_captured_serving_step(H):
+    """Plan, append and attention captured once: replays with other lengths, one of which ends a sequence and one of which
+    runs out of pages (that sequence is stopped: out = 0, lse = -inf, and it goes on when its length is written again)."""
+    g = torch.Generator(device="cuda").manual_seed(52)
+    n, Hq, Hkv, d, ps, n_pages, room = 3, 8, 2, 128, 16, 6, 40
+    pool = [torch.zeros(n_pages, ps, Hkv, d, dtype=torch.bfloat16, device="cuda").permute(0, 2, 1, 3) for _ in range(2)]
+    table, free, n_free = torch.full((n, 4), -1, dtype=torch.int32, device="cuda"), torch.arange(n_pages, device="cuda").int(), ints([n_pages])
+    lens, cu, new, flags = ints([0] * n), ints([0] * (n + 1)), ints([1] * n), ints([0])
+    q, k, v = rand(g, room, Hq, d), rand(g, room, Hkv, d), rand(g, room, Hkv, d)
+    q_out, out, lse = torch.zeros_like(q), torch.full((room, Hq, d), NAN, device="cuda"), torch.full((room, Hq), NAN, device="cuda")
+    pos, slots = torch.zeros(2, room, dtype=torch.int32, device="cuda"), torch.zeros(room, dtype=torch.int32, device="cuda")
+    paging, rope = H.make_paging(table, n_pages, ps, room), H.rope_axes(torch.ones(8, device="cuda"), [0, 1] * 4)
+    tok, cache = H.make_tokens(q, k, v, n, out_dtype=torch.float32), H.make_cache(*pool, table)
+    ws, opts = workspace(H, tok), H.score_opts(softcap=30.0, window=20)
+
+    def step():
+        H.hash_attn_plan_pages(paging, new, lens, lens, cu, table, free, n_free, n_free, slots=slots, dev_flags=flags)
+        H.hash_attn_append_axes(tok, cache, q, k, v, table, cu, lens, pos, q_out, *pool, rope=rope)
+        H.hash_attn_chunk_ex(tok, cache, opts, q_out, *pool, table, cu, lens, out, lse, workspace=ws)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    history = [np.zeros((0, Hkv, d))] * n
+    keys = [np.zeros((0, Hkv, d))] * n
+    for i, (ms, want) in enumerate([([20, 1, 10], [20, 1, 10]), ([1, 16, 1], [21, 17, 11]), ([1, 1, 30], [22, 18, -12]), ([1, -1, 0], [23, 0, -12]),
+                                    ([1, 0, 30], [24, 0, 41])]):
+        if i == 4:
+            lens[2] = 11  # the host lets it go on
+        new.copy_(ints(ms))
+        flags.zero_()
+        out.fill_(NAN)
+        graph.replay()
+        assert lens.tolist() == want, i
+        assert flags.item() == (H.HA_DEVERR_PAGES if i == 2 else 0), i
+        st = H.hash_attn_device_status(ws)
+        assert st == ((H.HA_ERR_DEVICE, H.HA_DEVERR_SEQLEN) if i in (2, 3) else (0, 0)), i
+        a = 0
+        for s, m in enumerate(ms):
+            if m < 0:
+                history[s] = keys[s] = np.zeros((0, Hkv, d))
+                continue
+            if want[s] < 0:
+                assert torch.all(out[a:a + m] == 0) and torch.all(torch.isneginf(lse[a:a + m])) and torch.all(slots[a:a + m] == -1)
+            elif m:
+                keys[s] = np.concatenate([keys[s], k[a:a + m].double().cpu().numpy()])   # (positions are 0: nothing turns)
+                history[s] = np.concatenate([history[s], v[a:a + m].double().cpu().numpy()])
+                for h in (0, 5):
+                    ref = SO.attention(q[a:a + m, h].double().cpu().numpy(), keys[s][:, h // 4], history[s][:, h // 4], cap=30.0, window=20)
+                    check_rows(out[a:a + m, h], lse[a:a + m, h], ref, f"step {i} seq {s} head {h}")
+            a += max(m, 0)
+        assert torch.isnan(out[a:]).all()
