@@ -1578,10 +1578,13 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const ha_score
     const bool f32 = t->out_dtype == HA_F32;
     const int kt = packed_key_tile(f32);
     const int max_len = c != nullptr ? c->max_pages * c->page_size : t->total;
-    const int64_t tiles = ceil_div(max_len, kt);
+    // key tiles of an item, at most (a window's last tokens see it and what the item's tokens add)
+    int64_t tiles = ceil_div(max_len, kt);
+    if (opts != nullptr && opts->window > 0 && opts->prefix == nullptr)
+        tiles = std::min(tiles, ceil_div((int64_t)opts->window + 2 * L.tq, kt) + 1);
     const int64_t items = (ceil_div(t->total, 2 * L.tq) + t->n_seq) * t->h_kv;
     // the kernel counts the work in 32 bits (a prompt's items see half of its tiles on average)
-    const bool half = c == nullptr && (opts == nullptr || opts->prefix == nullptr);
+    const bool half = c == nullptr && (opts == nullptr || (opts->prefix == nullptr && opts->window == 0));
     const int64_t work = items * ((half ? tiles / 2 : tiles) + 8);
     if (work >= (int64_t)1 << 32)
         return fail(HA_ERR_UNSUPPORTED, "too much for one call: up to %lld items of up to %lld key tiles (2^32 tiles in all)",

@@ -1,5 +1,5 @@
-// Causal attention of packed queries: whole prompts (K and V packed like the
-// queries) and chunks of new tokens over a paged cache.
+// Attention of packed queries: whole prompts (K and V packed like the queries) and
+// chunks of new tokens over a paged cache; causal, or with score options (below).
 //
 // Row (token i of sequence s, query head h) with g = h / G attends to the keys
 // j < L(i) = nk - nq + i + 1 of its sequence (nq new tokens, nk keys in all):
@@ -41,6 +41,26 @@
 // warps' latency, not by a unit); decode of 64 sequences of 1,000 to 16,000 keys: 345 us,
 // 6.4 TB/s, 95 %; one token over 131,072 keys, float32 out: 108 us, 5.0 TB/s, 73 % (bound by
 // the products: three for P V); 4 x 512 tokens over 20,000 to 32,000 keys: 574 us, 84 %.
+//
+// Score options (ha_score_opts) are kernels of their own (Mode), so that calls without them run the code
+// that they ran before. With pos the row's position, z_j becomes cap tanh(scale <q, K_j> / cap) - slope
+// |pos - j|, over max(first, pos - window + 1) <= j < max(pos + 1, prefix).
+// - Masks leave a row one interval of keys whose ends grow with the row, so an item has one range of
+//   key tiles, and their sum over a row of items a closed form (MaskedItems): tiles outside it are neither
+//   read nor multiplied. 16,384 tokens in a window of 1,024: 262 us (all of them: 1,393).
+// - A cap is a polynomial (shape_scores): five multiply-adds a column more, which is what bounds it
+//   (tensor cores 48 % busy at 4,096 tokens): 16,384 tokens capped at 50: 1.57 ms, 1.40 PFLOP/s, 74 % of
+//   cuBLAS's burst. Capped scores lie in a known range, so a row keeps the reference that its first keys
+//   give (no maximum, no rescaling).
+// - A bias grows towards the row's own position: key tiles are taken from the last one back, so that the
+//   reference is found in the first. 24 prompts of 33 to 2,500 tokens: 386 us, 48 %.
+// - The code of a tile decides as much as its operations: the instruction cache is shared by eight softmax
+//   warps that are never at the same place. So there is one short path for tiles that all rows see (fast_tile,
+//   fast_parts) and one for all others, in a loop of 32 columns. Masks in the fast path, or a first pass for an
+//   item's first reference, cost more than they saved (64 prompts of 300 tokens capped: 153 -> 217 us and
+//   153 -> 170).
+// 64 decodes in a window of 4,096 keys, capped, pages of 16: 175 us, 5.5 TB/s, 81 % (without options over
+// as many keys 180).
 //
 // 12 warps: two softmax warpgroups (thread = row: a tcgen05.ld gives a thread
 // its whole row of S, no shuffles), one warp that issues the MMAs, one that loads K

@@ -734,13 +734,14 @@ def hash_attn_append_axes(tokens, cache, q, k, v, page_table, cu, seq_lens, posi
     """hash_attn_append with rotations by several axes: ``rope`` from ``rope_axes``, ``positions``
     int32 [n_axes, total] (rows contiguous; more axes than the rope has are not read)."""
     _append_checked(tokens, cache, q, k, v, page_table, cu, seq_lens, q_out, K, V, W, k_sig, dev_flags)
-    pos_st = tokens.total
+    pos_st = T = tokens.total
     if positions.__class__ is not int:
-        axes, rows = positions.shape
-        pos_st = positions.stride(0)
-        if (axes < rope.n_axes or rows != tokens.total or positions.dtype is not _types()[2][0] or (positions.stride(1) != 1 and rows > 1)
-                or (pos_st < rows and axes > 1)):
-            raise ValueError(f"positions must be int32 [{rope.n_axes}, {tokens.total}] with contiguous rows")
+        i32, n = _types()[2][0], rope.n_axes
+        if not (positions.shape == (n, T) and positions.is_contiguous() and positions.dtype is i32):
+            axes, rows = positions.shape
+            pos_st = positions.stride(0)
+            if (axes < n or rows != T or positions.dtype is not i32 or (positions.stride(1) != 1 and rows > 1) or (pos_st < rows and axes > 1)):
+                raise ValueError(f"positions must be int32 [{n}, {T}] with contiguous rows")
     device = _device()
     a = _here(device, q, k, v, W, page_table, cu, seq_lens, q_out, K, V, k_sig, dev_flags, positions)
     if rope.tensor is not None and rope.tensor.get_device() != device:
