@@ -403,7 +403,7 @@ def hash_attn_workspace_size(shape: HAShape, m_max: int, n_sink: int, n_local: i
 
 
 def hash_attn_workspace_init(workspace, stream=None) -> None:
-    _check(lib().hash_attn_workspace_init(_ptr(workspace), workspace.numel() * workspace.element_size(),
+    _check(lib().hash_attn_workspace_init(_ptr(workspace), workspace.nbytes,
                                           _stream(stream)))
 
 
@@ -793,7 +793,8 @@ def hash_attn_packed_workspace_size(tokens) -> int:
     return out.value
 
 
-def _prefill_checked(tokens, q, K, V, cu, out, lse) -> None:
+def hash_attn_prefill(tokens, q, K, V, cu, out, lse, *, workspace, stream=None, _opts=None) -> None:
+    """Causal attention over packed prompts; out [total, Hq, d], lse [total, Hq] contiguous."""
     f32, types, ints = _types()
     n, T, h_q, h_kv, d, dtype, out_dtype, _, q_st, q_sh, k_st, k_sh, v_st, v_sh = _fields_of_tokens(tokens)
     dtype, out_dtype, rows = types[dtype], types[out_dtype], (T, h_kv, d)
@@ -811,18 +812,20 @@ def _prefill_checked(tokens, q, K, V, cu, out, lse) -> None:
         _int32s((cu, n + 1, "cu"))
         _as_made((q, (T, h_q, d), (q_st, q_sh, 1), dtype, "q"), (K, rows, (k_st, k_sh, 1), dtype, "K"),
                  (V, rows, (v_st, v_sh, 1), dtype, "V"))
-
-
-def hash_attn_prefill(tokens, q, K, V, cu, out, lse, *, workspace, stream=None) -> None:
-    """Causal attention over packed prompts; out [total, Hq, d], lse [total, Hq] contiguous."""
-    _prefill_checked(tokens, q, K, V, cu, out, lse)
     device = _device()
+    if _opts is not None:
+        _opts_checked(_opts, tokens, device)
     a = _here(device, q, K, V, cu, out, lse, workspace)
-    _check(lib().hash_attn_prefill(tokens, *a, workspace.numel() * workspace.element_size(),
+    if _opts is not None:
+        _check(lib().hash_attn_prefill_ex(tokens, _opts, *a, workspace.nbytes,
+                                          _raw_stream(device) if stream is None else _stream(stream)))
+        return
+    _check(lib().hash_attn_prefill(tokens, *a, workspace.nbytes,
                                    _raw_stream(device) if stream is None else _stream(stream)))
 
 
-def _chunk_checked(tokens, cache, q, K, V, page_table, cu, seq_lens, out, lse) -> None:
+def hash_attn_chunk(tokens, cache, q, K, V, page_table, cu, seq_lens, out, lse, *, workspace, stream=None, _opts=None) -> None:
+    """Attention of the packed new tokens over the paged cache (their keys are in it already)."""
     f32, types, ints = _types()
     n, T, h_q, h_kv, d, dtype, out_dtype, _, q_st, q_sh, _, _, _, _ = _fields_of_tokens(tokens)
     pool, n_pages, size, pages, table_st, K_sp, K_sh, K_sn, V_sp, V_sh, V_sn, _, _ = _fields_of_cache(cache)
@@ -844,14 +847,15 @@ def _chunk_checked(tokens, cache, q, K, V, page_table, cu, seq_lens, out, lse) -
         _as_made((q, (T, h_q, d), (q_st, q_sh, 1), dtype, "q"), (K, cached, (K_sp, K_sh, K_sn, 1), pool, "K"),
                  (V, cached, (V_sp, V_sh, V_sn, 1), pool, "V"))
         _table_as_made(page_table, n, pages, table_st)
-
-
-def hash_attn_chunk(tokens, cache, q, K, V, page_table, cu, seq_lens, out, lse, *, workspace, stream=None) -> None:
-    """Attention of the packed new tokens over the paged cache (their keys are in it already)."""
-    _chunk_checked(tokens, cache, q, K, V, page_table, cu, seq_lens, out, lse)
     device = _device()
+    if _opts is not None:
+        _opts_checked(_opts, tokens, device)
     a = _here(device, q, K, V, page_table, cu, seq_lens, out, lse, workspace)
-    _check(lib().hash_attn_chunk(tokens, cache, *a, workspace.numel() * workspace.element_size(),
+    if _opts is not None:
+        _check(lib().hash_attn_chunk_ex(tokens, cache, _opts, *a, workspace.nbytes,
+                                        _raw_stream(device) if stream is None else _stream(stream)))
+        return
+    _check(lib().hash_attn_chunk(tokens, cache, *a, workspace.nbytes,
                                  _raw_stream(device) if stream is None else _stream(stream)))
 
 
@@ -869,6 +873,8 @@ def score_opts(*, scale: float = 0.0, softcap: float = 0.0, window: int = 0, slo
 
 
 def _opts_checked(opts, tokens, device) -> None:
+    if opts.tensors is None:
+        return
     slopes, prefix, first = opts.tensors
     _whole((slopes, tokens.h_q, _types()[0], "slopes"))
     _int32s((prefix, tokens.n_seq, "prefix"), (first, tokens.n_seq, "first"))
@@ -877,24 +883,12 @@ def _opts_checked(opts, tokens, device) -> None:
 
 def hash_attn_prefill_ex(tokens, opts, q, K, V, cu, out, lse, *, workspace, stream=None) -> None:
     """hash_attn_prefill with score options (``score_opts``; None: without)."""
-    _prefill_checked(tokens, q, K, V, cu, out, lse)
-    device = _device()
-    if opts is not None and opts.tensors is not None:
-        _opts_checked(opts, tokens, device)
-    a = _here(device, q, K, V, cu, out, lse, workspace)
-    _check(lib().hash_attn_prefill_ex(tokens, opts, *a, workspace.numel() * workspace.element_size(),
-                                      _raw_stream(device) if stream is None else _stream(stream)))
+    hash_attn_prefill(tokens, q, K, V, cu, out, lse, workspace=workspace, stream=stream, _opts=opts)
 
 
 def hash_attn_chunk_ex(tokens, cache, opts, q, K, V, page_table, cu, seq_lens, out, lse, *, workspace, stream=None) -> None:
     """hash_attn_chunk with score options (``score_opts``; None: without)."""
-    _chunk_checked(tokens, cache, q, K, V, page_table, cu, seq_lens, out, lse)
-    device = _device()
-    if opts is not None and opts.tensors is not None:
-        _opts_checked(opts, tokens, device)
-    a = _here(device, q, K, V, page_table, cu, seq_lens, out, lse, workspace)
-    _check(lib().hash_attn_chunk_ex(tokens, cache, opts, *a, workspace.numel() * workspace.element_size(),
-                                    _raw_stream(device) if stream is None else _stream(stream)))
+    hash_attn_chunk(tokens, cache, q, K, V, page_table, cu, seq_lens, out, lse, workspace=workspace, stream=stream, _opts=opts)
 
 
 def hash_attn_device_status(workspace, stream=None) -> tuple[int, int]:
