@@ -386,6 +386,8 @@ struct PagesParams {
     uint32_t* flags;
     int64_t table_st;
     int n_seq, total, n_pages, page_size, max_pages;
+    int unit;                  // rows that a warp writes at a time
+    Quotient per_page, per_unit;
 };
 
 struct MergeNParams {

@@ -8,11 +8,13 @@
 // free[n_free + fb_s ..), page j of s is free[top - 1 - (tb_s + j - p0)] with top = n_free + all pages
 // given back. So nothing waits for another sequence, and the result does not depend on timing.
 //
-// Bound by latency: a launch, the lengths, a scan, the pages, the table. 64 sequences of one token 2.9 us
-// (one CTA), 6 prompts of 39,000 tokens 6.3, 3,000 sequences of which 10 % add 85,000 tokens and 5 %
-// end 16.6 (6.5 where all decode); the bytes would take 0.1. One cluster of up to 8 CTAs and no workspace:
-// up to 1,024 sequences every CTA scans all of them, one to a thread, and they share the rows; more
-// are cut among the CTAs, which tell each other their sums through distributed shared memory.
+// Bound by latency: a launch, the lengths, a scan, the pages, the table. 64 sequences of one token 2.8 us
+// (one CTA), 6 prompts of 39,000 tokens 5.1 to 5.6, 3,000 sequences of which 10 % add 85,000 tokens and 5 %
+// end 13.5 (4.9 where all decode); the bytes would take 0.1. One CTA for up to 1,024 sequences with few rows,
+// else one cluster of 8, and no workspace: up to kShared sequences every CTA scans all of them, one to a
+// thread, and they share the rows; more are cut among the CTAs, which write their sums into each
+// other's shared memory (1,000 sequences, 10 % prompts, 5 % ending: 13.3 us scanned by all, 10.4 cut; read
+// from there behind the barrier the sums took 1.4 us).
 #include <cooperative_groups.h>
 
 #include "ha_internal.cuh"
@@ -23,7 +25,8 @@ namespace ha {
 namespace {
 
 constexpr int kMostThreads = 1024, kCluster = 8;
-constexpr int kUnit = 256;    // rows that a warp writes at a time
+constexpr int kUnit = 256;    // least rows that a warp writes at a time (PagesParams::unit)
+constexpr int kShared = 128;  // sequences that all CTAs of a cluster look at
 constexpr int kDirect = 8;    // rows of a sequence that its own thread writes
 // A sum of rows that stays here is more than any buffer holds.
 constexpr uint32_t kManyRows = 1u << 26;
@@ -64,17 +67,18 @@ __global__ void __launch_bounds__(kMostThreads) k_plan_pages(const PagesParams p
     __shared__ PagesRecord s_rec[kMostThreads];
     __shared__ Ended s_ended[kMostThreads];
     __shared__ uint32_t s_back[kMostThreads];  // by thread: pages its ended sequence gives back
-    __shared__ Sums s_warp[32], s_sums;
+    __shared__ Sums s_warp[32], s_all[kCluster];  // s_all: the CTAs' sums, which each writes into all
     __shared__ int s_n_ended;
     const cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    // this CTA's sequences: all (then the rows are shared), or a part
+    const bool all = C == 1 || p.n_seq <= kShared;
     if (tid == 0) s_n_ended = 0;
+    if (!all) cluster.barrier_arrive();  // a CTA's shared memory may be written once it runs
     pdl_wait();
     pdl_launch_dependents();
 
-    // this CTA's sequences: all (then the rows are shared), or a part
-    const bool all = p.n_seq <= (int)blockDim.x;
     const int per = all ? p.n_seq : (p.n_seq + C - 1) / C;
     const int s_begin = all ? 0 : min(p.n_seq, rank * per), s_end = min(p.n_seq, s_begin + per);
     const int n_tiles = max(1, (s_end - s_begin + (int)blockDim.x - 1) / (int)blockDim.x);
@@ -88,6 +92,10 @@ __global__ void __launch_bounds__(kMostThreads) k_plan_pages(const PagesParams p
         int s, had, nq, p0, state;
         uint32_t takes, back;
     } x;
+    auto pages_of = [&](int tokens) {
+        const int n = p.per_page(tokens);
+        return n + (n * p.page_size < tokens ? 1 : 0);
+    };
     auto page_ok = [&](int page) { return page >= 0 && page < p.n_pages; };
     // Entries of an ended sequence, 8 a lane at a time; put(place, page) for each that is a page. Returns their number.
     auto walk = [&](const Ended& e, auto&& put) {
@@ -119,8 +127,7 @@ __global__ void __launch_bounds__(kMostThreads) k_plan_pages(const PagesParams p
         if (s < s_end) {
             x.had = p.seq_lens[s];
             const int fresh = p.new_lens[s];
-            const int tokens = min(x.had < 0 ? ~x.had : x.had, max_len);
-            x.p0 = tokens / p.page_size + (tokens % p.page_size != 0 ? 1 : 0);
+            x.p0 = pages_of(min(x.had < 0 ? ~x.had : x.had, max_len));
             x.nq = max(fresh, 0);
             if (fresh < 0) {
                 x.state = 2;
@@ -129,8 +136,7 @@ __global__ void __launch_bounds__(kMostThreads) k_plan_pages(const PagesParams p
                 if (x.had >= 0 || x.nq > 0) flags |= HA_DEVERR_SEQLEN;
             } else {
                 x.state = 1;
-                const int t = x.had + x.nq;
-                x.takes = (uint32_t)(t / p.page_size + (t % p.page_size != 0 ? 1 : 0) - x.p0);
+                x.takes = (uint32_t)(pages_of(x.had + x.nq) - x.p0);
             }
         }
         if (!__syncthreads_or(x.state == 2 && x.p0 > 0)) return;
@@ -149,7 +155,7 @@ __global__ void __launch_bounds__(kMostThreads) k_plan_pages(const PagesParams p
         listed = at;
     };
     auto sums_of = [&]() {
-        return Sums{(uint32_t)min(x.nq, (int)kManyRows), x.takes, x.back, x.nq > kDirect ? (uint32_t)(x.nq - 1) / kUnit + 1u : 0u};
+        return Sums{(uint32_t)min(x.nq, (int)kManyRows), x.takes, x.back, x.nq > kDirect ? (uint32_t)p.per_unit(x.nq - 1) + 1u : 0u};
     };
     // Exclusive sums over the CTA's threads; total: all of them.
     auto scan = [&](Sums& total) {
@@ -180,7 +186,8 @@ __global__ void __launch_bounds__(kMostThreads) k_plan_pages(const PagesParams p
         mine_before = scan(t);
         mine.add(t);
     }
-    if (tid == 0) s_sums = mine;
+    if (!all) cluster.barrier_wait();
+    if (!all && tid < C) *cluster.map_shared_rank(&s_all[rank], tid) = mine;
     if (C > 1) cluster.sync();  // every input has been read, too: outputs may lie where inputs did
     else __syncthreads();
     if (n_free < 0 || n_free > p.n_pages) {
@@ -189,7 +196,7 @@ __global__ void __launch_bounds__(kMostThreads) k_plan_pages(const PagesParams p
     }
     Sums before{0u, 0u, 0u, 0u}, total = mine;
     if (!all) {
-        const Sums v = lane < C ? *cluster.map_shared_rank(&s_sums, lane) : Sums{0u, 0u, 0u, 0u};
+        const Sums v = lane < C ? s_all[lane] : Sums{0u, 0u, 0u, 0u};
         const Sums incl = scan_warp(v, lane);
         total = from_lane(incl, 31);
         if (rank > 0) before = from_lane(incl, rank - 1);
@@ -232,8 +239,7 @@ __global__ void __launch_bounds__(kMostThreads) k_plan_pages(const PagesParams p
             at.add(t);
         }
     }
-    // what was given back is there; nobody reads another CTA's sums any more
-    if (C > 1 && (total.back != 0 || !all)) cluster.sync();
+    if (C > 1 && total.back != 0) cluster.sync();  // before a page that was given back is taken
     else __syncthreads();
 
     // ---- lengths, bounds, tables, slots
@@ -269,7 +275,7 @@ __global__ void __launch_bounds__(kMostThreads) k_plan_pages(const PagesParams p
             // few rows: by their sequence's thread
             if (x.nq > 0 && x.nq <= kDirect) {
                 int32_t* row = p.table + (int64_t)x.s * p.table_st;
-                int pg = x.had / p.page_size, r = x.had - pg * p.page_size, page = -1;
+                int pg = p.per_page(max(x.had, 0)), r = x.had - pg * p.page_size, page = -1;
                 if (goes && r != 0) page = row[pg];
                 for (int i = 0; i < x.nq; ++i) {
                     if (goes && r == 0) row[pg] = page = pop(tb + (uint32_t)(pg - x.p0));
@@ -279,29 +285,27 @@ __global__ void __launch_bounds__(kMostThreads) k_plan_pages(const PagesParams p
             }
         }
         __syncthreads();
-        // many: by the warps, kUnit rows at a time (32 rows on are so many pages and rows on: the one
+        // many: by the warps, p.unit rows at a time (32 rows on are so many pages and rows on: the one
         // division of a row would be most of what it costs)
-        const int step_pages = 32 / p.page_size, step_rows = 32 - step_pages * p.page_size;
+        const int step_pages = p.per_page(32), step_rows = 32 - step_pages * p.page_size;
         const uint32_t n_units = over ? 0u : t.units;
         for (uint32_t u = (uint32_t)(all ? warp * C + rank : warp); u < n_units; u += (uint32_t)(all ? warps * C : warps)) {
-            int lo = 0, hi = (int)blockDim.x - 1;  // the last record that begins at or before u: it has units
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if ((uint32_t)s_rec[mid].unit0 <= u) lo = mid;
-                else hi = mid - 1;
-            }
+            // the last record that begins at or before u (it has units): of 32 groups of records, then of the group's
+            int lo = 32 * lane < (int)blockDim.x && (uint32_t)s_rec[32 * lane].unit0 <= u ? 1 : 0;
+            lo = 32 * (31 - __clz((int)__ballot_sync(0xffffffffu, lo != 0)));
+            lo += 31 - __clz((int)__ballot_sync(0xffffffffu, (uint32_t)s_rec[lo + lane].unit0 <= u));
             const PagesRecord rec = s_rec[lo];
-            const int i0 = (int)(u - (uint32_t)rec.unit0) * kUnit, i1 = min(i0 + kUnit, rec.nq);
+            const int i0 = (int)(u - (uint32_t)rec.unit0) * p.unit, i1 = min(i0 + p.unit, rec.nq);
             if (rec.had < 0) {
                 if (p.slots != nullptr)
                     for (int i = i0 + lane; i < i1; i += 32) p.slots[rec.row0 + i] = -1;
                 continue;
             }
             int32_t* row = p.table + (int64_t)(s_begin + tile * (int)blockDim.x + lo) * p.table_st;
-            const int p0 = (rec.had + p.page_size - 1) / p.page_size, b0 = rec.had + i0, b1 = rec.had + i1;
+            const int p0 = pages_of(rec.had), b0 = rec.had + i0, b1 = rec.had + i1;
             // 32 of the unit's pages at a time, one to a lane, and the rows in them
-            const int pg1 = (b1 - 1) / p.page_size;
-            for (int pg0 = b0 / p.page_size; pg0 <= pg1; pg0 += 32) {
+            const int pg1 = p.per_page(b1 - 1);
+            for (int pg0 = p.per_page(b0); pg0 <= pg1; pg0 += 32) {
                 const int pg = pg0 + lane;
                 int page = -1;
                 if (pg <= pg1) {
@@ -311,7 +315,7 @@ __global__ void __launch_bounds__(kMostThreads) k_plan_pages(const PagesParams p
                 if (p.slots == nullptr) continue;
                 const int r0 = max(b0, pg0 * p.page_size);
                 const int r1 = (int)min((int64_t)b1, ((int64_t)pg0 + 32) * p.page_size);
-                int e = (r0 + lane) / p.page_size, off = r0 + lane - e * p.page_size;  // of this lane's row
+                int e = p.per_page(r0 + lane), off = r0 + lane - e * p.page_size;  // of this lane's row
 #pragma unroll 4
                 for (int q0 = r0; q0 < r1; q0 += 32) {
                     const int of = __shfl_sync(0xffffffffu, page, min(e - pg0, 31)), pos = q0 + lane;
@@ -338,7 +342,13 @@ __global__ void __launch_bounds__(kMostThreads) k_plan_pages(const PagesParams p
 
 }  // namespace
 
-cudaError_t launch_plan_pages(const PagesParams& p, cudaStream_t st) {
+cudaError_t launch_plan_pages(const PagesParams& p0, cudaStream_t st) {
+    PagesParams p = p0;
+    p.per_page = Quotient::of((uint32_t)p.page_size);
+    // What a warp does once for its rows (the search, the pages) costs as much as 200 rows, so with many rows it
+    // takes more of them (3,000 mixed sequences 16.6 -> 13.5 us, with pages found by a product instead of a division).
+    p.unit = p.total / 128 > kUnit ? p.total / 128 : kUnit;
+    p.per_unit = Quotient::of((uint32_t)p.unit);
     // One CTA as long as its threads have a sequence and a few rows each, else a cluster.
     const bool one = p.n_seq <= kMostThreads && p.total <= 4096;
     int threads = kMostThreads;

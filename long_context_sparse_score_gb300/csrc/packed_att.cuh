@@ -539,10 +539,11 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[32]) { tm
 //
 // 32 columns at a time in a loop: what bounds short prompts is the instruction cache, which the item's
 // first and last tiles share with this code. UNROLL 4 lets the exponentials of 32 columns run under the
-// multiplications of the next (in a kernel of its own: beside the loop it is no faster). Capped scores, loop / unrolled: 24 prompts of 1,000 tokens 267 / 288 us, 8 of
-// 2,048 286 / 282, 4 of 4,096 493 / 481, one of 16,384 1,730 / 1,657; at d 64 the loop is the faster at any
-// length (223 / 245, 235 / 245, 403 / 410, 1,384 / 1,383), and for biased ones at d 128 up to 4,096 tokens
-// (24 of 1,000: 260 / 292, 4 of 4,096: 477 / 477).
+// multiplications of the next (in a kernel of its own: beside the loop it is no faster). Capped scores,
+// loop / unrolled: 24 prompts of 1,000 tokens 267 / 288 us, 8 of 2,048 286 / 282, 4 of 4,096 493 / 481, one of
+// 16,384 1,730 / 1,657; at d 64 the loop is the faster at any length (223 / 245, 235 / 245, 403 / 410,
+// 1,384 / 1,383), and for biased ones at d 128 up to 4,096 tokens (24 of 1,000: 260 / 292, 4 of 4,096:
+// 477 / 477).
 template <bool CAP, bool BIAS, int UNROLL>
 __device__ __forceinline__ int fast_tile(uint32_t tS, const PackedParamsEx& p, float row, float slope, bool valid, uint64_t (&sum)[2]) {
     const uint64_t scale = pack2(p.scale, p.scale);

@@ -95,6 +95,9 @@ PLANS = {
     "short": ([1, 5, 1, 1], [4, 0, 8, 1], 4, 2), "short-long": ([10, 600, 300, 1, 9, 400], [0] * 6, 16, 30),
     "none-free": ([1, 1, 0], [16, 5, 16], 16, 0), "long-prompts": ([5000, 1, 2049], [0, 700, 31], 48, 300),
     "stopped": ([1, 0, -1, 700], [-6, -33, -18, -1], 16, 4),
+    # a cluster's CTAs that look at all sequences, and at a part of them each
+    "shared": ([40, -1, 33, 1] * 32, [0, 50, 7, 16] * 32, 16, 400), "parted": ([40, -1, 33, 1] * 32 + [900], [0, 50, 7, 16] * 32 + [3], 16, 460),
+    "parted-short": ([40, -1, 33, 1] * 64, [0, 50, 7, 16] * 64, 16, 20),
 }
 
 
