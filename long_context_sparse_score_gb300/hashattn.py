@@ -323,6 +323,7 @@ def _types() -> tuple:
 # 1 us less of a call's 8 (the rest of the checks' 2 is torch's own, for shapes, strides and types).
 _fields_of_tokens = struct.Struct("8i6q").unpack_from
 _fields_of_cache = struct.Struct("4i9q").unpack_from
+_fields_of_paging = struct.Struct("6iq").unpack_from
 
 
 def _whole(*specs) -> None:
@@ -765,23 +766,24 @@ def hash_attn_plan_pages(paging, new_lens, seq_lens, seq_lens_out, cu, page_tabl
                          dev_flags=None, stream=None) -> None:
     """Plan a step's pages: ``seq_lens_out`` and ``n_free_out`` may be ``seq_lens`` and ``n_free``; the table
     and the stack of free pages are updated in place (a plan changes neither if run again)."""
-    ints, n, pages = _types()[2], paging.n_seq, paging.max_pages
+    ints = _types()[2]
+    n, total, n_pages, _, pages, _, table_st = _fields_of_paging(paging)
     try:
         good = (new_lens.numel() == n and new_lens.dtype in ints and new_lens.is_contiguous()
                 and seq_lens.numel() == n and seq_lens.dtype in ints and seq_lens.is_contiguous()
                 and seq_lens_out.numel() == n and seq_lens_out.dtype in ints and seq_lens_out.is_contiguous()
                 and cu.numel() == n + 1 and cu.dtype in ints and cu.is_contiguous()
-                and page_table.shape == (n, pages) and page_table.stride() == (paging.table_st, 1) and page_table.dtype in ints
-                and free_pages.numel() == paging.n_pages and free_pages.dtype in ints and free_pages.is_contiguous()
+                and page_table.shape == (n, pages) and page_table.stride() == (table_st, 1) and page_table.dtype in ints
+                and free_pages.numel() == n_pages and free_pages.dtype in ints and free_pages.is_contiguous()
                 and n_free.numel() == 1 and n_free.dtype in ints and n_free_out.numel() == 1 and n_free_out.dtype in ints
-                and slots.numel() == paging.total and slots.dtype in ints and slots.is_contiguous() and dev_flags is None)
+                and slots.numel() == total and slots.dtype in ints and slots.is_contiguous() and dev_flags is None)
     except AttributeError:
         good = False
     if not good:
         _int32s((new_lens, n, "new_lens"), (seq_lens, n, "seq_lens"), (seq_lens_out, n, "seq_lens_out"), (cu, n + 1, "cu"),
-                (free_pages, paging.n_pages, "free_pages"), (n_free, 1, "n_free"), (n_free_out, 1, "n_free_out"),
-                (slots, paging.total, "slots"), (dev_flags, 1, "dev_flags"))
-        _table_as_made(page_table, n, pages, paging.table_st)
+                (free_pages, n_pages, "free_pages"), (n_free, 1, "n_free"), (n_free_out, 1, "n_free_out"),
+                (slots, total, "slots"), (dev_flags, 1, "dev_flags"))
+        _table_as_made(page_table, n, pages, table_st)
     device = _device()
     a = _here(device, new_lens, seq_lens, seq_lens_out, cu, page_table, slots, free_pages, n_free, n_free_out, dev_flags)
     _check(lib().hash_attn_plan_pages(paging, *a, _raw_stream(device) if stream is None else _stream(stream)))
