@@ -56,9 +56,9 @@
 //   reference is found in the first. 24 prompts of 33 to 2,500 tokens: 386 us, 48 %.
 // - The code of a tile decides as much as its operations: the instruction cache is shared by eight softmax
 //   warps that are never at the same place. So there is one short path for tiles that all rows see (fast_tile,
-//   fast_parts) and one for all others, in a loop of 32 columns. Masks in the fast path, or a first pass for an
-//   item's first reference, cost more than they saved (64 prompts of 300 tokens capped: 153 -> 217 us and
-//   153 -> 170).
+//   fast_parts) and one for all others, in a loop of 32 columns. Masks in the fast path cost more than they
+//   saved (64 prompts of 300 tokens capped: 153 -> 217 us), and so did shaping an item's first tile twice for its
+//   reference (153 -> 170; a pass over its raw products instead, see begin_fixed: 148 -> 146).
 // 64 decodes in a window of 4,096 keys, capped, pages of 16: 175 us, 5.5 TB/s, 81 % (without options over
 // as many keys 180).
 //
@@ -478,6 +478,13 @@ __device__ __forceinline__ uint64_t odd_poly(uint64_t v, const float (&c)[7], ui
     return fma2(v, y, plus);
 }
 
+// cap tanh(x scale / cap) log2(e), off by 2^-22 cap at most.
+__device__ __forceinline__ float cap_of(float x, const PackedParamsEx& p) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(x * p.twice)));
+    return fmaf(-2.f * p.cap, r, p.cap);
+}
+
 // Degrees of the polynomials for tanh(u) / u (PackedParamsEx::fit and poly).
 template <bool F32OUT>
 struct CapDegrees {
@@ -507,12 +514,7 @@ __device__ __forceinline__ void shape_scores(uint32_t (&x)[N], const PackedParam
             each_pair(x, [&](uint64_t v) { return odd_poly<Deg::high>(mul2(v, unit), p.poly[1], row2); });
         } else {
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const float t = ex2(__uint_as_float(x[k]) * p.twice);
-                float r;
-                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + t));
-                x[k] = __float_as_uint(fmaf(-2.f * p.cap, r, p.cap) + row);
-            }
+            for (int k = 0; k < N; ++k) x[k] = __float_as_uint(cap_of(__uint_as_float(x[k]), p) + row);
         }
     } else {
         const uint64_t s2 = pack2(p.scale, p.scale);
@@ -1544,6 +1546,24 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         }
                         return moves ? sub - to : 0.f;
                     };
+                    // A constant reference where rows see their first keys: the cap of their largest product of
+                    // this tile. (Weights are rounded to bf16, and a row's largest is exact where it is 1.) A pass
+                    // over the products before the tile takes the short path: 24 prompts of 1,000 tokens 268 -> 257 us;
+                    // in the kernel for long items it costs the others' code its place (16,384 tokens 1,574 -> 1,640).
+                    auto begin_fixed = [&](auto& x) {
+                        constexpr int W = sizeof(x) / 4;
+                        float top = -INFINITY;
+#pragma unroll 1
+                        for (int cc = 0; cc < KT; cc += W) {
+                            tmem_load(tS + (uint32_t)cc, x);
+                            tmem_landed(x);
+                            if (part) mask(x, lim, j, cc);
+                            top = max_of(x, top);
+                        }
+                        if constexpr (fixed) {
+                            if (valid && none && top != -INFINITY) m = fminf(fmaxf(cap_of(top, p), ref_low), ref_high);
+                        }
+                    };
                     // biased scores: whether the tile's keys all lie on one side of the rows, which have seen keys;
                     // a row's bias at the tile's first column, less the reference
                     auto fast_ok = [&](bool part) {
@@ -1619,7 +1639,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         if constexpr (shaped) {
                             const uint32_t part_at[3] = {(uint32_t)C::part_col(0), (uint32_t)C::part_col(1), (uint32_t)C::part_col(2)};
                             if constexpr (fixed) {
-                                if (!part && !looks) cc = fast_parts<true, false>(tS, part_at, p, -m, 0.f, valid, l);
+                                if (looks) {
+                                    uint32_t x[16];
+                                    begin_fixed(x);
+                                }
+                                if (!part) cc = fast_parts<true, false>(tS, part_at, p, -m, 0.f, valid, l);
                             } else if (fast_ok(part)) {
                                 const float row = fast_row();
                                 cc = p.cap != 0.f ? fast_parts<true, true>(tS, part_at, p, row, slope, valid, l)
@@ -1634,7 +1658,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                             if constexpr (shaped) {
                                 shape(x, j, cc, m == -INFINITY ? 0.f : m);
                                 if (part) mask(x, lim, j, cc);
-                                if (looks) {
+                                if constexpr (!fixed) {
                                     const float by = settle(max_of(x, -INFINITY), [&](float a) {
                                         tmem_wait_st();
 #pragma unroll 1
@@ -1657,8 +1681,14 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         uint32_t w[16];
                         if constexpr (shaped) {
                             int cc = 0;
-                            if constexpr (fixed) {
-                                if (!part && !looks) cc = fast_tile<true, false, MODE == kCappedLong ? 4 : 1>(tS, p, -m, 0.f, valid, sum);
+                            if constexpr (MODE == kCapped) {
+                                if (looks) {
+                                    uint32_t x[32];
+                                    begin_fixed(x);
+                                }
+                                if (!part) cc = fast_tile<true, false, 1>(tS, p, -m, 0.f, valid, sum);
+                            } else if constexpr (MODE == kCappedLong) {
+                                if (!part && !looks) cc = fast_tile<true, false, 4>(tS, p, -m, 0.f, valid, sum);
                             } else if (fast_ok(part)) {
                                 const float row = fast_row();
                                 cc = p.cap != 0.f ? fast_tile<true, true, 1>(tS, p, row, slope, valid, sum)
@@ -1672,7 +1702,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                                 tmem_landed(x);
                                 shape(x, j, cc, m == -INFINITY ? 0.f : m);
                                 if (part) mask(x, lim, j, cc);
-                                if (looks) {
+                                if (MODE != kCapped && looks) {
                                     const float by = settle(max_of(x, -INFINITY), [&](float a) {
                                         sum[0] = mul2(sum[0], pack2(a, a));
                                         sum[1] = mul2(sum[1], pack2(a, a));
