@@ -631,7 +631,12 @@ __device__ __forceinline__ int fast_parts(uint32_t tS, const uint32_t (&part_at)
     return 64;
 }
 
-// a times the pairs of bf16 in 8 columns of tensor memory.
+// 2^x of the whole number nearest to x <= 0; 0 below what normal numbers reach.
+__device__ __forceinline__ float whole_power(float x) {
+    return x < -126.f ? 0.f : __int_as_float((127 + __float2int_rn(x)) << 23);
+}
+
+// a times the pairs of bf16 in 8 columns of tensor memory (a power of 2: exact).
 __device__ __forceinline__ void scale_pairs8(uint32_t addr, float a) {
     uint32_t w[8];
     tmem_ld8(addr, w);
@@ -1498,7 +1503,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     // this tile came behind the products of the tiles before, so O holds those.
                     auto grow_to = [&](float mx, bool grow) {
                         if (NB == 3 && i > 0) wait_o(product(t, i - 1));
-                        const float a = grow ? ex2((m - mx) * p.qscale) : 1.f;  // 0 from -inf
+                        const float a = !grow ? 1.f : shaped ? whole_power(m - mx) : ex2((m - mx) * p.qscale);  // 0 from -inf
                         l *= a;
                         if (grow) m = mx;
                         if constexpr (F32OUT) {
@@ -1529,7 +1534,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     };
                     // Shaped scores come less the reference as it is. It moves where their maximum `top` (less it
                     // as well) asks for that; a constant one is set where a row sees its first keys.
-                    // Returns by how much, with what is to be scaled meanwhile done by scale(a).
+                    // Returns by how much, with what is to be scaled meanwhile done by scale(a). It moves by a
+                    // whole number, so a is a power of 2: the tile's weights are in bf16 parts by then, and would be
+                    // rounded again (three parts to those of one). Those of float32 results are whole
+                    // from the start, where the move is exact; of bf16 weights the largest is 1, which is.
                     const bool looks = !fixed || (bool)__any_sync(0xffffffffu, valid && l == 0.f && lim > 0 && first_key() < (j + 1) * KT);
                     bool none = l == 0.f;
                     auto settle = [&](float top, auto&& scale) {
@@ -1538,7 +1546,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         moves = moves && valid;
                         none = none && top == -INFINITY;
                         if (!__any_sync(0xffffffffu, moves)) return 0.f;
-                        const float to = fixed ? fminf(fmaxf(sub + top, ref_low), ref_high) : sub + top;
+                        const float to = fixed ? fminf(fmaxf(sub + top, ref_low), ref_high)
+                                               : sub + (F32OUT || m != -INFINITY ? ceilf(top) : top);
                         if constexpr (fixed) {
                             if (moves) m = to;
                         } else {

@@ -263,6 +263,25 @@ def test_bias_that_leaves_only_far_keys(H):
 
 
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("at", [16, 32, 48, 64, 96])
+def test_a_reference_that_moves_within_a_tile(H, at, d, out_dtype):
+    """Scores 0 to the first 16 (32, 64) keys, then about 2^39.8 times their weight at key at - 1 and 2^40.6
+    times at key `at`, with values of 1 and -1: the reference moves between the two, and the first one's
+    weight keeps its precision."""
+    g = torch.Generator(device="cuda").manual_seed(at)
+    n, Hq = 160, 4
+    q, k = torch.zeros(n, Hq, d, device="cuda"), torch.zeros(n, 1, d, device="cuda")
+    q[..., 0], q[..., 1] = 1.0, torch.rand(n, Hq, generator=g, device="cuda")
+    k[at - 1, 0, :2], k[at, 0, :2] = torch.tensor([27.5, 0.1]), torch.tensor([28.0, 0.2])
+    q, k, v = q.bfloat16(), k.bfloat16(), rand(g, n, 1, d)
+    v[at - 1], v[at] = 1.0, -1.0
+    opts = Opts(scale=1.0, slopes=[0.0] * Hq)
+    out, lse = prefill(H, q, k, v, [n], opts, out_dtype)
+    check_prefill(q, k, v, [n], opts, out, lse, f"at {at}")
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("cap", [30.0, 50.0])
 def test_weights_over_the_whole_range_of_the_cap(H, cap, out_dtype):
     """The first keys' scores saturate at -cap, the last ones' at +cap (or the other way round), with large values: from
