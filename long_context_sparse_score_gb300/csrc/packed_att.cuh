@@ -445,7 +445,28 @@ __device__ __forceinline__ void mask_before(uint32_t (&x)[N], int lo) {
         if (k < lo) x[k] = 0xff800000u;
 }
 
-// Largest magnitude (NaN apart).
+// The bits of the columns lo <= k < hi, of 32.
+__device__ __forceinline__ uint32_t column_bits(int lo, int hi) {
+    const uint32_t below = hi >= 32 ? ~0u : (hi <= 0 ? 0u : (1u << hi) - 1u);
+    return lo <= 0 ? below : (lo >= 32 ? 0u : below & (~0u << lo));
+}
+// -inf in the columns that are not seen.
+template <int N>
+__device__ __forceinline__ void mask_bits(uint32_t (&x)[N], uint32_t seen) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if ((seen >> k & 1u) == 0u) x[k] = 0xff800000u;
+}
+
+// Largest magnitude (NaN apart), and that of the columns that are seen.
+template <int N>
+__device__ __forceinline__ float magnitude(const uint32_t (&x)[N], uint32_t seen) {
+    float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if ((seen >> k & 1u) != 0u) m[k & 3] = fmaxf(m[k & 3], fabsf(__uint_as_float(x[k])));
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
 template <int N>
 __device__ __forceinline__ float magnitude(const uint32_t (&x)[N]) {
     float m[4] = {0.f, 0.f, 0.f, 0.f};
@@ -499,14 +520,17 @@ struct CapDegrees {
 // instruction takes as long as two), so tanh u is u P(u^2) with no more terms than the warp's
 // largest |u| asks for, and no exponential or reciprocal: P is fitted in relative error, to
 // 5.4e-7 at most (bf16 weights: they are rounded to 4e-3) or 5.0e-8 (float32 results: half a
-// rounding). Beyond |u| = 1 it is 1 - 2 / (1 + e^{2 u}), off by 2^-22 cap at most.
+// rounding). Beyond |u| = 1 it is 1 - 2 / (1 + e^{2 u}), off by 2^-22 cap at most. The choice shows in
+// a result's last bits, so the largest product is that of tokens' rows, over the keys that they see
+// (`mine`: this row's, 0 of a row of no token): whatever else lies in a tile of queries or keys has no part in it.
 template <bool F32OUT, bool BIAS, int N>
-__device__ __forceinline__ void shape_scores(uint32_t (&x)[N], const PackedParamsEx& p, float slope, float from, bool both_sides, float sub) {
+__device__ __forceinline__ void shape_scores(uint32_t (&x)[N], const PackedParamsEx& p, float slope, float from, bool both_sides, float mine,
+                                             float sub) {
     using Deg = CapDegrees<F32OUT>;
     const float row = BIAS && !both_sides ? fmaf(slope, from, -sub) : -sub;
     const uint64_t row2 = pack2(row, row);
     if (!BIAS || p.cap != 0.f) {
-        const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(magnitude(x))));
+        const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mine)));
         if (top <= p.fit[0]) {
             each_pair(x, [&](uint64_t v) { return odd_poly<Deg::low>(v, p.poly[0], row2); });
         } else if (top <= p.fit[1]) {
@@ -536,8 +560,10 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[32]) { tm
 
 // The weights of a tile of 128 columns of shaped scores, all seen, keys on one side of the rows: score k
 // of the tile, less the reference, is x scale (CAP: the polynomial) + row, and with BIAS + slope k.
-// Returns the columns done: those before the first 32 where a product of any of the warp's rows is too
-// large for the polynomial, or (BIAS) a score more than kShapedRescale above the reference.
+// Returns the columns done: those before the first 32 where a product of any of the warp's valid rows is too
+// large for the polynomial, or (BIAS) a score more than kShapedRescale above the reference. (All rows vote
+// and those of no token are left out of the outcome: 24 biased prompts 361 us, with that as a condition of each
+// row's vote 384.)
 //
 // 32 columns at a time in a loop: what bounds short prompts is the instruction cache, which the item's
 // first and last tiles share with this code. UNROLL 4 lets the exponentials of 32 columns run under the
@@ -549,6 +575,7 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[32]) { tm
 template <bool CAP, bool BIAS, int UNROLL>
 __device__ __forceinline__ int fast_tile(uint32_t tS, const PackedParamsEx& p, float row, float slope, bool valid, uint64_t (&sum)[2]) {
     const uint64_t scale = pack2(p.scale, p.scale);
+    const uint32_t tokens = __ballot_sync(0xffffffffu, valid);
 #pragma unroll UNROLL
     for (int c0 = 0; c0 < 128; c0 += 32) {
         uint32_t x[32], w[16];
@@ -574,8 +601,8 @@ __device__ __forceinline__ int fast_tile(uint32_t tS, const PackedParamsEx& p, f
                 top[u] = fmaxf(fmaxf(top[u], y[k]), y[k + 1]);
             }
         }
-        const bool stop = (bool)__any_sync(0xffffffffu, (CAP && fmaxf(big[0], big[1]) > p.fit[0]) ||
-                                                            (BIAS && valid && fmaxf(top[0], top[1]) > kShapedRescale));
+        const bool stop = (__ballot_sync(0xffffffffu, (CAP && fmaxf(big[0], big[1]) > p.fit[0]) ||
+                                                          (BIAS && fmaxf(top[0], top[1]) > kShapedRescale)) & tokens) != 0u;
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
             const float a = ex2(y[k]), b = ex2(y[k + 1]);
@@ -595,6 +622,7 @@ template <bool CAP, bool BIAS>
 __device__ __forceinline__ int fast_parts(uint32_t tS, const uint32_t (&part_at)[3], const PackedParamsEx& p, float row, float slope, bool valid,
                                           float& l) {
     const uint64_t scale = pack2(p.scale, p.scale);
+    const uint32_t tokens = __ballot_sync(0xffffffffu, valid);
 #pragma unroll 1
     for (int c0 = 0; c0 < 64; c0 += 16) {
         uint32_t x[16], q[3][8];
@@ -621,7 +649,7 @@ __device__ __forceinline__ int fast_parts(uint32_t tS, const uint32_t (&part_at)
             x[k] = __float_as_uint(a);
             x[k + 1] = __float_as_uint(b);
         }
-        const bool stop = (bool)__any_sync(0xffffffffu, (CAP && big > p.fit[0]) || (BIAS && valid && top > kShapedRescale));
+        const bool stop = (__ballot_sync(0xffffffffu, (CAP && big > p.fit[0]) || (BIAS && top > kShapedRescale)) & tokens) != 0u;
         const float more = parts16<16, true>(x, 0.f, 0.f, q);
         if (stop) return c0;
         l += more;
@@ -1411,17 +1439,26 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             if constexpr (MODE == kShaped) {
                 if (valid && p.slopes != nullptr) slope = p.slopes[g.head * p.G + hd] * 1.4426950408889634f;
             }
-            // shaped scores less sub of columns col, col + 1, .. of key tile j, and masks
-            auto shape = [&](auto& x, int j, int col, float sub) {
-                if constexpr (shaped) {
-                    const int from = j * KT + col - (g.kfirst + ltok);
-                    shape_scores<F32OUT, MODE == kShaped>(x, p, slope, (float)from, g.prefix > g.kfirst + 1 && (j + 1) * KT - 1 > g.kfirst, sub);
-                }
+            // which of the columns col, col + 1, .. (32 at most) of key tile j the row sees
+            auto seen_of = [&](int lim, int j, int col) {
+                return column_bits(klast > j * KT ? first_key() - j * KT - col : 0, lim - col);
             };
             auto mask = [&](auto& x, int lim, int j, int col) {
-                mask_columns(x, lim - col);
+                if constexpr (shaped) mask_bits(x, seen_of(lim, j, col));
+                else mask_columns(x, lim - col);
+            };
+            // shaped scores less sub of columns col, col + 1, .. of key tile j; `part`: some row of the warp does not
+            // see all of the tile
+            auto shape = [&](auto& x, int lim, int j, int col, bool part, float sub) {
                 if constexpr (shaped) {
-                    if (klast > j * KT) mask_before(x, first_key() - j * KT - col);
+                    const int from = j * KT + col - (g.kfirst + ltok);
+                    uint32_t seen = ~0u;
+                    float mine = 0.f;
+                    if (part) seen = seen_of(lim, j, col);
+                    if (!BACK || p.cap != 0.f) mine = part ? magnitude(x, seen) : magnitude(x);
+                    mine = valid ? mine : 0.f;
+                    shape_scores<F32OUT, BACK>(x, p, slope, (float)from, g.prefix > g.kfirst + 1 && (j + 1) * KT - 1 > g.kfirst, mine, sub);
+                    if (part) mask_bits(x, seen);
                 }
             };
             const bool any = __any_sync(0xffffffffu, valid);
@@ -1591,8 +1628,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         tmem_load(tS + (uint32_t)(w * Q), x);
                         tmem_landed(x);
                         if constexpr (shaped) {
-                            shape(x, j, w * Q, m == -INFINITY ? 0.f : m);
-                            if (part) mask(x, lim, j, w * Q);
+                            shape(x, lim, j, w * Q, part, m == -INFINITY ? 0.f : m);
                             if (looks) {
                                 const float by = settle(max_of(x, -INFINITY), [](float) {});
                                 if (__any_sync(0xffffffffu, by != 0.f)) shift(x, by);
@@ -1665,8 +1701,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                             tmem_load(tS + (uint32_t)cc, x);
                             tmem_landed(x);
                             if constexpr (shaped) {
-                                shape(x, j, cc, m == -INFINITY ? 0.f : m);
-                                if (part) mask(x, lim, j, cc);
+                                shape(x, lim, j, cc, part, m == -INFINITY ? 0.f : m);
                                 if constexpr (!fixed) {
                                     const float by = settle(max_of(x, -INFINITY), [&](float a) {
                                         tmem_wait_st();
@@ -1709,8 +1744,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                                 uint32_t x[32];
                                 tmem_ld32(tS + (uint32_t)cc, x);
                                 tmem_landed(x);
-                                shape(x, j, cc, m == -INFINITY ? 0.f : m);
-                                if (part) mask(x, lim, j, cc);
+                                shape(x, lim, j, cc, part, m == -INFINITY ? 0.f : m);
                                 if (MODE != kCapped && looks) {
                                     const float by = settle(max_of(x, -INFINITY), [&](float a) {
                                         sum[0] = mul2(sum[0], pack2(a, a));
