@@ -1529,13 +1529,16 @@ void set_opts(PackedParamsEx& p, const ha_score_opts* o, int d, bool f32) {
         p.cap = (float)(cap * log2e);
         p.unit = (float)(scale / cap);
         p.twice = (float)(2.0 * log2e * scale / cap);
-        // A polynomial of x itself saves a product; its terms (up to x^9) have to be normal numbers.
-        const bool plain = scale / cap >= std::ldexp(1.0, f32 ? -12 : -15) && scale / cap <= std::ldexp(1.0, 12);
-        for (int i = 0; i < 2; ++i) {
-            p.fit[i] = plain || i == 1 ? (float)(kCapTo[i] * cap / scale) : -1.f;
-            for (int k = 0; k < 7; ++k)
-                p.poly[i][k] = (float)((f32 ? kTanh32 : kTanh16)[i][k] * cap * log2e * (i == 0 ? std::pow(scale / cap, 2 * k + 1) : 1.0));
-        }
+        // A polynomial of x itself saves a product; its terms (up to x^9) and its coefficients, which grow with the
+        // cap, too, have to be normal numbers.
+        bool plain = scale / cap >= std::ldexp(1.0, f32 ? -12 : -15) && scale / cap <= std::ldexp(1.0, 12);
+        for (int i = 0; i < 2; ++i)
+            for (int k = 0; k < 7; ++k) {
+                const double c = (f32 ? kTanh32 : kTanh16)[i][k];
+                p.poly[i][k] = (float)(c * cap * log2e * (i == 0 ? std::pow(scale / cap, 2 * k + 1) : 1.0));
+                if (i == 0 && c != 0.0) plain = plain && std::isnormal(p.poly[i][k]);
+            }
+        for (int i = 0; i < 2; ++i) p.fit[i] = plain || i == 1 ? (float)(kCapTo[i] * cap / scale) : -1.f;
         // Weights up to 2^80 (sums of 2^24 of them, times V, stay in range) and down to what keeps a
         // float's (or, of three bf16 parts, the last one's) full precision.
         p.ref_low = p.cap - 80.f;
