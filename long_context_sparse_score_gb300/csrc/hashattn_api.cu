@@ -1539,11 +1539,10 @@ void set_opts(PackedParamsEx& p, const ha_score_opts* o, int d, bool f32) {
                 if (i == 0 && c != 0.0) plain = plain && std::isnormal(p.poly[i][k]);
             }
         for (int i = 0; i < 2; ++i) p.fit[i] = plain || i == 1 ? (float)(kCapTo[i] * cap / scale) : -1.f;
-        // Weights up to 2^80 (sums of 2^24 of them, times V, stay in range) and down to what keeps a
-        // float's (or, of three bf16 parts, the last one's) full precision.
-        p.ref_low = p.cap - 80.f;
-        p.ref_high = (f32 ? 100.f : 122.f) - p.cap;
-        p.fixed_ref = o->slopes == nullptr && p.ref_low <= p.ref_high;
+        const CapRange range = CapRange::of(cap * log2e);
+        p.ref_low = (float)range.low;
+        p.ref_high = (float)range.high;
+        p.fixed_ref = o->slopes == nullptr && range.fits();
     }
 }
 

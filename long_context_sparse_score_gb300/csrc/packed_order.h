@@ -96,6 +96,18 @@ struct MaskedItems {
     }
 };
 
+// The references that rows of capped scores may keep (scores within +-cap, in powers of 2). With a reference
+// r in [low, high] a weight 2^{score - r} is at most 2^kUp: 2^24 of them times values below 2^20 stay below
+// 2^124; and at least 2^-kDown, whose products with values are the smallest numbers that the
+// accumulators hold, multiples of 2^-149: a value from 2^-40 on keeps 24 bits beside it, three parts of a
+// weight included.
+struct CapRange {
+    static constexpr int kUp = 80, kDown = 85;
+    double low, high;
+    HA_HD static CapRange of(double cap) { return CapRange{cap - kUp, kDown - cap}; }
+    HA_HD bool fits() const { return low <= high; }
+};
+
 // The order of the products of a segment whose S and P have three places (head dim 64): which stream
 // and key tile product k belongs to, for the warp that issues them and the warps that wait for them.
 // One row tile: the key tiles in turn, even ones stream 0's. Two: key tile by key tile, row

@@ -36,3 +36,44 @@ def test_large_and_small_caps_beside_their_scales(H, cap, scale, out_dtype):  # 
             z = (np.abs(qh[:, h]) @ np.abs(kh[:, 0]).T).max(1) * scale
             tol, tol_lse = plain[2] + 2.0 ** -19 * z[:, None] * plain[4], plain[3] + 2.0 ** -20 * z
         S.check_rows(out[:, h], lse[:, h], (want, wl, tol, tol_lse, mag), f"head {h}")
+
+
+@TYPES
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("cap", [30.0, 50.0, 57.0, 60.0, 62.0, 66.0, 70.0, 100.0])
+def test_small_values_beside_a_saturated_cap(H, cap, sign, out_dtype):  # noqa: F811
+    """All of a row's scores saturate at -cap (or +cap), so all weights are equal: values of 2^-40 to 2^0 in turn along
+    the dims keep their precision.
+
+    out is a mean: weights, equal but for 2^-20 cap + 2^-22 (score and exponential, relative), and sums of n
+    terms of 2^-23 each; a bf16 result as in check_rows."""
+    g = torch.Generator(device="cuda").manual_seed(72)
+    n, d = 300, 128
+    q, k = S.rand(g, n, 1, d).abs() + 1, torch.full((n, 1, d), sign * 500.0, device="cuda").bfloat16()
+    v = (torch.rand(n, 1, d, generator=g, device="cuda") + 1) * 2.0 ** -(torch.arange(d, device="cuda") % 41).float()
+    v = (v * torch.where(torch.rand(n, 1, d, generator=g, device="cuda") < 0.3, -1.0, 1.0)).bfloat16()
+    out, lse, _, _, vh = attend(H, q, k, v, S.Opts(cap=cap), out_dtype)
+    count = np.arange(1, n + 1)[:, None]
+    want, mag = np.cumsum(vh[:, 0], 0) / count, np.cumsum(np.abs(vh[:, 0]), 0) / count
+    E = 2.0 ** -20 * cap + 2.0 ** -23 * (n + 16) + 2.0 ** -22
+    wl = sign * cap + np.log(count[:, 0])
+    S.check_rows(out[:, 0], lse[:, 0], (want, wl, 2 * E * mag, np.full(n, E + 2.0 ** -22 * (1 + 3 * cap)), mag), f"cap {cap}")
+    if out_dtype == torch.float32:  # the weights' common error cancels in the mean
+        off = np.abs(out[:, 0].double().cpu().numpy() - want) / mag
+        assert off.max() <= 2.0 ** -23 * (n + 16), off.max()
+
+
+@TYPES
+@pytest.mark.parametrize("cap", [57.0, 60.0, 62.0, 66.0, 70.0, 200.0])
+def test_weights_over_the_whole_range_of_larger_caps(H, cap, out_dtype):  # noqa: F811
+    """Scores from -cap to +cap in either order, with values up to 2^19."""
+    g = torch.Generator(device="cuda").manual_seed(73)
+    n, d = 400, 128
+    q, v = S.rand(g, n, 1, d).abs() + 1, (torch.rand(n, 1, d, generator=g, device="cuda") * 2.0 ** 19).bfloat16()
+    k = torch.full((n, 1, d), 500.0, device="cuda").bfloat16()
+    k[:200] = -500.0
+    for keys in (k, k.flip(0)):
+        out, lse, qh, kh, vh = attend(H, q, keys, v, S.Opts(cap=cap), out_dtype)
+        want, wl, _, _, mag = SO.attention(qh[:, 0], kh[:, 0], vh[:, 0], cap=cap)
+        E = 2.0 ** -20 * cap + 2.0 ** -23 * (n + 16) + 2.0 ** -19
+        S.check_rows(out[:, 0], lse[:, 0], (want, wl, 2 * E * mag, np.full(n, E + 2.0 ** -22 * (1 + 3 * cap)), mag), f"cap {cap}")
