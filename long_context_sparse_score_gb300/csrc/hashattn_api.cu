@@ -1539,7 +1539,7 @@ void set_opts(PackedParamsEx& p, const ha_score_opts* o, int d, bool f32) {
                 if (i == 0 && c != 0.0) plain = plain && std::isnormal(p.poly[i][k]);
             }
         for (int i = 0; i < 2; ++i) p.fit[i] = plain || i == 1 ? (float)(kCapTo[i] * cap / scale) : -1.f;
-        const CapRange range = CapRange::of(cap * log2e);
+        const CapRange range = CapRange::of(cap * log2e, p.max_len);
         p.ref_low = (float)range.low;
         p.ref_high = (float)range.high;
         p.fixed_ref = o->slopes == nullptr && range.fits();

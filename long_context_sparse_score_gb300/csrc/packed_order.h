@@ -96,15 +96,20 @@ struct MaskedItems {
     }
 };
 
-// The references that rows of capped scores may keep (scores within +-cap, in powers of 2). With a reference
-// r in [low, high] a weight 2^{score - r} is at most 2^kUp: 2^24 of them times values below 2^20 stay below
-// 2^124; and at least 2^-kDown, whose products with values are the smallest numbers that the
-// accumulators hold, multiples of 2^-149: a value from 2^-40 on keeps 24 bits beside it, three parts of a
-// weight included.
+// The references that rows of capped scores over up to `keys` keys may keep (scores within +-cap, in powers of 2). With
+// a reference r in [low, high] a weight 2^{score - r} is at most 2^(cap - low): as many of them as there are
+// keys times values below 2^20 stay below 2^125 (2^24 keys: 2^124). And it is at least 2^-kDown, whose
+// products with values are sums of the smallest numbers that the accumulators hold, multiples of 2^-149: a
+// value from 2^-40 on keeps 24 bits beside it, three parts of a weight included.
 struct CapRange {
-    static constexpr int kUp = 80, kDown = 85;
+    static constexpr int kUp = 80, kAll = 105, kDown = 85;
     double low, high;
-    HA_HD static CapRange of(double cap) { return CapRange{cap - kUp, kDown - cap}; }
+    HA_HD static CapRange of(double cap, int keys) {
+        int log2 = 0;  // of the keys, rounded up
+        while (((int64_t)1 << log2) < keys) ++log2;
+        const int up = kAll - log2 < kUp ? kAll - log2 : kUp;
+        return CapRange{cap - up, kDown - cap};
+    }
     HA_HD bool fits() const { return low <= high; }
 };
 
