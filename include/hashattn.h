@@ -831,9 +831,10 @@ typedef struct {
 /*
  * hash_attn_prefill and hash_attn_chunk with score options (opts may be NULL: the calls without).
  * Workspace, layouts, limits and errors are the same, and HA_ERR_INVALID_ARG for options outside
- * their ranges. V must be finite for the keys that a token of the sequence sees (with a softcap,
- * below 2^20 in magnitude: weights are kept up to 2^80 until a row's end), K and V may hold
- * anything elsewhere. slopes with a bias that outweighs float32 (slope x distance above 2^24) leave
+ * their ranges. V must be finite for the keys that a token of the sequence sees; with a softcap below
+ * 2^20 in magnitude, with slopes below 2^56 (until a row's end weights are kept up to 2^80, and 2^40).
+ * With a softcap, what V holds below 2^-40 in magnitude may lose precision. K and V may hold anything
+ * elsewhere, and change no bit of the results. slopes with a bias that outweighs float32 (slope x distance above 2^24) leave
  * the nearest keys' weights exact and round the others'.
  */
 ha_status hash_attn_prefill_ex(const ha_tokens* tokens, const ha_score_opts* opts, const void* q, const void* K,

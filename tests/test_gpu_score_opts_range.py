@@ -77,3 +77,20 @@ def test_weights_over_the_whole_range_of_larger_caps(H, cap, out_dtype):  # noqa
         want, wl, _, _, mag = SO.attention(qh[:, 0], kh[:, 0], vh[:, 0], cap=cap)
         E = 2.0 ** -20 * cap + 2.0 ** -23 * (n + 16) + 2.0 ** -19
         S.check_rows(out[:, 0], lse[:, 0], (want, wl, 2 * E * mag, np.full(n, E + 2.0 ** -22 * (1 + 3 * cap)), mag), f"cap {cap}")
+
+
+@TYPES
+@pytest.mark.parametrize("slope", [0.0, 0.01])
+def test_large_values_under_a_bias(H, slope, out_dtype):  # noqa: F811
+    """Values up to 2^56 (what slopes without a cap allow); the last keys give the reference, and all others weigh almost
+    2^40 times as much, which does not move it."""
+    g = torch.Generator(device="cuda").manual_seed(74)
+    n, Hq, d = 700, 2, 64
+    q, k = torch.zeros(n, Hq, d, device="cuda"), torch.zeros(n, 1, d, device="cuda")
+    q[..., 0] = 1.0
+    k[:300, 0, 0] = 27.5
+    v = (torch.rand(n, 1, d, generator=g, device="cuda") * 2.0 ** 56).bfloat16()
+    out, lse, qh, kh, vh = attend(H, q.bfloat16(), k.bfloat16(), v, S.Opts(scale=1.0, slopes=[slope, -slope / 4]), out_dtype)
+    for h, s in enumerate([slope, -slope / 4]):
+        ref = SO.attention(qh[:, h], kh[:, 0], vh[:, 0], scale=1.0, slope=float(np.float32(s)))
+        S.check_rows(out[:, h], lse[:, h], ref, f"head {h}")
