@@ -1,10 +1,13 @@
-"""The references of capped scores (csrc/packed_order.h), on the host: sums of weights stay within float32."""
+"""The references of capped scores and the fits of the tanh (csrc/packed_order.h, csrc/hashattn_api.cu), on the host:
+that sums of weights stay within float32, and that the polynomials are as close as their comments say."""
 import ctypes
 import math
 import os
+import re
 import shutil
 import subprocess
 
+import numpy as np
 import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "long_context_sparse_score_gb300", "csrc")
@@ -50,3 +53,23 @@ def test_sums_of_weights_stay_within_float32(cap_range, keys):
             assert -cap - high - 40 - 24 >= -149 - 1e-9
     assert fitting > 75  # caps of 50 e-folds (72 powers of 2) among them
     assert cap_range(50 / math.log(2), keys)[2]
+
+
+def coefficients(name):
+    text = open(os.path.join(CSRC, "hashattn_api.cu")).read()
+    body = re.search(name + r"\[2\]\[7\] = \{(.*?)\n\};", text, re.S).group(1)
+    rows = re.findall(r"\{([^}]*)\},  // degree (\d+) up to ([\d.]+): ([\d.e-]+)", body)
+    assert len(rows) == 2
+    return [([float(c) for c in row.split(",")], int(degree), float(to), float(err)) for row, degree, to, err in rows]
+
+
+@pytest.mark.parametrize("name", ["kTanh16", "kTanh32"])
+def test_fits_of_the_tanh(name):
+    """In relative error, over 20,000 points, by the coefficients as they are used: in float32, with the sums in 64 bits."""
+    for c, degree, to, err in coefficients(name):
+        assert len(c) == degree + 1
+        u = np.linspace(1e-6, to, 20001)
+        for cs, more in ((c, 0.0), ([float(np.float32(x)) for x in c], 2.0 ** -24)):
+            p = sum(x * u ** (2 * k) for k, x in enumerate(cs))
+            off = np.abs(p * u / np.tanh(u) - 1).max()
+            assert off <= err * 1.02 + more, (name, to, off)

@@ -94,3 +94,42 @@ def test_large_values_under_a_bias(H, slope, out_dtype):  # noqa: F811
     for h, s in enumerate([slope, -slope / 4]):
         ref = SO.attention(qh[:, h], kh[:, 0], vh[:, 0], scale=1.0, slope=float(np.float32(s)))
         S.check_rows(out[:, h], lse[:, h], ref, f"head {h}")
+
+
+# relative error of the tanh's polynomials (csrc/hashattn_api.cu) up to half the cap, and up to the cap
+FITS = {torch.bfloat16: (5.4e-7, 5.9e-7), torch.float32: (1.3e-8, 5.0e-8)}
+
+
+@TYPES
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("upto", [0.5, 1.0, 4.0])
+@pytest.mark.parametrize("bias", [False, True], ids=["cap", "cap-bias"])
+@pytest.mark.parametrize("whole", [True, False], ids=["tile", "part"])
+def test_the_cap_itself(H, whole, bias, upto, d, out_dtype):  # noqa: F811
+    """All keys of a row score x, a number of bf16: lse - log(keys) is the capped x, read off to the polynomial's own error
+    (that of bf16 weights would not do for float32 results). One tile of keys or less; slopes of 0 take the biased kernel.
+
+    Relative to the score: the fit; its roundings, 2.5 of 2^-24 up to half the cap (the first coefficient, the last sum
+    and a twelfth of what comes before) and 4.5 up to the cap (the ratio to the cap and the product with it, a
+    quarter of what comes before); 2.5 of lse (the sum with the logarithm, log 2 and the product with it). Absolute: the exponential
+    2^-22, the sum of the weights 2^-24 an addition (13 in a row for float32 results, 70 else), the logarithm 2^-21.
+    Beyond the cap 2^-22 cap."""
+    g = torch.Generator(device="cuda").manual_seed(75)
+    n, Hq, cap, keys = 60, 4, 50.0, (64 if out_dtype == torch.float32 else 128) - (0 if whole else 9)
+    x = ((torch.rand(n, Hq, generator=g, device="cuda") * 0.4 + 0.6) * upto * cap).bfloat16()
+    x[::2] *= -1
+    K, V, table = S.pages(g, [1] * n, [keys] * n, 128, 1, d, "token", S.Opts())
+    q = torch.zeros(n, Hq, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 3] = x
+    K.zero_()
+    K[..., 3] = 1.0
+    _, lse = S.chunk(H, q, K, V, table, [1] * n, [keys] * n, 1, S.Opts(cap=cap, scale=1.0, slopes=[0.0] * Hq if bias else None), out_dtype)
+    z = x.double().cpu().numpy()
+    want = cap * np.tanh(z / cap)
+    got = lse.double().cpu().numpy() - np.log(keys)
+    adds = 13 if out_dtype == torch.float32 else 70
+    tol = np.abs(want) * (FITS[out_dtype][upto > 0.5] + (5 if upto == 0.5 else 7) * 2.0 ** -24) + 2.0 ** -22 + adds * 2.0 ** -24 + 2.0 ** -21
+    if upto > 1:
+        tol = tol + 2.0 ** -22 * cap
+    off = np.abs(got - want) / tol
+    assert off.max() <= 1, off.max()
