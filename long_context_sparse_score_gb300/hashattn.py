@@ -762,6 +762,14 @@ def hash_attn_append_axes(tokens, cache, q, k, v, page_table, cu, seq_lens, posi
     _check(lib().hash_attn_append_axes(tokens, cache, rope, at, pos_st, *a, _raw_stream(device) if stream is None else _stream(stream)))
 
 
+def _int32(x, what) -> int:
+    """A structure's field would keep the low 32 bits of anything else, without a word."""
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{what} must be a 32-bit number (got {x})")
+    return x
+
+
 def make_paging(page_table, n_pages: int, page_size: int, total: int) -> HAPaging:
     """ha_paging of sequences whose pages are in ``page_table`` int32 [n_seq, max_pages], out of a pool
     of ``n_pages``; ``total``: rows that the packed buffers have room for."""
@@ -769,7 +777,7 @@ def make_paging(page_table, n_pages: int, page_size: int, total: int) -> HAPagin
         raise ValueError("page_table must be int32 [n_seq, max_pages] with contiguous rows")
     p = HAPaging()
     p.n_seq, p.max_pages = page_table.shape
-    p.total, p.n_pages, p.page_size = int(total), int(n_pages), int(page_size)
+    p.total, p.n_pages, p.page_size = _int32(total, "total"), _int32(n_pages, "n_pages"), _int32(page_size, "page_size")
     p.table_st = page_table.stride(0)
     return p
 
@@ -894,7 +902,9 @@ def score_opts(*, scale: float = 0.0, softcap: float = 0.0, window: int = 0, slo
     keys before first[s] by none. ``slopes`` float32 [h_q], ``prefix`` and ``first`` int32 [n_seq], contiguous device
     tensors (which it keeps), raw addresses or None."""
     o = HAScoreOpts()
-    o.scale, o.softcap, o.window = scale, softcap, int(window)
+    o.scale, o.softcap, o.window = scale, softcap, _int32(window, "window")
+    if (scale and not o.scale) or (softcap and not o.softcap):  # 0 would say: the default
+        raise ValueError(f"scale and softcap must be 0 or float32 numbers (got {scale}, {softcap})")
     o.slopes, o.prefix, o.first = (_ptr(t) for t in (slopes, prefix, first))
     tensors = tuple(None if t.__class__ is int else t for t in (slopes, prefix, first))
     o.tensors = tensors if any(t is not None for t in tensors) else None
