@@ -558,20 +558,26 @@ __device__ __forceinline__ void shape_scores(uint32_t (&x)[N], const PackedParam
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[16]) { tmem_ld16(addr, x); }
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&x)[32]) { tmem_ld32(addr, x); }
 
+// Whether `x` holds in any of the warp's rows of tokens (valid, `tokens` by lane). LATE: all rows vote and the others
+// are left out of the outcome (16,384 biased tokens at d 64: 1,241 us, with the condition in the vote 1,329; 24
+// capped prompts of 1,000 with float32 results 359 and 366; 16,384 capped tokens with bf16 results 1,479 and 1,441).
+template <bool LATE>
+__device__ __forceinline__ bool of_tokens(bool x, bool valid, uint32_t tokens) {
+    return LATE ? (__ballot_sync(0xffffffffu, x) & tokens) != 0u : (bool)__any_sync(0xffffffffu, valid && x);
+}
+
 // The weights of a tile of 128 columns of shaped scores, all seen, keys on one side of the rows: score k
 // of the tile, less the reference, is x scale (CAP: the polynomial) + row, and with BIAS + slope k.
 // Returns the columns done: those before the first 32 where a product of any of the warp's valid rows is too
-// large for the polynomial, or (BIAS) a score more than kShapedRescale above the reference. (All rows vote
-// and those of no token are left out of the outcome: 24 biased prompts 361 us, with that as a condition of each
-// row's vote 384.)
+// large for the polynomial, or (BIAS) a score more than kShapedRescale above the reference.
 //
 // 32 columns at a time in a loop: what bounds short prompts is the instruction cache, which the item's
 // first and last tiles share with this code. UNROLL 4 lets the exponentials of 32 columns run under the
 // multiplications of the next (in a kernel of its own: beside the loop it is no faster). Capped scores,
-// loop / unrolled: 24 prompts of 1,000 tokens 267 / 288 us, 8 of 2,048 286 / 282, 4 of 4,096 493 / 481, one of
-// 16,384 1,730 / 1,657; at d 64 the loop is the faster at any length (223 / 245, 235 / 245, 403 / 410,
-// 1,384 / 1,383), and for biased ones at d 128 up to 4,096 tokens (24 of 1,000: 260 / 292, 4 of 4,096:
-// 477 / 477).
+// loop / unrolled: 24 prompts of 1,000 tokens 261 / 303 us, 8 of 2,048 276 / 296, 4 of 4,096 469 / 480, one of
+// 8,192 445 / 448, two of 8,192 857 / 851, one of 12,288 950 / 930, one of 16,384 1,640 / 1,605, one of 24,576
+// 3,760 / 3,715; 64 decodes over up to 16,000 keys 343 / 348, in a window of 4,096 179 / 182, 48 over 500 to 1,500
+// keys 56 / 62. At d 64 the loop was the faster at any length, and for biased ones at d 128 up to 4,096 tokens.
 template <bool CAP, bool BIAS, int UNROLL>
 __device__ __forceinline__ int fast_tile(uint32_t tS, const PackedParamsEx& p, float row, float slope, bool valid, uint64_t (&sum)[2]) {
     const uint64_t scale = pack2(p.scale, p.scale);
@@ -601,8 +607,7 @@ __device__ __forceinline__ int fast_tile(uint32_t tS, const PackedParamsEx& p, f
                 top[u] = fmaxf(fmaxf(top[u], y[k]), y[k + 1]);
             }
         }
-        const bool stop = (__ballot_sync(0xffffffffu, (CAP && fmaxf(big[0], big[1]) > p.fit[0]) ||
-                                                          (BIAS && fmaxf(top[0], top[1]) > kShapedRescale)) & tokens) != 0u;
+        const bool stop = of_tokens<BIAS>((CAP && fmaxf(big[0], big[1]) > p.fit[0]) || (BIAS && fmaxf(top[0], top[1]) > kShapedRescale), valid, tokens);
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
             const float a = ex2(y[k]), b = ex2(y[k + 1]);
@@ -649,7 +654,7 @@ __device__ __forceinline__ int fast_parts(uint32_t tS, const uint32_t (&part_at)
             x[k] = __float_as_uint(a);
             x[k + 1] = __float_as_uint(b);
         }
-        const bool stop = (__ballot_sync(0xffffffffu, (CAP && big > p.fit[0]) || (BIAS && top > kShapedRescale)) & tokens) != 0u;
+        const bool stop = of_tokens<true>((CAP && big > p.fit[0]) || (BIAS && top > kShapedRescale), valid, tokens);
         const float more = parts16<16, true>(x, 0.f, 0.f, q);
         if (stop) return c0;
         l += more;
