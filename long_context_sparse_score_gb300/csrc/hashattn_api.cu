@@ -1397,7 +1397,7 @@ constexpr int64_t kMaxKeys = (int64_t)1 << 30;     // max_pages * page_size
 constexpr int64_t kMaxStride = (int64_t)1 << 36;   // elements; a tensor map holds strides below 2^40 bytes
 constexpr int kMaxGroup = 128;                     // query heads per KV head in a tile of 128 rows
 constexpr int kWholeTiles = 4;                     // items of no more key tiles are not parted
-constexpr int kLongItems = 2048;                   // keys a sequence from which fast_tile is unrolled (measured there)
+constexpr int kLongItems = 8192;                   // tokens a prompt from which fast_tile is unrolled (measured there)
 
 ha_status check_tokens(const ha_tokens* t) {
     if (t == nullptr) return fail(HA_ERR_INVALID_ARG, "tokens is NULL");
@@ -1667,7 +1667,7 @@ ha_status packed_attention(const ha_tokens* t, const ha_cache* c, const ha_score
     const bool merge = grid > 1 && p.split;
     if (opts != nullptr) {
         set_opts(p, opts, t->d, f32);
-        p.long_items = (c != nullptr ? max_len : t->total / t->n_seq) >= kLongItems;
+        p.long_items = c == nullptr && t->total / t->n_seq >= kLongItems;
     }
     const bool masked = p.window > 0 || p.prefix != nullptr || p.first != nullptr;
     if (!p.shaped && !masked) {

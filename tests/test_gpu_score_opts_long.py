@@ -1,9 +1,11 @@
-"""Capped scores of long sequences (2,048 keys or more have a kernel of their own for bf16 results of head dim 128), in
-items of two row tiles and of one, against the float64 oracle."""
+"""Capped scores of long sequences, in items of two row tiles and of one, against the float64 oracle. (Prompts of 8,192
+tokens or more have a kernel of their own for bf16 results of head dim 128.)"""
+import numpy as np
 import pytest
 import torch
 
 import test_gpu_score_opts as S
+from oracle import serving_oracle as SO
 from test_gpu_score_opts import H  # noqa: F401  (fixture)
 
 pytestmark = pytest.mark.gpu
@@ -44,3 +46,30 @@ def test_chunk_over_a_wide_table(H, cap, window, large, order):  # noqa: F811
     q = S.rand(g, sum(new), Hq, d, scale=3.0)
     out, lse = S.chunk(H, q, K, V, wide, new, lens, Hkv, o)
     S.check_chunk(q, K, V, wide, new, lens, o, out, lse, heads=[0, 7])
+
+
+LONG = {"cap": dict(cap=50.0), "cap-window": dict(cap=50.0, window=3000), "cap-first": dict(cap=30.0, first=[1000, 5])}
+
+
+@pytest.mark.parametrize("large", [False, True], ids=["ordinary", "some-large"])
+@pytest.mark.parametrize("G", [1, 3, 8])
+@pytest.mark.parametrize("name", LONG)
+def test_long_prompts(H, name, G, large):  # noqa: F811
+    """Two prompts of 8,192 tokens on average; rows at the ends of tiles and anywhere."""
+    g = torch.Generator(device="cuda").manual_seed(83)
+    new, d = [8300, 8090], 128
+    q, k, v = S.rand(g, sum(new), G, d, scale=3.0), S.rand(g, sum(new), 1, d), S.rand(g, sum(new), 1, d)
+    if large:
+        k[torch.randperm(sum(new), generator=g, device="cuda")[:300]] *= 6
+    o = S.Opts(**LONG[name])
+    out, lse = S.prefill(H, q, k, v, new, o)
+    a = 0
+    for s, n in enumerate(new):
+        kh, vh = (x[a:a + n, 0].double().cpu().numpy() for x in (k, v))
+        opts = o.of(s, 0)
+        for i in {0, 1, 127, 128, 129, 255, 256, 1000, 4000, 4095, 4096, n - 1, *np.random.default_rng(s).integers(0, n, 30).tolist()}:
+            ref = SO.attention(q[a + i:a + i + 1, G - 1].double().cpu().numpy(), kh[:i + 1], vh[:i + 1], **opts)
+            S.check_rows(out[a + i:a + i + 1, G - 1], lse[a + i:a + i + 1, G - 1], ref, f"seq {s} row {i}")
+        a += n
+    again = S.prefill(H, q, k, v, new, o)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
