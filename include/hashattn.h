@@ -757,7 +757,10 @@ typedef struct {
  *                 for a page outside [0, n_pages) (one given back is left out; one taken
  *                 is entered as -1), HA_DEVERR_STATE where more pages come back than there
  *                 are
- * A page belongs to one sequence. No other buffers may overlap.
+ * A page belongs to one sequence of the plan: ending two whose rows share a page would give it back
+ * twice. Documents of one sequence (ha_score_opts) are one sequence here and in the append; for
+ * the attention the caller makes cu, seq_lens, first and copies of the table's row out of what was
+ * planned. No other buffers may overlap.
  * Errors: HA_ERR_INVALID_ARG, HA_ERR_UNSUPPORTED (slots past 2^31) before anything is
  * enqueued; HA_ERR_CUDA on a failed launch.
  */
@@ -813,7 +816,8 @@ ha_status hash_attn_append_axes(const ha_tokens* tokens, const ha_cache* cache, 
  *            sequence, later ones too (an image, an instruction; prefix[s] = nk: attention both ways)
  *   first    int32 [n_seq] (device), or NULL: the sequence's first key (what lies before it is
  *            padding, or another document: tokens of several documents in one sequence are
- *            given as several sequences that share a row of the table)
+ *            given as several sequences of this call, each with the same pages in its row of the
+ *            table and its document's end as its length)
  *   reserved must be 0
  * prefix and first are clamped to [0, nk]. Pages whose keys no token of the sequence sees are not
  * read: their table entries and contents may be anything.

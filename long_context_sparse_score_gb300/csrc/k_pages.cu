@@ -9,8 +9,8 @@
 // given back. So nothing waits for another sequence, and the result does not depend on timing.
 //
 // Bound by latency: a launch, the lengths, a scan, the pages, the table. 64 sequences of one token 2.8 us
-// (one CTA), 6 prompts of 39,000 tokens 4.7, 3,000 sequences of which 10 % add 85,000 tokens and 5 %
-// end 13.1 (4.4 where all decode); the bytes would take 0.1. One CTA for up to 1,024 sequences with few rows,
+// (one CTA), 6 prompts of 39,000 tokens 5.2, 3,000 sequences of which 10 % add 85,000 tokens and 5 %
+// end 13.2 (4.4 where all decode); the bytes would take 0.1. One CTA for up to 1,024 sequences with few rows,
 // else one cluster of 8, and no workspace: up to kShared sequences every CTA scans all of them, one to a
 // thread, and they share the rows; more are cut among the CTAs, which write their sums into each
 // other's shared memory (1,000 sequences, 10 % prompts, 5 % ending: 13.3 us scanned by all, 10.4 cut; read
@@ -352,7 +352,7 @@ cudaError_t launch_plan_pages(const PagesParams& p0, cudaStream_t st) {
     // One CTA as long as its threads have a sequence and a few rows each, else a cluster.
     const bool one = p.n_seq <= kMostThreads && p.total <= 4096;
     // 768 threads: a barrier of fewer warps, as long as each has a sequence (3,000 mixed sequences 13.4 -> 13.1 us, all
-    // decoding 4.9 -> 4.4, 6 prompts 5.1 -> 4.7; with 512 14.6, 3.9 and 5.0).
+    // decoding 4.9 -> 4.4, 6 prompts 5.6 -> 5.2; with 512 14.6, 3.9 and 5.0).
     int threads = p.n_seq <= kCluster * kThreads ? kThreads : kMostThreads;
     if (one) {
         const int want = p.n_seq > p.total / 8 ? p.n_seq : p.total / 8;

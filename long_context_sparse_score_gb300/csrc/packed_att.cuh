@@ -47,19 +47,19 @@
 // |pos - j|, over max(first, pos - window + 1) <= j < max(pos + 1, prefix).
 // - Masks leave a row one interval of keys whose ends grow with the row, so an item has one range of
 //   key tiles, and their sum over a row of items a closed form (MaskedItems): tiles outside it are neither
-//   read nor multiplied. 16,384 tokens in a window of 1,024: 262 us (all of them: 1,393).
+//   read nor multiplied. 16,384 tokens in a window of 1,024: 265 us (all of them: 1,393).
 // - A cap is a polynomial (shape_scores): five multiply-adds a column more, which is what bounds it
-//   (tensor cores 48 % busy at 4,096 tokens): 16,384 tokens capped at 50: 1.57 ms, 1.40 PFLOP/s, 74 % of
+//   (tensor cores 47 % busy at 4,096 tokens): 16,384 tokens capped at 50: 1.61 ms, 1.36 PFLOP/s, 72 % of
 //   cuBLAS's burst. Capped scores lie in a known range, so a row keeps the reference that its first keys
 //   give (no maximum, no rescaling).
 // - A bias grows towards the row's own position: key tiles are taken from the last one back, so that the
-//   reference is found in the first. 24 prompts of 33 to 2,500 tokens: 386 us, 48 %.
+//   reference is found in the first. 24 prompts of 33 to 2,500 tokens: 364 us, 51 %.
 // - The code of a tile decides as much as its operations: the instruction cache is shared by eight softmax
 //   warps that are never at the same place. So there is one short path for tiles that all rows see (fast_tile,
 //   fast_parts) and one for all others, in a loop of 32 columns. Masks in the fast path cost more than they
 //   saved (64 prompts of 300 tokens capped: 153 -> 217 us), and so did shaping an item's first tile twice for its
 //   reference (153 -> 170; a pass over its raw products instead, see begin_fixed: 148 -> 146).
-// 64 decodes in a window of 4,096 keys, capped, pages of 16: 175 us, 5.5 TB/s, 81 % (without options over
+// 64 decodes in a window of 4,096 keys, capped, pages of 16: 169 us, 5.7 TB/s, 84 % (without options over
 // as many keys 180).
 //
 // 12 warps: two softmax warpgroups (thread = row: a tcgen05.ld gives a thread
